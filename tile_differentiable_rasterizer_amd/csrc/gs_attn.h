@@ -15,7 +15,9 @@ struct AttnArgs {
   int32_t batch, q_len, k_len, kv_heads, group, d;
   int32_t rows;    // q_len * group
   int32_t splits;  // of the long axis: keys (out, dq) or rows (dk, dv)
-  float scale, scale_log2;
+  float scale;
+  float slope;     // |scale| log2(e), above 0
+  uint32_t flip;   // sign of the scale, to be put on the queries: 0 or the sign bits of a register
   const int32_t* ranges;
   int64_t ranges_b, ranges_r;
   const uint8_t* mask;
@@ -78,7 +80,6 @@ __device__ __forceinline__ uint64_t wave_or(uint64_t x) {
   return x;
 }
 
-constexpr int kAttnRows = 128;  // rows of a workgroup: four wavefronts of 32
 constexpr int kAttnKeys = 64;   // keys of a tile
 
 // Ends of the keys that the workgroup's rows may see.
@@ -86,11 +87,23 @@ struct Seen {
   int first, last;      // some row sees something in here
   int all_from, all_to; // every row that sees anything sees all of this
 };
-// `mine`: the lane's range; `live`: its row exists and the range is not empty.
-__device__ __forceinline__ Seen block_seen(int2 mine, bool live, int (*scratch)[4]) {
+// `mine`: the ranges of the lane's NR rows, empty for a row that does not exist.
+template <int NR>
+__device__ __forceinline__ Seen block_seen(const int2 (&mine)[NR], int (*scratch)[4]) {
   const int w = threadIdx.x >> 6;
-  const int a = wave_min_i(live ? mine.x : INT32_MAX), b = wave_max_i(live ? mine.y : 0);
-  const int c = wave_max_i(live ? mine.x : 0), d = wave_min_i(live ? mine.y : INT32_MAX);
+  int a = INT32_MAX, b = 0, c = 0, d = INT32_MAX;
+#pragma unroll
+  for (int n = 0; n < NR; ++n)
+    if (mine[n].x < mine[n].y) {
+      a = min(a, mine[n].x);
+      b = max(b, mine[n].y);
+      c = max(c, mine[n].x);
+      d = min(d, mine[n].y);
+    }
+  a = wave_min_i(a);
+  b = wave_max_i(b);
+  c = wave_max_i(c);
+  d = wave_min_i(d);
   if (__lane_id() == 0) {
     scratch[w][0] = a;
     scratch[w][1] = b;
@@ -120,18 +133,71 @@ __device__ __forceinline__ uint64_t block_word(uint64_t mine, uint64_t* scratch)
   return r;
 }
 
-// Copies the rows whose bit is set in `word` from head (b, hk) of x, tokens t0.. , to a tile; the
-// other rows, and what lies past D, are zeros (nothing there is read).
-template <typename T, int DP, int ROWS>
-__device__ __forceinline__ void stage_tokens(char* tile, const gs_heads& x, int b, int h, int t0, int d, uint64_t word) {
+// Staging of 64 tokens of one head to a tile by 256 threads.  Where every token counts, the loads
+// go straight to LDS (16 bytes a lane, a wavefront's 64 chunks in a row), so that they are in
+// flight while the tile before is worked on, and cost no registers; the swizzle is in the address
+// that a lane reads.  Where some do not, the chunks pass through registers and the rows that do
+// not count are zeros (nothing there is read).  Chunks past D are zeros from clear() on.
+template <typename T, int DP>
+struct Stage {
   using Ti = Tile<T, DP>;
-  for (int c = threadIdx.x; c < ROWS * Ti::kChunks; c += 256) {
-    const int r = c / Ti::kChunks, ch = c - r * Ti::kChunks;
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (((word >> r) & 1) && ch * Ti::kPer < d)
-      v = *reinterpret_cast<const f32x4*>(head_ptr<T>(x, b, t0 + r, h) + ch * Ti::kPer);
-    *reinterpret_cast<f32x4*>(tile + Ti::at(r, ch)) = v;
+  static constexpr int kEach = kAttnKeys * Ti::kChunks / 256;
+  static constexpr int kBytes = kAttnKeys * Ti::kRowBytes;
+  static_assert(kEach * 256 == kAttnKeys * Ti::kChunks, "whole chunks a thread");
+
+  // Before the first tile, where D < DP: the chunks past D stay zero.
+  static __device__ __forceinline__ void clear(char* lds, int bytes) {
+    for (int i = threadIdx.x * 16; i < bytes; i += 256 * 16) *reinterpret_cast<f32x4*>(lds + i) = (f32x4)0.0f;
   }
-}
+
+  // Tokens t0 .. t0 + 63 of `head` (its token 0); bit r of `word`: token t0 + r counts.
+  static __device__ __forceinline__ void load(char* tile, const T* head, int64_t token_stride, int t0, int d,
+                                              uint64_t word) {
+    const T* base = head + t0 * token_stride;
+    if (word == ~0ull) {
+      const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int c = i * 256 + threadIdx.x, r = c / Ti::kChunks, ch = (c - r * Ti::kChunks) ^ Ti::mix(r);
+        if (ch * Ti::kPer < d)
+          __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(base + r * token_stride + ch * Ti::kPer),
+                                           (__attribute__((address_space(3))) void*)(tile + (i * 4 + wave) * 1024), 16, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int c = i * 256 + threadIdx.x, r = c / Ti::kChunks, ch = (c - r * Ti::kChunks) ^ Ti::mix(r);
+        f32x4 v = (f32x4)0.0f;
+        if (((word >> r) & 1) && ch * Ti::kPer < d) v = *reinterpret_cast<const f32x4*>(base + r * token_stride + ch * Ti::kPer);
+        *reinterpret_cast<f32x4*>(tile + c * 16) = v;
+      }
+    }
+  }
+};
+
+// The tiles of a workgroup's keys, one after another, without those that no row sees.  Every
+// thread of the workgroup calls next() (its answer is the same for all of them).
+struct Tiles {
+  int t, end;       // next to look at, past the last
+  int k0;           // the tile's first key
+  uint64_t word;    // keys that some row sees (0: no tile left)
+  bool ragged;      // some row sees only a part of them by its range
+
+  template <int NR>
+  __device__ __forceinline__ void next(const AttnArgs& a, int b, const Seen& seen, const int2 (&mine)[NR], uint64_t* scratch) {
+    word = 0;
+    for (; t < end && word == 0; ++t) {
+      k0 = t * kAttnKeys;
+      word = key_word(a, b, k0);
+      ragged = k0 < seen.all_from || k0 + kAttnKeys > seen.all_to;
+      if (ragged) {
+        uint64_t some = 0;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) some |= range_word(mine[n].x, mine[n].y, k0);
+        word &= block_word(some, scratch);
+      }
+    }
+  }
+};
 
 }  // namespace gs

@@ -10,13 +10,17 @@
 // of 2^-8 of each weight at most, of the order of the output's own rounding); everything else is float32.
 #include "gs_attn.h"
 
+#ifndef GS_NR
+#define GS_NR 1
+#endif
+
 namespace gs {
 
-template <typename T, int DP>
-__global__ __launch_bounds__(256) void k_attn_fwd(AttnArgs a) {
+template <typename T, int DP, int NR>
+__global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
   using Ti = Tile<T, DP>;
-  __shared__ __align__(16) char kt[kAttnKeys * Ti::kRowBytes];
-  __shared__ __align__(16) char vt[kAttnKeys * Ti::kRowBytes];
+  using St = Stage<T, DP>;
+  __shared__ __align__(16) char lds[4][St::kBytes];  // keys and values of two tiles
   __shared__ int scratch[4][4];
   __shared__ uint64_t words[4];
   const int nbh = a.batch * a.kv_heads;
@@ -24,110 +28,170 @@ __global__ __launch_bounds__(256) void k_attn_fwd(AttnArgs a) {
   const int split = rest % a.splits, rt = rest / a.splits;
   const int b = bh / a.kv_heads, hk = bh - b * a.kv_heads;
   const int lane = __lane_id(), half = lane >> 5;
-  const int row = rt * kAttnRows + (threadIdx.x >> 6) * 32 + (lane & 31);
-  const bool valid = row < a.rows;
-  const int i = valid ? row / a.group : 0, h = hk * a.group + (valid ? row - i * a.group : 0);
-  int2 range = row_range(a, b, i);
-  const bool live = valid && range.x < range.y;
-  const Seen seen = block_seen(range, live, scratch);
+  const int row0 = (rt * 4 + (threadIdx.x >> 6)) * 32 * NR + (lane & 31);
 
-  Frag<T> qf[DP / 16];
-  const T* qp = head_ptr<T>(a.q, b, i, h);
+  int2 range[NR];
+  Frag<T> qf[NR][DP / 16];
 #pragma unroll
-  for (int s = 0; s < DP / 16; ++s) qf[s] = frag_mem<T>(qp, a.d, s, live);
+  for (int n = 0; n < NR; ++n) {
+    const int row = row0 + 32 * n;
+    const bool valid = row < a.rows;
+    const int i = valid ? row / a.group : 0, h = hk * a.group + (valid ? row - i * a.group : 0);
+    range[n] = row_range(a, b, i);
+    const bool live = valid && range[n].x < range[n].y;
+    if (!live) range[n] = make_int2(0, 0);
+    const T* qp = head_ptr<T>(a.q, b, i, h);
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s) qf[n][s] = frag_flip(frag_mem<T>(qp, a.d, s, live), a.flip);
+  }
+  const Seen seen = block_seen<NR>(range, scratch);
 
-  f32x16 o[DP / 32];
+  f32x16 o[NR][DP / 32];
+  float m[NR], base[NR], l[NR];  // m: maximum of the raw scores that the sums are relative to; base = m * slope
 #pragma unroll
-  for (int t = 0; t < DP / 32; ++t) o[t] = (f32x16)0.0f;
-  float m = -INFINITY, l = 0.0f;
-
-  const int t_lo = seen.first / kAttnKeys, t_n = seen.last > seen.first ? (seen.last + kAttnKeys - 1) / kAttnKeys - t_lo : 0;
-  const int t_begin = t_lo + (int)((int64_t)t_n * split / a.splits), t_end = t_lo + (int)((int64_t)t_n * (split + 1) / a.splits);
-  for (int t = t_begin; t < t_end; ++t) {
-    const int k0 = t * kAttnKeys;
-    uint64_t word = key_word(a, b, k0);
-    const bool ragged = k0 < seen.all_from || k0 + kAttnKeys > seen.all_to;
-    if (ragged) word &= block_word(live ? range_word(range.x, range.y, k0) : 0, words);
-    if (word == 0) continue;  // the same for the workgroup
-    stage_tokens<T, DP, kAttnKeys>(kt, a.k, b, hk, k0, a.d, word);
-    stage_tokens<T, DP, kAttnKeys>(vt, a.v, b, hk, k0, a.d, word);
-    __syncthreads();
-
-    f32x16 s[2];
+  for (int n = 0; n < NR; ++n) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      s[j] = (f32x16)0.0f;
-#pragma unroll
-      for (int st = 0; st < DP / 16; ++st) s[j] = mma(Ti::frag_rows(kt, 32 * j, st), qf[st], s[j]);
-    }
-    uint64_t mine = word;
-    if (ragged && live) mine &= range_word(range.x, range.y, k0);
-    float top = m;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        float x = s[j][r] * a.scale_log2;
-        if (mine != ~0ull) x = (mine >> (32 * j + crow(r, half))) & 1 ? x : -INFINITY;
-        s[j][r] = x;
-        top = fmaxf(top, x);
-      }
-    top = pair_max(top);
-    const float base = top == -INFINITY ? 0.0f : top;  // nothing seen yet: every weight 2^-inf = 0
-    const float keep = __builtin_amdgcn_exp2f(m - base);
-    float sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const float p = __builtin_amdgcn_exp2f(s[j][r] - base);
-        s[j][r] = p;
-        sum += p;
-      }
-    l = l * keep + sum;
-    m = top;
-#pragma unroll
-    for (int dt = 0; dt < DP / 32; ++dt) o[dt] *= keep;
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      const Frag<T> p = frag_of<T>(s[ks >> 1], ks & 1);
-#pragma unroll
-      for (int dt = 0; dt < DP / 32; ++dt) o[dt] = mma(Ti::frag_cols(vt, 16 * ks, 32 * dt), p, o[dt]);
-    }
-    __syncthreads();
+    for (int t = 0; t < DP / 32; ++t) o[n][t] = (f32x16)0.0f;
+    m[n] = -INFINITY;
+    base[n] = l[n] = 0.0f;
   }
 
-  l = pair_sum(l);
-  if (!valid) return;
-  if (a.splits == 1) {
-    const bool none = !live || l == 0.0f;
-    const float inv = none ? 0.0f : 1.0f / l;
-    T* op = head_ptr<T>(a.out, b, i, h);
+  const int t_lo = seen.first / kAttnKeys, t_n = seen.last > seen.first ? (seen.last + kAttnKeys - 1) / kAttnKeys - t_lo : 0;
+  Tiles tile;
+  tile.t = t_lo + (int)((int64_t)t_n * split / a.splits);
+  tile.end = t_lo + (int)((int64_t)t_n * (split + 1) / a.splits);
+  const T* kh = head_ptr<T>(a.k, b, 0, hk);
+  const T* vh = head_ptr<T>(a.v, b, 0, hk);
+  if (a.d < DP) {
+    St::clear(lds[0], 4 * St::kBytes);
+    __syncthreads();
+  }
+  tile.next(a, b, seen, range, words);
+  int buf = 0;
+  if (tile.word) {
+    St::load(lds[0], kh, a.k.token_stride, tile.k0, a.d, tile.word);
+    St::load(lds[1], vh, a.v.token_stride, tile.k0, a.d, tile.word);
+  }
+  const float slack = 8.0f / a.slope;  // weights up to 2^8 before the sums are scaled again
+  while (tile.word) {
+    const uint64_t word = tile.word;
+    const int k0 = tile.k0;
+    const bool ragged = tile.ragged;
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt 0: this tile's loads to LDS
+    __syncthreads();                     // ... of every wavefront; and the tile before is done with
+    tile.next(a, b, seen, range, words);
+    if (tile.word) {
+      St::load(lds[2 - 2 * buf], kh, a.k.token_stride, tile.k0, a.d, tile.word);
+      St::load(lds[3 - 2 * buf], vh, a.v.token_stride, tile.k0, a.d, tile.word);
+    }
+    const char *kt = lds[2 * buf], *vt = lds[2 * buf + 1];
+    buf ^= 1;
+
+    f32x16 s[NR][2];
 #pragma unroll
-    for (int dt = 0; dt < DP / 32; ++dt)
+    for (int j = 0; j < 2; ++j) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int d = 32 * dt + 8 * c + 4 * half;
-        float x[4];
+      for (int n = 0; n < NR; ++n) s[n][j] = (f32x16)0.0f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = none ? 0.0f : o[dt][4 * c + e] * inv;
-        if (d < a.d) store_elems<4>(op + d, x);
+      for (int st = 0; st < DP / 16; ++st) {
+        const Frag<T> kf = Ti::frag_rows(kt, 32 * j, st);
+#pragma unroll
+        for (int n = 0; n < NR; ++n) s[n][j] = mma(kf, qf[n][st], s[n][j]);
       }
-    if (a.lse && half == 0)
-      a.lse[((int64_t)b * a.kv_heads * a.group + h) * a.q_len + i] = none ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
-  } else {
-    const int64_t at = ((int64_t)split * nbh + bh) * a.rows + row;
-    float* op = a.part + at * DP;
+    }
+    if (ragged || word != ~0ull) {
 #pragma unroll
-    for (int dt = 0; dt < DP / 32; ++dt)
+      for (int n = 0; n < NR; ++n) {
+        // a row that sees nothing takes the tile's keys as they are; its result is not used
+        uint64_t mine = word;
+        if (ragged && range[n].x < range[n].y) mine &= range_word(range[n].x, range[n].y, k0);
+        const uint32_t lo = (uint32_t)mine >> (4 * half), hi = (uint32_t)(mine >> 32) >> (4 * half);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = o[dt][4 * c + e];
-        store_elems<4>(op + 32 * dt + 8 * c + 4 * half, x);
+        for (int r = 0; r < 16; ++r) {
+          s[n][0][r] = (lo >> crow(r, 0)) & 1 ? s[n][0][r] : -INFINITY;
+          s[n][1][r] = (hi >> crow(r, 0)) & 1 ? s[n][1][r] : -INFINITY;
+        }
       }
-    if (half == 0) a.part_ml[at] = make_float2(live ? m : -INFINITY, live ? l : 0.0f);
+    }
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      float top = fmaxf(s[n][0][0], s[n][1][0]);
+#pragma unroll
+      for (int r = 1; r < 16; ++r) top = fmaxf(fmaxf(top, s[n][0][r]), s[n][1][r]);
+      top = pair_max(top);
+      if (__any(top > m[n] + slack)) {
+        const float to = fmaxf(m[n], top), before = base[n];
+        base[n] = to == -INFINITY ? 0.0f : to * a.slope;
+        const float keep = m[n] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(before - base[n]);
+        m[n] = to;
+        l[n] *= keep;
+#pragma unroll
+        for (int dt = 0; dt < DP / 32; ++dt) o[n][dt] *= keep;
+      }
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const float p = __builtin_amdgcn_exp2f(fmaf(s[n][j][r], a.slope, -base[n]));
+          s[n][j][r] = p;
+          sum += p;
+        }
+      l[n] += sum;
+    }
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      Frag<T> p[NR];
+#pragma unroll
+      for (int n = 0; n < NR; ++n) p[n] = frag_of<T>(s[n][ks >> 1], ks & 1);
+#pragma unroll
+      for (int dt = 0; dt < DP / 32; ++dt) {
+        const Frag<T> vf = Ti::frag_cols(vt, 16 * ks, 32 * dt);
+#pragma unroll
+        for (int n = 0; n < NR; ++n) o[n][dt] = mma(vf, p[n], o[n][dt]);
+      }
+    }
+  }
+
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+    const int row = row0 + 32 * n;
+    const float sum = pair_sum(l[n]);
+    if (row >= a.rows) continue;
+    const bool live = range[n].x < range[n].y;
+    const int i = row / a.group, h = hk * a.group + row - i * a.group;
+    const bool none = !live || sum == 0.0f;  // (a row of NaN is not none)
+    if (a.splits == 1) {
+      const float inv = none ? 0.0f : 1.0f / sum;
+      T* op = head_ptr<T>(a.out, b, i, h);
+#pragma unroll
+      for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int d = 32 * dt + 8 * c + 4 * half;
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = none ? 0.0f : o[n][dt][4 * c + e] * inv;
+          if (d < a.d) store_elems<4>(op + d, x);
+        }
+      if (a.lse && half == 0)
+        a.lse[((int64_t)b * a.kv_heads * a.group + h) * a.q_len + i] = none ? -INFINITY : (base[n] + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+    } else {
+      const int64_t at = ((int64_t)split * nbh + bh) * a.rows + row;
+      float* op = a.part + at * DP;
+      if (!none) {
+#pragma unroll
+        for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = o[n][dt][4 * c + e];
+            store_elems<4>(op + 32 * dt + 8 * c + 4 * half, x);
+          }
+      }
+      if (half == 0) a.part_ml[at] = make_float2(none ? -INFINITY : base[n], none ? 0.0f : sum);
+    }
   }
 }
 
@@ -152,7 +216,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = fmaf(v[e], w, x[e]);
   }
-  const bool none = l == 0.0f;
+  const bool none = m == -INFINITY;
   const float inv = none ? 0.0f : 1.0f / l;
 #pragma unroll
   for (int e = 0; e < 4; ++e) x[e] *= inv;
@@ -167,9 +231,10 @@ namespace {
 
 template <typename T, int DP>
 hipError_t fwd_launch(const AttnArgs& a, hipStream_t s) {
+  constexpr int NR = GS_NR;
   const int64_t nbh = (int64_t)a.batch * a.kv_heads;
-  const int64_t blocks = nbh * ((a.rows + kAttnRows - 1) / kAttnRows) * a.splits;
-  k_attn_fwd<T, DP><<<(unsigned)blocks, 256, 0, s>>>(a);
+  const int64_t blocks = nbh * ((a.rows + 128 * NR - 1) / (128 * NR)) * a.splits;
+  k_attn_fwd<T, DP, NR><<<(unsigned)blocks, 256, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t per = 256 / (DP / 4);
@@ -191,7 +256,7 @@ int attn_padded(int d) { return (d + 31) / 32 * 32; }
 
 int attn_fwd_splits(const gs_cross_attn& p) {
   const int64_t rows = p.q_len * (p.q_heads / p.kv_heads);
-  return attn_splits(p.batch * p.kv_heads * ((rows + kAttnRows - 1) / kAttnRows), (p.k_len + kAttnKeys - 1) / kAttnKeys);
+  return attn_splits(p.batch * p.kv_heads * ((rows + 127) / 128), (p.k_len + kAttnKeys - 1) / kAttnKeys);
 }
 
 hipError_t launch_attn_fwd(AttnArgs a, int type, hipStream_t s) {

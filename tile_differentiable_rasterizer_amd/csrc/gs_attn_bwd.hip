@@ -58,7 +58,7 @@ __global__ __launch_bounds__(256) void k_attn_bwd_kv(AttnArgs a) {
   Frag<T> kf[DP / 16], vf[DP / 16];
 #pragma unroll
   for (int s = 0; s < DP / 16; ++s) {
-    kf[s] = frag_mem<T>(head_ptr<T>(a.k, b, key, hk), a.d, s, open);
+    kf[s] = frag_flip(frag_mem<T>(head_ptr<T>(a.k, b, key, hk), a.d, s, open), a.flip);
     vf[s] = frag_mem<T>(head_ptr<T>(a.v, b, key, hk), a.d, s, open);
   }
   f32x16 dk[DP / 32], dv[DP / 32];
@@ -113,7 +113,7 @@ __global__ __launch_bounds__(256) void k_attn_bwd_kv(AttnArgs a) {
         for (int e = 0; e < 4; ++e) {
           bool sees = open;
           if (ragged) sees = sees && key >= first[r + e] && key < last[r + e];
-          const float p = sees ? __builtin_amdgcn_exp2f(fmaf(s[4 * c + e], a.scale_log2, -ls[e])) : 0.0f;
+          const float p = sees ? __builtin_amdgcn_exp2f(fmaf(s[4 * c + e], a.slope, -ls[e])) : 0.0f;
           s[4 * c + e] = p;
           dp[4 * c + e] = sees ? p * (dp[4 * c + e] - de[e]) : 0.0f;
         }
@@ -171,20 +171,21 @@ __global__ __launch_bounds__(256) void k_attn_bwd_q(AttnArgs a) {
   const int split = rest % a.splits, rt = rest / a.splits;
   const int b = bh / a.kv_heads, hk = bh - b * a.kv_heads;
   const int lane = __lane_id(), half = lane >> 5;
-  const int row = rt * kAttnRows + (threadIdx.x >> 6) * 32 + (lane & 31);
+  const int row = rt * 128 + (threadIdx.x >> 6) * 32 + (lane & 31);
   const bool valid = row < a.rows;
   const int i = valid ? row / a.group : 0, h = hk * a.group + (valid ? row - i * a.group : 0);
-  const int2 range = row_range(a, b, i);
+  int2 range[1] = {row_range(a, b, i)};
   const int64_t at = ((int64_t)b * a.kv_heads * a.group + h) * a.q_len + i;
   const float row_lse = a.lse[at];
-  const bool live = valid && range.x < range.y && row_lse != -INFINITY;
-  const Seen seen = block_seen(range, live, scratch);
+  const bool live = valid && range[0].x < range[0].y && row_lse != -INFINITY;
+  if (!live) range[0] = make_int2(0, 0);
+  const Seen seen = block_seen<1>(range, scratch);
   const float lse2 = live ? row_lse * kLog2e : INFINITY, delta = live ? a.delta[at] : 0.0f;
 
   Frag<T> qf[DP / 16], gf[DP / 16];
 #pragma unroll
   for (int s = 0; s < DP / 16; ++s) {
-    qf[s] = frag_mem<T>(head_ptr<T>(a.q, b, i, h), a.d, s, live);
+    qf[s] = frag_flip(frag_mem<T>(head_ptr<T>(a.q, b, i, h), a.d, s, live), a.flip);
     gf[s] = frag_mem<T>(head_ptr<T>(a.dout, b, i, h), a.d, s, live);
   }
   f32x16 dq[DP / 32];
@@ -192,18 +193,26 @@ __global__ __launch_bounds__(256) void k_attn_bwd_q(AttnArgs a) {
   for (int t = 0; t < DP / 32; ++t) dq[t] = (f32x16)0.0f;
 
   const int t_lo = seen.first / kAttnKeys, t_n = seen.last > seen.first ? (seen.last + kAttnKeys - 1) / kAttnKeys - t_lo : 0;
-  const int t_begin = t_lo + (int)((int64_t)t_n * split / a.splits), t_end = t_lo + (int)((int64_t)t_n * (split + 1) / a.splits);
-  for (int t = t_begin; t < t_end; ++t) {
-    const int k0 = t * kAttnKeys;
-    uint64_t word = key_word(a, b, k0);
-    const bool ragged = k0 < seen.all_from || k0 + kAttnKeys > seen.all_to;
-    if (ragged) word &= block_word(live ? range_word(range.x, range.y, k0) : 0, words);
-    if (word == 0) continue;
-    stage_tokens<T, DP, kAttnKeys>(kt, a.k, b, hk, k0, a.d, word);
-    stage_tokens<T, DP, kAttnKeys>(vt, a.v, b, hk, k0, a.d, word);
+  Tiles tile;
+  tile.t = t_lo + (int)((int64_t)t_n * split / a.splits);
+  tile.end = t_lo + (int)((int64_t)t_n * (split + 1) / a.splits);
+  if (a.d < DP) {
+    Stage<T, DP>::clear(kt, sizeof kt);
+    Stage<T, DP>::clear(vt, sizeof vt);
+    __syncthreads();
+  }
+  for (;;) {
+    tile.next(a, b, seen, range, words);
+    if (!tile.word) break;
+    const int k0 = tile.k0;
+    const uint64_t word = tile.word;
+    const bool ragged = tile.ragged;
+    Stage<T, DP>::load(kt, head_ptr<T>(a.k, b, 0, hk), a.k.token_stride, k0, a.d, word);
+    Stage<T, DP>::load(vt, head_ptr<T>(a.v, b, 0, hk), a.v.token_stride, k0, a.d, word);
+    __builtin_amdgcn_s_waitcnt(0x0f70);
     __syncthreads();
     uint64_t mine = word;
-    if (ragged) mine &= range_word(range.x, range.y, k0);
+    if (ragged) mine &= range_word(range[0].x, range[0].y, k0);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       f32x16 s = (f32x16)0.0f, dp = (f32x16)0.0f;
@@ -214,7 +223,7 @@ __global__ __launch_bounds__(256) void k_attn_bwd_q(AttnArgs a) {
       }
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const float p = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale_log2, -lse2));
+        const float p = __builtin_amdgcn_exp2f(fmaf(s[r], a.slope, -lse2));
         float ds = p * (dp[r] - delta);
         if (mine != ~0ull) ds = (mine >> (32 * j + crow(r, half))) & 1 ? ds : 0.0f;
         dp[r] = ds;
@@ -297,7 +306,7 @@ hipError_t bwd_launch(AttnArgs a, int q_splits, int kv_splits, hipStream_t s) {
   }
   if (vecs) {
     a.splits = q_splits;
-    k_attn_bwd_q<T, DP><<<(unsigned)(nbh * ((a.rows + kAttnRows - 1) / kAttnRows) * q_splits), 256, 0, s>>>(a);
+    k_attn_bwd_q<T, DP><<<(unsigned)(nbh * ((a.rows + 127) / 128) * q_splits), 256, 0, s>>>(a);
     if (q_splits > 1) k_attn_bwd_join<T, DP, false><<<(unsigned)((vecs + per - 1) / per), 256, 0, s>>>(a);
   }
   return hipGetLastError();

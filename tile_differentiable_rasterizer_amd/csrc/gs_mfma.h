@@ -145,11 +145,20 @@ __device__ __forceinline__ Frag<T> frag_mem(const T* p, int d, int s, bool count
   return f;
 }
 
-// max and sum with the lane of the other half that holds the same column.
-__device__ __forceinline__ float other_half(float x) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return __lane_id() < 32 ? __uint_as_float(r[1]) : __uint_as_float(r[0]);
+// The same with every sign bit flipped by `flip` (gs_attn.h).
+template <typename T>
+__device__ __forceinline__ Frag<T> frag_flip(Frag<T> f, uint32_t flip) {
+  union {
+    Frag<T> f;
+    uint32_t u[sizeof(Frag<T>) / 4];
+  } x;
+  x.f = f;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(Frag<T>) / 4); ++i) x.u[i] ^= flip;
+  return x.f;
 }
+
+// max and sum with the lane of the other half that holds the same column.
 __device__ __forceinline__ float pair_max(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
