@@ -23,14 +23,17 @@ struct AttnArgs {
   const uint8_t* mask;
   int64_t mask_b;
   float* lse;
-  float* delta;
+  float2* stat;    // [batch * kv_heads][tiles * 64]: (lse in base 2, delta) of each row, (inf, 0) where it sees nothing
+  struct RowTile* row_tiles;  // [batch * kv_heads][tiles of 64 rows]
   float* part;     // [splits][batch * kv_heads][rows][DP] sums, where splits > 1
   float2* part_ml; // [splits][batch * kv_heads][rows]: running maximum (base 2), sum
 };
 
-// One (sequence, key head) with typed, offset pointers.
-struct Where {
-  int b, hk;
+// What the rows of a tile may see (backward pass).
+struct RowTile {
+  uint64_t word;        // rows that see something
+  int first, last;      // some row sees something in here
+  int all_from, all_to; // every row that sees anything sees all of this
 };
 
 template <typename T>
@@ -133,47 +136,80 @@ __device__ __forceinline__ uint64_t block_word(uint64_t mine, uint64_t* scratch)
   return r;
 }
 
-// Staging of 64 tokens of one head to a tile by 256 threads.  Where every token counts, the loads
-// go straight to LDS (16 bytes a lane, a wavefront's 64 chunks in a row), so that they are in
-// flight while the tile before is worked on, and cost no registers; the swizzle is in the address
-// that a lane reads.  Where some do not, the chunks pass through registers and the rows that do
-// not count are zeros (nothing there is read).  Chunks past D are zeros from clear() on.
+// Sixteen bytes of zeros for the lanes of a load that have nothing to read.
+__device__ const uint32_t kZeros[4] __attribute__((aligned(16))) = {0, 0, 0, 0};
+
+// Staging of 64 vectors to a tile by 256 threads, 16 bytes a lane straight to LDS: a wavefront's 64
+// chunks lie in a row there, and the swizzle is in the address that a lane reads.  The loads are in
+// flight while the tile before is worked on, and cost no registers.
+//
+// Where every vector counts, the vectors are evenly spaced and D fills the tile's rows, a load's
+// address is a uniform base and an offset that the thread keeps from start to end.  Elsewhere each
+// lane's address is made for it, and lanes of vectors that do not count, or of chunks past D, read
+// zeros: nothing is read from there.
 template <typename T, int DP>
 struct Stage {
   using Ti = Tile<T, DP>;
   static constexpr int kEach = kAttnKeys * Ti::kChunks / 256;
   static constexpr int kBytes = kAttnKeys * Ti::kRowBytes;
   static_assert(kEach * 256 == kAttnKeys * Ti::kChunks, "whole chunks a thread");
+  // one offset serves all of a thread's chunks where they are whole rounds of the swizzle apart
+  static constexpr bool kRegular = 256 % Ti::kChunks == 0 && 256 / Ti::kChunks % 16 == 0;
 
-  // Before the first tile, where D < DP: the chunks past D stay zero.
-  static __device__ __forceinline__ void clear(char* lds, int bytes) {
-    for (int i = threadIdx.x * 16; i < bytes; i += 256 * 16) *reinterpret_cast<f32x4*>(lds + i) = (f32x4)0.0f;
+  uint32_t off[kRegular ? 1 : kEach];  // bytes from the tile's first vector
+  bool even;
+
+  // Row of the tile, and chunk of the vector, that the thread's i-th 16 bytes of the tile hold.
+  static __device__ __forceinline__ int row_of(int i, int tid) { return (i * 256 + tid) / Ti::kChunks; }
+  static __device__ __forceinline__ int chunk_of(int i, int tid) {
+    const int c = i * 256 + tid, r = c / Ti::kChunks;
+    return (c - r * Ti::kChunks) ^ Ti::mix(r);
   }
 
-  // Tokens t0 .. t0 + 63 of `head` (its token 0); bit r of `word`: token t0 + r counts.
-  static __device__ __forceinline__ void load(char* tile, const T* head, int64_t token_stride, int t0, int d,
-                                              uint64_t word) {
-    const T* base = head + t0 * token_stride;
-    if (word == ~0ull) {
-      const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // Vectors of `group` heads a token (`group` divides 64, else they are not even).
+  __device__ __forceinline__ void plan(const gs_heads& x, int group, int d) {
+    even = d == DP && 64 % group == 0 && (64 / group) * x.token_stride + group * x.head_stride < (1 << 28);
+#pragma unroll
+    for (int i = 0; i < (kRegular ? 1 : kEach); ++i) {
+      const int r = row_of(i, threadIdx.x), t = r / group;
+      off[i] = even ? (uint32_t)(t * x.token_stride + (r - t * group) * x.head_stride + chunk_of(i, threadIdx.x) * Ti::kPer) * (uint32_t)sizeof(T) : 0;
+    }
+  }
+
+  // first: the tile's vector 0; at(r): vector r; bit r of `word`: it counts.
+  template <class At>
+  __device__ __forceinline__ void load(char* tile, const gs_heads& x, int group, int d, uint64_t word, const T* first, At&& at) const {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (even && word == ~0ull) {
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        const int c = i * 256 + threadIdx.x, r = c / Ti::kChunks, ch = (c - r * Ti::kChunks) ^ Ti::mix(r);
-        if (ch * Ti::kPer < d)
-          __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(base + r * token_stride + ch * Ti::kPer),
-                                           (__attribute__((address_space(3))) void*)(tile + (i * 4 + wave) * 1024), 16, 0, 0);
+        const char* p = reinterpret_cast<const char*>(first);
+        if (kRegular) {  // i whole rounds of 256 / kChunks vectors further on
+          constexpr int kRows = kRegular ? 256 / Ti::kChunks : 1;
+          const int t = i * kRows / group;
+          p += (t * x.token_stride + (i * kRows - t * group) * x.head_stride) * (int64_t)sizeof(T);
+        }
+        to_lds(p + off[kRegular ? 0 : i], tile, i, wave);
       }
     } else {
+      int tid = threadIdx.x;
+      asm volatile("" : "+v"(tid));  // made again here: kept from tile to tile these addresses cost the other path its registers
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        const int c = i * 256 + threadIdx.x, r = c / Ti::kChunks, ch = (c - r * Ti::kChunks) ^ Ti::mix(r);
-        f32x4 v = (f32x4)0.0f;
-        if (((word >> r) & 1) && ch * Ti::kPer < d) v = *reinterpret_cast<const f32x4*>(base + r * token_stride + ch * Ti::kPer);
-        *reinterpret_cast<f32x4*>(tile + c * 16) = v;
+        const int r = row_of(i, tid), ch = chunk_of(i, tid);
+        const bool counts = ((word >> r) & 1) && ch * Ti::kPer < d;
+        to_lds(counts ? reinterpret_cast<const char*>(at(r) + ch * Ti::kPer) : reinterpret_cast<const char*>(kZeros), tile, i, wave);
       }
     }
   }
+  static __device__ __forceinline__ void to_lds(const char* p, char* tile, int i, int wave) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p,
+                                     (__attribute__((address_space(3))) void*)(tile + (i * 4 + wave) * 1024), 16, 0, 0);
+  }
 };
+
+// Waits for the wavefront's own loads to LDS (and every other load).
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt 0
 
 // The tiles of a workgroup's keys, one after another, without those that no row sees.  Every
 // thread of the workgroup calls next() (its answer is the same for all of them).
@@ -188,7 +224,7 @@ struct Tiles {
     word = 0;
     for (; t < end && word == 0; ++t) {
       k0 = t * kAttnKeys;
-      word = key_word(a, b, k0);
+      word = a.mask || k0 + kAttnKeys > a.k_len ? key_word(a, b, k0) : ~0ull;
       ragged = k0 < seen.all_from || k0 + kAttnKeys > seen.all_to;
       if (ragged) {
         uint64_t some = 0;

@@ -8,6 +8,8 @@
 // the halves, the row's statistics are one register, and the weights are at once the B operand of
 // O^T[d][row] = V^T P^T.  The weights enter that product in the element type (bfloat16: an error
 // of 2^-8 of each weight at most, of the order of the output's own rounding); everything else is float32.
+#include <type_traits>
+
 #include "gs_attn.h"
 
 #ifndef GS_NR
@@ -62,30 +64,28 @@ __global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
   tile.end = t_lo + (int)((int64_t)t_n * (split + 1) / a.splits);
   const T* kh = head_ptr<T>(a.k, b, 0, hk);
   const T* vh = head_ptr<T>(a.v, b, 0, hk);
-  if (a.d < DP) {
-    St::clear(lds[0], 4 * St::kBytes);
-    __syncthreads();
-  }
+  St ks, vs;
+  ks.plan(a.k, 1, a.d);
+  vs.plan(a.v, 1, a.d);
+  auto load = [&](int buf) {
+    const T *k = kh + tile.k0 * a.k.token_stride, *v = vh + tile.k0 * a.v.token_stride;
+    ks.load(lds[2 * buf], a.k, 1, a.d, tile.word, k, [&](int r) { return k + r * a.k.token_stride; });
+    vs.load(lds[2 * buf + 1], a.v, 1, a.d, tile.word, v, [&](int r) { return v + r * a.v.token_stride; });
+  };
   tile.next(a, b, seen, range, words);
-  int buf = 0;
-  if (tile.word) {
-    St::load(lds[0], kh, a.k.token_stride, tile.k0, a.d, tile.word);
-    St::load(lds[1], vh, a.v.token_stride, tile.k0, a.d, tile.word);
-  }
+  if (tile.word) load(0);
   const float slack = 8.0f / a.slope;  // weights up to 2^8 before the sums are scaled again
-  while (tile.word) {
+  // one tile, in the buffers that the compiler knows (offsets then are immediates)
+  auto one = [&](auto which) {
+    constexpr int buf = decltype(which)::value;
     const uint64_t word = tile.word;
     const int k0 = tile.k0;
     const bool ragged = tile.ragged;
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt 0: this tile's loads to LDS
-    __syncthreads();                     // ... of every wavefront; and the tile before is done with
+    wait_loads();     // this tile's
+    __syncthreads();  // ... of every wavefront; and the tile before is done with
     tile.next(a, b, seen, range, words);
-    if (tile.word) {
-      St::load(lds[2 - 2 * buf], kh, a.k.token_stride, tile.k0, a.d, tile.word);
-      St::load(lds[3 - 2 * buf], vh, a.v.token_stride, tile.k0, a.d, tile.word);
-    }
+    if (tile.word) load(buf ^ 1);
     const char *kt = lds[2 * buf], *vt = lds[2 * buf + 1];
-    buf ^= 1;
 
     f32x16 s[NR][2];
 #pragma unroll
@@ -140,17 +140,22 @@ __global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
       l[n] += sum;
     }
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
+    for (int step = 0; step < 4; ++step) {
       Frag<T> p[NR];
 #pragma unroll
-      for (int n = 0; n < NR; ++n) p[n] = frag_of<T>(s[n][ks >> 1], ks & 1);
+      for (int n = 0; n < NR; ++n) p[n] = frag_of<T>(s[n][step >> 1], step & 1);
 #pragma unroll
       for (int dt = 0; dt < DP / 32; ++dt) {
-        const Frag<T> vf = Ti::frag_cols(vt, 16 * ks, 32 * dt);
+        const Frag<T> vf = Ti::frag_cols(vt, 16 * step, 32 * dt);
 #pragma unroll
         for (int n = 0; n < NR; ++n) o[n][dt] = mma(vf, p[n], o[n][dt]);
       }
     }
+  };
+  while (tile.word) {
+    one(std::integral_constant<int, 0>());
+    if (!tile.word) break;
+    one(std::integral_constant<int, 1>());
   }
 
 #pragma unroll

@@ -10,49 +10,82 @@
 // operand of dV^T[d][key] = dO^T P and dK^T[d][key] = Q^T dS.  q: as the forward kernel, S^T and
 // dP^T = V dO^T, then dQ^T[d][row] = K^T dS^T.
 // p and dS enter the products in the element type (bfloat16: rounded once, 2^-8 of each at most).
+#include <type_traits>
+
 #include "gs_attn.h"
+
 
 namespace gs {
 
 constexpr int kBwdRows = 64;  // rows of a tile of the kv kernel
 
-// delta = dout . out for every (sequence, token, head): 16 lanes a vector, eight elements a lane.
+// Statistics of every row, in the order of (sequence, key head, row): lse in base 2 and delta =
+// dout . out, and what each tile of 64 rows may see.  One workgroup a tile; a vector takes 16
+// lanes, eight elements a lane.
 template <typename T>
-__global__ __launch_bounds__(256) void k_attn_delta(AttnArgs a) {
-  const int heads = a.kv_heads * a.group;
-  const int64_t n = (int64_t)a.batch * a.q_len * heads;
-  const int64_t v = (int64_t)blockIdx.x * 16 + threadIdx.x / 16;
-  if (v >= n) return;
-  const int64_t tok = v / heads;
-  const int h = (int)(v - tok * heads), b = (int)(tok / a.q_len), i = (int)(tok - (int64_t)b * a.q_len);
-  const int d = (threadIdx.x & 15) * 8;
-  float sum = 0.0f;
-  if (d < a.d) {
-    float x[8], y[8];
-    load_elems<8>(head_ptr<T>(a.out, b, i, h) + d, x);
-    load_elems<8>(head_ptr<T>(a.dout, b, i, h) + d, y);
+__global__ __launch_bounds__(256) void k_attn_stat(AttnArgs a) {
+  __shared__ float delta[kBwdRows];
+  const int tiles = (a.rows + kBwdRows - 1) / kBwdRows;
+  const int bh = blockIdx.x / tiles, t = blockIdx.x - bh * tiles;
+  const int b = bh / a.kv_heads, hk = bh - b * a.kv_heads, d = (threadIdx.x & 15) * 8;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
+  for (int p = 0; p < kBwdRows / 16; ++p) {
+    const int r = p * 16 + threadIdx.x / 16, row = t * kBwdRows + r;
+    float sum = 0.0f;
+    if (row < a.rows && d < a.d) {
+      const int i = row / a.group, h = hk * a.group + row - i * a.group;
+      float x[8], y[8];
+      load_elems<8>(head_ptr<T>(a.out, b, i, h) + d, x);
+      load_elems<8>(head_ptr<T>(a.dout, b, i, h) + d, y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
+    }
+#pragma unroll
+    for (int e = 1; e < 16; e <<= 1) sum += __shfl_xor(sum, e, 64);
+    if (d == 0) delta[r] = sum;
   }
-#pragma unroll
-  for (int e = 1; e < 16; e <<= 1) sum += __shfl_xor(sum, e, 64);
-  if (d == 0) a.delta[((int64_t)b * heads + h) * a.q_len + i] = sum;
+  __syncthreads();
+  if (threadIdx.x >= kBwdRows) return;
+  const int row = t * kBwdRows + threadIdx.x;
+  bool live = row < a.rows;
+  int2 range = make_int2(0, 0);
+  float lse = -INFINITY;
+  if (live) {
+    const int i = row / a.group, h = hk * a.group + row - i * a.group;
+    range = row_range(a, b, i);
+    lse = a.lse[((int64_t)b * a.kv_heads * a.group + h) * a.q_len + i];
+    live = range.x < range.y && lse != -INFINITY;
+  }
+  // a row without keys: every weight 2^-inf = 0
+  a.stat[(int64_t)blockIdx.x * kBwdRows + threadIdx.x] = live ? make_float2(lse * kLog2e, delta[threadIdx.x]) : make_float2(INFINITY, 0.0f);
+  RowTile w;
+  w.word = __ballot(live);
+  w.first = wave_min_i(live ? range.x : INT32_MAX);
+  w.last = wave_max_i(live ? range.y : 0);
+  w.all_from = wave_max_i(live ? range.x : 0);
+  w.all_to = wave_min_i(live ? range.y : INT32_MAX);
+  if (threadIdx.x == 0) a.row_tiles[blockIdx.x] = w;
 }
 
+// Wavefronts a SIMD: two where the results (DP registers) and the keys' and values' fragments leave
+// room in 256 (float32 D 64: 249 -> 201 us for the whole backward pass of 2 x 391 rows; bfloat16
+// D 64: 2.85 -> 2.25 ms), else one (bfloat16 D 128 spills with two: 5.4 -> 8.0 ms).
 template <typename T, int DP>
-__global__ __launch_bounds__(256) void k_attn_bwd_kv(AttnArgs a) {
+constexpr int kKvWaves = DP + DP * (int)sizeof(T) / 4 <= 150 ? 2 : 1;
+
+template <typename T, int DP>
+__global__ __launch_bounds__(256, (kKvWaves<T, DP>)) void k_attn_bwd_kv(AttnArgs a) {
   using Ti = Tile<T, DP>;
-  __shared__ __align__(16) char qt[kBwdRows * Ti::kRowBytes];
-  __shared__ __align__(16) char gt[kBwdRows * Ti::kRowBytes];
-  __shared__ __align__(16) float lse2[kBwdRows], delta[kBwdRows];
-  __shared__ __align__(16) int first[kBwdRows], last[kBwdRows];
+  using St = Stage<T, DP>;
+  __shared__ __align__(16) char lds[4][St::kBytes];  // queries and output gradients of two tiles
+  __shared__ __align__(32) float2 stat[2][kBwdRows];
   const int nbh = a.batch * a.kv_heads;
   const int bh = blockIdx.x % nbh, rest = blockIdx.x / nbh;
   const int split = rest % a.splits, kb = rest / a.splits;
   const int b = bh / a.kv_heads, hk = bh - b * a.kv_heads;
   const int lane = __lane_id(), half = lane >> 5;
   const int k0 = kb * 128, k1 = min(k0 + 128, a.k_len);
-  const int key = k0 + (threadIdx.x >> 6) * 32 + (lane & 31);
+  const int wk0 = k0 + (threadIdx.x >> 6) * 32, key = wk0 + (lane & 31);
   const bool open = key < a.k_len && (!a.mask || a.mask[b * a.mask_b + key] != 0);
 
   Frag<T> kf[DP / 16], vf[DP / 16];
@@ -66,37 +99,55 @@ __global__ __launch_bounds__(256) void k_attn_bwd_kv(AttnArgs a) {
   for (int t = 0; t < DP / 32; ++t) dk[t] = dv[t] = (f32x16)0.0f;
 
   const int tiles = (a.rows + kBwdRows - 1) / kBwdRows;
-  const int t_begin = (int)((int64_t)tiles * split / a.splits), t_end = (int)((int64_t)tiles * (split + 1) / a.splits);
-  for (int t = t_begin; t < t_end; ++t) {
+  const int t_end = (int)((int64_t)tiles * (split + 1) / a.splits);
+  const RowTile* info = a.row_tiles + (int64_t)bh * tiles;
+  const float2* row_stat = a.stat + (int64_t)bh * tiles * kBwdRows;
+  const T* qh = head_ptr<T>(a.q, b, 0, hk * a.group);
+  const T* gh = head_ptr<T>(a.dout, b, 0, hk * a.group);
+  // the next tile from t on whose rows see some of the keys (the same for every thread)
+  RowTile next;
+  auto find = [&](int t) {
+    for (; t < t_end; ++t) {
+      next = info[t];
+      if (next.word && next.first < k1 && next.last > k0) break;
+    }
+    return t;
+  };
+  St qs, gs;
+  qs.plan(a.q, a.group, a.d);
+  gs.plan(a.dout, a.group, a.d);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  auto load = [&](int t, int buf) {
     const int r0 = t * kBwdRows;
-    // every wavefront looks at the tile's 64 rows, one a lane
-    const int row = r0 + lane;
-    const int i = row < a.rows ? row / a.group : 0, h = hk * a.group + (row < a.rows ? row - i * a.group : 0);
-    const int2 range = row_range(a, b, i);
-    const int64_t at = ((int64_t)b * a.kv_heads * a.group + h) * a.q_len + i;
-    const float row_lse = a.lse[at];
-    const bool live = row < a.rows && range.x < range.y && row_lse != -INFINITY;
-    const uint64_t word = __ballot(live);
-    if (__ballot(live && range.x < k1 && range.y > k0) == 0) continue;  // the same for the workgroup
-    const bool ragged = __ballot(live && (range.x > k0 || range.y < k1)) != 0;
-    if (threadIdx.x < kBwdRows) {
-      lse2[lane] = live ? row_lse * kLog2e : INFINITY;  // a row without keys: every weight 2^-inf = 0
-      delta[lane] = live ? a.delta[at] : 0.0f;
-      first[lane] = range.x;
-      last[lane] = range.y;
-    }
-    for (int c = threadIdx.x; c < kBwdRows * Ti::kChunks; c += 256) {
-      const int r = c / Ti::kChunks, ch = c - r * Ti::kChunks;
-      f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
-      if (((word >> r) & 1) && ch * Ti::kPer < a.d) {
-        const int ri = (r0 + r) / a.group, rh = hk * a.group + (r0 + r) - ri * a.group;
-        x = *reinterpret_cast<const f32x4*>(head_ptr<T>(a.q, b, ri, rh) + ch * Ti::kPer);
-        y = *reinterpret_cast<const f32x4*>(head_ptr<T>(a.dout, b, ri, rh) + ch * Ti::kPer);
-      }
-      *reinterpret_cast<f32x4*>(qt + Ti::at(r, ch)) = x;
-      *reinterpret_cast<f32x4*>(gt + Ti::at(r, ch)) = y;
-    }
+    const uint64_t word = next.word;
+    auto offset = [&](int r, const gs_heads& x) {
+      const int i = r / a.group;
+      return i * x.token_stride + (r - i * a.group) * x.head_stride;
+    };
+    qs.load(lds[2 * buf], a.q, a.group, a.d, word, qh + offset(r0, a.q), [&](int r) { return qh + offset(r0 + r, a.q); });
+    gs.load(lds[2 * buf + 1], a.dout, a.group, a.d, word, gh + offset(r0, a.dout), [&](int r) { return gh + offset(r0 + r, a.dout); });
+    if (wave < 2)  // 64 words each
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)((const float*)(row_stat + r0) + wave * 64 + lane),
+                                       (__attribute__((address_space(3))) void*)((float*)stat[buf] + wave * 64), 4, 0, 0);
+  };
+  int t = find((int)((int64_t)tiles * split / a.splits));
+  if (t < t_end) load(t, 0);
+  auto one = [&](auto which) {  // in buffers that the compiler knows
+    constexpr int buf = decltype(which)::value;
+    wait_loads();
     __syncthreads();
+    const int now = t;
+    const bool ragged = next.all_from > k0 || next.all_to < k1;
+    t = find(t + 1);
+    if (t < t_end) load(t, buf ^ 1);
+    const char *qt = lds[2 * buf], *gt = lds[2 * buf + 1];
+    const float2* st2 = stat[buf];
+    uint32_t sees = ~0u;  // of row `lane` of the tile: the wavefront's keys that it sees
+    if (ragged) {
+      const int row = now * kBwdRows + lane;
+      const int2 range = row < a.rows ? row_range(a, b, row / a.group) : make_int2(0, 0);
+      sees = (uint32_t)range_word(range.x, range.y, wk0);
+    }
 #pragma unroll
     for (int j = 0; j < kBwdRows / 32; ++j) {
       f32x16 s = (f32x16)0.0f, dp = (f32x16)0.0f;
@@ -107,15 +158,20 @@ __global__ __launch_bounds__(256) void k_attn_bwd_kv(AttnArgs a) {
       }
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const int r = 32 * j + 8 * c + 4 * half;
-        const f32x4 ls = *reinterpret_cast<const f32x4*>(&lse2[r]), de = *reinterpret_cast<const f32x4*>(&delta[r]);
+        const f32x8 w = *reinterpret_cast<const f32x8*>(&st2[32 * j + 8 * c + 4 * half]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          bool sees = open;
-          if (ragged) sees = sees && key >= first[r + e] && key < last[r + e];
-          const float p = sees ? __builtin_amdgcn_exp2f(fmaf(s[4 * c + e], a.slope, -ls[e])) : 0.0f;
+          const float p = __builtin_amdgcn_exp2f(fmaf(s[4 * c + e], a.slope, -w[2 * e]));
           s[4 * c + e] = p;
-          dp[4 * c + e] = sees ? p * (dp[4 * c + e] - de[e]) : 0.0f;
+          dp[4 * c + e] = p * (dp[4 * c + e] - w[2 * e + 1]);
+        }
+      }
+      if (ragged) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const bool in = (__shfl((int)sees, 32 * j + crow(r, half), 64) >> (lane & 31)) & 1;
+          s[r] = in ? s[r] : 0.0f;
+          dp[r] = in ? dp[r] : 0.0f;
         }
       }
 #pragma unroll
@@ -128,7 +184,11 @@ __global__ __launch_bounds__(256) void k_attn_bwd_kv(AttnArgs a) {
         }
       }
     }
-    __syncthreads();
+  };
+  while (t < t_end) {
+    one(std::integral_constant<int, 0>());
+    if (t >= t_end) break;
+    one(std::integral_constant<int, 1>());
   }
 
   if (key >= a.k_len) return;
@@ -145,9 +205,9 @@ __global__ __launch_bounds__(256) void k_attn_bwd_kv(AttnArgs a) {
       const int d = 32 * dt + 8 * c + 4 * half;
       float x[4], y[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[e] = dk[dt][4 * c + e] * a.scale;
-        y[e] = dv[dt][4 * c + e];
+      for (int e = 0; e < 4; ++e) {  // a masked key's are products with its zeros' weights: not used
+        x[e] = open ? dk[dt][4 * c + e] * a.scale : 0.0f;
+        y[e] = open ? dv[dt][4 * c + e] : 0.0f;
       }
       if (parts) {
         store_elems<4>(kw + d, x);
@@ -160,10 +220,10 @@ __global__ __launch_bounds__(256) void k_attn_bwd_kv(AttnArgs a) {
 }
 
 template <typename T, int DP>
-__global__ __launch_bounds__(256) void k_attn_bwd_q(AttnArgs a) {
+__global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   using Ti = Tile<T, DP>;
-  __shared__ __align__(16) char kt[kAttnKeys * Ti::kRowBytes];
-  __shared__ __align__(16) char vt[kAttnKeys * Ti::kRowBytes];
+  using St = Stage<T, DP>;
+  __shared__ __align__(16) char lds[4][St::kBytes];  // keys and values of two tiles
   __shared__ int scratch[4][4];
   __shared__ uint64_t words[4];
   const int nbh = a.batch * a.kv_heads;
@@ -175,12 +235,11 @@ __global__ __launch_bounds__(256) void k_attn_bwd_q(AttnArgs a) {
   const bool valid = row < a.rows;
   const int i = valid ? row / a.group : 0, h = hk * a.group + (valid ? row - i * a.group : 0);
   int2 range[1] = {row_range(a, b, i)};
-  const int64_t at = ((int64_t)b * a.kv_heads * a.group + h) * a.q_len + i;
-  const float row_lse = a.lse[at];
-  const bool live = valid && range[0].x < range[0].y && row_lse != -INFINITY;
+  const int tiles = (a.rows + kBwdRows - 1) / kBwdRows;
+  const float2 stat = valid ? a.stat[(int64_t)bh * tiles * kBwdRows + row] : make_float2(INFINITY, 0.0f);
+  const bool live = stat.x != INFINITY;
   if (!live) range[0] = make_int2(0, 0);
   const Seen seen = block_seen<1>(range, scratch);
-  const float lse2 = live ? row_lse * kLog2e : INFINITY, delta = live ? a.delta[at] : 0.0f;
 
   Frag<T> qf[DP / 16], gf[DP / 16];
 #pragma unroll
@@ -196,21 +255,28 @@ __global__ __launch_bounds__(256) void k_attn_bwd_q(AttnArgs a) {
   Tiles tile;
   tile.t = t_lo + (int)((int64_t)t_n * split / a.splits);
   tile.end = t_lo + (int)((int64_t)t_n * (split + 1) / a.splits);
-  if (a.d < DP) {
-    Stage<T, DP>::clear(kt, sizeof kt);
-    Stage<T, DP>::clear(vt, sizeof vt);
-    __syncthreads();
-  }
-  for (;;) {
-    tile.next(a, b, seen, range, words);
-    if (!tile.word) break;
-    const int k0 = tile.k0;
+  const T* kh = head_ptr<T>(a.k, b, 0, hk);
+  const T* vh = head_ptr<T>(a.v, b, 0, hk);
+  St ks, vs;
+  ks.plan(a.k, 1, a.d);
+  vs.plan(a.v, 1, a.d);
+  auto load = [&](int buf) {
+    const T *k = kh + tile.k0 * a.k.token_stride, *v = vh + tile.k0 * a.v.token_stride;
+    ks.load(lds[2 * buf], a.k, 1, a.d, tile.word, k, [&](int r) { return k + r * a.k.token_stride; });
+    vs.load(lds[2 * buf + 1], a.v, 1, a.d, tile.word, v, [&](int r) { return v + r * a.v.token_stride; });
+  };
+  tile.next(a, b, seen, range, words);
+  if (tile.word) load(0);
+  auto one = [&](auto which) {
+    constexpr int buf = decltype(which)::value;
     const uint64_t word = tile.word;
+    const int k0 = tile.k0;
     const bool ragged = tile.ragged;
-    Stage<T, DP>::load(kt, head_ptr<T>(a.k, b, 0, hk), a.k.token_stride, k0, a.d, word);
-    Stage<T, DP>::load(vt, head_ptr<T>(a.v, b, 0, hk), a.v.token_stride, k0, a.d, word);
-    __builtin_amdgcn_s_waitcnt(0x0f70);
+    wait_loads();
     __syncthreads();
+    tile.next(a, b, seen, range, words);
+    if (tile.word) load(buf ^ 1);
+    const char *kt = lds[2 * buf], *vt = lds[2 * buf + 1];
     uint64_t mine = word;
     if (ragged) mine &= range_word(range[0].x, range[0].y, k0);
 #pragma unroll
@@ -223,10 +289,13 @@ __global__ __launch_bounds__(256) void k_attn_bwd_q(AttnArgs a) {
       }
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const float p = __builtin_amdgcn_exp2f(fmaf(s[r], a.slope, -lse2));
-        float ds = p * (dp[r] - delta);
-        if (mine != ~0ull) ds = (mine >> (32 * j + crow(r, half))) & 1 ? ds : 0.0f;
-        dp[r] = ds;
+        const float p = __builtin_amdgcn_exp2f(fmaf(s[r], a.slope, -stat.x));
+        dp[r] = p * (dp[r] - stat.y);
+      }
+      if (ragged || word != ~0ull) {
+        const uint32_t bits = (uint32_t)(mine >> (32 * j)) >> (4 * half);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) dp[r] = (bits >> crow(r, 0)) & 1 ? dp[r] : 0.0f;
       }
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
@@ -235,7 +304,11 @@ __global__ __launch_bounds__(256) void k_attn_bwd_q(AttnArgs a) {
         for (int dt = 0; dt < DP / 32; ++dt) dq[dt] = mma(Ti::frag_cols(kt, 32 * j + 16 * st, 32 * dt), df, dq[dt]);
       }
     }
-    __syncthreads();
+  };
+  while (tile.word) {
+    one(std::integral_constant<int, 0>());
+    if (!tile.word) break;
+    one(std::integral_constant<int, 1>());
   }
 
   if (!valid) return;
@@ -297,7 +370,7 @@ template <typename T, int DP>
 hipError_t bwd_launch(AttnArgs a, int q_splits, int kv_splits, hipStream_t s) {
   const int64_t nbh = (int64_t)a.batch * a.kv_heads, vecs = nbh * a.rows, per = 256 / (DP / 4);
   if (nbh == 0 || (a.rows == 0 && a.k_len == 0)) return hipSuccess;
-  if (vecs) k_attn_delta<T><<<(unsigned)((vecs + 15) / 16), 256, 0, s>>>(a);
+  if (vecs) k_attn_stat<T><<<(unsigned)(nbh * ((a.rows + kBwdRows - 1) / kBwdRows)), 256, 0, s>>>(a);
   if (nbh && a.k_len) {
     a.splits = kv_splits;
     k_attn_bwd_kv<T, DP><<<(unsigned)(nbh * ((a.k_len + 127) / 128) * kv_splits), 256, 0, s>>>(a);

@@ -12,7 +12,7 @@
 //
 // Tiles in LDS: rows of DP elements, dense, in chunks of 16 bytes whose place in the row is
 // permuted by the row (swizzle), so that both ways of reading a tile are free of bank conflicts:
-// eight rows at one chunk (frag_rows), and four rows at two chunks (frag_cols).
+// sixteen rows at one chunk (frag_rows), and four rows at four chunks (frag_cols).
 #pragma once
 
 #include "gs_elem.h"
@@ -63,12 +63,16 @@ struct Tile {
   static constexpr int kPer = 16 / sizeof(T);        // elements of a chunk
   static constexpr int kChunks = DP / kPer;          // chunks of a row
   static constexpr int kRowBytes = DP * sizeof(T);
-  // Chunk c of row r lies at c ^ mix(r).  Rows whose length is a multiple of 256 bytes (or half of
-  // it) start at the same banks: three bits of the row, the low two worth two chunks.  Rows of 64
-  // and 192 bytes already differ in where four neighbours start: two more bits.
+  // Chunk c of row r lies at c ^ mix(r).  The banks are 256 bytes wide: a read of 16-byte chunks
+  // takes 16 rows at once, which need 16 places, and a transposing read four rows of four chunks,
+  // which need the four quarters.  Rows of a multiple of 256 bytes all start at the same place: four
+  // bits of the row, the low two in quarters; rows of 128 bytes more alternate, rows of 64 or 192
+  // bytes more start at the four quarters by themselves.
   static __device__ __forceinline__ int mix(int r) {
-    if constexpr (kChunks % 8 == 0)
-      return ((r & 3) << 1) | ((r >> 2) & 1);
+    if constexpr (kRowBytes % 256 == 0)
+      return ((r & 3) << 2) | ((r >> 2) & 3);
+    else if constexpr (kRowBytes % 256 == 128)
+      return ((r & 2) << 1) | ((r >> 2) & 3);
     else
       return (r >> 2) & 3;
   }

@@ -135,6 +135,13 @@ AttnArgs attn_args(const gs_cross_attn& p) {
 
 int64_t attn_rows(const gs_cross_attn& p) { return p.batch * p.kv_heads * (p.q_len * (p.q_heads / p.kv_heads)); }
 
+// Tiles of 64 rows of all (sequence, key head)s, and the backward pass's arrays over them.
+int64_t attn_row_tiles(const gs_cross_attn& p) {
+  return p.batch * p.kv_heads * ((p.q_len * (p.q_heads / p.kv_heads) + 63) / 64);
+}
+size_t attn_stat_bytes(const gs_cross_attn& p) { return (size_t)attn_row_tiles(p) * 64 * sizeof(float2); }
+size_t attn_tile_bytes(const gs_cross_attn& p) { return round16((size_t)attn_row_tiles(p) * sizeof(RowTile)); }
+
 // Bytes of the parts of a sum over `vecs` vectors.
 size_t part_bytes(const gs_cross_attn& p, int splits, int64_t vecs) {
   return splits > 1 ? (size_t)splits * vecs * attn_padded(p.head_dim) * sizeof(float) : 0;
@@ -197,7 +204,7 @@ size_t gs_cross_attn_bwd_workspace_bytes(const gs_cross_attn* p) {
   if (attn_shape(p) != GS_OK) return 0;
   const size_t q = part_bytes(*p, attn_fwd_splits(*p), attn_rows(*p));
   const size_t kv = part_bytes(*p, attn_bwd_kv_splits(*p), 2 * p->batch * p->kv_heads * p->k_len);
-  return round16((size_t)attn_rows(*p) * sizeof(float)) + (q > kv ? q : kv);
+  return attn_stat_bytes(*p) + attn_tile_bytes(*p) + (q > kv ? q : kv);
 }
 
 gs_status gs_cross_attn_bwd(const gs_cross_attn* p, gs_heads dout, gs_heads q, gs_heads k, gs_heads v, gs_heads out,
@@ -222,8 +229,10 @@ gs_status gs_cross_attn_bwd(const gs_cross_attn* p, gs_heads dout, gs_heads q, g
   a.dk = dk;
   a.dv = dv;
   a.lse = const_cast<float*>(lse);
-  a.delta = static_cast<float*>(workspace);
-  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + round16((size_t)attn_rows(*p) * sizeof(float)));
+  char* at = static_cast<char*>(workspace);
+  a.stat = reinterpret_cast<float2*>(at);
+  a.row_tiles = reinterpret_cast<RowTile*>(at + attn_stat_bytes(*p));
+  a.part = reinterpret_cast<float*>(at + attn_stat_bytes(*p) + attn_tile_bytes(*p));
   return status_of(launch_attn_bwd(a, p->type, attn_fwd_splits(*p), attn_bwd_kv_splits(*p), static_cast<hipStream_t>(stream)));
 }
 
