@@ -139,6 +139,31 @@ __device__ __forceinline__ uint64_t block_word(uint64_t mine, uint64_t* scratch)
 // Sixteen bytes of zeros for the lanes of a load that have nothing to read.
 __device__ const uint32_t kZeros[4] __attribute__((aligned(16))) = {0, 0, 0, 0};
 
+// Loads straight to LDS, 16 (or 4) bytes a lane, in a row from `to` (the same for the wavefront).
+// They are written as assembly because the compiler orders every LDS read behind the builtin's
+// loads, wherever they go, and so would wait for the next tile before it works on this one.  They
+// write no register.  Whoever reads what they bring waits first: wait_loads(), then the barrier.
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p);
+}
+__device__ __forceinline__ void load_to_lds16(const void* base, uint32_t offset, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(offset), "s"(base), "s"(to)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void load_to_lds16(const void* p, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(p), "s"(to) : "memory", "m0");
+}
+__device__ __forceinline__ void load_to_lds4(const void* base, uint32_t offset, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+               :
+               : "v"(offset), "s"(base), "s"(to)
+               : "memory", "m0");
+}
+// Waits for the wavefront's own loads to LDS (and every other load).
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" : : : "memory"); }
+
 // Staging of 64 vectors to a tile by 256 threads, 16 bytes a lane straight to LDS: a wavefront's 64
 // chunks lie in a row there, and the swizzle is in the address that a lane reads.  The loads are in
 // flight while the tile before is worked on, and cost no registers.
@@ -179,7 +204,7 @@ struct Stage {
   // first: the tile's vector 0; at(r): vector r; bit r of `word`: it counts.
   template <class At>
   __device__ __forceinline__ void load(char* tile, const gs_heads& x, int group, int d, uint64_t word, const T* first, At&& at) const {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t to = lds_address(tile + (threadIdx.x >> 6) * 1024);
     if (even && word == ~0ull) {
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
@@ -189,7 +214,7 @@ struct Stage {
           const int t = i * kRows / group;
           p += (t * x.token_stride + (i * kRows - t * group) * x.head_stride) * (int64_t)sizeof(T);
         }
-        to_lds(p + off[kRegular ? 0 : i], tile, i, wave);
+        load_to_lds16(p, off[kRegular ? 0 : i], to + i * 4096);
       }
     } else {
       int tid = threadIdx.x;
@@ -198,18 +223,11 @@ struct Stage {
       for (int i = 0; i < kEach; ++i) {
         const int r = row_of(i, tid), ch = chunk_of(i, tid);
         const bool counts = ((word >> r) & 1) && ch * Ti::kPer < d;
-        to_lds(counts ? reinterpret_cast<const char*>(at(r) + ch * Ti::kPer) : reinterpret_cast<const char*>(kZeros), tile, i, wave);
+        load_to_lds16(counts ? static_cast<const void*>(at(r) + ch * Ti::kPer) : kZeros, to + i * 4096);
       }
     }
   }
-  static __device__ __forceinline__ void to_lds(const char* p, char* tile, int i, int wave) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p,
-                                     (__attribute__((address_space(3))) void*)(tile + (i * 4 + wave) * 1024), 16, 0, 0);
-  }
 };
-
-// Waits for the wavefront's own loads to LDS (and every other load).
-__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt 0
 
 // The tiles of a workgroup's keys, one after another, without those that no row sees.  Every
 // thread of the workgroup calls next() (its answer is the same for all of them).

@@ -88,17 +88,32 @@ __global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
     const char *kt = lds[2 * buf], *vt = lds[2 * buf + 1];
 
     f32x16 s[NR][2];
+#if GS_PRIO
+    __builtin_amdgcn_s_setprio(1);
+#endif
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int n = 0; n < NR; ++n) s[n][0] = s[n][1] = (f32x16)0.0f;
 #pragma unroll
-      for (int n = 0; n < NR; ++n) s[n][j] = (f32x16)0.0f;
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int st = 0; st < DP / 16; ++st) {
         const Frag<T> kf = Ti::frag_rows(kt, 32 * j, st);
 #pragma unroll
         for (int n = 0; n < NR; ++n) s[n][j] = mma(kf, qf[n][st], s[n][j]);
       }
+#if GS_SG
+    constexpr int N = DP / 8, G = GS_SG < N ? GS_SG : N;
+    __builtin_amdgcn_sched_group_barrier(0x100, G, 0);
+#pragma unroll
+    for (int i = 0; i < N - G; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     }
+    __builtin_amdgcn_sched_group_barrier(0x008, G, 0);
+#endif
+#if GS_PRIO
+    __builtin_amdgcn_s_setprio(0);
+#endif
     if (ragged || word != ~0ull) {
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
@@ -139,6 +154,9 @@ __global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
         }
       l[n] += sum;
     }
+#if GS_PRIO > 1
+    __builtin_amdgcn_s_setprio(1);
+#endif
 #pragma unroll
     for (int step = 0; step < 4; ++step) {
       Frag<T> p[NR];
@@ -151,6 +169,9 @@ __global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
         for (int n = 0; n < NR; ++n) o[n][dt] = mma(vf, p[n], o[n][dt]);
       }
     }
+#if GS_PRIO > 1
+    __builtin_amdgcn_s_setprio(0);
+#endif
   };
   while (tile.word) {
     one(std::integral_constant<int, 0>());

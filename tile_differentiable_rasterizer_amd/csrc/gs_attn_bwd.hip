@@ -10,8 +10,6 @@
 // operand of dV^T[d][key] = dO^T P and dK^T[d][key] = Q^T dS.  q: as the forward kernel, S^T and
 // dP^T = V dO^T, then dQ^T[d][row] = K^T dS^T.
 // p and dS enter the products in the element type (bfloat16: rounded once, 2^-8 of each at most).
-#include <type_traits>
-
 #include "gs_attn.h"
 
 
@@ -127,13 +125,11 @@ __global__ __launch_bounds__(256, (kKvWaves<T, DP>)) void k_attn_bwd_kv(AttnArgs
     qs.load(lds[2 * buf], a.q, a.group, a.d, word, qh + offset(r0, a.q), [&](int r) { return qh + offset(r0 + r, a.q); });
     gs.load(lds[2 * buf + 1], a.dout, a.group, a.d, word, gh + offset(r0, a.dout), [&](int r) { return gh + offset(r0 + r, a.dout); });
     if (wave < 2)  // 64 words each
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)((const float*)(row_stat + r0) + wave * 64 + lane),
-                                       (__attribute__((address_space(3))) void*)((float*)stat[buf] + wave * 64), 4, 0, 0);
+      load_to_lds4((const float*)(row_stat + r0) + wave * 64, lane * 4, lds_address((const float*)stat[buf] + wave * 64));
   };
   int t = find((int)((int64_t)tiles * split / a.splits));
   if (t < t_end) load(t, 0);
-  auto one = [&](auto which) {  // in buffers that the compiler knows
-    constexpr int buf = decltype(which)::value;
+  for (int buf = 0; t < t_end; buf ^= 1) {
     wait_loads();
     __syncthreads();
     const int now = t;
@@ -148,7 +144,7 @@ __global__ __launch_bounds__(256, (kKvWaves<T, DP>)) void k_attn_bwd_kv(AttnArgs
       const int2 range = row < a.rows ? row_range(a, b, row / a.group) : make_int2(0, 0);
       sees = (uint32_t)range_word(range.x, range.y, wk0);
     }
-#pragma unroll
+#pragma unroll (DP <= 64 ? 2 : 1)
     for (int j = 0; j < kBwdRows / 32; ++j) {
       f32x16 s = (f32x16)0.0f, dp = (f32x16)0.0f;
 #pragma unroll
@@ -184,11 +180,6 @@ __global__ __launch_bounds__(256, (kKvWaves<T, DP>)) void k_attn_bwd_kv(AttnArgs
         }
       }
     }
-  };
-  while (t < t_end) {
-    one(std::integral_constant<int, 0>());
-    if (t >= t_end) break;
-    one(std::integral_constant<int, 1>());
   }
 
   if (key >= a.k_len) return;
@@ -267,8 +258,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   };
   tile.next(a, b, seen, range, words);
   if (tile.word) load(0);
-  auto one = [&](auto which) {
-    constexpr int buf = decltype(which)::value;
+  for (int buf = 0; tile.word; buf ^= 1) {
     const uint64_t word = tile.word;
     const int k0 = tile.k0;
     const bool ragged = tile.ragged;
@@ -279,7 +269,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
     const char *kt = lds[2 * buf], *vt = lds[2 * buf + 1];
     uint64_t mine = word;
     if (ragged) mine &= range_word(range[0].x, range[0].y, k0);
-#pragma unroll
+#pragma unroll (DP <= 64 ? 2 : 1)
     for (int j = 0; j < 2; ++j) {
       f32x16 s = (f32x16)0.0f, dp = (f32x16)0.0f;
 #pragma unroll
@@ -304,11 +294,6 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
         for (int dt = 0; dt < DP / 32; ++dt) dq[dt] = mma(Ti::frag_cols(kt, 32 * j + 16 * st, 32 * dt), df, dq[dt]);
       }
     }
-  };
-  while (tile.word) {
-    one(std::integral_constant<int, 0>());
-    if (!tile.word) break;
-    one(std::integral_constant<int, 1>());
   }
 
   if (!valid) return;
