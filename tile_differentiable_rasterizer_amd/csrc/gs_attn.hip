@@ -12,8 +12,8 @@
 
 #include "gs_attn.h"
 
-#ifndef GS_NR
-#define GS_NR 1
+#ifndef GS_UNEVEN
+#define GS_UNEVEN 2048
 #endif
 
 namespace gs {
@@ -74,6 +74,7 @@ __global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
   };
   tile.next(a, b, seen, range, words);
   if (tile.word) load(0);
+  const bool idle = row0 - (lane & 31) >= a.rows;  // no row: such a wavefront only loads
   const float slack = 8.0f / a.slope;  // weights up to 2^8 before the sums are scaled again
   // one tile, in the buffers that the compiler knows (offsets then are immediates)
   auto one = [&](auto which) {
@@ -87,10 +88,8 @@ __global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
     if (tile.word) load(buf ^ 1);
     const char *kt = lds[2 * buf], *vt = lds[2 * buf + 1];
 
+    if (idle) return;
     f32x16 s[NR][2];
-#if GS_PRIO
-    __builtin_amdgcn_s_setprio(1);
-#endif
 #pragma unroll
     for (int n = 0; n < NR; ++n) s[n][0] = s[n][1] = (f32x16)0.0f;
 #pragma unroll
@@ -101,19 +100,6 @@ __global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
 #pragma unroll
         for (int n = 0; n < NR; ++n) s[n][j] = mma(kf, qf[n][st], s[n][j]);
       }
-#if GS_SG
-    constexpr int N = DP / 8, G = GS_SG < N ? GS_SG : N;
-    __builtin_amdgcn_sched_group_barrier(0x100, G, 0);
-#pragma unroll
-    for (int i = 0; i < N - G; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    }
-    __builtin_amdgcn_sched_group_barrier(0x008, G, 0);
-#endif
-#if GS_PRIO
-    __builtin_amdgcn_s_setprio(0);
-#endif
     if (ragged || word != ~0ull) {
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
@@ -154,9 +140,6 @@ __global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
         }
       l[n] += sum;
     }
-#if GS_PRIO > 1
-    __builtin_amdgcn_s_setprio(1);
-#endif
 #pragma unroll
     for (int step = 0; step < 4; ++step) {
       Frag<T> p[NR];
@@ -169,9 +152,6 @@ __global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
         for (int n = 0; n < NR; ++n) o[n][dt] = mma(vf, p[n], o[n][dt]);
       }
     }
-#if GS_PRIO > 1
-    __builtin_amdgcn_s_setprio(0);
-#endif
   };
   while (tile.word) {
     one(std::integral_constant<int, 0>());
@@ -221,34 +201,58 @@ __global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
   }
 }
 
-// Joins the splits of a row: weights 2^(m_s - max m).  DP / 4 lanes a row, four elements a lane.
-template <typename T, int DP>
+// Joins the splits of a row: weights 2^(m_s - max m).  One workgroup for kRows rows; a row's splits
+// are shared out over its 256 / (kRows * DP / 4) groups of DP / 4 lanes (four elements a lane), which
+// meet in LDS.  Few rows leave the splits' loads as the only parallelism.
+template <typename T, int DP, int ROWS>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-  constexpr int kPer = 256 / (DP / 4);  // rows of a workgroup
-  const int64_t nbh = (int64_t)a.batch * a.kv_heads, n = nbh * a.rows;
-  const int64_t at = (int64_t)blockIdx.x * kPer + threadIdx.x / (DP / 4);
-  const int d = (threadIdx.x % (DP / 4)) * 4;
-  if ((int)threadIdx.x >= kPer * (DP / 4) || at >= n) return;
-  float m = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.part_ml[s * n + at].x);
-  const float base = m == -INFINITY ? 0.0f : m;
-  float l = 0.0f, x[4] = {};
-  for (int s = 0; s < a.splits; ++s) {
-    const float2 ml = a.part_ml[s * n + at];
-    if (ml.x == -INFINITY) continue;  // nothing seen there (or no row: its sums are not written)
-    const float w = __builtin_amdgcn_exp2f(ml.x - base);
-    l += ml.y * w;
-    const f32x4 v = *reinterpret_cast<const f32x4*>(a.part + (s * n + at) * DP + d);
+  constexpr int kLanes = DP / 4, kGroups = 256 / kLanes / ROWS;
+  __shared__ float4 sum[ROWS][kGroups][kLanes];
+  __shared__ float2 ml[ROWS][kGroups];
+  const int64_t n = (int64_t)a.batch * a.kv_heads * a.rows;
+  const int g = threadIdx.x / kLanes, r = g % ROWS, part = g / ROWS, d = (threadIdx.x % kLanes) * 4;
+  const int64_t at = (int64_t)blockIdx.x * ROWS + r;
+  const bool here = part < kGroups && at < n;
+  float m = -INFINITY, l = 0.0f;
+  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (here) {
+    for (int s = part; s < a.splits; s += kGroups) {
+      const float2 w = a.part_ml[s * n + at];
+      if (w.x == -INFINITY) continue;  // nothing seen there: its sums are not written
+      const float4 v = *reinterpret_cast<const float4*>(a.part + (s * n + at) * DP + d);
+      const float to = fmaxf(m, w.x);
+      const float keep = __builtin_amdgcn_exp2f(m - to), add = __builtin_amdgcn_exp2f(w.x - to);
+      m = to;
+      l = l * keep + w.y * add;
+      x = make_float4(fmaf(v.x, add, x.x * keep), fmaf(v.y, add, x.y * keep), fmaf(v.z, add, x.z * keep), fmaf(v.w, add, x.w * keep));
+    }
+    sum[r][part][d / 4] = x;
+    if (d == 0) ml[r][part] = make_float2(m, l);
+  }
+  __syncthreads();
+  if (part != 0 || at >= n) return;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = fmaf(v[e], w, x[e]);
+  for (int i = 0; i < kGroups; ++i) m = fmaxf(m, ml[r][i].x);
+  const float base = m == -INFINITY ? 0.0f : m;
+  l = 0.0f;
+  float y[4] = {};
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) {
+    const float w = __builtin_amdgcn_exp2f(ml[r][i].x - base);
+    const float4 v = sum[r][i][d / 4];
+    l = fmaf(ml[r][i].y, w, l);
+    y[0] = fmaf(v.x, w, y[0]);
+    y[1] = fmaf(v.y, w, y[1]);
+    y[2] = fmaf(v.z, w, y[2]);
+    y[3] = fmaf(v.w, w, y[3]);
   }
   const bool none = m == -INFINITY;
   const float inv = none ? 0.0f : 1.0f / l;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) x[e] *= inv;
+  for (int e = 0; e < 4; ++e) y[e] *= inv;
   const int bh = (int)(at / a.rows), row = (int)(at - (int64_t)bh * a.rows);
   const int b = bh / a.kv_heads, i = row / a.group, h = (bh - b * a.kv_heads) * a.group + row - i * a.group;
-  if (d < a.d) store_elems<4>(head_ptr<T>(a.out, b, i, h) + d, x);
+  if (d < a.d) store_elems<4>(head_ptr<T>(a.out, b, i, h) + d, y);
   if (a.lse && d == 0)
     a.lse[((int64_t)b * a.kv_heads * a.group + h) * a.q_len + i] = none ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
 }
@@ -257,24 +261,32 @@ namespace {
 
 template <typename T, int DP>
 hipError_t fwd_launch(const AttnArgs& a, hipStream_t s) {
-  constexpr int NR = GS_NR;
+  constexpr int NR = 1;
   const int64_t nbh = (int64_t)a.batch * a.kv_heads;
   const int64_t blocks = nbh * ((a.rows + 128 * NR - 1) / (128 * NR)) * a.splits;
   k_attn_fwd<T, DP, NR><<<(unsigned)blocks, 256, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  const int64_t per = 256 / (DP / 4);
-  k_attn_join<T, DP><<<(unsigned)((nbh * a.rows + per - 1) / per), 256, 0, s>>>(a);
+  // rows a workgroup: all that its lanes hold where there are rows enough, else one (a token at a
+  // time, 16 splits: 14 -> 5 us)
+  constexpr int kAll = 256 / (DP / 4);
+  const int64_t n = nbh * a.rows;
+  if (n >= 4096)
+    k_attn_join<T, DP, kAll><<<(unsigned)((n + kAll - 1) / kAll), 256, 0, s>>>(a);
+  else
+    k_attn_join<T, DP, 1><<<(unsigned)n, 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 // Parts that a long axis of `tiles` tiles is split into when `blocks` workgroups are too few for
-// 256 CUs: enough for two workgroups a CU, at least two tiles a part.
-int attn_splits(int64_t blocks, int64_t tiles) {
-  if (blocks <= 0 || blocks >= 512) return 1;
-  const int64_t want = (512 + blocks - 1) / blocks, most = tiles / 2;
+// 256 CUs: enough for two workgroups a CU, at least two tiles a part.  Where rows see ranges of
+// their own, workgroups differ in length, and eight a CU let the short ones make room.
+int attn_splits(int64_t blocks, int64_t tiles, bool uneven) {
+  const int64_t aim = uneven ? GS_UNEVEN : 512;
+  if (blocks <= 0 || blocks >= aim) return 1;
+  const int64_t want = (aim + blocks - 1) / blocks, most = tiles / 2;
   return (int)(want < most ? want : most < 1 ? 1 : most);
 }
 
@@ -282,7 +294,8 @@ int attn_padded(int d) { return (d + 31) / 32 * 32; }
 
 int attn_fwd_splits(const gs_cross_attn& p) {
   const int64_t rows = p.q_len * (p.q_heads / p.kv_heads);
-  return attn_splits(p.batch * p.kv_heads * ((rows + 127) / 128), (p.k_len + kAttnKeys - 1) / kAttnKeys);
+  return attn_splits(p.batch * p.kv_heads * ((rows + 127) / 128), (p.k_len + kAttnKeys - 1) / kAttnKeys,
+                     p.ranges && p.ranges_row_stride);
 }
 
 hipError_t launch_attn_fwd(AttnArgs a, int type, hipStream_t s) {

@@ -138,13 +138,14 @@ __global__ __launch_bounds__(256, (kKvWaves<T, DP>)) void k_attn_bwd_kv(AttnArgs
     if (t < t_end) load(t, buf ^ 1);
     const char *qt = lds[2 * buf], *gt = lds[2 * buf + 1];
     const float2* st2 = stat[buf];
+    if (wk0 >= k1) continue;  // no key: such a wavefront only loads
     uint32_t sees = ~0u;  // of row `lane` of the tile: the wavefront's keys that it sees
     if (ragged) {
       const int row = now * kBwdRows + lane;
       const int2 range = row < a.rows ? row_range(a, b, row / a.group) : make_int2(0, 0);
       sees = (uint32_t)range_word(range.x, range.y, wk0);
     }
-#pragma unroll (DP <= 64 ? 2 : 1)
+#pragma unroll (DP * sizeof(T) <= 128 ? 2 : 1)
     for (int j = 0; j < kBwdRows / 32; ++j) {
       f32x16 s = (f32x16)0.0f, dp = (f32x16)0.0f;
 #pragma unroll
@@ -258,6 +259,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   };
   tile.next(a, b, seen, range, words);
   if (tile.word) load(0);
+  const bool idle = row - (lane & 31) >= a.rows;  // no row: such a wavefront only loads
   for (int buf = 0; tile.word; buf ^= 1) {
     const uint64_t word = tile.word;
     const int k0 = tile.k0;
@@ -267,9 +269,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
     tile.next(a, b, seen, range, words);
     if (tile.word) load(buf ^ 1);
     const char *kt = lds[2 * buf], *vt = lds[2 * buf + 1];
+    if (idle) continue;
     uint64_t mine = word;
     if (ragged) mine &= range_word(range[0].x, range[0].y, k0);
-#pragma unroll (DP <= 64 ? 2 : 1)
+#pragma unroll (DP * sizeof(T) <= 128 ? 2 : 1)
     for (int j = 0; j < 2; ++j) {
       f32x16 s = (f32x16)0.0f, dp = (f32x16)0.0f;
 #pragma unroll
@@ -341,12 +344,13 @@ __global__ __launch_bounds__(256) void k_attn_bwd_join(AttnArgs a) {
   }
 }
 
-int attn_splits(int64_t blocks, int64_t tiles);
+int attn_splits(int64_t blocks, int64_t tiles, bool uneven);
 int attn_padded(int d);
 
 int attn_bwd_kv_splits(const gs_cross_attn& p) {
   const int64_t rows = p.q_len * (p.q_heads / p.kv_heads);
-  return attn_splits(p.batch * p.kv_heads * ((p.k_len + 127) / 128), (rows + kBwdRows - 1) / kBwdRows);
+  return attn_splits(p.batch * p.kv_heads * ((p.k_len + 127) / 128), (rows + kBwdRows - 1) / kBwdRows,
+                     p.ranges && p.ranges_row_stride);
 }
 
 namespace {

@@ -171,21 +171,34 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_rotate(NormArgs a, float*
   }
 }
 
-// dw[side][e] = sum over the side's workgroups of their parts: one workgroup for each side and
-// 16 elements, 16 threads an element, in a fixed order.
-__global__ __launch_bounds__(256) void k_norm_dw(const float* __restrict__ part, int D, uint32_t blocks0,
-                                                 uint32_t blocks, float* __restrict__ dwq, float* __restrict__ dwk) {
-  __shared__ float sum[16][17];
+// dw[side][e] = sum over the side's workgroups of their parts, in a fixed order: one workgroup for
+// each side and 16 elements, 64 threads an element, then a tree.
+__global__ __launch_bounds__(1024) void k_norm_dw(const float* __restrict__ part, int D, uint32_t blocks0,
+                                                  uint32_t blocks, float* __restrict__ dwq, float* __restrict__ dwk) {
+  __shared__ float sum[16][16];
   const int e = blockIdx.x * 16 + (threadIdx.x & 15), row = threadIdx.x >> 4;
   const uint32_t b0 = blockIdx.y ? blocks0 : 0, b1 = blockIdx.y ? blocks : blocks0;
   float t = 0.0f;
-  if (e < D)
-    for (uint32_t b = b0 + row; b < b1; b += 16) t += part[(int64_t)b * D + e];
-  sum[row][threadIdx.x & 15] = t;
+  if (e < D) {
+    const float* p = part + e;
+    uint32_t b = b0 + row;
+    for (; b + 64 * 7 < b1; b += 64 * 8) {  // eight loads in flight
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = p[(int64_t)(b + 64 * i) * D];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t += x[i];
+    }
+    for (; b < b1; b += 64) t += p[(int64_t)b * D];
+  }
+  t += __shfl_xor(t, 16, 64);
+  t += __shfl_xor(t, 32, 64);
+  if (__lane_id() < 16) sum[threadIdx.x >> 6][threadIdx.x & 15] = t;
   __syncthreads();
-  if (row == 0 && e < D) {
+  if (threadIdx.x < 16 && e < D) {
     t = 0.0f;
-    for (int i = 0; i < 16; ++i) t += sum[i][threadIdx.x & 15];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += sum[i][threadIdx.x];
     (blockIdx.y ? dwk : dwq)[e] = t;
   }
 }
@@ -287,7 +300,7 @@ hipError_t launch_norm_rotate(const gs_norm_rotate& p, const gs_heads& q, const 
     if (e != hipSuccess) return e;
   }
   if (!dq) return hipSuccess;
-  k_norm_dw<<<dim3((p.head_dim + 15) / 16, 2), 256, 0, s>>>(part, p.head_dim, a.blocks0, blocks, dwq, dwk);
+  k_norm_dw<<<dim3((p.head_dim + 15) / 16, 2), 1024, 0, s>>>(part, p.head_dim, a.blocks0, blocks, dwq, dwk);
   return hipGetLastError();
 }
 

@@ -20,7 +20,7 @@ import ctypes as C
 import torch
 
 from . import raster
-from .raster import _check, _stream
+from .raster import _check
 
 BF16, F32 = 0, 1
 TYPES = {torch.bfloat16: BF16, torch.float32: F32}
@@ -75,63 +75,89 @@ def lib():
     return _lib
 
 
+# The smallest calls are bound by the host, so the checks are few and plain: no generators, no
+# tuples made, the current stream's handle without a Stream object.
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _require(ok, what):
-    if not ok:
-        raise ValueError(what)
+def _stream(stream, t):
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+
+
+def _refuse(what):
+    raise ValueError(what)
 
 
 def _heads(t) -> GsHeads:
-    s = t.stride()
-    _require(s[3] == 1 or t.shape[3] == 1, "the last axis must be dense")
-    return GsHeads(t.data_ptr(), s[0], s[1], s[2])
+    b, n, h, d = t.stride()
+    if d != 1 and t.shape[3] > 1:
+        _refuse("the last axis must be dense")
+    return GsHeads(t.data_ptr(), b, n, h)
 
 
-def _type(*tensors) -> int:
-    t = tensors[0].dtype
-    _require(t in TYPES, f"bfloat16 or float32, not {t}")
-    dev = tensors[0].device
-    _require(dev.type == "cuda", "tensors on the GPU")
-    for x in tensors:
-        _require(x.dtype == t and x.device == dev, "one type and one device for all of a call's vectors")
-    return TYPES[t]
+def _type(t) -> int:
+    ty = TYPES.get(t.dtype)
+    if ty is None:
+        _refuse(f"bfloat16 or float32, not {t.dtype}")
+    if not t.is_cuda:
+        _refuse("tensors on the GPU")
+    return ty
 
 
-def _floats(t, shape, what):
-    _require(t.dtype == torch.float32 and tuple(t.shape) == shape and t.is_contiguous() and t.is_cuda,
-             f"{what}: float32 {shape}, contiguous, on the GPU")
+def _same(t, x, shape):
+    """x has t's type, is on its GPU and has this shape."""
+    if x.dtype != t.dtype or x.get_device() != t.get_device():
+        _refuse("one type and one GPU for all of a call's vectors")
+    if x.shape != shape:
+        _refuse(f"a tensor of shape {tuple(x.shape)} in the place of one of {tuple(shape)}")
 
 
-def _workspace(given, need, device):
+def _floats(x, shape, t, what):
+    if x.dtype != torch.float32 or x.shape != shape or not x.is_contiguous() or x.get_device() != t.get_device():
+        _refuse(f"{what}: float32 {tuple(shape)}, contiguous, on the vectors' GPU")
+
+
+def _dense(shape, t):
+    return torch.empty(shape, dtype=t.dtype, device=t.device)
+
+
+def _workspace(given, need, t):
     if given is not None:
-        _require(given.is_contiguous() and given.device == device, "workspace: contiguous, on the same GPU")
+        if not given.is_contiguous() or given.get_device() != t.get_device():
+            _refuse("workspace: contiguous, on the vectors' GPU")
         return given, given.numel() * given.element_size()
     if need == 0:
         return None, 0
-    return torch.empty(need, dtype=torch.uint8, device=device), need
+    return torch.empty(need, dtype=torch.uint8, device=t.device), need
 
 
 # -- norm with rotation ----------------------------------------------------------------------
 
 
 def _norm_shape(q, k, wq, wk, cos, sin, pos_q, pos_k, eps, pairs) -> GsNormRotate:
-    _require(q.dim() == 4 and k.dim() == 4 and q.shape[0] == k.shape[0] and q.shape[3] == k.shape[3],
-             "q [batch][tokens][heads][d] and k of the same batch and d")
-    _require(pairs in PAIRS, f"pairs: one of {tuple(PAIRS)}")
+    if q.dim() != 4 or k.dim() != 4:
+        _refuse("q [batch][tokens][heads][d], k [batch][keys][heads][d]")
     B, Lq, Hq, D = q.shape
-    _floats(wq, (D,), "wq")
-    _floats(wk, (D,), "wk")
-    _require(cos.dim() == 2, "cos, sin: [positions][pairs]")
-    _floats(cos, tuple(cos.shape), "cos")
-    _floats(sin, tuple(cos.shape), "sin")
-    for pos, n in ((pos_q, Lq), (pos_k, k.shape[1])):
-        _require(pos is None or (pos.dtype == torch.int32 and tuple(pos.shape) == (B, n) and pos.is_contiguous()
-                                 and pos.is_cuda), "positions: int32 [batch][tokens], contiguous, on the GPU")
-    return GsNormRotate(B, Lq, k.shape[1], Hq, k.shape[2], D, 2 * cos.shape[1], PAIRS[pairs], _type(q, k), eps,
-                        cos.shape[0])
+    _, Lk, Hk, _ = k.shape
+    if pairs not in PAIRS:
+        _refuse(f"pairs: one of {tuple(PAIRS)}")
+    ty = _type(q)
+    _same(q, k, (B, Lk, Hk, D))
+    _floats(wq, (D,), q, "wq")
+    _floats(wk, (D,), q, "wk")
+    if cos.dim() != 2:
+        _refuse("cos, sin: [positions][pairs]")
+    n, half = cos.shape
+    _floats(cos, (n, half), q, "cos")
+    _floats(sin, (n, half), q, "sin")
+    for pos, length in ((pos_q, Lq), (pos_k, Lk)):
+        if pos is not None and (pos.dtype != torch.int32 or pos.shape != (B, length) or not pos.is_contiguous()
+                                or pos.get_device() != q.get_device()):
+            _refuse("positions: int32 [batch][tokens], contiguous, on the vectors' GPU")
+    return GsNormRotate(B, Lq, Lk, Hq, Hk, D, 2 * half, PAIRS[pairs], ty, eps, n)
 
 
 def norm_rotate_fwd(q, k, wq, wk, cos, sin, pos_q=None, pos_k=None, eps: float = 1e-6, pairs: str = "halves",
@@ -140,12 +166,14 @@ def norm_rotate_fwd(q, k, wq, wk, cos, sin, pos_q=None, pos_k=None, eps: float =
     k [B, Lk, Hk, D]; cos, sin [positions, pairs]; ``out``: the two outputs' tensors (may be q, k)."""
     p = _norm_shape(q, k, wq, wk, cos, sin, pos_q, pos_k, eps, pairs)
     if out is None:
-        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device), torch.empty(k.shape, dtype=k.dtype, device=k.device))
-    oq, ok = out
-    _require(oq.shape == q.shape and ok.shape == k.shape, "out: the inputs' shapes")
-    _type(q, oq, ok)
-    _check(lib().gs_norm_rotate_fwd(p, _heads(q), _heads(k), _ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin), _ptr(pos_q),
-                                    _ptr(pos_k), _heads(oq), _heads(ok), _stream(stream)), "gs_norm_rotate_fwd")
+        oq, ok = _dense(q.shape, q), _dense(k.shape, k)
+    else:
+        oq, ok = out
+        _same(q, oq, q.shape)
+        _same(q, ok, k.shape)
+    _check(lib().gs_norm_rotate_fwd(p, _heads(q), _heads(k), wq.data_ptr(), wk.data_ptr(), cos.data_ptr(), sin.data_ptr(),
+                                    _ptr(pos_q), _ptr(pos_k), _heads(oq), _heads(ok), _stream(stream, q)),
+           "gs_norm_rotate_fwd")
     return oq, ok
 
 
@@ -153,16 +181,15 @@ def norm_rotate_bwd(dout_q, dout_k, q, k, wq, wk, cos, sin, pos_q=None, pos_k=No
                     pairs: str = "halves", workspace=None, stream=None) -> tuple:
     """gs_norm_rotate_bwd: (dq, dk, dwq, dwk) from the inputs of the forward call and its outputs' gradients."""
     p = _norm_shape(q, k, wq, wk, cos, sin, pos_q, pos_k, eps, pairs)
-    _require(dout_q.shape == q.shape and dout_k.shape == k.shape, "dout_q, dout_k: the inputs' shapes")
-    _type(q, dout_q, dout_k)
-    L, dev, D = lib(), q.device, q.shape[3]
-    dq, dk = torch.empty(q.shape, dtype=q.dtype, device=dev), torch.empty(k.shape, dtype=k.dtype, device=dev)
-    dw = torch.empty((2, D), dtype=torch.float32, device=dev)
-    dwq, dwk = dw.unbind(0)
-    ws, n = _workspace(workspace, L.gs_norm_rotate_workspace_bytes(p), dev)
-    _check(L.gs_norm_rotate_bwd(p, _heads(dout_q), _heads(dout_k), _heads(q), _heads(k), _ptr(wq), _ptr(wk), _ptr(cos),
-                                _ptr(sin), _ptr(pos_q), _ptr(pos_k), _heads(dq), _heads(dk), _ptr(dwq), _ptr(dwk),
-                                _ptr(ws), n, _stream(stream)), "gs_norm_rotate_bwd")
+    _same(q, dout_q, q.shape)
+    _same(q, dout_k, k.shape)
+    L = lib()
+    dq, dk = _dense(q.shape, q), _dense(k.shape, k)
+    dwq, dwk = torch.empty_like(wq), torch.empty_like(wk)
+    ws, n = _workspace(workspace, L.gs_norm_rotate_workspace_bytes(p), q)
+    _check(L.gs_norm_rotate_bwd(p, _heads(dout_q), _heads(dout_k), _heads(q), _heads(k), wq.data_ptr(), wk.data_ptr(),
+                                cos.data_ptr(), sin.data_ptr(), _ptr(pos_q), _ptr(pos_k), _heads(dq), _heads(dk),
+                                dwq.data_ptr(), dwk.data_ptr(), _ptr(ws), n, _stream(stream, q)), "gs_norm_rotate_bwd")
     return dq, dk, dwq, dwk
 
 
@@ -170,22 +197,27 @@ def norm_rotate_bwd(dout_q, dout_k, q, k, wq, wk, cos, sin, pos_q=None, pos_k=No
 
 
 def _attn_shape(q, k, v, scale, ranges, key_mask) -> GsCrossAttn:
-    _require(q.dim() == 4 and k.dim() == 4 and k.shape == v.shape and q.shape[0] == k.shape[0] and q.shape[3] == k.shape[3],
-             "q [batch][rows][heads][d]; k and v [batch][keys][kv heads][d]")
+    if q.dim() != 4 or k.dim() != 4:
+        _refuse("q [batch][rows][heads][d]; k and v [batch][keys][kv heads][d]")
     B, Lq, Hq, D = q.shape
-    Lk, Hk = k.shape[1], k.shape[2]
-    p = GsCrossAttn(B, Lq, Lk, Hq, Hk, D, _type(q, k, v), D**-0.5 if scale is None else scale)
+    _, Lk, Hk, _ = k.shape
+    ty = _type(q)
+    _same(q, k, (B, Lk, Hk, D))
+    _same(q, v, (B, Lk, Hk, D))
+    p = GsCrossAttn(B, Lq, Lk, Hq, Hk, D, ty, D**-0.5 if scale is None else scale)
     if ranges is not None:
-        _require(ranges.dtype == torch.int32 and ranges.is_cuda and ranges.dim() == 3 and ranges.shape[0] in (1, B)
-                 and ranges.shape[1] in (1, Lq) and ranges.shape[2] == 2 and (ranges.numel() == 0 or ranges.stride(2) == 1)
-                 and ranges.stride(0) % 2 == 0 and ranges.stride(1) % 2 == 0,
-                 "ranges: int32 [batch or 1][rows or 1][2], pairs dense, on the GPU")
+        if (ranges.dtype != torch.int32 or ranges.get_device() != q.get_device() or ranges.dim() != 3
+                or ranges.shape[0] not in (1, B) or ranges.shape[1] not in (1, Lq) or ranges.shape[2] != 2
+                or (ranges.numel() and (ranges.stride(2) != 1 or ranges.stride(0) % 2 or ranges.stride(1) % 2))):
+            _refuse("ranges: int32 [batch or 1][rows or 1][2], pairs dense, on the vectors' GPU")
         p.ranges = ranges.data_ptr()
         p.ranges_batch_stride = ranges.stride(0) // 2 if ranges.shape[0] > 1 else 0
         p.ranges_row_stride = ranges.stride(1) // 2 if ranges.shape[1] > 1 else 0
     if key_mask is not None:
-        _require(key_mask.dtype in (torch.uint8, torch.bool) and key_mask.is_cuda and tuple(key_mask.shape) in ((B, Lk), (1, Lk))
-                 and (Lk <= 1 or key_mask.stride(1) == 1), "key_mask: bytes or truth values [batch or 1][keys], on the GPU")
+        if (key_mask.dtype not in (torch.uint8, torch.bool) or key_mask.get_device() != q.get_device()
+                or key_mask.dim() != 2 or key_mask.shape[0] not in (1, B) or key_mask.shape[1] != Lk
+                or (Lk > 1 and key_mask.stride(1) != 1)):
+            _refuse("key_mask: bytes or truth values [batch or 1][keys], on the vectors' GPU")
         p.key_mask = key_mask.data_ptr()
         p.key_mask_batch_stride = key_mask.stride(0) if key_mask.shape[0] > 1 else 0
     return p
@@ -197,19 +229,19 @@ def cross_attn_fwd(q, k, v, scale: float | None = None, ranges=None, key_mask=No
     keys [first, last) of each row (one row: lengths of sequences); ``key_mask`` [B or 1, Lk]: 0 hides a key; ``scale``
     None: 1 / sqrt(D)."""
     p = _attn_shape(q, k, v, scale, ranges, key_mask)
-    dev = q.device
-    B, Lq, Hq, _ = q.shape
+    shape = (p.batch, p.q_heads, p.q_len)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        out = _dense(q.shape, q)
+    else:
+        _same(q, out, q.shape)
     if lse is None:
-        lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=dev)
-    _require(out.shape == q.shape, "out: q's shape")
-    _type(q, out)
-    _floats(lse, (B, Hq, Lq), "lse")
+        lse = torch.empty(shape, dtype=torch.float32, device=q.device)
+    else:
+        _floats(lse, shape, q, "lse")
     L = lib()
-    ws, n = _workspace(workspace, L.gs_cross_attn_fwd_workspace_bytes(p), dev)
-    _check(L.gs_cross_attn_fwd(p, _heads(q), _heads(k), _heads(v), _heads(out), _ptr(lse), _ptr(ws), n, _stream(stream)),
-           "gs_cross_attn_fwd")
+    ws, n = _workspace(workspace, L.gs_cross_attn_fwd_workspace_bytes(p), q)
+    _check(L.gs_cross_attn_fwd(p, _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(), _ptr(ws), n,
+                               _stream(stream, q)), "gs_cross_attn_fwd")
     return out, lse
 
 
@@ -217,60 +249,67 @@ def cross_attn_bwd(dout, q, k, v, out, lse, scale: float | None = None, ranges=N
                    stream=None) -> tuple:
     """gs_cross_attn_bwd: (dq, dk, dv) from the forward call's inputs and outputs and the gradient of out."""
     p = _attn_shape(q, k, v, scale, ranges, key_mask)
-    dev = q.device
-    _require(dout.shape == q.shape and out.shape == q.shape, "dout, out: q's shape")
-    _type(q, dout, out)
-    _floats(lse, (q.shape[0], q.shape[2], q.shape[1]), "lse")
-    dq, dk, dv = (torch.empty(x.shape, dtype=x.dtype, device=dev) for x in (q, k, v))
+    _same(q, dout, q.shape)
+    _same(q, out, q.shape)
+    _floats(lse, (p.batch, p.q_heads, p.q_len), q, "lse")
+    dq, dk, dv = _dense(q.shape, q), _dense(k.shape, k), _dense(v.shape, v)
     L = lib()
-    ws, n = _workspace(workspace, L.gs_cross_attn_bwd_workspace_bytes(p), dev)
-    _check(L.gs_cross_attn_bwd(p, _heads(dout), _heads(q), _heads(k), _heads(v), _heads(out), _ptr(lse), _heads(dq), _heads(dk),
-                               _heads(dv), _ptr(ws), n, _stream(stream)), "gs_cross_attn_bwd")
+    ws, n = _workspace(workspace, L.gs_cross_attn_bwd_workspace_bytes(p), q)
+    _check(L.gs_cross_attn_bwd(p, _heads(dout), _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(), _heads(dq),
+                               _heads(dk), _heads(dv), _ptr(ws), n, _stream(stream, q)), "gs_cross_attn_bwd")
     return dq, dk, dv
 
 
 # -- gated activation with 8-bit checkpoints -------------------------------------------------
 
 
-def _matrix(t, rows, width):
-    _require(t.dim() == 2 and t.shape[0] == rows and t.shape[1] == width and (width <= 1 or t.stride(1) == 1),
-             "matrices [rows][width] of one shape, rows dense")
-    return t.data_ptr(), t.stride(0)
+def _stride(x, t, rows, width):
+    """x's row stride; it is a matrix [rows][width] of t's type on its GPU, its rows dense."""
+    _same(t, x, (rows, width))
+    if width > 1 and x.stride(1) != 1:
+        _refuse("matrices [rows][width], rows dense")
+    return x.stride(0)
 
 
 def gate8_fwd(gate, up, act: str = "silu", stream=None) -> tuple:
     """gs_gate8_fwd: (y, codes, bounds) of act(gate) * up; gate, up [rows, width] (views of one projection's output
     are taken as they are).  codes uint8 [2, rows, width] and bounds float32 [2, rows, blocks, 2] are what
     gate8_bwd needs."""
-    _require(act in ACTS, f"act: one of {tuple(ACTS)}")
-    _require(gate.dim() == 2, "matrices [rows][width]")
+    if act not in ACTS:
+        _refuse(f"act: one of {tuple(ACTS)}")
+    if gate.dim() != 2:
+        _refuse("matrices [rows][width]")
+    ty = _type(gate)
     rows, width = gate.shape
-    dev, ty = gate.device, _type(gate, up)
+    gs, us = _stride(gate, gate, rows, width), _stride(up, gate, rows, width)
+    dev = gate.device
     y = torch.empty((rows, width), dtype=gate.dtype, device=dev)
     codes = torch.empty((2, rows, width), dtype=torch.uint8, device=dev)
     bounds = torch.empty((2, rows, (width + CODE_BLOCK - 1) // CODE_BLOCK, 2), dtype=torch.float32, device=dev)
-    _check(lib().gs_gate8_fwd(rows, width, ACTS[act], ty, *_matrix(gate, rows, width), *_matrix(up, rows, width),
-                              *_matrix(y, rows, width), _ptr(codes), _ptr(bounds), _stream(stream)), "gs_gate8_fwd")
+    _check(lib().gs_gate8_fwd(rows, width, ACTS[act], ty, gate.data_ptr(), gs, up.data_ptr(), us, y.data_ptr(), width,
+                              codes.data_ptr(), bounds.data_ptr(), _stream(stream, gate)), "gs_gate8_fwd")
     return y, codes, bounds
 
 
 def gate8_bwd(dy, codes, bounds, act: str = "silu", with_y: bool = True, dgate=None, dup=None, stream=None) -> tuple:
     """gs_gate8_bwd: (dgate, dup, y again or None) from the codes; ``dgate``, ``dup``: tensors to write to, such as the
     halves of one [rows, 2 * width] gradient."""
-    _require(act in ACTS, f"act: one of {tuple(ACTS)}")
-    _require(dy.dim() == 2, "matrices [rows][width]")
+    if act not in ACTS:
+        _refuse(f"act: one of {tuple(ACTS)}")
+    if dy.dim() != 2:
+        _refuse("matrices [rows][width]")
+    ty = _type(dy)
     rows, width = dy.shape
-    dev = dy.device
-    _require(codes.dtype == torch.uint8 and tuple(codes.shape) == (2, rows, width) and codes.is_contiguous()
-             and codes.device == dev, "codes: gate8_fwd's")
-    _floats(bounds, (2, rows, (width + CODE_BLOCK - 1) // CODE_BLOCK, 2), "bounds")
-    dgate = torch.empty((rows, width), dtype=dy.dtype, device=dev) if dgate is None else dgate
-    dup = torch.empty((rows, width), dtype=dy.dtype, device=dev) if dup is None else dup
-    y = torch.empty((rows, width), dtype=dy.dtype, device=dev) if with_y else None
-    ty = _type(dy, dgate, dup)
-    _check(lib().gs_gate8_bwd(rows, width, ACTS[act], ty, *_matrix(dy, rows, width), _ptr(codes), _ptr(bounds),
-                              *_matrix(dgate, rows, width), *_matrix(dup, rows, width),
-                              *(_matrix(y, rows, width) if with_y else (None, 0)), _stream(stream)), "gs_gate8_bwd")
+    if codes.dtype != torch.uint8 or codes.shape != (2, rows, width) or not codes.is_contiguous() or codes.get_device() != dy.get_device():
+        _refuse("codes: gate8_fwd's")
+    _floats(bounds, (2, rows, (width + CODE_BLOCK - 1) // CODE_BLOCK, 2), dy, "bounds")
+    ds = _stride(dy, dy, rows, width)
+    dgate = _dense((rows, width), dy) if dgate is None else dgate
+    dup = _dense((rows, width), dy) if dup is None else dup
+    y = _dense((rows, width), dy) if with_y else None
+    _check(lib().gs_gate8_bwd(rows, width, ACTS[act], ty, dy.data_ptr(), ds, codes.data_ptr(), bounds.data_ptr(),
+                              dgate.data_ptr(), _stride(dgate, dy, rows, width), dup.data_ptr(), _stride(dup, dy, rows, width),
+                              _ptr(y), width, _stream(stream, dy)), "gs_gate8_bwd")
     return dgate, dup, y
 
 
