@@ -164,24 +164,26 @@ __device__ __forceinline__ void load_to_lds4(const void* base, uint32_t offset, 
 // Waits for the wavefront's own loads to LDS (and every other load).
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" : : : "memory"); }
 
-// Staging of 64 vectors to a tile by 256 threads, 16 bytes a lane straight to LDS: a wavefront's 64
-// chunks lie in a row there, and the swizzle is in the address that a lane reads.  The loads are in
-// flight while the tile before is worked on, and cost no registers.
+// Staging of ROWS vectors to a tile by 256 threads, 16 bytes a lane straight to LDS: a wavefront's
+// 64 chunks lie in a row there, and the swizzle is in the address that a lane reads.  The loads are
+// in flight while the tile before is worked on, and cost no registers.
 //
 // Where every vector counts, the vectors are evenly spaced and D fills the tile's rows, a load's
 // address is a uniform base and an offset that the thread keeps from start to end.  Elsewhere each
 // lane's address is made for it, and lanes of vectors that do not count, or of chunks past D, read
 // zeros: nothing is read from there.
-template <typename T, int DP>
+template <typename T, int DP, int ROWS>
 struct Stage {
   using Ti = Tile<T, DP>;
-  static constexpr int kEach = kAttnKeys * Ti::kChunks / 256;
-  static constexpr int kBytes = kAttnKeys * Ti::kRowBytes;
-  static_assert(kEach * 256 == kAttnKeys * Ti::kChunks, "whole chunks a thread");
+  static constexpr int kEach = ROWS * Ti::kChunks / 256;
+  static constexpr int kBytes = ROWS * Ti::kRowBytes;
+  static_assert(kEach * 256 == ROWS * Ti::kChunks, "whole chunks a thread");
   // one offset serves all of a thread's chunks where they are whole rounds of the swizzle apart
-  static constexpr bool kRegular = 256 % Ti::kChunks == 0 && 256 / Ti::kChunks % 16 == 0;
+  static constexpr bool kRegular = kEach == 1 || (256 % Ti::kChunks == 0 && 256 / Ti::kChunks % 16 == 0);
+  static constexpr int kRound = kRegular && kEach > 1 ? 256 / Ti::kChunks : ROWS;  // vectors between two chunks
 
   uint32_t off[kRegular ? 1 : kEach];  // bytes from the tile's first vector
+  int64_t round;                       // bytes of kRound vectors
   bool even;
 
   // Row of the tile, and chunk of the vector, that the thread's i-th 16 bytes of the tile hold.
@@ -191,9 +193,10 @@ struct Stage {
     return (c - r * Ti::kChunks) ^ Ti::mix(r);
   }
 
-  // Vectors of `group` heads a token (`group` divides 64, else they are not even).
+  // Vectors of `group` heads a token; they are even where a round holds whole tokens.
   __device__ __forceinline__ void plan(const gs_heads& x, int group, int d) {
-    even = d == DP && 64 % group == 0 && (64 / group) * x.token_stride + group * x.head_stride < (1 << 28);
+    even = d == DP && kRound % group == 0 && (ROWS / group) * x.token_stride + group * x.head_stride < (1 << 28);
+    round = even ? kRound / group * x.token_stride * (int64_t)sizeof(T) : 0;
 #pragma unroll
     for (int i = 0; i < (kRegular ? 1 : kEach); ++i) {
       const int r = row_of(i, threadIdx.x), t = r / group;
@@ -203,18 +206,14 @@ struct Stage {
 
   // first: the tile's vector 0; at(r): vector r; bit r of `word`: it counts.
   template <class At>
-  __device__ __forceinline__ void load(char* tile, const gs_heads& x, int group, int d, uint64_t word, const T* first, At&& at) const {
+  __device__ __forceinline__ void load(char* tile, int d, uint64_t word, const T* first, At&& at) const {
     const uint32_t to = lds_address(tile + (threadIdx.x >> 6) * 1024);
-    if (even && word == ~0ull) {
+    if (even && word == (~0ull >> (64 - ROWS))) {
+      const char* p = reinterpret_cast<const char*>(first);
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        const char* p = reinterpret_cast<const char*>(first);
-        if (kRegular) {  // i whole rounds of 256 / kChunks vectors further on
-          constexpr int kRows = kRegular ? 256 / Ti::kChunks : 1;
-          const int t = i * kRows / group;
-          p += (t * x.token_stride + (i * kRows - t * group) * x.head_stride) * (int64_t)sizeof(T);
-        }
         load_to_lds16(p, off[kRegular ? 0 : i], to + i * 4096);
+        if (kRegular) p += round;
       }
     } else {
       int tid = threadIdx.x;

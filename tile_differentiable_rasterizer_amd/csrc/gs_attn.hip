@@ -21,7 +21,7 @@ namespace gs {
 template <typename T, int DP, int NR>
 __global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
   using Ti = Tile<T, DP>;
-  using St = Stage<T, DP>;
+  using St = Stage<T, DP, kAttnKeys>;
   __shared__ __align__(16) char lds[4][St::kBytes];  // keys and values of two tiles
   __shared__ int scratch[4][4];
   __shared__ uint64_t words[4];
@@ -69,12 +69,13 @@ __global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
   vs.plan(a.v, 1, a.d);
   auto load = [&](int buf) {
     const T *k = kh + tile.k0 * a.k.token_stride, *v = vh + tile.k0 * a.v.token_stride;
-    ks.load(lds[2 * buf], a.k, 1, a.d, tile.word, k, [&](int r) { return k + r * a.k.token_stride; });
-    vs.load(lds[2 * buf + 1], a.v, 1, a.d, tile.word, v, [&](int r) { return v + r * a.v.token_stride; });
+    ks.load(lds[2 * buf], a.d, tile.word, k, [&](int r) { return k + r * a.k.token_stride; });
+    vs.load(lds[2 * buf + 1], a.d, tile.word, v, [&](int r) { return v + r * a.v.token_stride; });
   };
   tile.next(a, b, seen, range, words);
   if (tile.word) load(0);
   const bool idle = row0 - (lane & 31) >= a.rows;  // no row: such a wavefront only loads
+  const typename Ti::Lane at;
   const float slack = 8.0f / a.slope;  // weights up to 2^8 before the sums are scaled again
   // one tile, in the buffers that the compiler knows (offsets then are immediates)
   auto one = [&](auto which) {
@@ -96,7 +97,7 @@ __global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int st = 0; st < DP / 16; ++st) {
-        const Frag<T> kf = Ti::frag_rows(kt, 32 * j, st);
+        const Frag<T> kf = Ti::frag_rows(kt, at, 32 * j, st);
 #pragma unroll
         for (int n = 0; n < NR; ++n) s[n][j] = mma(kf, qf[n][st], s[n][j]);
       }
@@ -147,7 +148,7 @@ __global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
       for (int n = 0; n < NR; ++n) p[n] = frag_of<T>(s[n][step >> 1], step & 1);
 #pragma unroll
       for (int dt = 0; dt < DP / 32; ++dt) {
-        const Frag<T> vf = Ti::frag_cols(vt, 16 * step, 32 * dt);
+        const Frag<T> vf = Ti::frag_cols(vt, at, 16 * step, 32 * dt);
 #pragma unroll
         for (int n = 0; n < NR; ++n) o[n][dt] = mma(vf, p[n], o[n][dt]);
       }

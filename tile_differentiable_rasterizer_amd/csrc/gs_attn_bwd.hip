@@ -11,6 +11,12 @@
 // dP^T = V dO^T, then dQ^T[d][row] = K^T dS^T.
 // p and dS enter the products in the element type (bfloat16: rounded once, 2^-8 of each at most).
 #include "gs_attn.h"
+#ifndef GS_VL
+#define GS_VL 1
+#endif
+#ifndef GS_P
+#define GS_P 4
+#endif
 
 
 namespace gs {
@@ -65,68 +71,86 @@ __global__ __launch_bounds__(256) void k_attn_stat(AttnArgs a) {
   if (threadIdx.x == 0) a.row_tiles[blockIdx.x] = w;
 }
 
-// Wavefronts a SIMD: two where the results (DP registers) and the keys' and values' fragments leave
-// room in 256 (float32 D 64: 249 -> 201 us for the whole backward pass of 2 x 391 rows; bfloat16
-// D 64: 2.85 -> 2.25 ms), else one (bfloat16 D 128 spills with two: 5.4 -> 8.0 ms).
+// How the kv kernel fits its registers.  Its results take DP of them, and the fragments of its keys
+// and values DP / 4 a byte of the type.
 template <typename T, int DP>
-constexpr int kKvWaves = DP + DP * (int)sizeof(T) / 4 <= 150 ? 2 : 1;
+struct KvShape {
+  // bfloat16 D 128: the values' fragments stay in LDS, and tiles of 32 rows make room there, so that
+  // two wavefronts share a SIMD
+  static constexpr bool kValuesInLds = GS_VL && sizeof(T) == 2 && DP == 128;
+  static constexpr int kRows = kValuesInLds ? 32 : kBwdRows;  // of a tile
+  static constexpr int kWaves = kValuesInLds || DP + DP * (int)sizeof(T) / 4 <= 150 ? 2 : 1;  // a SIMD
+};
 
 template <typename T, int DP>
-__global__ __launch_bounds__(256, (kKvWaves<T, DP>)) void k_attn_bwd_kv(AttnArgs a) {
+__global__ __launch_bounds__(256, (KvShape<T, DP>::kWaves)) void k_attn_bwd_kv(AttnArgs a) {
   using Ti = Tile<T, DP>;
-  using St = Stage<T, DP>;
-  __shared__ __align__(16) char lds[4][St::kBytes];  // queries and output gradients of two tiles
-  __shared__ __align__(32) float2 stat[2][kBwdRows];
+  using Sh = KvShape<T, DP>;
+  using St = Stage<T, DP, Sh::kRows>;
+  constexpr int kRows = Sh::kRows, kPerInfo = kBwdRows / kRows;
+  constexpr int kS = DP / 16, kD = DP / 32;  // k steps of the scores; blocks of the results' elements
+  __shared__ __align__(32) char lds[4][St::kBytes];  // queries and output gradients of two tiles
+  __shared__ __align__(32) float2 stat[2][kRows];
+  __shared__ __align__(16) char vt[Sh::kValuesInLds ? 128 * Ti::kRowBytes : 16];
   const int nbh = a.batch * a.kv_heads;
   const int bh = blockIdx.x % nbh, rest = blockIdx.x / nbh;
   const int split = rest % a.splits, kb = rest / a.splits;
   const int b = bh / a.kv_heads, hk = bh - b * a.kv_heads;
   const int lane = __lane_id(), half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int k0 = kb * 128, k1 = min(k0 + 128, a.k_len);
-  const int wk0 = k0 + (threadIdx.x >> 6) * 32, key = wk0 + (lane & 31);
+  const int wk0 = k0 + wave * 32, key = wk0 + (lane & 31);
   const bool open = key < a.k_len && (!a.mask || a.mask[b * a.mask_b + key] != 0);
 
-  Frag<T> kf[DP / 16], vf[DP / 16];
+  Frag<T> kf[kS], vf[kS];
 #pragma unroll
-  for (int s = 0; s < DP / 16; ++s) {
+  for (int s = 0; s < kS; ++s) {
     kf[s] = frag_flip(frag_mem<T>(head_ptr<T>(a.k, b, key, hk), a.d, s, open), a.flip);
     vf[s] = frag_mem<T>(head_ptr<T>(a.v, b, key, hk), a.d, s, open);
   }
-  f32x16 dk[DP / 32], dv[DP / 32];
+  if constexpr (Sh::kValuesInLds) {  // each wavefront's own 32 rows
 #pragma unroll
-  for (int t = 0; t < DP / 32; ++t) dk[t] = dv[t] = (f32x16)0.0f;
+    for (int s = 0; s < kS; ++s)
+      *reinterpret_cast<Frag<T>*>(vt + Ti::at(wave * 32 + (lane & 31), 2 * s + half)) = vf[s];
+  }
+  f32x16 dk[kD], dv[kD];
+#pragma unroll
+  for (int t = 0; t < kD; ++t) dk[t] = dv[t] = (f32x16)0.0f;
 
-  const int tiles = (a.rows + kBwdRows - 1) / kBwdRows;
+  const int infos = (a.rows + kBwdRows - 1) / kBwdRows, tiles = infos * kPerInfo;
   const int t_end = (int)((int64_t)tiles * (split + 1) / a.splits);
-  const RowTile* info = a.row_tiles + (int64_t)bh * tiles;
-  const float2* row_stat = a.stat + (int64_t)bh * tiles * kBwdRows;
+  const RowTile* info = a.row_tiles + (int64_t)bh * infos;
+  const float2* row_stat = a.stat + (int64_t)bh * infos * kBwdRows;
   const T* qh = head_ptr<T>(a.q, b, 0, hk * a.group);
   const T* gh = head_ptr<T>(a.dout, b, 0, hk * a.group);
+  St qs, gs;
+  qs.plan(a.q, a.group, a.d);
+  gs.plan(a.dout, a.group, a.d);
   // the next tile from t on whose rows see some of the keys (the same for every thread)
   RowTile next;
   auto find = [&](int t) {
     for (; t < t_end; ++t) {
-      next = info[t];
+      next = info[t / kPerInfo];
       if (next.word && next.first < k1 && next.last > k0) break;
     }
     return t;
   };
-  St qs, gs;
-  qs.plan(a.q, a.group, a.d);
-  gs.plan(a.dout, a.group, a.d);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t q_step = kRows / a.group * a.q.token_stride, g_step = kRows / a.group * a.dout.token_stride;  // used where even
   auto load = [&](int t, int buf) {
-    const int r0 = t * kBwdRows;
-    const uint64_t word = next.word;
+    const int r0 = t * kRows;
+    uint64_t word = next.word;
+    if constexpr (kPerInfo == 2) word = t & 1 ? word >> 32 : word & 0xffffffffu;
     auto offset = [&](int r, const gs_heads& x) {
       const int i = r / a.group;
       return i * x.token_stride + (r - i * a.group) * x.head_stride;
     };
-    qs.load(lds[2 * buf], a.q, a.group, a.d, word, qh + offset(r0, a.q), [&](int r) { return qh + offset(r0 + r, a.q); });
-    gs.load(lds[2 * buf + 1], a.dout, a.group, a.d, word, gh + offset(r0, a.dout), [&](int r) { return gh + offset(r0 + r, a.dout); });
-    if (wave < 2)  // 64 words each
+    qs.load(lds[2 * buf], a.d, word, qh + t * q_step, [&](int r) { return qh + offset(r0 + r, a.q); });
+    gs.load(lds[2 * buf + 1], a.d, word, gh + t * g_step, [&](int r) { return gh + offset(r0 + r, a.dout); });
+    if (wave < kRows / 32)  // 64 words each
       load_to_lds4((const float*)(row_stat + r0) + wave * 64, lane * 4, lds_address((const float*)stat[buf] + wave * 64));
   };
+
+  const typename Ti::Lane at;
   int t = find((int)((int64_t)tiles * split / a.splits));
   if (t < t_end) load(t, 0);
   for (int buf = 0; t < t_end; buf ^= 1) {
@@ -141,57 +165,76 @@ __global__ __launch_bounds__(256, (kKvWaves<T, DP>)) void k_attn_bwd_kv(AttnArgs
     if (wk0 >= k1) continue;  // no key: such a wavefront only loads
     uint32_t sees = ~0u;  // of row `lane` of the tile: the wavefront's keys that it sees
     if (ragged) {
-      const int row = now * kBwdRows + lane;
+      const int row = now * kRows + lane;
       const int2 range = row < a.rows ? row_range(a, b, row / a.group) : make_int2(0, 0);
       sees = (uint32_t)range_word(range.x, range.y, wk0);
     }
-#pragma unroll (DP * sizeof(T) <= 128 ? 2 : 1)
-    for (int j = 0; j < kBwdRows / 32; ++j) {
+#pragma unroll 1
+    for (int j = 0; j < kRows / 32; ++j) {
       f32x16 s = (f32x16)0.0f, dp = (f32x16)0.0f;
+      Frag<T> pf, df, held;
+      // scores and dP of 32 rows (their operands in turn), then dV and dK
+      constexpr int kEach = Sh::kValuesInLds ? 3 : 2, kFirst = kEach * kS;
+      stream<T, kFirst + 4 * kD, GS_P>(
+          [&](auto index) {
+            constexpr int i = decltype(index)::value, m = i - kFirst, w = i % kEach;
+            if constexpr (i >= kFirst)
+              return Ti::frag_cols(m & 1 ? qt : gt, at, 32 * j + 16 * (m / (2 * kD)), 32 * ((m >> 1) % kD));
+            else if constexpr (w == 2)
+              return Ti::frag_rows(vt, at, wave * 32, i / kEach);
+            else
+              return Ti::frag_rows(w ? gt : qt, at, 32 * j, i / kEach);
+          },
+          [&](auto index, const Frag<T>& f) {
+            constexpr int i = decltype(index)::value, m = i - kFirst, w = i % kEach, dt = (m >> 1) % kD;
+            if constexpr (i < kFirst) {
+              if constexpr (w == 0) s = mma(f, kf[i / kEach], s);
+              if constexpr (w == 1 && kEach == 2) dp = mma(f, vf[i / kEach], dp);
+              if constexpr (w == 1 && kEach == 3) held = f;
+              if constexpr (w == 2) dp = mma(held, f, dp);
+              if constexpr (i == kFirst - 1) {
 #pragma unroll
-      for (int st = 0; st < DP / 16; ++st) {
-        s = mma(Ti::frag_rows(qt, 32 * j, st), kf[st], s);
-        dp = mma(Ti::frag_rows(gt, 32 * j, st), vf[st], dp);
-      }
+                for (int c = 0; c < 4; ++c) {
+                  const f32x8 x = *reinterpret_cast<const f32x8*>(&st2[32 * j + 8 * c + 4 * half]);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const f32x8 w = *reinterpret_cast<const f32x8*>(&st2[32 * j + 8 * c + 4 * half]);
+                  for (int e = 0; e < 4; ++e) {
+                    const float p = __builtin_amdgcn_exp2f(fmaf(s[4 * c + e], a.slope, -x[2 * e]));
+                    s[4 * c + e] = p;
+                    dp[4 * c + e] = p * (dp[4 * c + e] - x[2 * e + 1]);
+                  }
+                }
+                if (ragged) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(s[4 * c + e], a.slope, -w[2 * e]));
-          s[4 * c + e] = p;
-          dp[4 * c + e] = p * (dp[4 * c + e] - w[2 * e + 1]);
-        }
-      }
-      if (ragged) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const bool in = (__shfl((int)sees, 32 * j + crow(r, half), 64) >> (lane & 31)) & 1;
-          s[r] = in ? s[r] : 0.0f;
-          dp[r] = in ? dp[r] : 0.0f;
-        }
-      }
-#pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        const Frag<T> pf = frag_of<T>(s, st), df = frag_of<T>(dp, st);
-#pragma unroll
-        for (int dt = 0; dt < DP / 32; ++dt) {
-          dv[dt] = mma(Ti::frag_cols(gt, 32 * j + 16 * st, 32 * dt), pf, dv[dt]);
-          dk[dt] = mma(Ti::frag_cols(qt, 32 * j + 16 * st, 32 * dt), df, dk[dt]);
-        }
-      }
+                  for (int r = 0; r < 16; ++r) {
+                    const bool in = (__shfl((int)sees, 32 * j + crow(r, half), 64) >> (lane & 31)) & 1;
+                    s[r] = in ? s[r] : 0.0f;
+                    dp[r] = in ? dp[r] : 0.0f;
+                  }
+                }
+              }
+            } else {
+              if constexpr (m % (2 * kD) == 0) {
+                pf = frag_of<T>(s, m / (2 * kD));
+                df = frag_of<T>(dp, m / (2 * kD));
+              }
+              if constexpr (m & 1)
+                dk[dt] = mma(f, df, dk[dt]);
+              else
+                dv[dt] = mma(f, pf, dv[dt]);
+            }
+          });
     }
   }
 
   if (key >= a.k_len) return;
   const bool parts = a.splits > 1;
-  const int64_t n = (int64_t)nbh * a.k_len, at = (int64_t)bh * a.k_len + key;
+  const int64_t n = (int64_t)nbh * a.k_len, place = (int64_t)bh * a.k_len + key;
   T* kp = head_ptr<T>(a.dk, b, key, hk);
   T* vp = head_ptr<T>(a.dv, b, key, hk);
-  float* kw = a.part + (split * 2 * n + at) * DP;
+  float* kw = a.part + (split * 2 * n + place) * DP;
   float* vw = kw + n * DP;
 #pragma unroll
-  for (int dt = 0; dt < DP / 32; ++dt)
+  for (int dt = 0; dt < kD; ++dt)
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int d = 32 * dt + 8 * c + 4 * half;
@@ -214,7 +257,7 @@ __global__ __launch_bounds__(256, (kKvWaves<T, DP>)) void k_attn_bwd_kv(AttnArgs
 template <typename T, int DP>
 __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   using Ti = Tile<T, DP>;
-  using St = Stage<T, DP>;
+  using St = Stage<T, DP, kAttnKeys>;
   __shared__ __align__(16) char lds[4][St::kBytes];  // keys and values of two tiles
   __shared__ int scratch[4][4];
   __shared__ uint64_t words[4];
@@ -254,11 +297,12 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   vs.plan(a.v, 1, a.d);
   auto load = [&](int buf) {
     const T *k = kh + tile.k0 * a.k.token_stride, *v = vh + tile.k0 * a.v.token_stride;
-    ks.load(lds[2 * buf], a.k, 1, a.d, tile.word, k, [&](int r) { return k + r * a.k.token_stride; });
-    vs.load(lds[2 * buf + 1], a.v, 1, a.d, tile.word, v, [&](int r) { return v + r * a.v.token_stride; });
+    ks.load(lds[2 * buf], a.d, tile.word, k, [&](int r) { return k + r * a.k.token_stride; });
+    vs.load(lds[2 * buf + 1], a.d, tile.word, v, [&](int r) { return v + r * a.v.token_stride; });
   };
   tile.next(a, b, seen, range, words);
   if (tile.word) load(0);
+  const typename Ti::Lane at;
   const bool idle = row - (lane & 31) >= a.rows;  // no row: such a wavefront only loads
   for (int buf = 0; tile.word; buf ^= 1) {
     const uint64_t word = tile.word;
@@ -272,13 +316,13 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
     if (idle) continue;
     uint64_t mine = word;
     if (ragged) mine &= range_word(range[0].x, range[0].y, k0);
-#pragma unroll (DP * sizeof(T) <= 128 ? 2 : 1)
+#pragma unroll (DP * (int)sizeof(T) <= 128 ? 2 : 1)
     for (int j = 0; j < 2; ++j) {
       f32x16 s = (f32x16)0.0f, dp = (f32x16)0.0f;
 #pragma unroll
       for (int st = 0; st < DP / 16; ++st) {
-        s = mma(Ti::frag_rows(kt, 32 * j, st), qf[st], s);
-        dp = mma(Ti::frag_rows(vt, 32 * j, st), gf[st], dp);
+        s = mma(Ti::frag_rows(kt, at, 32 * j, st), qf[st], s);
+        dp = mma(Ti::frag_rows(vt, at, 32 * j, st), gf[st], dp);
       }
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
@@ -294,7 +338,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
       for (int st = 0; st < 2; ++st) {
         const Frag<T> df = frag_of<T>(dp, st);
 #pragma unroll
-        for (int dt = 0; dt < DP / 32; ++dt) dq[dt] = mma(Ti::frag_cols(kt, 32 * j + 16 * st, 32 * dt), df, dq[dt]);
+        for (int dt = 0; dt < DP / 32; ++dt) dq[dt] = mma(Ti::frag_cols(kt, at, 32 * j + 16 * st, 32 * dt), df, dq[dt]);
       }
     }
   }

@@ -15,6 +15,9 @@
 // sixteen rows at one chunk (frag_rows), and four rows at four chunks (frag_cols).
 #pragma once
 
+#include <type_traits>
+#include <utility>
+
 #include "gs_elem.h"
 
 namespace gs {
@@ -78,15 +81,28 @@ struct Tile {
   }
   static __device__ __forceinline__ int at(int r, int c) { return r * kRowBytes + ((c ^ mix(r)) << 4); }
 
-  // A operand, row m0 + l % 32, k = 16 s + 8 (l / 32) + 0..7: k runs along the tile's rows.
-  static __device__ __forceinline__ Frag<T> frag_rows(const char* tile, int m0, int s) {
-    const int l = __lane_id(), r = m0 + (l & 31), h = l >> 5;
+  // Where the lane reads, from the start of a tile; made once a kernel.
+  struct Lane {
+    int row, col;
+    __device__ __forceinline__ Lane() {
+      const int l = __lane_id(), h = l >> 5, i = l & 15;
+      row = at(l & 31, sizeof(T) == 2 ? h : 2 * h);
+      col = at(4 * h + (i >> 2), 2 * ((l >> 4) & 1) + ((i & 3) >> 1)) + 8 * (i & 1);
+    }
+  };
+
+  // A (or B) operand, row (or column) m0 + l % 32, k = 16 s + 8 (l / 32) + 0..7: k runs along the
+  // tile's rows.  m0 is a multiple of 32.  The steps differ in chunk bits above the lane's own, which
+  // are an exclusive-or away (or, past four chunks of a row of 192 bytes, a sum).
+  static __device__ __forceinline__ Frag<T> frag_rows(const char* tile, const Lane& lane, int m0, int s) {
     Frag<T> f;
     if constexpr (sizeof(T) == 2) {
-      f.v = *reinterpret_cast<const bf16x8*>(tile + at(r, 2 * s + h));
+      const int o = kChunks % 8 == 4 && kChunks > 4 ? (lane.row ^ ((s & 1) << 5)) + ((s >> 1) << 6) : lane.row ^ (s << 5);
+      f.v = *reinterpret_cast<const bf16x8*>(tile + m0 * kRowBytes + o);
     } else {
-      const f32x4 a = *reinterpret_cast<const f32x4*>(tile + at(r, 4 * s + 2 * h));
-      const f32x4 b = *reinterpret_cast<const f32x4*>(tile + at(r, 4 * s + 2 * h + 1));
+      const int o = kChunks == 24 ? (lane.row ^ ((s & 1) << 6)) + ((s >> 1) << 7) : lane.row ^ (s << 6);
+      const f32x4 a = *reinterpret_cast<const f32x4*>(tile + m0 * kRowBytes + o);
+      const f32x4 b = *reinterpret_cast<const f32x4*>(tile + m0 * kRowBytes + (o ^ 16));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         f.v[j] = a[j];
@@ -97,26 +113,25 @@ struct Tile {
   }
 
   // A operand of the transposed tile: row m = column c0 + l % 32 of the tile, k = the tile's rows
-  // r0 + {0..3, 8..11} + 4 (l / 32) (the order of a result's registers).
-  static __device__ __forceinline__ Frag<T> frag_cols(const char* tile, int r0, int c0) {
-    const int l = __lane_id(), h = l >> 5;
+  // r0 + {0..3, 8..11} + 4 (l / 32) (the order of a result's registers).  r0 is a multiple of 16, c0
+  // of 32.
+  static __device__ __forceinline__ Frag<T> frag_cols(const char* tile, const Lane& lane, int r0, int c0) {
     Frag<T> f;
     if constexpr (sizeof(T) == 2) {
       // Each group of 16 lanes names four rows of 16 columns, eight bytes a lane, and receives
-      // their transpose: lane i column i of the four rows.
+      // their transpose: lane i column i of the four rows.  Eight rows on the swizzle differs by 2.
       typedef short s16x4 __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-      const int i = l & 15, c = c0 + 16 * ((l >> 4) & 1) + 4 * (i & 3);
-      const int r = r0 + 4 * h + (i >> 2);
+      const int o = kChunks % 8 == 4 ? lane.col + 2 * c0 : lane.col ^ (2 * c0);
       union {
         s16x4 q[2];
         bf16x8 v;
       } u;
-      u.q[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(tile + at(r, c >> 3) + 2 * (c & 7)));
-      u.q[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(tile + at(r + 8, c >> 3) + 2 * (c & 7)));
+      u.q[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(tile + r0 * kRowBytes + o));
+      u.q[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(tile + (r0 + 8) * kRowBytes + (o ^ 32)));
       f.v = u.v;
     } else {
-      const int c = c0 + (l & 31);
+      const int l = __lane_id(), h = l >> 5, c = c0 + (l & 31);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         f.v[j] = *reinterpret_cast<const float*>(tile + at(r0 + 8 * (j >> 2) + 4 * h + (j & 3), c >> 2) + 4 * (c & 3));
@@ -147,6 +162,38 @@ __device__ __forceinline__ Frag<T> frag_mem(const T* p, int d, int s, bool count
     for (int j = 0; j < 8; ++j) f.v[j] = 0;
   }
   return f;
+}
+
+// N products in a row whose A operands come from LDS, P of them on the way at any time: load(i) reads
+// operand i, use(i, operand) multiplies (and does what comes between).  LDS reads and products keep
+// this order; vector arithmetic may move between them.  Left to itself the compiler reads an
+// operand just before its product and waits out the latency each time.
+// The indices are compile-time constants (every operand a register of its own).
+template <int I>
+using Index = std::integral_constant<int, I>;
+
+template <typename T, int N, int P, class Load, class Use, int... I>
+__device__ __forceinline__ void stream_all(Load&& load, Use&& use, std::integer_sequence<int, I...>) {
+  Frag<T> f[N];
+  auto ahead = [&](auto i) {
+    if constexpr (decltype(i)::value < N) f[decltype(i)::value] = load(i);
+  };
+  auto first = [&](auto i) {
+    if constexpr (decltype(i)::value < P) ahead(i);
+  };
+  auto step = [&](auto i) {
+    constexpr int k = decltype(i)::value;
+    __builtin_amdgcn_sched_barrier(0x6);  // only vector and scalar arithmetic cross
+    use(i, f[k]);
+    __builtin_amdgcn_sched_barrier(0x6);
+    ahead(Index<k + P>());
+  };
+  (first(Index<I>()), ...);
+  (step(Index<I>()), ...);
+}
+template <typename T, int N, int P, class Load, class Use>
+__device__ __forceinline__ void stream(Load&& load, Use&& use) {
+  stream_all<T, N, P>(load, use, std::make_integer_sequence<int, N>());
 }
 
 // The same with every sign bit flipped by `flip` (gs_attn.h).
