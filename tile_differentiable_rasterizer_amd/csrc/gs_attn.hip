@@ -18,8 +18,14 @@
 
 namespace gs {
 
-template <typename T, int DP, int NR>
-__global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
+// A tile's weights are taken relative to the maximum known before it, and the tile's sum tells
+// whether that was too low: only then (and on a row's first tile) the maximum is looked for, the
+// sums are scaled and the weights taken again.  Weights of up to this cost float32 and bfloat16
+// nothing (they are relative in both).
+constexpr float kMostWeight = 1024.0f;
+
+template <typename T, int DP>
+__global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
   using Ti = Tile<T, DP>;
   using St = Stage<T, DP, kAttnKeys>;
   __shared__ __align__(16) char lds[4][St::kBytes];  // keys and values of two tiles
@@ -30,33 +36,23 @@ __global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
   const int split = rest % a.splits, rt = rest / a.splits;
   const int b = bh / a.kv_heads, hk = bh - b * a.kv_heads;
   const int lane = __lane_id(), half = lane >> 5;
-  const int row0 = (rt * 4 + (threadIdx.x >> 6)) * 32 * NR + (lane & 31);
+  const int row = (rt * 4 + (threadIdx.x >> 6)) * 32 + (lane & 31);
+  const bool valid = row < a.rows;
+  const int i = valid ? row / a.group : 0, h = hk * a.group + (valid ? row - i * a.group : 0);
+  int2 range[1] = {row_range(a, b, i)};
+  const bool live = valid && range[0].x < range[0].y;
+  if (!live) range[0] = make_int2(0, 0);
+  const Seen seen = block_seen<1>(range, scratch);
 
-  int2 range[NR];
-  Frag<T> qf[NR][DP / 16];
+  Frag<T> qf[DP / 16];
 #pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    const int row = row0 + 32 * n;
-    const bool valid = row < a.rows;
-    const int i = valid ? row / a.group : 0, h = hk * a.group + (valid ? row - i * a.group : 0);
-    range[n] = row_range(a, b, i);
-    const bool live = valid && range[n].x < range[n].y;
-    if (!live) range[n] = make_int2(0, 0);
-    const T* qp = head_ptr<T>(a.q, b, i, h);
+  for (int s = 0; s < DP / 16; ++s) qf[s] = frag_flip(frag_mem<T>(head_ptr<T>(a.q, b, i, h), a.d, s, live), a.flip);
+  f32x16 o[DP / 32];
 #pragma unroll
-    for (int s = 0; s < DP / 16; ++s) qf[n][s] = frag_flip(frag_mem<T>(qp, a.d, s, live), a.flip);
-  }
-  const Seen seen = block_seen<NR>(range, scratch);
-
-  f32x16 o[NR][DP / 32];
-  float m[NR], base[NR], l[NR];  // m: maximum of the raw scores that the sums are relative to; base = m * slope
-#pragma unroll
-  for (int n = 0; n < NR; ++n) {
-#pragma unroll
-    for (int t = 0; t < DP / 32; ++t) o[n][t] = (f32x16)0.0f;
-    m[n] = -INFINITY;
-    base[n] = l[n] = 0.0f;
-  }
+  for (int t = 0; t < DP / 32; ++t) o[t] = (f32x16)0.0f;
+  // m: the score that the weights are relative to (not below the row's maximum by more than
+  // kMostWeight allows); base = m * slope; l: sum of the lane's weights
+  float m = live ? -INFINITY : 0.0f, base = 0.0f, l = 0.0f;
 
   const int t_lo = seen.first / kAttnKeys, t_n = seen.last > seen.first ? (seen.last + kAttnKeys - 1) / kAttnKeys - t_lo : 0;
   Tiles tile;
@@ -74,9 +70,8 @@ __global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
   };
   tile.next(a, b, seen, range, words);
   if (tile.word) load(0);
-  const bool idle = row0 - (lane & 31) >= a.rows;  // no row: such a wavefront only loads
+  const bool idle = row - (lane & 31) >= a.rows;  // no row: such a wavefront only loads
   const typename Ti::Lane at;
-  const float slack = 8.0f / a.slope;  // weights up to 2^8 before the sums are scaled again
   // one tile, in the buffers that the compiler knows (offsets then are immediates)
   auto one = [&](auto which) {
     constexpr int buf = decltype(which)::value;
@@ -90,69 +85,58 @@ __global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
     const char *kt = lds[2 * buf], *vt = lds[2 * buf + 1];
 
     if (idle) return;
-    f32x16 s[NR][2];
+    f32x16 s[2];
 #pragma unroll
-    for (int n = 0; n < NR; ++n) s[n][0] = s[n][1] = (f32x16)0.0f;
+    for (int j = 0; j < 2; ++j) {
+      s[j] = (f32x16)0.0f;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int st = 0; st < DP / 16; ++st) {
-        const Frag<T> kf = Ti::frag_rows(kt, at, 32 * j, st);
-#pragma unroll
-        for (int n = 0; n < NR; ++n) s[n][j] = mma(kf, qf[n][st], s[n][j]);
-      }
+      for (int st = 0; st < DP / 16; ++st) s[j] = mma(Ti::frag_rows(kt, at, 32 * j, st), qf[st], s[j]);
+    }
     if (ragged || word != ~0ull) {
+      // a row that sees nothing takes the tile's keys as they are; its result is not used
+      uint64_t mine = word;
+      if (ragged && live) mine &= range_word(range[0].x, range[0].y, k0);
+      const uint32_t lo = (uint32_t)mine >> (4 * half), hi = (uint32_t)(mine >> 32) >> (4 * half);
 #pragma unroll
-      for (int n = 0; n < NR; ++n) {
-        // a row that sees nothing takes the tile's keys as they are; its result is not used
-        uint64_t mine = word;
-        if (ragged && range[n].x < range[n].y) mine &= range_word(range[n].x, range[n].y, k0);
-        const uint32_t lo = (uint32_t)mine >> (4 * half), hi = (uint32_t)(mine >> 32) >> (4 * half);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          s[n][0][r] = (lo >> crow(r, 0)) & 1 ? s[n][0][r] : -INFINITY;
-          s[n][1][r] = (hi >> crow(r, 0)) & 1 ? s[n][1][r] : -INFINITY;
-        }
+      for (int r = 0; r < 16; ++r) {
+        s[0][r] = (lo >> crow(r, 0)) & 1 ? s[0][r] : -INFINITY;
+        s[1][r] = (hi >> crow(r, 0)) & 1 ? s[1][r] : -INFINITY;
       }
     }
+    Frag<T> p[4];
+    float sum;
+    auto weigh = [&] {
+      sum = 0.0f;
 #pragma unroll
-    for (int n = 0; n < NR; ++n) {
-      float top = fmaxf(s[n][0][0], s[n][1][0]);
+      for (int step = 0; step < 4; ++step) {
+        f32x8 w;
 #pragma unroll
-      for (int r = 1; r < 16; ++r) top = fmaxf(fmaxf(top, s[n][0][r]), s[n][1][r]);
-      top = pair_max(top);
-      if (__any(top > m[n] + slack)) {
-        const float to = fmaxf(m[n], top), before = base[n];
-        base[n] = to == -INFINITY ? 0.0f : to * a.slope;
-        const float keep = m[n] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(before - base[n]);
-        m[n] = to;
-        l[n] *= keep;
+        for (int e = 0; e < 8; ++e) w[e] = __builtin_amdgcn_exp2f(fmaf(s[step >> 1][8 * (step & 1) + e], a.slope, -base));
+        p[step] = frag_from<T>(w);
 #pragma unroll
-        for (int dt = 0; dt < DP / 32; ++dt) o[n][dt] *= keep;
+        for (int e = 0; e < 8; ++e) sum += w[e];  // before they are rounded: lse is float32
       }
-      float sum = 0.0f;
+    };
+    weigh();
+    if (__any(!(m > -INFINITY) || sum > kMostWeight)) {
+      float top = fmaxf(s[0][0], s[1][0]);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int r = 1; r < 16; ++r) top = fmaxf(fmaxf(top, s[0][r]), s[1][r]);
+      top = fmaxf(m, pair_max(top));
+      const float before = base;
+      base = top == -INFINITY ? 0.0f : top * a.slope;
+      const float keep = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(before - base);
+      m = top;
+      l *= keep;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(s[n][j][r], a.slope, -base[n]));
-          s[n][j][r] = p;
-          sum += p;
-        }
-      l[n] += sum;
+      for (int dt = 0; dt < DP / 32; ++dt) o[dt] *= keep;
+      weigh();
     }
+    l += sum;
 #pragma unroll
-    for (int step = 0; step < 4; ++step) {
-      Frag<T> p[NR];
+    for (int step = 0; step < 4; ++step)
 #pragma unroll
-      for (int n = 0; n < NR; ++n) p[n] = frag_of<T>(s[n][step >> 1], step & 1);
-#pragma unroll
-      for (int dt = 0; dt < DP / 32; ++dt) {
-        const Frag<T> vf = Ti::frag_cols(vt, at, 16 * step, 32 * dt);
-#pragma unroll
-        for (int n = 0; n < NR; ++n) o[n][dt] = mma(vf, p[n], o[n][dt]);
-      }
-    }
+      for (int dt = 0; dt < DP / 32; ++dt) o[dt] = mma(Ti::frag_cols(vt, at, 16 * step, 32 * dt), p[step], o[dt]);
   };
   while (tile.word) {
     one(std::integral_constant<int, 0>());
@@ -160,45 +144,39 @@ __global__ __launch_bounds__(256, NR == 1 ? 2 : 1) void k_attn_fwd(AttnArgs a) {
     one(std::integral_constant<int, 1>());
   }
 
+  const float sum = pair_sum(l);
+  if (!valid) return;
+  const bool none = !live || sum == 0.0f;  // (a row of NaN is not none)
+  if (a.splits == 1) {
+    const float inv = none ? 0.0f : 1.0f / sum;
+    T* op = head_ptr<T>(a.out, b, i, h);
 #pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    const int row = row0 + 32 * n;
-    const float sum = pair_sum(l[n]);
-    if (row >= a.rows) continue;
-    const bool live = range[n].x < range[n].y;
-    const int i = row / a.group, h = hk * a.group + row - i * a.group;
-    const bool none = !live || sum == 0.0f;  // (a row of NaN is not none)
-    if (a.splits == 1) {
-      const float inv = none ? 0.0f : 1.0f / sum;
-      T* op = head_ptr<T>(a.out, b, i, h);
+    for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int d = 32 * dt + 8 * c + 4 * half;
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = none ? 0.0f : o[dt][4 * c + e] * inv;
+        if (d < a.d) store_elems<4>(op + d, x);
+      }
+    if (a.lse && half == 0)
+      a.lse[((int64_t)b * a.kv_heads * a.group + h) * a.q_len + i] = none ? -INFINITY : (base + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+  } else {
+    const int64_t place = ((int64_t)split * nbh + bh) * a.rows + row;
+    float* op = a.part + place * DP;
+    if (!none) {
 #pragma unroll
       for (int dt = 0; dt < DP / 32; ++dt)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int d = 32 * dt + 8 * c + 4 * half;
           float x[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = none ? 0.0f : o[n][dt][4 * c + e] * inv;
-          if (d < a.d) store_elems<4>(op + d, x);
+          for (int e = 0; e < 4; ++e) x[e] = o[dt][4 * c + e];
+          store_elems<4>(op + 32 * dt + 8 * c + 4 * half, x);
         }
-      if (a.lse && half == 0)
-        a.lse[((int64_t)b * a.kv_heads * a.group + h) * a.q_len + i] = none ? -INFINITY : (base[n] + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
-    } else {
-      const int64_t at = ((int64_t)split * nbh + bh) * a.rows + row;
-      float* op = a.part + at * DP;
-      if (!none) {
-#pragma unroll
-        for (int dt = 0; dt < DP / 32; ++dt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = o[n][dt][4 * c + e];
-            store_elems<4>(op + 32 * dt + 8 * c + 4 * half, x);
-          }
-      }
-      if (half == 0) a.part_ml[at] = make_float2(none ? -INFINITY : base[n], none ? 0.0f : sum);
     }
+    if (half == 0) a.part_ml[place] = make_float2(none ? -INFINITY : base, none ? 0.0f : sum);
   }
 }
 
@@ -262,10 +240,9 @@ namespace {
 
 template <typename T, int DP>
 hipError_t fwd_launch(const AttnArgs& a, hipStream_t s) {
-  constexpr int NR = 1;
   const int64_t nbh = (int64_t)a.batch * a.kv_heads;
-  const int64_t blocks = nbh * ((a.rows + 128 * NR - 1) / (128 * NR)) * a.splits;
-  k_attn_fwd<T, DP, NR><<<(unsigned)blocks, 256, 0, s>>>(a);
+  const int64_t blocks = nbh * ((a.rows + 127) / 128) * a.splits;
+  k_attn_fwd<T, DP><<<(unsigned)blocks, 256, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   // rows a workgroup: all that its lanes hold where there are rows enough, else one (a token at a

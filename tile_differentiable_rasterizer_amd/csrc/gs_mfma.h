@@ -61,6 +61,19 @@ __device__ __forceinline__ Frag<__bf16> frag_of<__bf16>(const f32x16& c, int s) 
   return f;
 }
 
+// Eight float32 values as a fragment.
+template <typename T>
+__device__ __forceinline__ Frag<T> frag_from(const f32x8& x) {
+  Frag<T> f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (sizeof(T) == 2)
+      f.v[j] = (__bf16)x[j];
+    else
+      f.v[j] = x[j];
+  }
+  return f;
+}
 template <typename T, int DP>
 struct Tile {
   static constexpr int kPer = 16 / sizeof(T);        // elements of a chunk
