@@ -11,17 +11,11 @@
 // dP^T = V dO^T, then dQ^T[d][row] = K^T dS^T.
 // p and dS enter the products in the element type (bfloat16: rounded once, 2^-8 of each at most).
 #include "gs_attn.h"
-#ifndef GS_VL
-#define GS_VL 1
-#endif
-#ifndef GS_P
-#define GS_P 4
-#endif
-
 
 namespace gs {
 
-constexpr int kBwdRows = 64;  // rows of a tile of the kv kernel
+constexpr int kBwdRows = 64;  // rows that the statistics are kept for together
+constexpr int kAhead = 4;     // LDS operands on the way (2: 1% slower; 6: bfloat16 D 128 spills, 13% slower)
 
 // Statistics of every row, in the order of (sequence, key head, row): lse in base 2 and delta =
 // dout . out, and what each tile of 64 rows may see.  One workgroup a tile; a vector takes 16
@@ -77,7 +71,7 @@ template <typename T, int DP>
 struct KvShape {
   // bfloat16 D 128: the values' fragments stay in LDS, and tiles of 32 rows make room there, so that
   // two wavefronts share a SIMD
-  static constexpr bool kValuesInLds = GS_VL && sizeof(T) == 2 && DP == 128;
+  static constexpr bool kValuesInLds = sizeof(T) == 2 && DP == 128;
   static constexpr int kRows = kValuesInLds ? 32 : kBwdRows;  // of a tile
   static constexpr int kWaves = kValuesInLds || DP + DP * (int)sizeof(T) / 4 <= 150 ? 2 : 1;  // a SIMD
 };
@@ -175,7 +169,7 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::kWaves)) void k_attn_bwd_kv(A
       Frag<T> pf, df, held;
       // scores and dP of 32 rows (their operands in turn), then dV and dK
       constexpr int kEach = Sh::kValuesInLds ? 3 : 2, kFirst = kEach * kS;
-      stream<T, kFirst + 4 * kD, GS_P>(
+      stream<T, kFirst + 4 * kD, kAhead>(
           [&](auto index) {
             constexpr int i = decltype(index)::value, m = i - kFirst, w = i % kEach;
             if constexpr (i >= kFirst)
@@ -257,6 +251,7 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::kWaves)) void k_attn_bwd_kv(A
 template <typename T, int DP>
 __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   using Ti = Tile<T, DP>;
+  constexpr int kS = DP / 16, kD = DP / 32;
   using St = Stage<T, DP, kAttnKeys>;
   __shared__ __align__(16) char lds[4][St::kBytes];  // keys and values of two tiles
   __shared__ int scratch[4][4];
@@ -316,30 +311,43 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
     if (idle) continue;
     uint64_t mine = word;
     if (ragged) mine &= range_word(range[0].x, range[0].y, k0);
-#pragma unroll (DP * (int)sizeof(T) <= 128 ? 2 : 1)
+#pragma unroll (sizeof(T) == 2 ? 2 : 1)
     for (int j = 0; j < 2; ++j) {
       f32x16 s = (f32x16)0.0f, dp = (f32x16)0.0f;
+      Frag<T> df;
+      constexpr int kFirst = 2 * kS;
+      stream<T, kFirst + 2 * kD, kAhead>(
+          [&](auto index) {
+            constexpr int i = decltype(index)::value, m = i - kFirst;
+            if constexpr (i >= kFirst)
+              return Ti::frag_cols(kt, at, 32 * j + 16 * (m / kD), 32 * (m % kD));
+            else
+              return Ti::frag_rows(i & 1 ? vt : kt, at, 32 * j, i / 2);
+          },
+          [&](auto index, const Frag<T>& f) {
+            constexpr int i = decltype(index)::value, m = i - kFirst;
+            if constexpr (i < kFirst) {
+              if constexpr (i & 1)
+                dp = mma(f, gf[i / 2], dp);
+              else
+                s = mma(f, qf[i / 2], s);
+              if constexpr (i == kFirst - 1) {
 #pragma unroll
-      for (int st = 0; st < DP / 16; ++st) {
-        s = mma(Ti::frag_rows(kt, at, 32 * j, st), qf[st], s);
-        dp = mma(Ti::frag_rows(vt, at, 32 * j, st), gf[st], dp);
-      }
+                for (int r = 0; r < 16; ++r) {
+                  const float p = __builtin_amdgcn_exp2f(fmaf(s[r], a.slope, -stat.x));
+                  dp[r] = p * (dp[r] - stat.y);
+                }
+                if (ragged || word != ~0ull) {
+                  const uint32_t bits = (uint32_t)(mine >> (32 * j)) >> (4 * half);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const float p = __builtin_amdgcn_exp2f(fmaf(s[r], a.slope, -stat.x));
-        dp[r] = p * (dp[r] - stat.y);
-      }
-      if (ragged || word != ~0ull) {
-        const uint32_t bits = (uint32_t)(mine >> (32 * j)) >> (4 * half);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) dp[r] = (bits >> crow(r, 0)) & 1 ? dp[r] : 0.0f;
-      }
-#pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        const Frag<T> df = frag_of<T>(dp, st);
-#pragma unroll
-        for (int dt = 0; dt < DP / 32; ++dt) dq[dt] = mma(Ti::frag_cols(kt, at, 32 * j + 16 * st, 32 * dt), df, dq[dt]);
-      }
+                  for (int r = 0; r < 16; ++r) dp[r] = (bits >> crow(r, 0)) & 1 ? dp[r] : 0.0f;
+                }
+              }
+            } else {
+              if constexpr (m % kD == 0) df = frag_of<T>(dp, m / kD);
+              dq[m % kD] = mma(f, df, dq[m % kD]);
+            }
+          });
     }
   }
 
