@@ -452,6 +452,33 @@ def test_tokens_on_another_stream():
     assert torch.equal(ref[0], want[0]) and torch.equal(ref[1], want[1])
 
 
+def test_tokens_stream_argument():
+    """Work on a stream given by argument while the current one allocates and overwrites: what the calls allocate
+    belongs to their stream."""
+    side = torch.cuda.Stream()
+    q, k, v = qkv("bf16", 2, 40, 6000, 4, 2, 64)
+    w, cs = torch.ones(64, device="cuda"), torch.ones(6000, 32, device="cuda")
+    h = normal(gen(2), 500, 600, t=torch.bfloat16)
+
+    def step(stream):
+        a, b = tokens.norm_rotate_fwd(q, k, w, w, cs, cs, stream=stream)
+        out, lse = tokens.cross_attn_fwd(a, b, v, stream=stream)
+        grads = tokens.cross_attn_bwd(out, a, b, v, out, lse, stream=stream)
+        more = tokens.norm_rotate_bwd(grads[0], grads[1], q, k, w, w, cs, cs, stream=stream)
+        y, codes, bounds = tokens.gate8_fwd(h[:, :300], h[:, 300:], stream=stream)
+        return [out, lse, *grads, *more, y, *tokens.gate8_bwd(y, codes, bounds, stream=stream)]
+
+    want = step(None)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        side.wait_stream(torch.cuda.current_stream())
+        got = step(side)
+        junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (1 << 12, 1 << 16, 1 << 20, 1 << 22, 1 << 24)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        del junk
+
+
 def test_tokens_in_a_graph():
     """A captured layer step replays to the eager results, with other work between the replays."""
     q, k, v = qkv("bf16", 2, 3, 2000, 4, 2, 64)

@@ -8,7 +8,8 @@ Tensors are bfloat16 or float32 on the GPU, laid out as include/gs_tokens.h says
 their last axis, on 16-byte boundaries, any strides else (views of one projection's output are
 taken as they are).  Shapes and types are checked here (the C calls do not see them: ValueError),
 everything else by the C calls (raster.GsError).  Work goes to the current stream, or to
-``stream``; outputs and workspaces are torch tensors made on the calling stream unless given.
+``stream``; outputs and workspaces that are not given are torch tensors made on that same stream
+(a workspace is given back to torch when the call returns, in stream order).
 
 ``norm_rotate``, ``cross_attention`` and ``gated8`` are the same operators as differentiable
 torch functions.
@@ -83,8 +84,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream, t):
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+def _stream(t):
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _on(stream, call, *args):
+    """The call with `stream` as the current one, so that what it allocates belongs to the work."""
+    with torch.cuda.stream(stream):
+        return call(*args)
 
 
 def _refuse(what):
@@ -118,10 +125,6 @@ def _same(t, x, shape):
 def _floats(x, shape, t, what):
     if x.dtype != torch.float32 or x.shape != shape or not x.is_contiguous() or x.get_device() != t.get_device():
         _refuse(f"{what}: float32 {tuple(shape)}, contiguous, on the vectors' GPU")
-
-
-def _dense(shape, t):
-    return torch.empty(shape, dtype=t.dtype, device=t.device)
 
 
 def _workspace(given, need, t):
@@ -164,15 +167,17 @@ def norm_rotate_fwd(q, k, wq, wk, cos, sin, pos_q=None, pos_k=None, eps: float =
                     out: tuple | None = None, stream=None) -> tuple:
     """gs_norm_rotate_fwd: (q, k) normed by head, weighted and rotated.  q [B, Lq, Hq, D],
     k [B, Lk, Hk, D]; cos, sin [positions, pairs]; ``out``: the two outputs' tensors (may be q, k)."""
+    if stream is not None:
+        return _on(stream, norm_rotate_fwd, q, k, wq, wk, cos, sin, pos_q, pos_k, eps, pairs, out)
     p = _norm_shape(q, k, wq, wk, cos, sin, pos_q, pos_k, eps, pairs)
     if out is None:
-        oq, ok = _dense(q.shape, q), _dense(k.shape, k)
+        oq, ok = torch.empty_like(q), torch.empty_like(k)
     else:
         oq, ok = out
         _same(q, oq, q.shape)
         _same(q, ok, k.shape)
     _check(lib().gs_norm_rotate_fwd(p, _heads(q), _heads(k), wq.data_ptr(), wk.data_ptr(), cos.data_ptr(), sin.data_ptr(),
-                                    _ptr(pos_q), _ptr(pos_k), _heads(oq), _heads(ok), _stream(stream, q)),
+                                    _ptr(pos_q), _ptr(pos_k), _heads(oq), _heads(ok), _stream(q)),
            "gs_norm_rotate_fwd")
     return oq, ok
 
@@ -180,16 +185,18 @@ def norm_rotate_fwd(q, k, wq, wk, cos, sin, pos_q=None, pos_k=None, eps: float =
 def norm_rotate_bwd(dout_q, dout_k, q, k, wq, wk, cos, sin, pos_q=None, pos_k=None, eps: float = 1e-6,
                     pairs: str = "halves", workspace=None, stream=None) -> tuple:
     """gs_norm_rotate_bwd: (dq, dk, dwq, dwk) from the inputs of the forward call and its outputs' gradients."""
+    if stream is not None:
+        return _on(stream, norm_rotate_bwd, dout_q, dout_k, q, k, wq, wk, cos, sin, pos_q, pos_k, eps, pairs, workspace)
     p = _norm_shape(q, k, wq, wk, cos, sin, pos_q, pos_k, eps, pairs)
     _same(q, dout_q, q.shape)
     _same(q, dout_k, k.shape)
     L = lib()
-    dq, dk = _dense(q.shape, q), _dense(k.shape, k)
+    dq, dk = torch.empty_like(q), torch.empty_like(k)
     dwq, dwk = torch.empty_like(wq), torch.empty_like(wk)
     ws, n = _workspace(workspace, L.gs_norm_rotate_workspace_bytes(p), q)
     _check(L.gs_norm_rotate_bwd(p, _heads(dout_q), _heads(dout_k), _heads(q), _heads(k), wq.data_ptr(), wk.data_ptr(),
                                 cos.data_ptr(), sin.data_ptr(), _ptr(pos_q), _ptr(pos_k), _heads(dq), _heads(dk),
-                                dwq.data_ptr(), dwk.data_ptr(), _ptr(ws), n, _stream(stream, q)), "gs_norm_rotate_bwd")
+                                dwq.data_ptr(), dwk.data_ptr(), _ptr(ws), n, _stream(q)), "gs_norm_rotate_bwd")
     return dq, dk, dwq, dwk
 
 
@@ -228,10 +235,12 @@ def cross_attn_fwd(q, k, v, scale: float | None = None, ranges=None, key_mask=No
     """gs_cross_attn_fwd: (out, lse).  q [B, Lq, Hq, D], k and v [B, Lk, Hk, D]; ``ranges`` [B or 1, Lq or 1, 2]: the
     keys [first, last) of each row (one row: lengths of sequences); ``key_mask`` [B or 1, Lk]: 0 hides a key; ``scale``
     None: 1 / sqrt(D)."""
+    if stream is not None:
+        return _on(stream, cross_attn_fwd, q, k, v, scale, ranges, key_mask, out, lse, workspace)
     p = _attn_shape(q, k, v, scale, ranges, key_mask)
     shape = (p.batch, p.q_heads, p.q_len)
     if out is None:
-        out = _dense(q.shape, q)
+        out = torch.empty_like(q)
     else:
         _same(q, out, q.shape)
     if lse is None:
@@ -241,22 +250,24 @@ def cross_attn_fwd(q, k, v, scale: float | None = None, ranges=None, key_mask=No
     L = lib()
     ws, n = _workspace(workspace, L.gs_cross_attn_fwd_workspace_bytes(p), q)
     _check(L.gs_cross_attn_fwd(p, _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(), _ptr(ws), n,
-                               _stream(stream, q)), "gs_cross_attn_fwd")
+                               _stream(q)), "gs_cross_attn_fwd")
     return out, lse
 
 
 def cross_attn_bwd(dout, q, k, v, out, lse, scale: float | None = None, ranges=None, key_mask=None, workspace=None,
                    stream=None) -> tuple:
     """gs_cross_attn_bwd: (dq, dk, dv) from the forward call's inputs and outputs and the gradient of out."""
+    if stream is not None:
+        return _on(stream, cross_attn_bwd, dout, q, k, v, out, lse, scale, ranges, key_mask, workspace)
     p = _attn_shape(q, k, v, scale, ranges, key_mask)
     _same(q, dout, q.shape)
     _same(q, out, q.shape)
     _floats(lse, (p.batch, p.q_heads, p.q_len), q, "lse")
-    dq, dk, dv = _dense(q.shape, q), _dense(k.shape, k), _dense(v.shape, v)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     L = lib()
     ws, n = _workspace(workspace, L.gs_cross_attn_bwd_workspace_bytes(p), q)
     _check(L.gs_cross_attn_bwd(p, _heads(dout), _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(), _heads(dq),
-                               _heads(dk), _heads(dv), _ptr(ws), n, _stream(stream, q)), "gs_cross_attn_bwd")
+                               _heads(dk), _heads(dv), _ptr(ws), n, _stream(q)), "gs_cross_attn_bwd")
     return dq, dk, dv
 
 
@@ -275,6 +286,8 @@ def gate8_fwd(gate, up, act: str = "silu", stream=None) -> tuple:
     """gs_gate8_fwd: (y, codes, bounds) of act(gate) * up; gate, up [rows, width] (views of one projection's output
     are taken as they are).  codes uint8 [2, rows, width] and bounds float32 [2, rows, blocks, 2] are what
     gate8_bwd needs."""
+    if stream is not None:
+        return _on(stream, gate8_fwd, gate, up, act)
     if act not in ACTS:
         _refuse(f"act: one of {tuple(ACTS)}")
     if gate.dim() != 2:
@@ -283,17 +296,19 @@ def gate8_fwd(gate, up, act: str = "silu", stream=None) -> tuple:
     rows, width = gate.shape
     gs, us = _stride(gate, gate, rows, width), _stride(up, gate, rows, width)
     dev = gate.device
-    y = torch.empty((rows, width), dtype=gate.dtype, device=dev)
+    y = torch.empty_like(gate)
     codes = torch.empty((2, rows, width), dtype=torch.uint8, device=dev)
     bounds = torch.empty((2, rows, (width + CODE_BLOCK - 1) // CODE_BLOCK, 2), dtype=torch.float32, device=dev)
-    _check(lib().gs_gate8_fwd(rows, width, ACTS[act], ty, gate.data_ptr(), gs, up.data_ptr(), us, y.data_ptr(), width,
-                              codes.data_ptr(), bounds.data_ptr(), _stream(stream, gate)), "gs_gate8_fwd")
+    _check(lib().gs_gate8_fwd(rows, width, ACTS[act], ty, gate.data_ptr(), gs, up.data_ptr(), us, y.data_ptr(), y.stride(0),
+                              codes.data_ptr(), bounds.data_ptr(), _stream(gate)), "gs_gate8_fwd")
     return y, codes, bounds
 
 
 def gate8_bwd(dy, codes, bounds, act: str = "silu", with_y: bool = True, dgate=None, dup=None, stream=None) -> tuple:
     """gs_gate8_bwd: (dgate, dup, y again or None) from the codes; ``dgate``, ``dup``: tensors to write to, such as the
     halves of one [rows, 2 * width] gradient."""
+    if stream is not None:
+        return _on(stream, gate8_bwd, dy, codes, bounds, act, with_y, dgate, dup)
     if act not in ACTS:
         _refuse(f"act: one of {tuple(ACTS)}")
     if dy.dim() != 2:
@@ -304,12 +319,12 @@ def gate8_bwd(dy, codes, bounds, act: str = "silu", with_y: bool = True, dgate=N
         _refuse("codes: gate8_fwd's")
     _floats(bounds, (2, rows, (width + CODE_BLOCK - 1) // CODE_BLOCK, 2), dy, "bounds")
     ds = _stride(dy, dy, rows, width)
-    dgate = _dense((rows, width), dy) if dgate is None else dgate
-    dup = _dense((rows, width), dy) if dup is None else dup
-    y = _dense((rows, width), dy) if with_y else None
+    dgate = torch.empty_like(dy) if dgate is None else dgate
+    dup = torch.empty_like(dy) if dup is None else dup
+    y = torch.empty_like(dy) if with_y else None
     _check(lib().gs_gate8_bwd(rows, width, ACTS[act], ty, dy.data_ptr(), ds, codes.data_ptr(), bounds.data_ptr(),
                               dgate.data_ptr(), _stride(dgate, dy, rows, width), dup.data_ptr(), _stride(dup, dy, rows, width),
-                              _ptr(y), width, _stream(stream, dy)), "gs_gate8_bwd")
+                              _ptr(y), y.stride(0) if with_y else 0, _stream(dy)), "gs_gate8_bwd")
     return dgate, dup, y
 
 
