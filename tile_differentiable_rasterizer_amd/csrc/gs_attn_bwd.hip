@@ -5,6 +5,7 @@
 // order is fixed: k_attn_bwd_kv owns 128 keys and walks the rows (of every query head that shares
 // them), k_attn_bwd_q owns 128 rows and walks the keys.  That computes the scores twice (7
 // products of a tile instead of 5).
+// The row kernel goes first: it finishes the rows' statistics where they see few keys.
 //
 // kv: S[row][key] = Q K^T and dP[row][key] = dO V^T leave a lane with one key and 16 rows, the B
 // operand of dV^T[d][key] = dO^T P and dK^T[d][key] = Q^T dS.  q: as the forward kernel, S^T and
@@ -15,6 +16,7 @@
 namespace gs {
 
 constexpr int kBwdRows = 64;  // rows that the statistics are kept for together
+constexpr int kShortTiles = 4;  // key tiles up to which a row's delta is taken from its weights
 constexpr int kAhead = 4;     // LDS operands on the way (2: 1% slower; 6: bfloat16 D 128 spills, 13% slower)
 
 // Statistics of every row, in the order of (sequence, key head, row): lse in base 2 and delta =
@@ -266,55 +268,93 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   const int i = valid ? row / a.group : 0, h = hk * a.group + (valid ? row - i * a.group : 0);
   int2 range[1] = {row_range(a, b, i)};
   const int tiles = (a.rows + kBwdRows - 1) / kBwdRows;
-  const float2 stat = valid ? a.stat[(int64_t)bh * tiles * kBwdRows + row] : make_float2(INFINITY, 0.0f);
+  float2* const place = a.stat + (int64_t)bh * tiles * kBwdRows + row;
+  float2 stat = valid ? *place : make_float2(INFINITY, 0.0f);
   const bool live = stat.x != INFINITY;
   if (!live) range[0] = make_int2(0, 0);
   const Seen seen = block_seen<1>(range, scratch);
 
-  Frag<T> qf[DP / 16], gf[DP / 16];
+  Frag<T> qf[kS], gf[kS];
 #pragma unroll
-  for (int s = 0; s < DP / 16; ++s) {
+  for (int s = 0; s < kS; ++s) {
     qf[s] = frag_flip(frag_mem<T>(head_ptr<T>(a.q, b, i, h), a.d, s, live), a.flip);
     gf[s] = frag_mem<T>(head_ptr<T>(a.dout, b, i, h), a.d, s, live);
   }
-  f32x16 dq[DP / 32];
-#pragma unroll
-  for (int t = 0; t < DP / 32; ++t) dq[t] = (f32x16)0.0f;
-
-  const int t_lo = seen.first / kAttnKeys, t_n = seen.last > seen.first ? (seen.last + kAttnKeys - 1) / kAttnKeys - t_lo : 0;
-  Tiles tile;
-  tile.t = t_lo + (int)((int64_t)t_n * split / a.splits);
-  tile.end = t_lo + (int)((int64_t)t_n * (split + 1) / a.splits);
   const T* kh = head_ptr<T>(a.k, b, 0, hk);
   const T* vh = head_ptr<T>(a.v, b, 0, hk);
   St ks, vs;
   ks.plan(a.k, 1, a.d);
   vs.plan(a.v, 1, a.d);
-  auto load = [&](int buf) {
-    const T *k = kh + tile.k0 * a.k.token_stride, *v = vh + tile.k0 * a.v.token_stride;
-    ks.load(lds[2 * buf], a.d, tile.word, k, [&](int r) { return k + r * a.k.token_stride; });
-    vs.load(lds[2 * buf + 1], a.d, tile.word, v, [&](int r) { return v + r * a.v.token_stride; });
-  };
-  tile.next(a, b, seen, range, words);
-  if (tile.word) load(0);
   const typename Ti::Lane at;
   const bool idle = row - (lane & 31) >= a.rows;  // no row: such a wavefront only loads
-  for (int buf = 0; tile.word; buf ^= 1) {
-    const uint64_t word = tile.word;
-    const int k0 = tile.k0;
-    const bool ragged = tile.ragged;
-    wait_loads();
-    __syncthreads();
+
+  // Calls body(keys' tile, values' tile, the row's keys of the tile, whether it sees less than all)
+  // for each tile from `begin` to `end` that some row sees something of.
+  auto walk = [&](int begin, int end, auto&& body) {
+    Tiles tile;
+    tile.t = begin;
+    tile.end = end;
+    auto load = [&](int buf) {
+      const T *k = kh + tile.k0 * a.k.token_stride, *v = vh + tile.k0 * a.v.token_stride;
+      ks.load(lds[2 * buf], a.d, tile.word, k, [&](int r) { return k + r * a.k.token_stride; });
+      vs.load(lds[2 * buf + 1], a.d, tile.word, v, [&](int r) { return v + r * a.v.token_stride; });
+    };
     tile.next(a, b, seen, range, words);
-    if (tile.word) load(buf ^ 1);
-    const char *kt = lds[2 * buf], *vt = lds[2 * buf + 1];
-    if (idle) continue;
-    uint64_t mine = word;
-    if (ragged) mine &= range_word(range[0].x, range[0].y, k0);
+    if (tile.word) load(0);
+    for (int buf = 0; tile.word; buf ^= 1) {
+      const uint64_t word = tile.word;
+      const int k0 = tile.k0;
+      const bool ragged = tile.ragged;
+      wait_loads();
+      __syncthreads();
+      tile.next(a, b, seen, range, words);
+      if (tile.word) load(buf ^ 1);
+      if (!idle)
+        body(lds[2 * buf], lds[2 * buf + 1], ragged ? word & range_word(range[0].x, range[0].y, k0) : word, ragged || word != ~0ull);
+    }
+  };
+  const int t_lo = seen.first / kAttnKeys, t_n = seen.last > seen.first ? (seen.last + kAttnKeys - 1) / kAttnKeys - t_lo : 0;
+
+  // Over few keys `out` is as large as the values, and its rounding shows in delta = dout . out, which
+  // enters every dS of the row: there delta is taken from the weights, sum_j p_j dout . v_j (a row of
+  // two keys: error of dq and dk 2.0 -> 1.4 times that of their own rounding).  From 256 keys on
+  // out is an average and its rounding does not show.
+  if (t_n <= kShortTiles) {
+    float delta = 0.0f;
+    walk(t_lo, t_lo + t_n, [&](const char* kt, const char* vt, uint64_t mine, bool part) {
+#pragma unroll 1
+      for (int j = 0; j < 2; ++j) {
+        f32x16 s = (f32x16)0.0f, dp = (f32x16)0.0f;
+#pragma unroll
+        for (int st = 0; st < kS; ++st) {
+          s = mma(Ti::frag_rows(kt, at, 32 * j, st), qf[st], s);
+          dp = mma(Ti::frag_rows(vt, at, 32 * j, st), gf[st], dp);
+        }
+        const uint32_t bits = (uint32_t)(mine >> (32 * j)) >> (4 * half);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const float w = __builtin_amdgcn_exp2f(fmaf(s[r], a.slope, -stat.x)) * dp[r];
+          delta += !part || ((bits >> crow(r, 0)) & 1) ? w : 0.0f;
+        }
+      }
+    });
+    if (live) {
+      stat.y = pair_sum(delta);
+      if (split == 0 && half == 0) place->y = stat.y;  // for the kv kernel
+    }
+    __syncthreads();  // the tiles are read again
+  }
+
+  f32x16 dq[kD];
+#pragma unroll
+  for (int t = 0; t < kD; ++t) dq[t] = (f32x16)0.0f;
+  const int t_begin = t_lo + (int)((int64_t)t_n * split / a.splits), t_end = t_lo + (int)((int64_t)t_n * (split + 1) / a.splits);
+  walk(t_begin, t_end, [&](const char* kt, const char* vt, uint64_t mine, bool part) {
 #pragma unroll (sizeof(T) == 2 ? 2 : 1)
     for (int j = 0; j < 2; ++j) {
       f32x16 s = (f32x16)0.0f, dp = (f32x16)0.0f;
       Frag<T> df;
+      constexpr bool kRest = sizeof(T) == 2 && DP == 32;
       constexpr int kFirst = 2 * kS;
       stream<T, kFirst + 2 * kD, kAhead>(
           [&](auto index) {
@@ -337,7 +377,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
                   const float p = __builtin_amdgcn_exp2f(fmaf(s[r], a.slope, -stat.x));
                   dp[r] = p * (dp[r] - stat.y);
                 }
-                if (ragged || word != ~0ull) {
+                if (part) {
                   const uint32_t bits = (uint32_t)(mine >> (32 * j)) >> (4 * half);
 #pragma unroll
                   for (int r = 0; r < 16; ++r) dp[r] = (bits >> crow(r, 0)) & 1 ? dp[r] : 0.0f;
@@ -346,10 +386,14 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
             } else {
               if constexpr (m % kD == 0) df = frag_of<T>(dp, m / kD);
               dq[m % kD] = mma(f, df, dq[m % kD]);
+              // Short vectors: delta's own error weighs more against dq (by 1 / sqrt(D)), so what dS lost
+              // to its rounding is added (bfloat16 D 32, 4000 keys: dq's error 1.52 -> 1.06 times that of
+              // rounding dq alone).
+              if constexpr (kRest) dq[m % kD] = mma(f, frag_rest(dp, m / kD, df), dq[m % kD]);
             }
           });
     }
-  }
+  });
 
   if (!valid) return;
   T* op = head_ptr<T>(a.dq, b, i, h);
@@ -412,16 +456,16 @@ hipError_t bwd_launch(AttnArgs a, int q_splits, int kv_splits, hipStream_t s) {
   const int64_t nbh = (int64_t)a.batch * a.kv_heads, vecs = nbh * a.rows, per = 256 / (DP / 4);
   if (nbh == 0 || (a.rows == 0 && a.k_len == 0)) return hipSuccess;
   if (vecs) k_attn_stat<T><<<(unsigned)(nbh * ((a.rows + kBwdRows - 1) / kBwdRows)), 256, 0, s>>>(a);
+  if (vecs) {
+    a.splits = q_splits;
+    k_attn_bwd_q<T, DP><<<(unsigned)(nbh * ((a.rows + 127) / 128) * q_splits), 256, 0, s>>>(a);
+    if (q_splits > 1) k_attn_bwd_join<T, DP, false><<<(unsigned)((vecs + per - 1) / per), 256, 0, s>>>(a);
+  }
   if (nbh && a.k_len) {
     a.splits = kv_splits;
     k_attn_bwd_kv<T, DP><<<(unsigned)(nbh * ((a.k_len + 127) / 128) * kv_splits), 256, 0, s>>>(a);
     if (kv_splits > 1)
       k_attn_bwd_join<T, DP, true><<<dim3((unsigned)((nbh * a.k_len + per - 1) / per), 2), 256, 0, s>>>(a);
-  }
-  if (vecs) {
-    a.splits = q_splits;
-    k_attn_bwd_q<T, DP><<<(unsigned)(nbh * ((a.rows + 127) / 128) * q_splits), 256, 0, s>>>(a);
-    if (q_splits > 1) k_attn_bwd_join<T, DP, false><<<(unsigned)((vecs + per - 1) / per), 256, 0, s>>>(a);
   }
   return hipGetLastError();
 }

@@ -61,6 +61,20 @@ __device__ __forceinline__ Frag<__bf16> frag_of<__bf16>(const f32x16& c, int s) 
   return f;
 }
 
+// What the rounding of frag_of(c, s) = f left out, as a fragment.
+template <typename T>
+__device__ __forceinline__ Frag<T> frag_rest(const f32x16& c, int s, const Frag<T>& f) {
+  Frag<T> g;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (sizeof(T) == 2)
+      g.v[j] = (__bf16)(c[8 * s + j] - (float)f.v[j]);
+    else
+      g.v[j] = 0;
+  }
+  return g;
+}
+
 // Eight float32 values as a fragment.
 template <typename T>
 __device__ __forceinline__ Frag<T> frag_from(const f32x8& x) {
