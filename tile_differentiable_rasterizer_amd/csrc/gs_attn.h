@@ -90,28 +90,23 @@ struct Seen {
   int first, last;      // some row sees something in here
   int all_from, all_to; // every row that sees anything sees all of this
 };
-// `mine`: the ranges of the lane's NR rows, empty for a row that does not exist.
-template <int NR>
-__device__ __forceinline__ Seen block_seen(const int2 (&mine)[NR], int (*scratch)[4]) {
+// `mine`: the range of the lane's row, empty for a row that does not exist.  Rows without ranges of
+// their own need no exchange.
+__device__ __forceinline__ Seen block_seen(const AttnArgs& a, int b, int2 mine, int (*scratch)[4]) {
+  if (!a.ranges || a.ranges_r == 0) {
+    const int2 r = row_range(a, b, 0);
+    if (r.x >= r.y) return {INT32_MAX, 0, 0, INT32_MAX};
+    return {r.x, r.y, r.x, r.y};
+  }
   const int w = threadIdx.x >> 6;
-  int a = INT32_MAX, b = 0, c = 0, d = INT32_MAX;
-#pragma unroll
-  for (int n = 0; n < NR; ++n)
-    if (mine[n].x < mine[n].y) {
-      a = min(a, mine[n].x);
-      b = max(b, mine[n].y);
-      c = max(c, mine[n].x);
-      d = min(d, mine[n].y);
-    }
-  a = wave_min_i(a);
-  b = wave_max_i(b);
-  c = wave_max_i(c);
-  d = wave_min_i(d);
+  const bool live = mine.x < mine.y;
+  const int first = wave_min_i(live ? mine.x : INT32_MAX), last = wave_max_i(live ? mine.y : 0);
+  const int from = wave_max_i(live ? mine.x : 0), to = wave_min_i(live ? mine.y : INT32_MAX);
   if (__lane_id() == 0) {
-    scratch[w][0] = a;
-    scratch[w][1] = b;
-    scratch[w][2] = c;
-    scratch[w][3] = d;
+    scratch[w][0] = first;
+    scratch[w][1] = last;
+    scratch[w][2] = from;
+    scratch[w][3] = to;
   }
   __syncthreads();
   Seen s = {INT32_MAX, 0, 0, INT32_MAX};
@@ -236,18 +231,17 @@ struct Tiles {
   uint64_t word;    // keys that some row sees (0: no tile left)
   bool ragged;      // some row sees only a part of them by its range
 
-  template <int NR>
-  __device__ __forceinline__ void next(const AttnArgs& a, int b, const Seen& seen, const int2 (&mine)[NR], uint64_t* scratch) {
+  __device__ __forceinline__ void next(const AttnArgs& a, int b, const Seen& seen, int2 mine, uint64_t* scratch) {
     word = 0;
     for (; t < end && word == 0; ++t) {
       k0 = t * kAttnKeys;
       word = a.mask || k0 + kAttnKeys > a.k_len ? key_word(a, b, k0) : ~0ull;
       ragged = k0 < seen.all_from || k0 + kAttnKeys > seen.all_to;
       if (ragged) {
-        uint64_t some = 0;
-#pragma unroll
-        for (int n = 0; n < NR; ++n) some |= range_word(mine[n].x, mine[n].y, k0);
-        word &= block_word(some, scratch);
+        if (a.ranges_r == 0)  // the same range for all rows
+          word &= range_word(seen.first, seen.last, k0);
+        else
+          word &= block_word(range_word(mine.x, mine.y, k0), scratch);
       }
     }
   }

@@ -39,10 +39,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
   const int row = (rt * 4 + (threadIdx.x >> 6)) * 32 + (lane & 31);
   const bool valid = row < a.rows;
   const int i = valid ? row / a.group : 0, h = hk * a.group + (valid ? row - i * a.group : 0);
-  int2 range[1] = {row_range(a, b, i)};
-  const bool live = valid && range[0].x < range[0].y;
-  if (!live) range[0] = make_int2(0, 0);
-  const Seen seen = block_seen<1>(range, scratch);
+  int2 range = row_range(a, b, i);
+  const bool live = valid && range.x < range.y;
+  if (!live) range = make_int2(0, 0);
+  const Seen seen = block_seen(a, b, range, scratch);
 
   Frag<T> qf[DP / 16];
 #pragma unroll
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
     if (ragged || word != ~0ull) {
       // a row that sees nothing takes the tile's keys as they are; its result is not used
       uint64_t mine = word;
-      if (ragged && live) mine &= range_word(range[0].x, range[0].y, k0);
+      if (ragged && live) mine &= range_word(range.x, range.y, k0);
       const uint32_t lo = (uint32_t)mine >> (4 * half), hi = (uint32_t)(mine >> 32) >> (4 * half);
 #pragma unroll
       for (int r = 0; r < 16; ++r) {

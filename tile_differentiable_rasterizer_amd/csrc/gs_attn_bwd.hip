@@ -266,13 +266,13 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   const int row = rt * 128 + (threadIdx.x >> 6) * 32 + (lane & 31);
   const bool valid = row < a.rows;
   const int i = valid ? row / a.group : 0, h = hk * a.group + (valid ? row - i * a.group : 0);
-  int2 range[1] = {row_range(a, b, i)};
+  int2 range = row_range(a, b, i);
   const int tiles = (a.rows + kBwdRows - 1) / kBwdRows;
   float2* const place = a.stat + (int64_t)bh * tiles * kBwdRows + row;
   float2 stat = valid ? *place : make_float2(INFINITY, 0.0f);
   const bool live = stat.x != INFINITY;
-  if (!live) range[0] = make_int2(0, 0);
-  const Seen seen = block_seen<1>(range, scratch);
+  if (!live) range = make_int2(0, 0);
+  const Seen seen = block_seen(a, b, range, scratch);
 
   Frag<T> qf[kS], gf[kS];
 #pragma unroll
@@ -310,7 +310,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
       tile.next(a, b, seen, range, words);
       if (tile.word) load(buf ^ 1);
       if (!idle)
-        body(lds[2 * buf], lds[2 * buf + 1], ragged ? word & range_word(range[0].x, range[0].y, k0) : word, ragged || word != ~0ull);
+        body(lds[2 * buf], lds[2 * buf + 1], ragged ? word & range_word(range.x, range.y, k0) : word, ragged || word != ~0ull);
     }
   };
   const int t_lo = seen.first / kAttnKeys, t_n = seen.last > seen.first ? (seen.last + kAttnKeys - 1) / kAttnKeys - t_lo : 0;
