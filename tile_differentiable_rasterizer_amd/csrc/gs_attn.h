@@ -83,7 +83,12 @@ __device__ __forceinline__ uint64_t wave_or(uint64_t x) {
   return x;
 }
 
-constexpr int kAttnKeys = 64;   // keys of a tile
+constexpr int kAttnKeys = 64;  // keys of a tile
+
+// Wavefronts a SIMD of the kernels that own rows: two hide each other's waits; float32 operands of more
+// than 64 elements (three registers for each of bfloat16's) leave room for one.
+template <typename T, int DP>
+constexpr int kWavesOf = sizeof(T) == 2 || DP <= 64 ? 2 : 1;
 
 // Ends of the keys that the workgroup's rows may see.
 struct Seen {
@@ -168,10 +173,15 @@ __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)"
 // lane's address is made for it, and lanes of vectors that do not count, or of chunks past D, read
 // zeros: nothing is read from there.
 template <typename T, int DP, int ROWS>
-struct Stage {
+struct Stage;
+
+template <int DP, int ROWS>
+struct Stage<__bf16, DP, ROWS> {
+  using T = __bf16;
   using Ti = Tile<T, DP>;
   static constexpr int kEach = ROWS * Ti::kChunks / 256;
   static constexpr int kBytes = ROWS * Ti::kRowBytes;
+  static constexpr int kBuffers = 2;  // tiles held: the next one's loads go to the other
   static_assert(kEach * 256 == ROWS * Ti::kChunks, "whole chunks a thread");
   // one offset serves all of a thread's chunks where they are whole rounds of the swizzle apart
   static constexpr bool kRegular = kEach == 1 || (256 % Ti::kChunks == 0 && 256 / Ti::kChunks % 16 == 0);
@@ -191,15 +201,15 @@ struct Stage {
   // Vectors of `group` heads a token; they are even where a round holds whole tokens.
   __device__ __forceinline__ void plan(const gs_heads& x, int group, int d) {
     even = d == DP && kRound % group == 0 && (ROWS / group) * x.token_stride + group * x.head_stride < (1 << 28);
-    round = even ? kRound / group * x.token_stride * (int64_t)sizeof(T) : 0;
+    round = even ? kRound / group * x.token_stride * 2 : 0;
 #pragma unroll
     for (int i = 0; i < (kRegular ? 1 : kEach); ++i) {
       const int r = row_of(i, threadIdx.x), t = r / group;
-      off[i] = even ? (uint32_t)(t * x.token_stride + (r - t * group) * x.head_stride + chunk_of(i, threadIdx.x) * Ti::kPer) * (uint32_t)sizeof(T) : 0;
+      off[i] = even ? (uint32_t)(t * x.token_stride + (r - t * group) * x.head_stride + chunk_of(i, threadIdx.x) * 8) * 2u : 0;
     }
   }
 
-  // first: the tile's vector 0; at(r): vector r; bit r of `word`: it counts.
+  // Starts the loads of a tile.  first: its vector 0; at(r): vector r; bit r of `word`: it counts.
   template <class At>
   __device__ __forceinline__ void load(char* tile, int d, uint64_t word, const T* first, At&& at) const {
     const uint32_t to = lds_address(tile + (threadIdx.x >> 6) * 1024);
@@ -216,10 +226,75 @@ struct Stage {
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
         const int r = row_of(i, tid), ch = chunk_of(i, tid);
-        const bool counts = ((word >> r) & 1) && ch * Ti::kPer < d;
-        load_to_lds16(counts ? static_cast<const void*>(at(r) + ch * Ti::kPer) : kZeros, to + i * 4096);
+        const bool counts = ((word >> r) & 1) && ch * 8 < d;
+        load_to_lds16(counts ? static_cast<const void*>(at(r) + ch * 8) : kZeros, to + i * 4096);
       }
     }
+  }
+  // What is left to do between the barriers when the loads are in: nothing.
+  __device__ __forceinline__ void store(char*) const {}
+};
+
+// float32 tiles are made of parts (gs_mfma.h), so the loads pass through registers: they are started
+// a tile ahead, split, and stored when the tile before is done with.  That splits an element once for
+// the workgroup instead of once for each of its wavefronts, and makes one tile in LDS enough.
+template <int DP, int ROWS>
+struct Stage<float, DP, ROWS> {
+  using T = float;
+  using Ti = Tile<float, DP>;
+  using Part = typename Ti::Part;
+  static constexpr int kEach = ROWS * Part::kChunks / 256;  // eights of elements a thread
+  static constexpr int kBytes = 3 * Ti::kPart;
+  static constexpr int kBuffers = 1;
+  static_assert(ROWS == 64 && kEach * 256 == ROWS * Part::kChunks, "tiles of 64 rows, whole eights a thread");
+
+  f32x8 x[kEach];
+
+  __device__ __forceinline__ void plan(const gs_heads&, int, int) {}
+
+  template <class At>
+  __device__ __forceinline__ void load(char*, int d, uint64_t word, const T*, At&& at) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int c = i * 256 + (int)threadIdx.x, r = c / Part::kChunks, e = (c - r * Part::kChunks) * 8;
+      float y[8] = {};
+      if (((word >> r) & 1) && e < d) load_elems<8>(at(r) + e, y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[i][j] = y[j];
+    }
+  }
+  __device__ __forceinline__ void store(char* tile) const {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int c = i * 256 + (int)threadIdx.x, r = c / Part::kChunks;
+      const Frag<float> f = frag_split(x[i]);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) *reinterpret_cast<bf16x8*>(tile + k * Ti::kPart + Part::at(r, c - r * Part::kChunks)) = f.p[k];
+    }
+  }
+};
+
+// Two tensors' tiles that are worked on together, in LDS that the kernel declares: tiles[kTiles][kBytes].
+template <typename T, int DP, int ROWS>
+struct Pair {
+  using St = Stage<T, DP, ROWS>;
+  static constexpr int kBytes = St::kBytes, kTiles = 2 * St::kBuffers;
+  St a, b;
+
+  // Before a tile is worked on: its loads are in (wait_loads: every load that the thread has started),
+  // and nobody works on the tile before any more.
+  __device__ __forceinline__ void ready(char (*tiles)[kBytes]) {
+    if constexpr (St::kBuffers == 1) {
+      __syncthreads();
+      a.store(tiles[0]);
+      b.store(tiles[1]);
+    }
+    wait_loads();
+    __syncthreads();
+  }
+  // Tile `which` (0: a's, 1: b's) of buffer `buf`.
+  static __device__ __forceinline__ char* at(char (*tiles)[kBytes], int buf, int which) {
+    return tiles[St::kBuffers == 2 ? 2 * buf + which : which];
   }
 };
 

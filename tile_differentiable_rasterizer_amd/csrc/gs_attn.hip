@@ -12,9 +12,6 @@
 
 #include "gs_attn.h"
 
-#ifndef GS_UNEVEN
-#define GS_UNEVEN 2048
-#endif
 
 namespace gs {
 
@@ -25,10 +22,10 @@ namespace gs {
 constexpr float kMostWeight = 1024.0f;
 
 template <typename T, int DP>
-__global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
+__global__ __launch_bounds__(256, (kWavesOf<T, DP>)) void k_attn_fwd(AttnArgs a) {
   using Ti = Tile<T, DP>;
-  using St = Stage<T, DP, kAttnKeys>;
-  __shared__ __align__(16) char lds[4][St::kBytes];  // keys and values of two tiles
+  using Both = Pair<T, DP, kAttnKeys>;
+  __shared__ __align__(16) char lds[Both::kTiles][Both::kBytes];  // keys and values
   __shared__ int scratch[4][4];
   __shared__ uint64_t words[4];
   const int nbh = a.batch * a.kv_heads;
@@ -60,13 +57,13 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
   tile.end = t_lo + (int)((int64_t)t_n * (split + 1) / a.splits);
   const T* kh = head_ptr<T>(a.k, b, 0, hk);
   const T* vh = head_ptr<T>(a.v, b, 0, hk);
-  St ks, vs;
-  ks.plan(a.k, 1, a.d);
-  vs.plan(a.v, 1, a.d);
+  Both kv;
+  kv.a.plan(a.k, 1, a.d);
+  kv.b.plan(a.v, 1, a.d);
   auto load = [&](int buf) {
     const T *k = kh + tile.k0 * a.k.token_stride, *v = vh + tile.k0 * a.v.token_stride;
-    ks.load(lds[2 * buf], a.d, tile.word, k, [&](int r) { return k + r * a.k.token_stride; });
-    vs.load(lds[2 * buf + 1], a.d, tile.word, v, [&](int r) { return v + r * a.v.token_stride; });
+    kv.a.load(kv.at(lds, buf, 0), a.d, tile.word, k, [&](int r) { return k + r * a.k.token_stride; });
+    kv.b.load(kv.at(lds, buf, 1), a.d, tile.word, v, [&](int r) { return v + r * a.v.token_stride; });
   };
   tile.next(a, b, seen, range, words);
   if (tile.word) load(0);
@@ -78,11 +75,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
     const uint64_t word = tile.word;
     const int k0 = tile.k0;
     const bool ragged = tile.ragged;
-    wait_loads();     // this tile's
-    __syncthreads();  // ... of every wavefront; and the tile before is done with
+    kv.ready(lds);
     tile.next(a, b, seen, range, words);
     if (tile.word) load(buf ^ 1);
-    const char *kt = lds[2 * buf], *vt = lds[2 * buf + 1];
+    const char *kt = kv.at(lds, buf, 0), *vt = kv.at(lds, buf, 1);
 
     if (idle) return;
     f32x16 s[2];
@@ -262,7 +258,7 @@ hipError_t fwd_launch(const AttnArgs& a, hipStream_t s) {
 // 256 CUs: enough for two workgroups a CU, at least two tiles a part.  Where rows see ranges of
 // their own, workgroups differ in length, and eight a CU let the short ones make room.
 int attn_splits(int64_t blocks, int64_t tiles, bool uneven) {
-  const int64_t aim = uneven ? GS_UNEVEN : 512;
+  const int64_t aim = uneven ? 2048 : 512;
   if (blocks <= 0 || blocks >= aim) return 1;
   const int64_t want = (aim + blocks - 1) / blocks, most = tiles / 2;
   return (int)(want < most ? want : most < 1 ? 1 : most);

@@ -17,7 +17,10 @@ namespace gs {
 
 constexpr int kBwdRows = 64;  // rows that the statistics are kept for together
 constexpr int kShortTiles = 4;  // key tiles up to which a row's delta is taken from its weights
-constexpr int kAhead = 4;     // LDS operands on the way (2: 1% slower; 6: bfloat16 D 128 spills, 13% slower)
+// LDS operands on the way.  bfloat16: 2 is 1% slower, 6 spills at D 128 (13%).  float32, whose operands
+// are three times as large and feed six products: 1 up to D 64 (2: 4-9% slower), above 2 (1: 7%).
+template <typename T, int DP>
+constexpr int kAhead = sizeof(T) == 2 ? 4 : DP <= 64 ? 1 : 2;
 
 // Statistics of every row, in the order of (sequence, key head, row): lse in base 2 and delta =
 // dout . out, and what each tile of 64 rows may see.  One workgroup a tile; a vector takes 16
@@ -67,27 +70,27 @@ __global__ __launch_bounds__(256) void k_attn_stat(AttnArgs a) {
   if (threadIdx.x == 0) a.row_tiles[blockIdx.x] = w;
 }
 
-// How the kv kernel fits its registers.  Its results take DP of them, and the fragments of its keys
-// and values DP / 4 a byte of the type.
+// How the kv kernel fits its registers: the results take DP of them, the fragments of its keys and
+// values DP / 2 (bfloat16) or 3 DP / 2.
 template <typename T, int DP>
 struct KvShape {
   // bfloat16 D 128: the values' fragments stay in LDS, and tiles of 32 rows make room there, so that
   // two wavefronts share a SIMD
   static constexpr bool kValuesInLds = sizeof(T) == 2 && DP == 128;
   static constexpr int kRows = kValuesInLds ? 32 : kBwdRows;  // of a tile
-  static constexpr int kWaves = kValuesInLds || DP + DP * (int)sizeof(T) / 4 <= 150 ? 2 : 1;  // a SIMD
+  static constexpr int kWaves = kValuesInLds || DP <= (sizeof(T) == 2 ? 96 : 64) ? 2 : 1;  // a SIMD
 };
 
 template <typename T, int DP>
 __global__ __launch_bounds__(256, (KvShape<T, DP>::kWaves)) void k_attn_bwd_kv(AttnArgs a) {
   using Ti = Tile<T, DP>;
   using Sh = KvShape<T, DP>;
-  using St = Stage<T, DP, Sh::kRows>;
+  using Both = Pair<T, DP, Sh::kRows>;
   constexpr int kRows = Sh::kRows, kPerInfo = kBwdRows / kRows;
   constexpr int kS = DP / 16, kD = DP / 32;  // k steps of the scores; blocks of the results' elements
-  __shared__ __align__(32) char lds[4][St::kBytes];  // queries and output gradients of two tiles
+  __shared__ __align__(32) char lds[Both::kTiles][Both::kBytes];  // queries and output gradients
   __shared__ __align__(32) float2 stat[2][kRows];
-  __shared__ __align__(16) char vt[Sh::kValuesInLds ? 128 * Ti::kRowBytes : 16];
+  __shared__ __align__(16) char vt[Sh::kValuesInLds ? 128 * DP * 2 : 16];
   const int nbh = a.batch * a.kv_heads;
   const int bh = blockIdx.x % nbh, rest = blockIdx.x / nbh;
   const int split = rest % a.splits, kb = rest / a.splits;
@@ -119,9 +122,9 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::kWaves)) void k_attn_bwd_kv(A
   const float2* row_stat = a.stat + (int64_t)bh * infos * kBwdRows;
   const T* qh = head_ptr<T>(a.q, b, 0, hk * a.group);
   const T* gh = head_ptr<T>(a.dout, b, 0, hk * a.group);
-  St qs, gs;
-  qs.plan(a.q, a.group, a.d);
-  gs.plan(a.dout, a.group, a.d);
+  Both qg;
+  qg.a.plan(a.q, a.group, a.d);
+  qg.b.plan(a.dout, a.group, a.d);
   // the next tile from t on whose rows see some of the keys (the same for every thread)
   RowTile next;
   auto find = [&](int t) {
@@ -140,8 +143,8 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::kWaves)) void k_attn_bwd_kv(A
       const int i = r / a.group;
       return i * x.token_stride + (r - i * a.group) * x.head_stride;
     };
-    qs.load(lds[2 * buf], a.d, word, qh + t * q_step, [&](int r) { return qh + offset(r0 + r, a.q); });
-    gs.load(lds[2 * buf + 1], a.d, word, gh + t * g_step, [&](int r) { return gh + offset(r0 + r, a.dout); });
+    qg.a.load(qg.at(lds, buf, 0), a.d, word, qh + t * q_step, [&](int r) { return qh + offset(r0 + r, a.q); });
+    qg.b.load(qg.at(lds, buf, 1), a.d, word, gh + t * g_step, [&](int r) { return gh + offset(r0 + r, a.dout); });
     if (wave < kRows / 32)  // 64 words each
       load_to_lds4((const float*)(row_stat + r0) + wave * 64, lane * 4, lds_address((const float*)stat[buf] + wave * 64));
   };
@@ -150,13 +153,12 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::kWaves)) void k_attn_bwd_kv(A
   int t = find((int)((int64_t)tiles * split / a.splits));
   if (t < t_end) load(t, 0);
   for (int buf = 0; t < t_end; buf ^= 1) {
-    wait_loads();
-    __syncthreads();
+    qg.ready(lds);
     const int now = t;
     const bool ragged = next.all_from > k0 || next.all_to < k1;
     t = find(t + 1);
     if (t < t_end) load(t, buf ^ 1);
-    const char *qt = lds[2 * buf], *gt = lds[2 * buf + 1];
+    const char *qt = qg.at(lds, buf, 0), *gt = qg.at(lds, buf, 1);
     const float2* st2 = stat[buf];
     if (wk0 >= k1) continue;  // no key: such a wavefront only loads
     uint32_t sees = ~0u;  // of row `lane` of the tile: the wavefront's keys that it sees
@@ -171,7 +173,7 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::kWaves)) void k_attn_bwd_kv(A
       Frag<T> pf, df, held;
       // scores and dP of 32 rows (their operands in turn), then dV and dK
       constexpr int kEach = Sh::kValuesInLds ? 3 : 2, kFirst = kEach * kS;
-      stream<T, kFirst + 4 * kD, kAhead>(
+      stream<T, kFirst + 4 * kD, kAhead<T, DP>>(
           [&](auto index) {
             constexpr int i = decltype(index)::value, m = i - kFirst, w = i % kEach;
             if constexpr (i >= kFirst)
@@ -251,11 +253,11 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::kWaves)) void k_attn_bwd_kv(A
 }
 
 template <typename T, int DP>
-__global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
+__global__ __launch_bounds__(256, (kWavesOf<T, DP>)) void k_attn_bwd_q(AttnArgs a) {
   using Ti = Tile<T, DP>;
   constexpr int kS = DP / 16, kD = DP / 32;
-  using St = Stage<T, DP, kAttnKeys>;
-  __shared__ __align__(16) char lds[4][St::kBytes];  // keys and values of two tiles
+  using Both = Pair<T, DP, kAttnKeys>;
+  __shared__ __align__(16) char lds[Both::kTiles][Both::kBytes];  // keys and values
   __shared__ int scratch[4][4];
   __shared__ uint64_t words[4];
   const int nbh = a.batch * a.kv_heads;
@@ -282,9 +284,9 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   }
   const T* kh = head_ptr<T>(a.k, b, 0, hk);
   const T* vh = head_ptr<T>(a.v, b, 0, hk);
-  St ks, vs;
-  ks.plan(a.k, 1, a.d);
-  vs.plan(a.v, 1, a.d);
+  Both kv;
+  kv.a.plan(a.k, 1, a.d);
+  kv.b.plan(a.v, 1, a.d);
   const typename Ti::Lane at;
   const bool idle = row - (lane & 31) >= a.rows;  // no row: such a wavefront only loads
 
@@ -296,8 +298,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
     tile.end = end;
     auto load = [&](int buf) {
       const T *k = kh + tile.k0 * a.k.token_stride, *v = vh + tile.k0 * a.v.token_stride;
-      ks.load(lds[2 * buf], a.d, tile.word, k, [&](int r) { return k + r * a.k.token_stride; });
-      vs.load(lds[2 * buf + 1], a.d, tile.word, v, [&](int r) { return v + r * a.v.token_stride; });
+      kv.a.load(kv.at(lds, buf, 0), a.d, tile.word, k, [&](int r) { return k + r * a.k.token_stride; });
+      kv.b.load(kv.at(lds, buf, 1), a.d, tile.word, v, [&](int r) { return v + r * a.v.token_stride; });
     };
     tile.next(a, b, seen, range, words);
     if (tile.word) load(0);
@@ -305,12 +307,11 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
       const uint64_t word = tile.word;
       const int k0 = tile.k0;
       const bool ragged = tile.ragged;
-      wait_loads();
-      __syncthreads();
+      kv.ready(lds);
       tile.next(a, b, seen, range, words);
       if (tile.word) load(buf ^ 1);
       if (!idle)
-        body(lds[2 * buf], lds[2 * buf + 1], ragged ? word & range_word(range.x, range.y, k0) : word, ragged || word != ~0ull);
+        body(kv.at(lds, buf, 0), kv.at(lds, buf, 1), ragged ? word & range_word(range.x, range.y, k0) : word, ragged || word != ~0ull);
     }
   };
   const int t_lo = seen.first / kAttnKeys, t_n = seen.last > seen.first ? (seen.last + kAttnKeys - 1) / kAttnKeys - t_lo : 0;
@@ -356,7 +357,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
       Frag<T> df;
       constexpr bool kRest = sizeof(T) == 2 && DP == 32;
       constexpr int kFirst = 2 * kS;
-      stream<T, kFirst + 2 * kD, kAhead>(
+      stream<T, kFirst + 2 * kD, kAhead<T, DP>>(
           [&](auto index) {
             constexpr int i = decltype(index)::value, m = i - kFirst;
             if constexpr (i >= kFirst)

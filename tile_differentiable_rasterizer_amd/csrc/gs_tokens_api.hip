@@ -124,7 +124,7 @@ AttnArgs attn_args(const gs_cross_attn& p) {
   // the kernels take the maximum before they scale, so the slope is positive; a scale of 0 becomes
   // one that no float32 score can tell from it, and keeps -inf where a key is not seen
   a.slope = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);
-  a.flip = p.scale < 0.0f ? (p.type == GS_BF16 ? 0x80008000u : 0x80000000u) : 0u;
+  a.flip = p.scale < 0.0f ? 0x80008000u : 0u;
   a.ranges = p.ranges;
   a.ranges_b = p.ranges_batch_stride;
   a.ranges_r = p.ranges_row_stride;
