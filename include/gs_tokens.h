@@ -12,7 +12,7 @@
  * The conventions are gs_raster.h's: device pointers owned by the caller unless marked [host],
  * no allocation, scratch from a caller workspace, arguments checked before any HIP call, work
  * enqueued on `stream`, no state between calls, no host wait.  Results do not depend on the
- * order in which workgroups run: the calls use no atomics, and a call repeated on the same
+ * order in which workgroups run: no sum goes through atomics, and a call repeated on the same
  * inputs gives the same bits.
  *
  * Element types: GS_BF16 or GS_F32, one for all gs_heads / matrix arguments of a call; norm

@@ -25,6 +25,7 @@ struct AttnArgs {
   float* lse;
   float2* stat;    // [batch * kv_heads][tiles * 64]: (lse in base 2, delta) of each row, (inf, 0) where it sees nothing
   struct RowTile* row_tiles;  // [batch * kv_heads][tiles of 64 rows]
+  const int32_t* order;  // blocks of 128 rows (sequence, block), longest first; NULL: by number
   float* part;     // [splits][batch * kv_heads][rows][DP] sums, where splits > 1
   float2* part_ml; // [splits][batch * kv_heads][rows]: running maximum (base 2), sum
 };
@@ -84,6 +85,32 @@ __device__ __forceinline__ uint64_t wave_or(uint64_t x) {
 }
 
 constexpr int kAttnKeys = 64;  // keys of a tile
+
+// What a workgroup of the kernels that own rows works on.  Consecutive workgroups, which go to the
+// XCDs in turn, take the (sequence, key head)s in turn, so that the workgroups that read the same keys
+// share an XCD's L2 where there are eight of them; with an order the key heads in turn.
+struct RowBlock {
+  int b, hk, split, rt;
+  __device__ __forceinline__ explicit RowBlock(const AttnArgs& a) {
+    int rest;
+    if (a.order) {
+      const int each = a.kv_heads * a.splits, rank = blockIdx.x / each, blocks = (a.rows + 127) / 128;
+      rest = blockIdx.x - rank * each;
+      const int item = a.order[rank];
+      b = item / blocks;
+      rt = item - b * blocks;
+      split = rest / a.kv_heads;
+      hk = rest - split * a.kv_heads;
+    } else {
+      const int nbh = a.batch * a.kv_heads, bh = blockIdx.x % nbh;
+      rest = blockIdx.x / nbh;
+      rt = rest / a.splits;
+      split = rest - rt * a.splits;
+      b = bh / a.kv_heads;
+      hk = bh - b * a.kv_heads;
+    }
+  }
+};
 
 // Wavefronts a SIMD of the kernels that own rows: two hide each other's waits; float32 operands of more
 // than 64 elements (three registers for each of bfloat16's) leave room for one.

@@ -28,12 +28,10 @@ __global__ __launch_bounds__(256, (kWavesOf<T, DP>)) void k_attn_fwd(AttnArgs a)
   __shared__ __align__(16) char lds[Both::kTiles][Both::kBytes];  // keys and values
   __shared__ int scratch[4][4];
   __shared__ uint64_t words[4];
-  const int nbh = a.batch * a.kv_heads;
-  const int bh = blockIdx.x % nbh, rest = blockIdx.x / nbh;
-  const int split = rest % a.splits, rt = rest / a.splits;
-  const int b = bh / a.kv_heads, hk = bh - b * a.kv_heads;
+  const RowBlock block(a);
+  const int b = block.b, hk = block.hk, split = block.split;
   const int lane = __lane_id(), half = lane >> 5;
-  const int row = (rt * 4 + (threadIdx.x >> 6)) * 32 + (lane & 31);
+  const int row = (block.rt * 4 + (threadIdx.x >> 6)) * 32 + (lane & 31);
   const bool valid = row < a.rows;
   const int i = valid ? row / a.group : 0, h = hk * a.group + (valid ? row - i * a.group : 0);
   int2 range = row_range(a, b, i);
@@ -159,7 +157,7 @@ __global__ __launch_bounds__(256, (kWavesOf<T, DP>)) void k_attn_fwd(AttnArgs a)
     if (a.lse && half == 0)
       a.lse[((int64_t)b * a.kv_heads * a.group + h) * a.q_len + i] = none ? -INFINITY : (base + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
   } else {
-    const int64_t place = ((int64_t)split * nbh + bh) * a.rows + row;
+    const int64_t place = ((int64_t)(split * a.batch + b) * a.kv_heads + hk) * a.rows + row;
     float* op = a.part + place * DP;
     if (!none) {
 #pragma unroll
@@ -174,6 +172,46 @@ __global__ __launch_bounds__(256, (kWavesOf<T, DP>)) void k_attn_fwd(AttnArgs a)
     }
     if (half == 0) a.part_ml[place] = make_float2(none ? -INFINITY : base, none ? 0.0f : sum);
   }
+}
+
+// Key tiles that each block of 128 rows (sequence, block) may see: one wavefront each.
+__global__ __launch_bounds__(256) void k_attn_lengths(AttnArgs a, int items, int32_t* __restrict__ lengths) {
+  const int item = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (item >= items) return;
+  const int blocks = (a.rows + 127) / 128, b = item / blocks, rt = item - b * blocks;
+  int first = INT32_MAX, last = 0;
+  for (int i = rt * 128 / a.group + (int)__lane_id(); i <= min(rt * 128 + 127, a.rows - 1) / a.group; i += 64) {
+    const int2 r = row_range(a, b, i);
+    if (r.x < r.y) {
+      first = min(first, r.x);
+      last = max(last, r.y);
+    }
+  }
+  first = wave_min_i(first);
+  last = wave_max_i(last);
+  if (__lane_id() == 0) lengths[item] = last > first ? (last - 1) / kAttnKeys - first / kAttnKeys + 1 : 0;
+}
+
+// order[] = the blocks, longest first (by 1024 classes of length; within a class in no certain order,
+// which no result depends on).  One workgroup.
+__global__ __launch_bounds__(1024) void k_attn_order(int items, int tiles, const int32_t* __restrict__ lengths,
+                                                     int32_t* __restrict__ order) {
+  __shared__ int count[1024];
+  __shared__ int waves[16];
+  const int t = threadIdx.x;
+  count[t] = 0;
+  __syncthreads();
+  auto place = [&](int i) { return 1023 - (int)((int64_t)lengths[i] * 1023 / tiles); };
+  for (int i = t; i < items; i += 1024) atomicAdd(&count[place(i)], 1);
+  __syncthreads();
+  const int mine = count[t], upto = wave_inclusive_scan(mine);
+  if (__lane_id() == 63) waves[t >> 6] = upto;
+  __syncthreads();
+  int before = upto - mine;
+  for (int w = 0; w < (t >> 6); ++w) before += waves[w];
+  count[t] = before;
+  __syncthreads();
+  for (int i = t; i < items; i += 1024) order[atomicAdd(&count[place(i)], 1)] = i;
 }
 
 // Joins the splits of a row: weights 2^(m_s - max m).  One workgroup for kRows rows; a row's splits
@@ -265,6 +303,23 @@ int attn_splits(int64_t blocks, int64_t tiles, bool uneven) {
 }
 
 int attn_padded(int d) { return (d + 31) / 32 * 32; }
+
+// Blocks of 128 rows to be put in order of length, or 0.  Rows with ranges of their own, or sequences
+// of several lengths, make workgroups of different lengths; longest first, the short ones fill the
+// end.  Worth its two launches (8 us) where the kernel takes ten times that: from 2^28 (row, key) pairs.
+int attn_order_items(const gs_cross_attn& p) {
+  const int64_t rows = p.q_len * (p.q_heads / p.kv_heads), items = p.batch * ((rows + 127) / 128);
+  if (!p.ranges || items < 64 || items > 65536) return 0;
+  return p.batch * p.kv_heads * rows >= ((int64_t)1 << 28) / (p.k_len > 0 ? p.k_len : 1) ? (int)items : 0;
+}
+
+// space: two int32 for each of attn_order_items().
+hipError_t launch_attn_order(AttnArgs& a, int items, int32_t* space, hipStream_t s) {
+  k_attn_lengths<<<(unsigned)((items + 3) / 4), 256, 0, s>>>(a, items, space);
+  k_attn_order<<<1, 1024, 0, s>>>(items, (a.k_len + kAttnKeys - 1) / kAttnKeys, space, space + items);
+  a.order = space + items;
+  return hipGetLastError();
+}
 
 int attn_fwd_splits(const gs_cross_attn& p) {
   const int64_t rows = p.q_len * (p.q_heads / p.kv_heads);

@@ -260,12 +260,10 @@ __global__ __launch_bounds__(256, (kWavesOf<T, DP>)) void k_attn_bwd_q(AttnArgs 
   __shared__ __align__(16) char lds[Both::kTiles][Both::kBytes];  // keys and values
   __shared__ int scratch[4][4];
   __shared__ uint64_t words[4];
-  const int nbh = a.batch * a.kv_heads;
-  const int bh = blockIdx.x % nbh, rest = blockIdx.x / nbh;
-  const int split = rest % a.splits, rt = rest / a.splits;
-  const int b = bh / a.kv_heads, hk = bh - b * a.kv_heads;
+  const RowBlock block(a);
+  const int b = block.b, hk = block.hk, split = block.split, bh = b * a.kv_heads + hk;
   const int lane = __lane_id(), half = lane >> 5;
-  const int row = rt * 128 + (threadIdx.x >> 6) * 32 + (lane & 31);
+  const int row = block.rt * 128 + (threadIdx.x >> 6) * 32 + (lane & 31);
   const bool valid = row < a.rows;
   const int i = valid ? row / a.group : 0, h = hk * a.group + (valid ? row - i * a.group : 0);
   int2 range = row_range(a, b, i);
@@ -398,7 +396,7 @@ __global__ __launch_bounds__(256, (kWavesOf<T, DP>)) void k_attn_bwd_q(AttnArgs 
 
   if (!valid) return;
   T* op = head_ptr<T>(a.dq, b, i, h);
-  float* pp = a.part + (((int64_t)split * nbh + bh) * a.rows + row) * DP;
+  float* pp = a.part + (((int64_t)split * a.batch * a.kv_heads + bh) * a.rows + row) * DP;
 #pragma unroll
   for (int dt = 0; dt < DP / 32; ++dt)
 #pragma unroll

@@ -13,6 +13,8 @@ hipError_t launch_norm_rotate(const gs_norm_rotate& p, const gs_heads& q, const 
 int attn_padded(int d);
 int attn_fwd_splits(const gs_cross_attn& p);
 int attn_bwd_kv_splits(const gs_cross_attn& p);
+int attn_order_items(const gs_cross_attn& p);
+hipError_t launch_attn_order(AttnArgs& a, int items, int32_t* space, hipStream_t s);
 hipError_t launch_attn_fwd(AttnArgs a, int type, hipStream_t s);
 hipError_t launch_attn_bwd(AttnArgs a, int type, int q_splits, int kv_splits, hipStream_t s);
 hipError_t launch_gate8_fwd(bool vec, int64_t rows, int64_t width, int act, int type, const void* gate, int64_t gs,
@@ -146,6 +148,7 @@ size_t attn_tile_bytes(const gs_cross_attn& p) { return round16((size_t)attn_row
 size_t part_bytes(const gs_cross_attn& p, int splits, int64_t vecs) {
   return splits > 1 ? (size_t)splits * vecs * attn_padded(p.head_dim) * sizeof(float) : 0;
 }
+size_t order_bytes(const gs_cross_attn& p) { return round16((size_t)attn_order_items(p) * 2 * sizeof(int32_t)); }
 
 }  // namespace
 
@@ -173,8 +176,8 @@ gs_status gs_norm_rotate_bwd(const gs_norm_rotate* shape, gs_heads dout_q, gs_he
 size_t gs_cross_attn_fwd_workspace_bytes(const gs_cross_attn* p) {
   if (attn_shape(p) != GS_OK) return 0;
   const int splits = attn_fwd_splits(*p);
-  if (splits == 1) return 0;
-  return part_bytes(*p, splits, attn_rows(*p)) + round16((size_t)splits * attn_rows(*p) * sizeof(float2));
+  if (splits == 1) return order_bytes(*p);
+  return order_bytes(*p) + part_bytes(*p, splits, attn_rows(*p)) + round16((size_t)splits * attn_rows(*p) * sizeof(float2));
 }
 
 gs_status gs_cross_attn_fwd(const gs_cross_attn* p, gs_heads q, gs_heads k, gs_heads v, gs_heads out, float* lse,
@@ -195,8 +198,13 @@ gs_status gs_cross_attn_fwd(const gs_cross_attn* p, gs_heads q, gs_heads k, gs_h
   a.out = out;
   a.lse = lse;
   a.splits = attn_fwd_splits(*p);
-  a.part = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + part_bytes(*p, a.splits, attn_rows(*p)));
+  char* at = static_cast<char*>(workspace) + order_bytes(*p);
+  a.part = reinterpret_cast<float*>(at);
+  a.part_ml = reinterpret_cast<float2*>(at + part_bytes(*p, a.splits, attn_rows(*p)));
+  if (const int items = attn_order_items(*p)) {
+    const hipError_t e = launch_attn_order(a, items, static_cast<int32_t*>(workspace), static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return GS_ERR_HIP;
+  }
   return status_of(launch_attn_fwd(a, p->type, static_cast<hipStream_t>(stream)));
 }
 
@@ -204,7 +212,7 @@ size_t gs_cross_attn_bwd_workspace_bytes(const gs_cross_attn* p) {
   if (attn_shape(p) != GS_OK) return 0;
   const size_t q = part_bytes(*p, attn_fwd_splits(*p), attn_rows(*p));
   const size_t kv = part_bytes(*p, attn_bwd_kv_splits(*p), 2 * p->batch * p->kv_heads * p->k_len);
-  return attn_stat_bytes(*p) + attn_tile_bytes(*p) + (q > kv ? q : kv);
+  return order_bytes(*p) + attn_stat_bytes(*p) + attn_tile_bytes(*p) + (q > kv ? q : kv);
 }
 
 gs_status gs_cross_attn_bwd(const gs_cross_attn* p, gs_heads dout, gs_heads q, gs_heads k, gs_heads v, gs_heads out,
@@ -229,10 +237,14 @@ gs_status gs_cross_attn_bwd(const gs_cross_attn* p, gs_heads dout, gs_heads q, g
   a.dk = dk;
   a.dv = dv;
   a.lse = const_cast<float*>(lse);
-  char* at = static_cast<char*>(workspace);
+  char* at = static_cast<char*>(workspace) + order_bytes(*p);
   a.stat = reinterpret_cast<float2*>(at);
   a.row_tiles = reinterpret_cast<RowTile*>(at + attn_stat_bytes(*p));
   a.part = reinterpret_cast<float*>(at + attn_stat_bytes(*p) + attn_tile_bytes(*p));
+  if (const int items = attn_order_items(*p)) {
+    const hipError_t e = launch_attn_order(a, items, static_cast<int32_t*>(workspace), static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return GS_ERR_HIP;
+  }
   return status_of(launch_attn_bwd(a, p->type, attn_fwd_splits(*p), attn_bwd_kv_splits(*p), static_cast<hipStream_t>(stream)));
 }
 
