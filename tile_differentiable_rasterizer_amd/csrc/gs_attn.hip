@@ -292,14 +292,21 @@ hipError_t fwd_launch(const AttnArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Parts that a long axis of `tiles` tiles is split into when `blocks` workgroups are too few for
-// 256 CUs: enough for two workgroups a CU, at least two tiles a part.  Where rows see ranges of
-// their own, workgroups differ in length, and eight a CU let the short ones make room.
-int attn_splits(int64_t blocks, int64_t tiles, bool uneven) {
-  const int64_t aim = uneven ? 2048 : 512;
+// Parts that a long axis of `tiles` tiles is split into when the workgroups, `each` for every one of
+// `heads` (sequence, key head)s, are too few for 256 CUs: enough for two workgroups a CU, at least two
+// tiles a part.  Where rows see ranges of their own, workgroups differ in length, and four a CU let the
+// short ones fill in.  heads times the parts is made a multiple of the eight XCDs where it can be: the
+// workgroups that read the same keys then share one's L2 (16 x 3907 rows, 4 heads, 65280 keys: 2 or 4
+// parts 670 us, 5 or 6 parts 680, 12 parts 700, none 955).
+int attn_splits(int64_t heads, int64_t each, int64_t tiles, bool uneven) {
+  const int64_t aim = uneven ? 1024 : 512, blocks = heads * each;
   if (blocks <= 0 || blocks >= aim) return 1;
-  const int64_t want = (aim + blocks - 1) / blocks, most = tiles / 2;
-  return (int)(want < most ? want : most < 1 ? 1 : most);
+  const int64_t most = tiles / 2 < 1 ? 1 : tiles / 2;
+  int64_t s = (aim + blocks - 1) / blocks;
+  if (s >= most) return (int)most;
+  for (int64_t t = s; t < s + 8 && t <= most; ++t)
+    if (heads * t % 8 == 0) return (int)t;
+  return (int)s;
 }
 
 int attn_padded(int d) { return (d + 31) / 32 * 32; }
@@ -323,7 +330,7 @@ hipError_t launch_attn_order(AttnArgs& a, int items, int32_t* space, hipStream_t
 
 int attn_fwd_splits(const gs_cross_attn& p) {
   const int64_t rows = p.q_len * (p.q_heads / p.kv_heads);
-  return attn_splits(p.batch * p.kv_heads * ((rows + 127) / 128), (p.k_len + kAttnKeys - 1) / kAttnKeys,
+  return attn_splits(p.batch * p.kv_heads, (rows + 127) / 128, (p.k_len + kAttnKeys - 1) / kAttnKeys,
                      p.ranges && p.ranges_row_stride);
 }
 

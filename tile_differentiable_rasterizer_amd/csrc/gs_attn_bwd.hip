@@ -439,12 +439,12 @@ __global__ __launch_bounds__(256) void k_attn_bwd_join(AttnArgs a) {
   }
 }
 
-int attn_splits(int64_t blocks, int64_t tiles, bool uneven);
+int attn_splits(int64_t heads, int64_t each, int64_t tiles, bool uneven);
 int attn_padded(int d);
 
 int attn_bwd_kv_splits(const gs_cross_attn& p) {
   const int64_t rows = p.q_len * (p.q_heads / p.kv_heads);
-  return attn_splits(p.batch * p.kv_heads * ((p.k_len + 127) / 128), (rows + kBwdRows - 1) / kBwdRows,
+  return attn_splits(p.batch * p.kv_heads, (p.k_len + 127) / 128, (rows + kBwdRows - 1) / kBwdRows,
                      p.ranges && p.ranges_row_stride);
 }
 
