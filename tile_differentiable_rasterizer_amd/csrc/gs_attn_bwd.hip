@@ -5,7 +5,9 @@
 // order is fixed: k_attn_bwd_kv owns 128 keys and walks the rows (of every query head that shares
 // them), k_attn_bwd_q owns 128 rows and walks the keys.  That computes the scores twice (7
 // products of a tile instead of 5).
-// The row kernel goes first: it finishes the rows' statistics where they see few keys.
+// The row kernel goes first and leaves the rows' statistics for the other: lse in base 2, delta = dout . out,
+// and what each tile of 64 rows may see (a kernel of their own before it: 4 x 256 x 256, 16 heads of 64,
+// 44 us instead of 40; 3907 x 8160, 32 heads of 128 +0.4%).
 //
 // kv: S[row][key] = Q K^T and dP[row][key] = dO V^T leave a lane with one key and 16 rows, the B
 // operand of dV^T[d][key] = dO^T P and dK^T[d][key] = Q^T dS.  q: as the forward kernel, S^T and
@@ -15,60 +17,12 @@
 
 namespace gs {
 
-constexpr int kBwdRows = 64;  // rows that the statistics are kept for together
+constexpr int kBwdRows = 64;  // rows of a RowTile
 constexpr int kShortTiles = 4;  // key tiles up to which a row's delta is taken from its weights
 // LDS operands on the way.  bfloat16: 2 is 1% slower, 6 spills at D 128 (13%).  float32, whose operands
 // are three times as large and feed six products: 1 up to D 64 (2: 4-9% slower), above 2 (1: 7%).
 template <typename T, int DP>
 constexpr int kAhead = sizeof(T) == 2 ? 4 : DP <= 64 ? 1 : 2;
-
-// Statistics of every row, in the order of (sequence, key head, row): lse in base 2 and delta =
-// dout . out, and what each tile of 64 rows may see.  One workgroup a tile; a vector takes 16
-// lanes, eight elements a lane.
-template <typename T>
-__global__ __launch_bounds__(256) void k_attn_stat(AttnArgs a) {
-  __shared__ float delta[kBwdRows];
-  const int tiles = (a.rows + kBwdRows - 1) / kBwdRows;
-  const int bh = blockIdx.x / tiles, t = blockIdx.x - bh * tiles;
-  const int b = bh / a.kv_heads, hk = bh - b * a.kv_heads, d = (threadIdx.x & 15) * 8;
-#pragma unroll
-  for (int p = 0; p < kBwdRows / 16; ++p) {
-    const int r = p * 16 + threadIdx.x / 16, row = t * kBwdRows + r;
-    float sum = 0.0f;
-    if (row < a.rows && d < a.d) {
-      const int i = row / a.group, h = hk * a.group + row - i * a.group;
-      float x[8], y[8];
-      load_elems<8>(head_ptr<T>(a.out, b, i, h) + d, x);
-      load_elems<8>(head_ptr<T>(a.dout, b, i, h) + d, y);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
-    }
-#pragma unroll
-    for (int e = 1; e < 16; e <<= 1) sum += __shfl_xor(sum, e, 64);
-    if (d == 0) delta[r] = sum;
-  }
-  __syncthreads();
-  if (threadIdx.x >= kBwdRows) return;
-  const int row = t * kBwdRows + threadIdx.x;
-  bool live = row < a.rows;
-  int2 range = make_int2(0, 0);
-  float lse = -INFINITY;
-  if (live) {
-    const int i = row / a.group, h = hk * a.group + row - i * a.group;
-    range = row_range(a, b, i);
-    lse = a.lse[((int64_t)b * a.kv_heads * a.group + h) * a.q_len + i];
-    live = range.x < range.y && lse != -INFINITY;
-  }
-  // a row without keys: every weight 2^-inf = 0
-  a.stat[(int64_t)blockIdx.x * kBwdRows + threadIdx.x] = live ? make_float2(lse * kLog2e, delta[threadIdx.x]) : make_float2(INFINITY, 0.0f);
-  RowTile w;
-  w.word = __ballot(live);
-  w.first = wave_min_i(live ? range.x : INT32_MAX);
-  w.last = wave_max_i(live ? range.y : 0);
-  w.all_from = wave_max_i(live ? range.x : 0);
-  w.all_to = wave_min_i(live ? range.y : INT32_MAX);
-  if (threadIdx.x == 0) a.row_tiles[blockIdx.x] = w;
-}
 
 // How the kv kernel fits its registers: the results take DP of them, the fragments of its keys and
 // values DP / 2 (bfloat16) or 3 DP / 2.
@@ -267,18 +221,37 @@ __global__ __launch_bounds__(256, (kWavesOf<T, DP>)) void k_attn_bwd_q(AttnArgs 
   const bool valid = row < a.rows;
   const int i = valid ? row / a.group : 0, h = hk * a.group + (valid ? row - i * a.group : 0);
   int2 range = row_range(a, b, i);
-  const int tiles = (a.rows + kBwdRows - 1) / kBwdRows;
-  float2* const place = a.stat + (int64_t)bh * tiles * kBwdRows + row;
-  float2 stat = valid ? *place : make_float2(INFINITY, 0.0f);
-  const bool live = stat.x != INFINITY;
-  if (!live) range = make_int2(0, 0);
+  float2 stat = make_float2(INFINITY, 0.0f);  // a row without keys: every weight is 2^-inf = 0
+  const float lse = valid ? a.lse[((int64_t)b * a.kv_heads * a.group + h) * a.q_len + i] : -INFINITY;
+  const bool live = valid && range.x < range.y && lse != -INFINITY;
+  if (live)
+    stat.x = lse * kLog2e;
+  else
+    range = make_int2(0, 0);
   const Seen seen = block_seen(a, b, range, scratch);
+  const int t_lo = seen.first / kAttnKeys, t_n = seen.last > seen.first ? (seen.last + kAttnKeys - 1) / kAttnKeys - t_lo : 0;
 
   Frag<T> qf[kS], gf[kS];
 #pragma unroll
   for (int s = 0; s < kS; ++s) {
     qf[s] = frag_flip(frag_mem<T>(head_ptr<T>(a.q, b, i, h), a.d, s, live), a.flip);
     gf[s] = frag_mem<T>(head_ptr<T>(a.dout, b, i, h), a.d, s, live);
+  }
+  if (t_n > kShortTiles) {
+    const T *op = head_ptr<T>(a.out, b, i, h), *gp = head_ptr<T>(a.dout, b, i, h);
+    float delta = 0.0f;
+#pragma unroll
+    for (int s = 0; s < kS; ++s) {
+      const int d = 16 * s + 8 * half;
+      if (live && d < a.d) {
+        float x[8], y[8];
+        load_elems<8>(op + d, x);
+        load_elems<8>(gp + d, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) delta = fmaf(x[e], y[e], delta);
+      }
+    }
+    if (live) stat.y = pair_sum(delta);
   }
   const T* kh = head_ptr<T>(a.k, b, 0, hk);
   const T* vh = head_ptr<T>(a.v, b, 0, hk);
@@ -312,7 +285,6 @@ __global__ __launch_bounds__(256, (kWavesOf<T, DP>)) void k_attn_bwd_q(AttnArgs 
         body(kv.at(lds, buf, 0), kv.at(lds, buf, 1), ragged ? word & range_word(range.x, range.y, k0) : word, ragged || word != ~0ull);
     }
   };
-  const int t_lo = seen.first / kAttnKeys, t_n = seen.last > seen.first ? (seen.last + kAttnKeys - 1) / kAttnKeys - t_lo : 0;
 
   // Over few keys `out` is as large as the values, and its rounding shows in delta = dout . out, which
   // enters every dS of the row: there delta is taken from the weights, sum_j p_j dout . v_j (a row of
@@ -337,11 +309,35 @@ __global__ __launch_bounds__(256, (kWavesOf<T, DP>)) void k_attn_bwd_q(AttnArgs 
         }
       }
     });
-    if (live) {
-      stat.y = pair_sum(delta);
-      if (split == 0 && half == 0) place->y = stat.y;  // for the kv kernel
-    }
+    if (live) stat.y = pair_sum(delta);
     __syncthreads();  // the tiles are read again
+  }
+  if (split == 0) {  // for the kv kernel
+    const int infos = (a.rows + kBwdRows - 1) / kBwdRows, wave = threadIdx.x >> 6;
+    if (half == 0 && row < infos * kBwdRows) a.stat[(int64_t)bh * infos * kBwdRows + row] = stat;
+    const uint32_t word = (uint32_t)__ballot(live);
+    const int first = wave_min_i(live ? range.x : INT32_MAX), last = wave_max_i(live ? range.y : 0);
+    const int from = wave_max_i(live ? range.x : 0), to = wave_min_i(live ? range.y : INT32_MAX);
+    if (lane == 0) {
+      words[wave] = word;
+      scratch[wave][0] = first;
+      scratch[wave][1] = last;
+      scratch[wave][2] = from;
+      scratch[wave][3] = to;
+    }
+    __syncthreads();
+    const int info = block.rt * 2 + threadIdx.x;
+    if (threadIdx.x < 2 && info < infos) {
+      const int w = 2 * threadIdx.x;
+      RowTile x;
+      x.word = words[w] | words[w + 1] << 32;
+      x.first = min(scratch[w][0], scratch[w + 1][0]);
+      x.last = max(scratch[w][1], scratch[w + 1][1]);
+      x.all_from = max(scratch[w][2], scratch[w + 1][2]);
+      x.all_to = min(scratch[w][3], scratch[w + 1][3]);
+      a.row_tiles[(int64_t)bh * infos + info] = x;
+    }
+    __syncthreads();  // the words are written again
   }
 
   f32x16 dq[kD];
@@ -454,7 +450,6 @@ template <typename T, int DP>
 hipError_t bwd_launch(AttnArgs a, int q_splits, int kv_splits, hipStream_t s) {
   const int64_t nbh = (int64_t)a.batch * a.kv_heads, vecs = nbh * a.rows, per = 256 / (DP / 4);
   if (nbh == 0 || (a.rows == 0 && a.k_len == 0)) return hipSuccess;
-  if (vecs) k_attn_stat<T><<<(unsigned)(nbh * ((a.rows + kBwdRows - 1) / kBwdRows)), 256, 0, s>>>(a);
   if (vecs) {
     a.splits = q_splits;
     k_attn_bwd_q<T, DP><<<(unsigned)(nbh * ((a.rows + 127) / 128) * q_splits), 256, 0, s>>>(a);
