@@ -7,11 +7,13 @@
 // row only (its column of the result): maximum and sum are in-lane but for one exchange between
 // the halves, the row's statistics are one register, and the weights are at once the B operand of
 // O^T[d][row] = V^T P^T.  The weights enter that product in the element type (bfloat16: an error
-// of 2^-8 of each weight at most, of the order of the output's own rounding); everything else is float32.
+// of 2^-8 of each weight at most, of the order of the output's own rounding; float32: in three bfloat16
+// parts that hold all of its bits); everything else is float32.
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "gs_attn.h"
-
 
 namespace gs {
 
@@ -292,24 +294,53 @@ hipError_t fwd_launch(const AttnArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Parts that a long axis of `tiles` tiles is split into when the workgroups, `each` for every one of
-// `heads` (sequence, key head)s, are too few for 256 CUs: enough for two workgroups a CU, at least two
-// tiles a part.  Where rows see ranges of their own, workgroups differ in length, and four a CU let the
-// short ones fill in.  heads times the parts is made a multiple of the eight XCDs where it can be: the
-// workgroups that read the same keys then share one's L2 (16 x 3907 rows, 4 heads, 65280 keys: 2 or 4
-// parts 670 us, 5 or 6 parts 680, 12 parts 700, none 955).
-int attn_splits(int64_t heads, int64_t each, int64_t tiles, bool uneven) {
-  const int64_t aim = uneven ? 1024 : 512, blocks = heads * each;
-  if (blocks <= 0 || blocks >= aim) return 1;
-  const int64_t most = tiles / 2 < 1 ? 1 : tiles / 2;
-  int64_t s = (aim + blocks - 1) / blocks;
-  if (s >= most) return (int)most;
-  for (int64_t t = s; t < s + 8 && t <= most; ++t)
-    if (heads * t % 8 == 0) return (int)t;
-  return (int)s;
+int attn_padded(int d) { return (d + 31) / 32 * 32; }
+
+// Parts that a long axis is split into: those for which a model of the time gives the least.
+//
+// blocks workgroups, each over `tiles` tiles of tile_us (another workgroup of its CU beside it), become n = blocks s
+// of 1 / s the length on `slots` places: full rounds of them, then a rest.  A rest of up to half the places leaves
+// every CU one workgroup at most, which alone runs 1.4 times as fast (float32 above 64 elements has one place a
+// CU anyway).  Where rows see ranges of their own, workgroups fill in for each other and the longest end late.
+// 3 us a round start and end it; the parts cost 4 us for the launch that joins them and part_us each, written and
+// read.  At most four rounds.  heads s that is a multiple of the eight XCDs lets the workgroups of one key head
+// share an L2 (2%).  Too few blocks for a quarter of the places: a part for each place.
+//
+// Measured: 2 x 2600 rows x 1000 keys, 8 heads of 128 (336 blocks): 1, 2, 3 parts 36, 53, 54 us; 2 x 2400 x 2500 in
+// float32, 64 elements (304 blocks): 243, 229, 191, 4 parts 191; 3907 x 30000, ranges of their own, 4 heads (492
+// blocks): 477, 334, 348, 335; backward over 8704 keys, 4 heads of 128 (272 blocks of keys): 1166, 1252, 1023,
+// 1094; a token at a time, 32 blocks: 8 parts 29 us, 16 25, 32 28.  92 shapes of 100 to 1300 blocks, against as many
+// parts as give each place a workgroup: forward 1.10, backward 1.15 times as fast.
+int attn_splits(int64_t heads, int64_t each, int64_t tiles, bool uneven, int slots, double tile_us, double part_us) {
+  const int64_t blocks = heads * each, most = tiles / 2;
+  if (blocks <= 0 || most < 2) return 1;
+  if (blocks < slots / 4) return (int)std::min(most, slots / blocks);  // nothing to weigh
+  const double alone = slots > 256 ? 0.72 : 1.0;
+  double least = 0.0;
+  int best = 0;
+  for (int s = 1; s == 1 || (s <= most && s * blocks <= 4 * slots); ++s) {
+    const double n = (double)(blocks * s) / slots, full = std::floor(n), rest = n - full;
+    double rounds = full + (rest == 0.0 ? 0.0 : rest <= 0.5 ? alone : 1.0 - (1.0 - alone) * (1.0 - rest) / 2.0);
+    if (uneven) rounds = std::max(alone, 0.55 * n + 0.35);
+    double us = rounds * (tile_us * tiles / s + 3.0) + (s > 1 ? 4.0 + s * part_us : 0.0);
+    if (s > 1 && heads * s % 8) us *= 1.02;
+    if (best == 0 || us < least) {
+      least = us;
+      best = s;
+    }
+  }
+  return best;
 }
 
-int attn_padded(int d) { return (d + 31) / 32 * 32; }
+// Workgroups that the device holds of the kernels that own rows or keys.
+int attn_slots(const gs_cross_attn& p) { return p.type == GS_BF16 || attn_padded(p.head_dim) <= 64 ? 512 : 256; }
+
+// Time of one forward tile (128 rows, 64 keys) with all places taken, as measured: bfloat16 1.3 us of 64
+// elements, 2.3 of 128; float32 7.2 and 9.1.
+double attn_tile_us(const gs_cross_attn& p) {
+  const int d = attn_padded(p.head_dim);
+  return p.type == GS_BF16 ? 0.35 + 0.015 * d : d <= 64 ? 0.112 * d : 0.071 * d;
+}
 
 // Blocks of 128 rows to be put in order of length, or 0.  Rows with ranges of their own, or sequences
 // of several lengths, make workgroups of different lengths; longest first, the short ones fill the
@@ -328,11 +359,15 @@ hipError_t launch_attn_order(AttnArgs& a, int items, int32_t* space, hipStream_t
   return hipGetLastError();
 }
 
-int attn_fwd_splits(const gs_cross_attn& p) {
-  const int64_t rows = p.q_len * (p.q_heads / p.kv_heads);
-  return attn_splits(p.batch * p.kv_heads, (rows + 127) / 128, (p.k_len + kAttnKeys - 1) / kAttnKeys,
-                     p.ranges && p.ranges_row_stride);
+int attn_row_splits(const gs_cross_attn& p, double tile_us) {
+  const int64_t rows = p.q_len * (p.q_heads / p.kv_heads), heads = p.batch * p.kv_heads;
+  const double part_us = 8e-6 / 4 * heads * rows * attn_padded(p.head_dim);  // 8 bytes an element at 4 TB/s
+  return attn_splits(heads, (rows + 127) / 128, (p.k_len + kAttnKeys - 1) / kAttnKeys, p.ranges && p.ranges_row_stride,
+                     attn_slots(p), tile_us, part_us);
 }
+
+int attn_fwd_splits(const gs_cross_attn& p) { return attn_row_splits(p, attn_tile_us(p)); }
+int attn_bwd_q_splits(const gs_cross_attn& p) { return attn_row_splits(p, 1.4 * attn_tile_us(p)); }
 
 hipError_t launch_attn_fwd(AttnArgs a, int type, hipStream_t s) {
   switch (attn_padded(a.d) + type) {

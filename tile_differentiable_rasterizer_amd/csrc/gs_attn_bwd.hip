@@ -435,13 +435,17 @@ __global__ __launch_bounds__(256) void k_attn_bwd_join(AttnArgs a) {
   }
 }
 
-int attn_splits(int64_t heads, int64_t each, int64_t tiles, bool uneven);
+int attn_splits(int64_t heads, int64_t each, int64_t tiles, bool uneven, int slots, double tile_us, double part_us);
 int attn_padded(int d);
+int attn_slots(const gs_cross_attn& p);
+double attn_tile_us(const gs_cross_attn& p);
 
+// A tile of 128 keys and 64 rows takes 2.4 times the forward pass's; dk and dv have parts.
 int attn_bwd_kv_splits(const gs_cross_attn& p) {
-  const int64_t rows = p.q_len * (p.q_heads / p.kv_heads);
-  return attn_splits(p.batch * p.kv_heads, (p.k_len + 127) / 128, (rows + kBwdRows - 1) / kBwdRows,
-                     p.ranges && p.ranges_row_stride);
+  const int64_t rows = p.q_len * (p.q_heads / p.kv_heads), heads = p.batch * p.kv_heads;
+  const double part_us = 16e-6 / 4 * heads * p.k_len * attn_padded(p.head_dim);
+  return attn_splits(heads, (p.k_len + 127) / 128, (rows + kBwdRows - 1) / kBwdRows, p.ranges && p.ranges_row_stride,
+                     attn_slots(p), 2.4 * attn_tile_us(p), part_us);
 }
 
 namespace {

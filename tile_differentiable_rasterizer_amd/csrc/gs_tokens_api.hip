@@ -12,6 +12,7 @@ hipError_t launch_norm_rotate(const gs_norm_rotate& p, const gs_heads& q, const 
                               float* dwq, float* dwk, void* ws, hipStream_t s);
 int attn_padded(int d);
 int attn_fwd_splits(const gs_cross_attn& p);
+int attn_bwd_q_splits(const gs_cross_attn& p);
 int attn_bwd_kv_splits(const gs_cross_attn& p);
 int attn_order_items(const gs_cross_attn& p);
 hipError_t launch_attn_order(AttnArgs& a, int items, int32_t* space, hipStream_t s);
@@ -210,7 +211,7 @@ gs_status gs_cross_attn_fwd(const gs_cross_attn* p, gs_heads q, gs_heads k, gs_h
 
 size_t gs_cross_attn_bwd_workspace_bytes(const gs_cross_attn* p) {
   if (attn_shape(p) != GS_OK) return 0;
-  const size_t q = part_bytes(*p, attn_fwd_splits(*p), attn_rows(*p));
+  const size_t q = part_bytes(*p, attn_bwd_q_splits(*p), attn_rows(*p));
   const size_t kv = part_bytes(*p, attn_bwd_kv_splits(*p), 2 * p->batch * p->kv_heads * p->k_len);
   return order_bytes(*p) + attn_stat_bytes(*p) + attn_tile_bytes(*p) + (q > kv ? q : kv);
 }
@@ -245,7 +246,7 @@ gs_status gs_cross_attn_bwd(const gs_cross_attn* p, gs_heads dout, gs_heads q, g
     const hipError_t e = launch_attn_order(a, items, static_cast<int32_t*>(workspace), static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return GS_ERR_HIP;
   }
-  return status_of(launch_attn_bwd(a, p->type, attn_fwd_splits(*p), attn_bwd_kv_splits(*p), static_cast<hipStream_t>(stream)));
+  return status_of(launch_attn_bwd(a, p->type, attn_bwd_q_splits(*p), attn_bwd_kv_splits(*p), static_cast<hipStream_t>(stream)));
 }
 
 namespace {
