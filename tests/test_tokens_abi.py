@@ -126,6 +126,15 @@ def test_cross_attn_limits():
     assert L.gs_cross_attn_fwd_workspace_bytes(None) == 0
 
 
+def test_cross_attn_orders_nothing_without_keys():
+    """Rows are put in order by the key tiles they see: of none, as many rows as there may be."""
+    p = tokens().GsCrossAttn(batch=1, q_len=1 << 23, k_len=1, q_heads=32, kv_heads=32, head_dim=8, type=0, scale=1.0, ranges=A, ranges_row_stride=1)
+    L = tokens().lib()
+    assert L.gs_cross_attn_fwd_workspace_bytes(p) == 8 << 16
+    p.k_len = 0
+    assert L.gs_cross_attn_fwd_workspace_bytes(p) == 0
+
+
 def gate_call(rows=3, width=64, act=0, type=0, x=A, stride=64, codes=A, bounds=A, bwd=False):
     L = tokens().lib()
     if bwd:

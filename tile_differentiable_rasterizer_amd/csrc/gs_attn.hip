@@ -347,8 +347,8 @@ double attn_tile_us(const gs_cross_attn& p) {
 // end.  Worth its two launches (8 us) where the kernel takes ten times that: from 2^28 (row, key) pairs.
 int attn_order_items(const gs_cross_attn& p) {
   const int64_t rows = p.q_len * (p.q_heads / p.kv_heads), items = p.batch * ((rows + 127) / 128);
-  if (!p.ranges || items < 64 || items > 65536) return 0;
-  return p.batch * p.kv_heads * rows >= ((int64_t)1 << 28) / (p.k_len > 0 ? p.k_len : 1) ? (int)items : 0;
+  if (!p.ranges || p.k_len <= 0 || items < 64 || items > 65536) return 0;
+  return p.batch * p.kv_heads * rows >= ((int64_t)1 << 28) / p.k_len ? (int)items : 0;
 }
 
 // space: two int32 for each of attn_order_items().
