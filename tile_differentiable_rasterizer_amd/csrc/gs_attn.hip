@@ -9,6 +9,18 @@
 // O^T[d][row] = V^T P^T.  The weights enter that product in the element type (bfloat16: an error
 // of 2^-8 of each weight at most, of the order of the output's own rounding; float32: in three bfloat16
 // parts that hold all of its bits); everything else is float32.
+//
+// A workgroup has 128 rows, 32 a wavefront (a matrix instruction's columns), and walks tiles of 64 keys, whose next
+// one's loads run beside this one's products.  64 rows a wavefront halve the LDS reads, but leave one wavefront a
+// SIMD: 400 TFLOP/s instead of 900 at D 128.
+//
+// What bounds it are the products and the vector arithmetic of the softmax (a score's multiply and add, exponential, sum,
+// half a rounding), which the SIMDs do one or the other: busy 56% and 39% of the time at D 128, 42% and 58% at 64.
+// Two tiles at once with one's exponentials between the other's products changes nothing (D 64 711 -> 669).
+// Whole calls: D 128, 2 x 3907 x 8160, 32 heads 975 us, 1.07 PFLOP/s; D 64, 3907 x 32768, 16 heads 740 us, 0.71;
+// D 64, 3 x 3907 x 3600, 16 heads 262 us, 0.66; float32 D 64, 2 x 2400 x 2500, 8 heads 191 us, 0.13 (a product of
+// 8192 x 8192: bfloat16 1.35, float32 0.15).  One token of 32 heads for each of 8 sequences of up to 8160
+// states, 79 MB: 22 us and 4 to join, 3.1 TB/s.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -20,7 +32,8 @@ namespace gs {
 // A tile's weights are taken relative to the maximum known before it, and the tile's sum tells
 // whether that was too low: only then (and on a row's first tile) the maximum is looked for, the
 // sums are scaled and the weights taken again.  Weights of up to this cost float32 and bfloat16
-// nothing (they are relative in both).
+// nothing (they are relative in both).  (The maximum sought on every tile: D 64 724 TFLOP/s instead of 782, D 128
+// 900 instead of 938.)
 constexpr float kMostWeight = 1024.0f;
 
 template <typename T, int DP>
@@ -216,9 +229,10 @@ __global__ __launch_bounds__(1024) void k_attn_order(int items, int tiles, const
   for (int i = t; i < items; i += 1024) order[atomicAdd(&count[place(i)], 1)] = i;
 }
 
-// Joins the splits of a row: weights 2^(m_s - max m).  One workgroup for kRows rows; a row's splits
-// are shared out over its 256 / (kRows * DP / 4) groups of DP / 4 lanes (four elements a lane), which
-// meet in LDS.  Few rows leave the splits' loads as the only parallelism.
+// Joins the splits of a row: weights 2^(m_s - max m).  One workgroup for ROWS rows; a row's splits
+// are shared out over its 256 / (ROWS * DP / 4) groups of DP / 4 lanes (four elements a lane), which
+// meet in LDS.  Few rows leave the splits' loads as the only parallelism.  Memory bound: 4 parts of 62512 rows
+// of 64 15 us, 4.7 TB/s.
 template <typename T, int DP, int ROWS>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   constexpr int kLanes = DP / 4, kGroups = 256 / kLanes / ROWS;

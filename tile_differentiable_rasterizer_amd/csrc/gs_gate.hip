@@ -10,6 +10,11 @@
 // the extremes across 32 lanes, codes and y written.  The code is decided in float64, as the
 // definition says (ties are not rare with bfloat16's few values in a block); a product and an addition of
 // 1.5 * 2^52 leave rint() of the product in the sum's low word.
+//
+// Forward 2 inputs, y and 2 codes a unit; back 2 codes and dy, 2 gradients and y: the memory bounds both.  39063 x 2752 in
+// float32: 285 us, 5.3 TB/s; back 361 us, 5.4 TB/s (a copy of 2 GiB: 4.8).  3907 x 4096 in bfloat16: 30 us, 4.3 TB/s;
+// back 25 us, 6.3 TB/s (what the forward call left in the last cache).  4 x 1001: 5 us each.  No loop over blocks of
+// units: a half wavefront has one, so that a workgroup's reads are a row's next kilobytes.
 #include "gs_device.h"
 #include "gs_elem.h"
 
