@@ -15,8 +15,8 @@
 // SIMD: 400 TFLOP/s instead of 900 at D 128.
 //
 // What bounds it are the products and the vector arithmetic of the softmax (a score's multiply and add, exponential, sum,
-// half a rounding), which the SIMDs do one or the other: busy 56% and 39% of the time at D 128, 42% and 58% at 64.
-// Two tiles at once with one's exponentials between the other's products changes nothing (D 64 711 -> 669).
+// half a rounding), which the SIMDs do one or the other: busy 56% and 39% of the time at D 128, 42% and 60% at 64.
+// Two tiles at once with one's exponentials between the other's products is no faster (D 64 711 -> 669 TFLOP/s).
 // Whole calls: D 128, 2 x 3907 x 8160, 32 heads 975 us, 1.07 PFLOP/s; D 64, 3907 x 32768, 16 heads 740 us, 0.71;
 // D 64, 3 x 3907 x 3600, 16 heads 262 us, 0.66; float32 D 64, 2 x 2400 x 2500, 8 heads 191 us, 0.13 (a product of
 // 8192 x 8192: bfloat16 1.35, float32 0.15).  One token of 32 heads for each of 8 sequences of up to 8160

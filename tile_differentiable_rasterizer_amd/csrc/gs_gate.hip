@@ -13,7 +13,7 @@
 //
 // Forward 2 inputs, y and 2 codes a unit; back 2 codes and dy, 2 gradients and y: the memory bounds both.  39063 x 2752 in
 // float32: 285 us, 5.3 TB/s; back 361 us, 5.4 TB/s (a copy of 2 GiB: 4.8).  3907 x 4096 in bfloat16: 30 us, 4.3 TB/s;
-// back 25 us, 6.3 TB/s (what the forward call left in the last cache).  4 x 1001: 5 us each.  No loop over blocks of
+// back 25 to 32 us, 6.3 to 4.9 TB/s (as much as the last cache has kept of the forward call).  4 x 1001: 5 us each.  No loop over blocks of
 // units: a half wavefront has one, so that a workgroup's reads are a row's next kilobytes.
 #include "gs_device.h"
 #include "gs_elem.h"
