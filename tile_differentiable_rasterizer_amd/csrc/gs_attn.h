@@ -68,6 +68,12 @@ __device__ __forceinline__ uint64_t range_word(int first, int last, int k0) {
   return (~0ull >> (64 - (hi - lo))) << lo;
 }
 
+// A value that is the same in every lane, in scalar registers: what is decided by it is decided once.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ uint64_t uniform(uint64_t x) {
+  return (uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32 | (uint32_t)uniform((int)x);
+}
+
 __device__ __forceinline__ int wave_min_i(int x) {
 #pragma unroll
   for (int d = 32; d; d >>= 1) x = min(x, __shfl_xor(x, d, 64));
@@ -150,6 +156,10 @@ __device__ __forceinline__ Seen block_seen(const AttnArgs& a, int b, int2 mine, 
     s.all_to = min(s.all_to, scratch[i][3]);
   }
   __syncthreads();
+  s.first = uniform(s.first);
+  s.last = uniform(s.last);
+  s.all_from = uniform(s.all_from);
+  s.all_to = uniform(s.all_to);
   return s;
 }
 
@@ -160,7 +170,7 @@ __device__ __forceinline__ uint64_t block_word(uint64_t mine, uint64_t* scratch)
   __syncthreads();
   const uint64_t r = scratch[0] | scratch[1] | scratch[2] | scratch[3];
   __syncthreads();
-  return r;
+  return uniform(r);
 }
 
 // Sixteen bytes of zeros for the lanes of a load that have nothing to read.

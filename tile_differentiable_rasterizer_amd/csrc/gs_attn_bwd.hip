@@ -91,7 +91,12 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::kWaves)) void k_attn_bwd_kv(A
   RowTile next;
   auto find = [&](int t) {
     for (; t < t_end; ++t) {
-      next = info[t / kPerInfo];
+      const RowTile x = info[t / kPerInfo];
+      next.word = uniform(x.word);
+      next.first = uniform(x.first);
+      next.last = uniform(x.last);
+      next.all_from = uniform(x.all_from);
+      next.all_to = uniform(x.all_to);
       if (next.word && next.first < k1 && next.last > k0) break;
     }
     return t;
