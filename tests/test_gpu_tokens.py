@@ -132,6 +132,11 @@ def test_norm_rotate(case, strided):
         close(dw, rw, (e + (terms / 2048 + 64) * U) * rwm, "dw" + side)
 
 
+def test_norm_rotate_more_vectors_than_a_grid_takes():
+    """Workgroups walk the vectors: forward from 65536 workgroups on, back with more parts of dw than 2048."""
+    test_norm_rotate(("bf16", 1, 40000, 1000, 16, 4, 256, 64, "halves"), False)
+
+
 def test_norm_rotate_in_place_and_positions_outside_the_table():
     q, k, wq, wk, cos, sin = norm_inputs(("bf16", 2, 33, 12, 4, 2, 64, 64, "halves"), False)
     n = cos.shape[0]
@@ -321,6 +326,38 @@ def test_cross_attn_row_ranges(case):
     ranges[..., 0] = torch.where(cut, lo, lo.clamp(min=gap.stop))
     k[:, gap] = float("nan")
     v[:, gap] = float("nan")
+    attn_check(q, k, v, ranges=ranges)
+
+
+@pytest.mark.parametrize("case", [("bf16", 2, 1300, 2600, 8, 8, 32), ("f32", 2, 2000, 1100, 8, 8, 32), ("f32", 1, 900, 1500, 16, 8, 104)], ids=str)
+@pytest.mark.parametrize("kind", ["all", "rows", "lengths"])
+def test_cross_attn_many_blocks(case, kind):
+    """Enough workgroups for a part of the GPU or for more than it holds: long axes in a few parts."""
+    q, k, v = qkv(*case)
+    B, Lq, Lk = q.shape[0], q.shape[1], k.shape[1]
+    ranges = None
+    if kind == "rows":
+        first = torch.randint(0, Lk, (B, Lq), generator=gen(13), device="cuda")
+        ranges = torch.stack([first, first + torch.randint(0, Lk, (B, Lq), generator=gen(14), device="cuda")], -1).int()
+    if kind == "lengths":
+        ranges = torch.tensor([[0, Lk - 70], [65, 67]], device="cuda", dtype=torch.int32)[:B, None]
+    attn_check(q, k, v, ranges=ranges)
+
+
+@pytest.mark.parametrize("kind", ["rows", "lengths"])
+def test_cross_attn_longest_first(kind):
+    """From 2^28 pairs on, blocks of rows with ranges are worked on by length."""
+    q, k, v = qkv("bf16", 2, 4200, 2100, 16, 16, 32)
+    p = tokens.GsCrossAttn(2, 4200, 2100, 16, 16, 32, tokens.BF16, 1.0)
+    plain = tokens.lib().gs_cross_attn_fwd_workspace_bytes(p)
+    p.ranges, p.ranges_batch_stride = 1 << 20, 1
+    assert tokens.lib().gs_cross_attn_fwd_workspace_bytes(p) > plain  # room for the order
+    if kind == "lengths":
+        ranges = torch.tensor([[[3, 1000]], [[0, 2100]]], device="cuda", dtype=torch.int32)
+    else:
+        first = torch.randint(0, 2000, (2, 4200 // 60, 1), generator=gen(15), device="cuda").expand(-1, -1, 60).reshape(2, -1)
+        n = torch.randint(0, 2100, (2, 4200 // 60, 1), generator=gen(16), device="cuda").expand(-1, -1, 60).reshape(2, -1)
+        ranges = torch.stack([first, first + n], -1).int().contiguous()
     attn_check(q, k, v, ranges=ranges)
 
 
