@@ -98,7 +98,9 @@ gs_status gs_norm_rotate_bwd(const gs_norm_rotate* shape, gs_heads dout_q, gs_he
  *              key_mask_batch_stride b.  NULL: none masked.
  * Keys and values that no row of a sequence may see are not part of any result, whatever they
  * hold.  (A value that some row sees and another does not has to be finite for the other's
- * result to be: weights of 0 are products like the rest.) */
+ * result to be: weights of 0 are products like the rest.  So do a row's query and output gradient
+ * for the gradients of keys that it does not see and others do; those of a row that sees nothing
+ * are not part of any result.) */
 typedef struct gs_cross_attn {
   int64_t batch, q_len, k_len;
   int32_t q_heads, kv_heads, head_dim, type;
@@ -146,8 +148,8 @@ gs_status gs_cross_attn_bwd(const gs_cross_attn* a, gs_heads dout, gs_heads q, g
  *  bounds        float32 [2][rows][ceil(width / 256)][2], 8-byte aligned: (lo, hi) = the minimum
  *                and maximum of each 256 consecutive units of a row (the last block may be
  *                shorter); code = rint((x - lo) * (255 * (1 / (hi - lo)))) with every operation
- *                rounded to float64, 0 where hi == lo.  A block that holds a NaN or an infinity has NaN bounds and codes 0, so
- *                that it stays visible in the gradients.
+ *                rounded to float64, 0 where hi == lo.  A block that holds a NaN or an infinity
+ *                has NaN bounds and codes 0, so that it stays visible in the gradients.
  * Any width, stride and alignment (of whole elements) is taken; rows that all start at 16-byte
  * boundaries (codes: 8) go faster.
  * Errors: INVALID_ARG, OVERFLOW (2^31 blocks or more), HIP.
