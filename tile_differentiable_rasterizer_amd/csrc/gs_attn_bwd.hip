@@ -422,30 +422,44 @@ __global__ __launch_bounds__(256, (kWavesOf<T, DP>)) void k_attn_bwd_q(AttnArgs 
     }
 }
 
-// Sums of the splits, in order: dq (KV false, over rows) or dk and dv (KV true, over keys; the
-// second half of the grid's y axis is dv).
-template <typename T, int DP, bool KV>
+// Sums of the splits, in a fixed order: dq (KV false, over rows) or dk and dv (KV true, over keys; the
+// second half of the grid's y axis is dv).  One workgroup for VECS vectors; a vector's splits are shared
+// out over its groups of DP / 4 lanes (four elements a lane), which meet in LDS: few vectors leave the
+// splits' loads as the only parallelism (4 rows of 96, 130 splits: 35 us by one group, 5 by ten; 208 keys
+// of 128, 32 splits: 11 and 6).
+template <typename T, int DP, bool KV, int VECS>
 __global__ __launch_bounds__(256) void k_attn_bwd_join(AttnArgs a) {
-  constexpr int kPer = 256 / (DP / 4);
+  constexpr int kLanes = DP / 4, kGroups = 256 / kLanes / VECS;
+  __shared__ f32x4 sum[kGroups > 1 ? VECS : 1][kGroups][kLanes];
   const int len = KV ? a.k_len : a.rows;
   const int64_t n = (int64_t)a.batch * a.kv_heads * len, step = KV ? 2 * n : n;
-  const int64_t at = (int64_t)blockIdx.x * kPer + threadIdx.x / (DP / 4);
-  const int d = (threadIdx.x % (DP / 4)) * 4;
-  if ((int)threadIdx.x >= kPer * (DP / 4) || at >= n || d >= a.d) return;
-  const float* p = a.part + ((KV && blockIdx.y ? n : 0) + at) * DP + d;
-  float x[4] = {};
-  for (int s = 0; s < a.splits; ++s) {
-    const f32x4 v = *reinterpret_cast<const f32x4*>(p + s * step * DP);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] += v[e];
+  const int g = threadIdx.x / kLanes, part = g / VECS, d = (threadIdx.x % kLanes) * 4;
+  const int64_t at = (int64_t)blockIdx.x * VECS + g % VECS;
+  const bool here = part < kGroups && at < n;
+  f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (here) {
+    const float* p = a.part + ((KV && blockIdx.y ? n : 0) + at) * DP + d;
+#pragma unroll 4
+    for (int s = part; s < a.splits; s += kGroups) x += *reinterpret_cast<const f32x4*>(p + s * step * DP);
   }
+  if constexpr (kGroups > 1) {
+    if (here) sum[g % VECS][part][d / 4] = x;
+    __syncthreads();
+    if (!here || part != 0) return;
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) x += sum[g][i][d / 4];
+  }
+  if (!here || d >= a.d) return;
+  float y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = x[e];
   const int bh = (int)(at / len), j = (int)(at - (int64_t)bh * len);
   const int b = bh / a.kv_heads, hk = bh - b * a.kv_heads;
   if constexpr (KV) {
-    store_elems<4>(head_ptr<T>(blockIdx.y ? a.dv : a.dk, b, j, hk) + d, x);
+    store_elems<4>(head_ptr<T>(blockIdx.y ? a.dv : a.dk, b, j, hk) + d, y);
   } else {
     const int i = j / a.group;
-    store_elems<4>(head_ptr<T>(a.dq, b, i, hk * a.group + j - i * a.group) + d, x);
+    store_elems<4>(head_ptr<T>(a.dq, b, i, hk * a.group + j - i * a.group) + d, y);
   }
 }
 
@@ -464,20 +478,28 @@ int attn_bwd_kv_splits(const gs_cross_attn& p) {
 
 namespace {
 
+template <typename T, int DP, bool KV>
+void bwd_join(const AttnArgs& a, int64_t n, hipStream_t s) {
+  constexpr int kAll = 256 / (DP / 4);
+  if (n >= 4096)
+    k_attn_bwd_join<T, DP, KV, kAll><<<dim3((unsigned)((n + kAll - 1) / kAll), KV ? 2 : 1), 256, 0, s>>>(a);
+  else
+    k_attn_bwd_join<T, DP, KV, 1><<<dim3((unsigned)n, KV ? 2 : 1), 256, 0, s>>>(a);
+}
+
 template <typename T, int DP>
 hipError_t bwd_launch(AttnArgs a, int q_splits, int kv_splits, hipStream_t s) {
-  const int64_t nbh = (int64_t)a.batch * a.kv_heads, vecs = nbh * a.rows, per = 256 / (DP / 4);
+  const int64_t nbh = (int64_t)a.batch * a.kv_heads, vecs = nbh * a.rows;
   if (nbh == 0 || (a.rows == 0 && a.k_len == 0)) return hipSuccess;
   if (vecs) {
     a.splits = q_splits;
     k_attn_bwd_q<T, DP><<<(unsigned)(nbh * ((a.rows + 127) / 128) * q_splits), 256, 0, s>>>(a);
-    if (q_splits > 1) k_attn_bwd_join<T, DP, false><<<(unsigned)((vecs + per - 1) / per), 256, 0, s>>>(a);
+    if (q_splits > 1) bwd_join<T, DP, false>(a, vecs, s);
   }
   if (nbh && a.k_len) {
     a.splits = kv_splits;
     k_attn_bwd_kv<T, DP><<<(unsigned)(nbh * ((a.k_len + 127) / 128) * kv_splits), 256, 0, s>>>(a);
-    if (kv_splits > 1)
-      k_attn_bwd_join<T, DP, true><<<dim3((unsigned)((nbh * a.k_len + per - 1) / per), 2), 256, 0, s>>>(a);
+    if (kv_splits > 1) bwd_join<T, DP, true>(a, nbh * a.k_len, s);
   }
   return hipGetLastError();
 }
