@@ -245,15 +245,15 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   float m = -INFINITY, l = 0.0f;
   float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (here) {
+    for (int s = part; s < a.splits; s += kGroups) m = fmaxf(m, a.part_ml[s * n + at].x);
+#pragma unroll 4
     for (int s = part; s < a.splits; s += kGroups) {
       const float2 w = a.part_ml[s * n + at];
-      if (w.x == -INFINITY) continue;  // nothing seen there: its sums are not written
       const float4 v = *reinterpret_cast<const float4*>(a.part + (s * n + at) * DP + d);
-      const float to = fmaxf(m, w.x);
-      const float keep = __builtin_amdgcn_exp2f(m - to), add = __builtin_amdgcn_exp2f(w.x - to);
-      m = to;
-      l = l * keep + w.y * add;
-      x = make_float4(fmaf(v.x, add, x.x * keep), fmaf(v.y, add, x.y * keep), fmaf(v.z, add, x.z * keep), fmaf(v.w, add, x.w * keep));
+      const bool seen = w.x != -INFINITY;  // else its sums are not written
+      const float add = seen ? __builtin_amdgcn_exp2f(w.x - m) : 0.0f;
+      l = fmaf(w.y, add, l);
+      x = make_float4(fmaf(seen ? v.x : 0.0f, add, x.x), fmaf(seen ? v.y : 0.0f, add, x.y), fmaf(seen ? v.z : 0.0f, add, x.z), fmaf(seen ? v.w : 0.0f, add, x.w));
     }
     sum[r][part][d / 4] = x;
     if (d == 0) ml[r][part] = make_float2(m, l);
