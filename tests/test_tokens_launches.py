@@ -1,0 +1,89 @@
+"""CPU-side checks of what the token operators launch: a small library that stands in for HIP's launch
+calls counts them, refuses a grid that HIP refuses, and fails a launch where a test asks for it.
+
+The stand-in is loaded before libgsraster in a process of its own, so that the library's launches
+reach it; no kernel runs."""
+import json
+import os
+import subprocess
+import sys
+
+import pytest
+
+from test_tokens_abi import LIB
+
+pytestmark = pytest.mark.skipif(not os.path.exists(LIB), reason="libgsraster.so not built")
+
+OK, OVERFLOW, HIP = 0, 3, 4
+
+# hipLaunchKernel takes grids of fewer than 2^32 work items an axis
+STAND_IN = """
+#include <stddef.h>
+#include <stdint.h>
+typedef struct { uint32_t x, y, z; } dim3;
+int fail_at = -1, launches = 0, last = 0;
+double workgroups[64];
+int hipLaunchKernel(const void* f, dim3 g, dim3 b, void** args, size_t lds, void* stream) {
+  int fits = (uint64_t)g.x * b.x >> 32 == 0 && (uint64_t)g.y * b.y >> 32 == 0 && g.x && g.y && g.z;
+  if (launches < 64) workgroups[launches] = fits ? (double)g.x * g.y * g.z : -1.0;
+  if (!fits || launches == fail_at) last = 9;
+  return launches++ == fail_at || !fits ? 9 : 0;
+}
+static dim3 grid, block;
+int __hipPushCallConfiguration(dim3 g, dim3 b, size_t lds, void* stream) { grid = g; block = b; return 0; }
+int __hipPopCallConfiguration(dim3* g, dim3* b, size_t* lds, void** stream) {
+  *g = grid; *b = block; *lds = 0; *stream = 0;
+  return 0;
+}
+int hipGetLastError(void) { int e = last; last = 0; return e; }
+"""
+
+CHILD = """
+import ctypes, json, sys
+stand_in = ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)
+sys.path[:0] = sys.argv[2:4]
+import test_tokens_abi as abi
+var = lambda name, t=ctypes.c_int: t.in_dll(stand_in, name)
+out = []
+for call, how, fail_at in json.loads(sys.argv[4]):
+    var("fail_at").value, var("launches").value, var("last").value = fail_at, 0, 0
+    status = getattr(abi, call)(**how)
+    n = var("launches").value
+    out.append((status, list(var("workgroups", ctypes.c_double * 64)[:n])))
+print(json.dumps(out))
+"""
+
+
+@pytest.fixture(scope="module")
+def launched(tmp_path_factory):
+    """calls [(function of test_tokens_abi, its arguments, the launch that fails or -1)] -> [(status, workgroups of each launch)]"""
+    where = tmp_path_factory.mktemp("stand_in")
+    (where / "hip.c").write_text(STAND_IN)
+    subprocess.run(["gcc", "-O1", "-fPIC", "-shared", "-o", str(where / "hip.so"), str(where / "hip.c")], check=True)
+
+    def run(calls):
+        tests = os.path.dirname(os.path.abspath(__file__))
+        r = subprocess.run([sys.executable, "-c", CHILD, str(where / "hip.so"), tests, os.path.dirname(tests), json.dumps(calls)],
+                           capture_output=True, text=True, timeout=300)
+        assert r.returncode == 0, r.stderr
+        return json.loads(r.stdout.strip().splitlines()[-1])
+
+    return run
+
+
+A = 1 << 20
+# rows with ranges of their own from 2^28 pairs on (ordered), and long axes that are split and joined
+ORDERED = dict(batch=2, q_len=4200, k_len=2100, q_heads=16, kv_heads=16, head_dim=32, ranges=A, ranges_batch_stride=4200, ranges_row_stride=1)
+SPLIT_KEYS, SPLIT_ROWS = dict(batch=1, q_len=4, k_len=9000), dict(batch=1, q_len=9000, k_len=4)
+CHAINS = [("attn_call", SPLIT_KEYS), ("attn_call", ORDERED), ("attn_call", dict(SPLIT_KEYS, bwd=True)), ("attn_call", dict(SPLIT_ROWS, bwd=True)),
+          ("attn_call", dict(ORDERED, bwd=True)), ("norm_call", dict(bwd=True))]
+
+
+@pytest.mark.parametrize("call, how", CHAINS, ids=str)
+def test_nothing_follows_a_failed_launch(launched, call, how):
+    """Kernels read what the ones before them leave (the rows' tiles, lengths, parts): after a launch that failed none is made."""
+    got = launched([(call, how, i) for i in range(-1, 5)])
+    status, every = got[0]
+    assert status == OK and len(every) >= 2
+    for i, (status, launches) in enumerate(got[1: len(every) + 1]):
+        assert status == HIP and len(launches) == i + 1, f"launch {i} fails, {len(launches)} are made"

@@ -368,6 +368,8 @@ int attn_order_items(const gs_cross_attn& p) {
 // space: two int32 for each of attn_order_items().
 hipError_t launch_attn_order(AttnArgs& a, int items, int32_t* space, hipStream_t s) {
   k_attn_lengths<<<(unsigned)((items + 3) / 4), 256, 0, s>>>(a, items, space);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;  // the order takes LDS addresses by the lengths
   k_attn_order<<<1, 1024, 0, s>>>(items, (a.k_len + kAttnKeys - 1) / kAttnKeys, space, space + items);
   a.order = space + items;
   return hipGetLastError();

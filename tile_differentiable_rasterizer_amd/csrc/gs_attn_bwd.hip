@@ -479,29 +479,35 @@ int attn_bwd_kv_splits(const gs_cross_attn& p) {
 namespace {
 
 template <typename T, int DP, bool KV>
-void bwd_join(const AttnArgs& a, int64_t n, hipStream_t s) {
+hipError_t bwd_join(const AttnArgs& a, int64_t n, hipStream_t s) {
   constexpr int kAll = 256 / (DP / 4);
   if (n >= 4096)
     k_attn_bwd_join<T, DP, KV, kAll><<<dim3((unsigned)((n + kAll - 1) / kAll), KV ? 2 : 1), 256, 0, s>>>(a);
   else
     k_attn_bwd_join<T, DP, KV, 1><<<dim3((unsigned)n, KV ? 2 : 1), 256, 0, s>>>(a);
+  return hipGetLastError();
 }
 
+// Each launch is checked before the next: the keys' kernel takes addresses by what the rows' kernel leaves.
 template <typename T, int DP>
 hipError_t bwd_launch(AttnArgs a, int q_splits, int kv_splits, hipStream_t s) {
   const int64_t nbh = (int64_t)a.batch * a.kv_heads, vecs = nbh * a.rows;
   if (nbh == 0 || (a.rows == 0 && a.k_len == 0)) return hipSuccess;
+  hipError_t e = hipSuccess;
   if (vecs) {
     a.splits = q_splits;
     k_attn_bwd_q<T, DP><<<(unsigned)(nbh * ((a.rows + 127) / 128) * q_splits), 256, 0, s>>>(a);
-    if (q_splits > 1) bwd_join<T, DP, false>(a, vecs, s);
+    e = hipGetLastError();
+    if (e == hipSuccess && q_splits > 1) e = bwd_join<T, DP, false>(a, vecs, s);
+    if (e != hipSuccess) return e;
   }
   if (nbh && a.k_len) {
     a.splits = kv_splits;
     k_attn_bwd_kv<T, DP><<<(unsigned)(nbh * ((a.k_len + 127) / 128) * kv_splits), 256, 0, s>>>(a);
-    if (kv_splits > 1) bwd_join<T, DP, true>(a, nbh * a.k_len, s);
+    e = hipGetLastError();
+    if (e == hipSuccess && kv_splits > 1) e = bwd_join<T, DP, true>(a, nbh * a.k_len, s);
   }
-  return hipGetLastError();
+  return e;
 }
 
 }  // namespace
