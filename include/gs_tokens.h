@@ -119,7 +119,8 @@ typedef struct gs_cross_attn {
  *  workspace   gs_cross_attn_fwd_workspace_bytes(a) bytes, 16-byte aligned (0 for many shapes:
  *              it holds the parts of a long key axis that is split over workgroups)
  * One query row for each sequence (a token at a time) is the same call with q_len 1.
- * Errors: INVALID_ARG, OVERFLOW (a length of 2^31 or more, or too many workgroups), WORKSPACE, HIP.
+ * Errors: INVALID_ARG, OVERFLOW (a length of 2^31 or more, or 2^24 blocks of 128 rows or more over all
+ * sequences and key heads; a key head has q_len * q_heads / kv_heads rows), WORKSPACE, HIP.
  */
 size_t gs_cross_attn_fwd_workspace_bytes(const gs_cross_attn* a);
 gs_status gs_cross_attn_fwd(const gs_cross_attn* a, gs_heads q, gs_heads k, gs_heads v, gs_heads out, float* lse,
@@ -133,7 +134,7 @@ gs_status gs_cross_attn_fwd(const gs_cross_attn* a, gs_heads q, gs_heads k, gs_h
  * (rows of every query head that shares the key head).  Everything is overwritten; rows that see
  * nothing and keys that no row sees get 0.
  *  workspace   gs_cross_attn_bwd_workspace_bytes(a) bytes, 16-byte aligned
- * Errors: as the forward call.
+ * Errors: as the forward call, and OVERFLOW for 2^24 blocks of 128 keys or more.
  */
 size_t gs_cross_attn_bwd_workspace_bytes(const gs_cross_attn* a);
 gs_status gs_cross_attn_bwd(const gs_cross_attn* a, gs_heads dout, gs_heads q, gs_heads k, gs_heads v, gs_heads out,

@@ -704,3 +704,22 @@ def test_errors_name_the_call():
         tokens.cross_attn_fwd(q, k, v.float())
     with pytest.raises(ValueError):
         tokens.cross_attn_fwd(q, k.transpose(2, 3), v.transpose(2, 3))
+
+
+def test_gate8_more_blocks_than_a_grid_axis_takes():
+    """2^27 rows and some, a block each: the grid is folded, and every row is worked on."""
+    rows, g = 2**27 + 5, gen(41)
+    t = torch.bfloat16
+    gate, up, dy = (torch.empty((rows, 1), dtype=t, device="cuda").normal_(generator=g) for _ in range(3))
+    y, codes, bounds = tokens.gate8_fwd(gate, up)
+    dg, du, again = tokens.gate8_bwd(dy, codes, bounds)
+    assert not codes.any()
+    for i, x in enumerate((gate, up)):  # a block of one unit is its own minimum and maximum
+        assert torch.equal(bounds[i, :, 0, 0], x[:, 0].float()) and torch.equal(bounds[i, :, 0, 1], x[:, 0].float())
+    assert torch.equal(y, again)
+    for part in torch.arange(rows, device="cuda").split(2**24):
+        part = slice(int(part[0]), int(part[-1]) + 1)
+        a, da = act_ref(gate[part], "silu")
+        d, u, e = dy[part].double(), up[part].double(), act_tol(gate[part], "silu")
+        for got, want, tol, what in ((dg, d * u * da, e * (d * u).abs(), "dgate"), (du, d * a, e * d.abs(), "dup"), (y, a * u, e * u.abs(), "y")):
+            close(got[part], want, tol + V * want.abs(), what)

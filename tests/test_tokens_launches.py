@@ -87,3 +87,36 @@ def test_nothing_follows_a_failed_launch(launched, call, how):
     assert status == OK and len(every) >= 2
     for i, (status, launches) in enumerate(got[1: len(every) + 1]):
         assert status == HIP and len(launches) == i + 1, f"launch {i} fails, {len(launches)} are made"
+
+
+@pytest.mark.parametrize("bwd", [False, True])
+def test_grids_of_the_gate(launched, bwd):
+    """Blocks up to 2^31 are taken, on grids that HIP takes, eight a workgroup; the strides are the width's."""
+    blocks = [(1 << 27) - 1, 1 << 27, (1 << 27) + 1, (1 << 30) + 12345, (1 << 31) - 1]
+    got = launched([("gate_call", dict(rows=n, width=8, stride=8, bwd=bwd), -1) for n in blocks])
+    for n, (status, launches) in zip(blocks, got):
+        assert status == OK and len(launches) == 1 and -(-n // 8) <= launches[0] < -(-n // 8) + 256, n
+    wide = launched([("gate_call", dict(rows=2, width=(1 << 30) * 256, stride=(1 << 30) * 256, bwd=bwd), -1),
+                     ("gate_call", dict(rows=1, width=(1 << 30) * 256 + 1, stride=0, bwd=bwd), -1)])
+    assert wide[0][0] == OVERFLOW and wide[1][0] == OK
+
+
+@pytest.mark.parametrize("bwd", [False, True])
+@pytest.mark.parametrize("how", [dict(batch=(1 << 24) - 1), dict(batch=1 << 20, q_heads=16, kv_heads=16), dict(batch=1 << 20, q_heads=8, kv_heads=8, q_len=129),
+                                 dict(batch=1 << 20, q_heads=32, kv_heads=8, k_len=129), dict(batch=1 << 30), dict(batch=1, q_len=(1 << 31) - 129, k_len=1)], ids=str)
+def test_grids_of_the_attention(launched, how, bwd):
+    """2^24 blocks of 128 rows (back: or keys) are one more than a grid of 256 threads each takes: refused before any launch."""
+    how = {**dict(q_len=1, k_len=1, q_heads=1, kv_heads=1, head_dim=8), **how}
+    rows = how["q_len"] * how["q_heads"] // how["kv_heads"]
+    blocks = how["batch"] * how["kv_heads"] * -(-max(rows, how["k_len"] if bwd else 0) // 128)
+    [(status, launches)] = launched([("attn_call", dict(how, bwd=bwd), -1)])
+    if blocks < 1 << 24:
+        assert status == OK and launches and min(launches) > 0
+    else:
+        assert status == OVERFLOW and not launches
+
+
+def test_grids_of_the_norm(launched):
+    how = dict(batch=1, q_len=(1 << 31) - 1, k_len=(1 << 31) - 1, q_heads=1, k_heads=1, head_dim=256, n_pos=5)
+    for status, launches in launched([("norm_call", how, -1), ("norm_call", dict(how, bwd=True), -1)]):
+        assert status == OK and min(launches) > 0

@@ -122,12 +122,17 @@ __device__ __forceinline__ void gate_encode(const float (&x)[8], int n, uint8_t*
   if ((__lane_id() & 31) == 0) *bounds = make_float2(lo, hi);
 }
 
+// The half wavefront's block (large grids have a second axis: gate_grid).
+__device__ __forceinline__ uint32_t gate_item() {
+  return (blockIdx.y * gridDim.x + blockIdx.x) * 8 + threadIdx.x / 32;
+}
+
 template <typename T, int ACT, bool VEC>
 __global__ __launch_bounds__(256) void k_gate8_fwd(uint32_t items, uint32_t blocks, int64_t rows, int64_t width,
                                                    const T* __restrict__ gate, int64_t gs, const T* __restrict__ up,
                                                    int64_t us, T* __restrict__ y, int64_t ys,
                                                    uint8_t* __restrict__ codes, float2* __restrict__ bounds) {
-  const uint32_t item = blockIdx.x * 8 + threadIdx.x / 32;
+  const uint32_t item = gate_item();
   if (item >= items) return;  // uniform over half wavefronts, which do not exchange with each other
   const uint32_t row = item / blocks, blk = item - row * blocks;
   const int64_t u0 = (int64_t)blk * kGateBlock + (threadIdx.x & 31) * kGateUnits;
@@ -169,7 +174,7 @@ __global__ __launch_bounds__(256) void k_gate8_bwd(uint32_t items, uint32_t bloc
                                                    const uint8_t* __restrict__ codes, const float2* __restrict__ bounds,
                                                    T* __restrict__ dgate, int64_t gs, T* __restrict__ dup, int64_t us,
                                                    T* __restrict__ y, int64_t ys) {
-  const uint32_t item = blockIdx.x * 8 + threadIdx.x / 32;
+  const uint32_t item = gate_item();
   if (item >= items) return;
   const uint32_t row = item / blocks, blk = item - row * blocks;
   const int64_t u0 = (int64_t)blk * kGateBlock + (threadIdx.x & 31) * kGateUnits;
@@ -194,8 +199,15 @@ __global__ __launch_bounds__(256) void k_gate8_bwd(uint32_t items, uint32_t bloc
 }
 
 namespace {
+// Workgroups of eight blocks each, as few rows of them as a grid's axis (fewer than 2^32 work items) allows.
+dim3 gate_grid(uint32_t items) {
+  constexpr uint32_t kMost = 1u << 23;
+  const uint32_t groups = (items + 7) / 8, rows = (groups + kMost - 1) / kMost;
+  return dim3((groups + rows - 1) / rows, rows);
+}
+
 template <typename T, int ACT>
-void gate_fwd(bool vec, unsigned groups, uint32_t items, uint32_t blocks, int64_t rows, int64_t width,
+void gate_fwd(bool vec, dim3 groups, uint32_t items, uint32_t blocks, int64_t rows, int64_t width,
               const void* gate, int64_t gs, const void* up, int64_t us, void* y, int64_t ys, uint8_t* codes,
               float* bounds, hipStream_t s) {
   const T *g = static_cast<const T*>(gate), *u = static_cast<const T*>(up);
@@ -206,7 +218,7 @@ void gate_fwd(bool vec, unsigned groups, uint32_t items, uint32_t blocks, int64_
     k_gate8_fwd<T, ACT, false><<<groups, 256, 0, s>>>(items, blocks, rows, width, g, gs, u, us, static_cast<T*>(y), ys, codes, b);
 }
 template <typename T, int ACT>
-void gate_bwd(bool vec, unsigned groups, uint32_t items, uint32_t blocks, int64_t rows, int64_t width, const void* dy,
+void gate_bwd(bool vec, dim3 groups, uint32_t items, uint32_t blocks, int64_t rows, int64_t width, const void* dy,
               int64_t dys, const uint8_t* codes, const float* bounds, void* dgate, int64_t gs, void* dup, int64_t us,
               void* y, int64_t ys, hipStream_t s) {
   const T* d = static_cast<const T*>(dy);
@@ -224,7 +236,7 @@ hipError_t launch_gate8_fwd(bool vec, int64_t rows, int64_t width, int act, int 
                             const void* up, int64_t us, void* y, int64_t ys, uint8_t* codes, float* bounds,
                             hipStream_t s) {
   const uint32_t blocks = (uint32_t)((width + kGateBlock - 1) / kGateBlock), items = (uint32_t)(rows * blocks);
-  const unsigned groups = (items + 7) / 8;
+  const dim3 groups = gate_grid(items);
   auto f = type == GS_BF16 ? (act == GS_ACT_SILU ? gate_fwd<__bf16, GS_ACT_SILU> : gate_fwd<__bf16, GS_ACT_GELU>)
                            : (act == GS_ACT_SILU ? gate_fwd<float, GS_ACT_SILU> : gate_fwd<float, GS_ACT_GELU>);
   f(vec, groups, items, blocks, rows, width, gate, gs, up, us, y, ys, codes, bounds, s);
@@ -235,7 +247,7 @@ hipError_t launch_gate8_bwd(bool vec, int64_t rows, int64_t width, int act, int 
                             const uint8_t* codes, const float* bounds, void* dgate, int64_t gs, void* dup, int64_t us,
                             void* y, int64_t ys, hipStream_t s) {
   const uint32_t blocks = (uint32_t)((width + kGateBlock - 1) / kGateBlock), items = (uint32_t)(rows * blocks);
-  const unsigned groups = (items + 7) / 8;
+  const dim3 groups = gate_grid(items);
   auto f = type == GS_BF16 ? (act == GS_ACT_SILU ? gate_bwd<__bf16, GS_ACT_SILU> : gate_bwd<__bf16, GS_ACT_GELU>)
                            : (act == GS_ACT_SILU ? gate_bwd<float, GS_ACT_SILU> : gate_bwd<float, GS_ACT_GELU>);
   f(vec, groups, items, blocks, rows, width, dy, dys, codes, bounds, dgate, gs, dup, us, y, ys, s);

@@ -30,7 +30,8 @@ using namespace gs;
 
 namespace {
 
-constexpr int64_t kMost = (int64_t)1 << 31;  // lengths, vectors, workgroups: counted in 31 bits
+constexpr int64_t kMost = (int64_t)1 << 31;    // lengths, vectors, blocks of codes: counted in 31 bits
+constexpr int64_t kGroups = (int64_t)1 << 24;  // workgroups of 256 threads: a grid has fewer than 2^32 work items
 
 bool on(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 int64_t size_of(int type) { return type == GS_BF16 ? 2 : 4; }
@@ -95,7 +96,7 @@ gs_status norm_call(const gs_norm_rotate* p, gs_heads dout_q, gs_heads dout_k, g
                                       pos_k, yq, yk, dwq, dwk, ws, static_cast<hipStream_t>(stream)));
 }
 
-gs_status attn_shape(const gs_cross_attn* p) {
+gs_status attn_shape(const gs_cross_attn* p, bool bwd) {
   if (!p) return GS_ERR_INVALID_ARG;
   if (p->batch < 0 || p->q_len < 0 || p->k_len < 0 || p->q_heads < 1 || p->kv_heads < 1 || p->q_heads % p->kv_heads)
     return GS_ERR_INVALID_ARG;
@@ -105,12 +106,12 @@ gs_status attn_shape(const gs_cross_attn* p) {
   if (p->ranges && (!on(p->ranges, 4) || p->ranges_batch_stride < 0 || p->ranges_row_stride < 0)) return GS_ERR_INVALID_ARG;
   if (p->key_mask && p->key_mask_batch_stride < 0) return GS_ERR_INVALID_ARG;
   const int64_t rows = times(p->q_len, p->q_heads / p->kv_heads);
-  // workgroups: 128 rows or keys each, in at most 512 parts
   const int64_t all = times(p->batch, p->kv_heads);
   if (rows < 0 || rows >= kMost - 128 || p->k_len >= kMost - 128 || all < 0 || all >= kMost) return GS_ERR_OVERFLOW;
   const int64_t vq = times(all, rows), vk = times(all, p->k_len);
-  const int64_t wide = times(all, ((rows > p->k_len ? rows : p->k_len) + 127) / 128);
-  if (vq < 0 || vk < 0 || wide < 0 || wide >= kMost || vq / 2 >= kMost || vk / 2 >= kMost) return GS_ERR_OVERFLOW;
+  // workgroups: 128 rows, and 128 keys for the gradients (in parts only where there are few)
+  const int64_t wide = times(all, ((bwd && p->k_len > rows ? p->k_len : rows) + 127) / 128);
+  if (vq < 0 || vk < 0 || wide < 0 || wide >= kGroups || vq / 2 >= kMost || vk / 2 >= kMost) return GS_ERR_OVERFLOW;
   return GS_OK;
 }
 
@@ -175,7 +176,7 @@ gs_status gs_norm_rotate_bwd(const gs_norm_rotate* shape, gs_heads dout_q, gs_he
 }
 
 size_t gs_cross_attn_fwd_workspace_bytes(const gs_cross_attn* p) {
-  if (attn_shape(p) != GS_OK) return 0;
+  if (attn_shape(p, false) != GS_OK) return 0;
   const int splits = attn_fwd_splits(*p);
   if (splits == 1) return order_bytes(*p);
   return order_bytes(*p) + part_bytes(*p, splits, attn_rows(*p)) + round16((size_t)splits * attn_rows(*p) * sizeof(float2));
@@ -183,7 +184,7 @@ size_t gs_cross_attn_fwd_workspace_bytes(const gs_cross_attn* p) {
 
 gs_status gs_cross_attn_fwd(const gs_cross_attn* p, gs_heads q, gs_heads k, gs_heads v, gs_heads out, float* lse,
                             void* workspace, size_t workspace_bytes, void* stream) {
-  const gs_status st = attn_shape(p);
+  const gs_status st = attn_shape(p, false);
   if (st != GS_OK) return st;
   if (!heads_ok(&q, p->batch, p->q_len, p->q_heads, p->type) || !heads_ok(&out, p->batch, p->q_len, p->q_heads, p->type) ||
       !heads_ok(&k, p->batch, p->k_len, p->kv_heads, p->type) || !heads_ok(&v, p->batch, p->k_len, p->kv_heads, p->type) ||
@@ -210,7 +211,7 @@ gs_status gs_cross_attn_fwd(const gs_cross_attn* p, gs_heads q, gs_heads k, gs_h
 }
 
 size_t gs_cross_attn_bwd_workspace_bytes(const gs_cross_attn* p) {
-  if (attn_shape(p) != GS_OK) return 0;
+  if (attn_shape(p, true) != GS_OK) return 0;
   const size_t q = part_bytes(*p, attn_bwd_q_splits(*p), attn_rows(*p));
   const size_t kv = part_bytes(*p, attn_bwd_kv_splits(*p), 2 * p->batch * p->kv_heads * p->k_len);
   return order_bytes(*p) + attn_stat_bytes(*p) + attn_tile_bytes(*p) + (q > kv ? q : kv);
@@ -219,7 +220,7 @@ size_t gs_cross_attn_bwd_workspace_bytes(const gs_cross_attn* p) {
 gs_status gs_cross_attn_bwd(const gs_cross_attn* p, gs_heads dout, gs_heads q, gs_heads k, gs_heads v, gs_heads out,
                             const float* lse, gs_heads dq, gs_heads dk, gs_heads dv, void* workspace,
                             size_t workspace_bytes, void* stream) {
-  const gs_status st = attn_shape(p);
+  const gs_status st = attn_shape(p, true);
   if (st != GS_OK) return st;
   for (gs_heads* x : {&dout, &q, &out, &dq})
     if (!heads_ok(x, p->batch, p->q_len, p->q_heads, p->type)) return GS_ERR_INVALID_ARG;
