@@ -1,0 +1,106 @@
+"""CPU-side checks of the differentiable functions around the token operators and the rasteriser: the calls that
+need the GPU are replaced by plain torch, so that what is tested is the way gradients take."""
+import os
+import types
+
+import pytest
+import torch
+
+from test_tokens_abi import LIB
+
+pytestmark = pytest.mark.skipif(not os.path.exists(LIB), reason="libgsraster.so not built")
+
+
+@pytest.fixture
+def t(monkeypatch):
+    """tokens with cubes in the place of the operators: y = x^3, dx = 3 x^2 dy, whatever the shape."""
+    from tile_differentiable_rasterizer_amd import tokens
+
+    plain = torch.no_grad()  # the C calls are not recorded
+    cube, slope = plain(lambda x: x**3), plain(lambda x, d: 3 * x * x * d)
+
+    def gate_fwd(gate, up, act):
+        gate_fwd.last = (gate.clone(), up.clone())
+        return gate**3 * up, torch.zeros(2, *gate.shape, dtype=torch.uint8), torch.zeros(1)
+
+    @plain
+    def gate_bwd(dy, codes, bounds, act, with_y, dgate, dup):
+        gate, up = gate_fwd.last
+        dgate.copy_(3 * gate**2 * up * dy)
+        dup.copy_(gate**3 * dy)
+
+    monkeypatch.setattr(tokens, "norm_rotate_fwd", lambda q, k, *a: (cube(q), cube(k)))
+    monkeypatch.setattr(tokens, "norm_rotate_bwd", lambda dq, dk, q, k, wq, wk, *a: (slope(q, dq), slope(k, dk), torch.zeros_like(wq), torch.zeros_like(wk)))
+    monkeypatch.setattr(tokens, "cross_attn_fwd", lambda q, k, v, *a: (cube(q) + cube(k) + cube(v), q.sum()))
+    monkeypatch.setattr(tokens, "cross_attn_bwd", lambda d, q, k, v, *a: (slope(q, d), slope(k, d), slope(v, d)))
+    monkeypatch.setattr(tokens, "gate8_fwd", gate_fwd)
+    monkeypatch.setattr(tokens, "gate8_bwd", gate_bwd)
+    return tokens
+
+
+class Frames:
+    """In the place of raster.Rasterizer: an image of the cubes."""
+
+    def __init__(self, means, *rest, **more):
+        self.means = means
+
+    def forward(self, cam, with_keys=True):
+        return dict(image=self.means**3, grads=None)
+
+    @torch.no_grad()
+    def backward(self, fwd, dimage):
+        zero = torch.zeros(4, 6)
+        return dict(dmeans=3 * self.means**2 * dimage, dscales=zero, dquats=zero, grad_screen=zero, dsh=zero)
+
+
+def function(t, monkeypatch, which):
+    """(an operator of one tensor, the tensor)"""
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(1, 4, 2, 8, generator=g).requires_grad_()
+    w = torch.ones(8)
+    if which == "norm_rotate":
+        return (lambda x: t.norm_rotate(x, x, w, w, None, None)[1]), x
+    if which == "cross_attention":
+        return (lambda x: t.cross_attention(x, x, x)), x
+    if which == "gated8":
+        return (lambda x: t.gated8(x)), x
+    from tile_differentiable_rasterizer_amd import token_decoder
+
+    monkeypatch.setattr(token_decoder.raster, "Rasterizer", Frames)
+    rest = [torch.zeros(4, 6) for _ in range(4)]
+    return (lambda x: token_decoder.Render.apply(x, *rest, types.SimpleNamespace())), torch.randn(4, 6, generator=g).requires_grad_()
+
+
+FUNCTIONS = ["norm_rotate", "cross_attention", "gated8", "render"]
+
+
+@pytest.mark.parametrize("squared", [False, True])
+@pytest.mark.parametrize("way", ["grad", "backward"])
+@pytest.mark.parametrize("which", FUNCTIONS)
+def test_second_derivatives_are_refused(t, monkeypatch, which, way, squared):
+    """The backward passes are not differentiable: a gradient's gradient is an error, on whichever path it is asked for and
+    with whatever beside it, and never one without the operator's part.  First derivatives come with create_graph too."""
+    f, x = function(t, monkeypatch, which)
+
+    def loss():
+        y = f(x)
+        return (y * y if squared else y).sum() + (x * x).sum()
+
+    plain, = torch.autograd.grad(loss(), x)
+    first, = torch.autograd.grad(loss(), x, create_graph=True)
+    assert torch.equal(first.detach(), plain)
+    with pytest.raises(RuntimeError, match="differentiated once"):
+        if way == "grad":
+            torch.autograd.grad((first * first).sum(), x)
+        else:
+            (first * first).sum().backward()
+
+
+@pytest.mark.parametrize("which", FUNCTIONS)
+def test_second_derivatives_of_the_rest_are_not_refused(t, monkeypatch, which):
+    """What does not lead through an operator's gradient has its second derivative."""
+    f, x = function(t, monkeypatch, which)
+    z = torch.ones(3, requires_grad=True)
+    gx, gz = torch.autograd.grad(f(x).sum() + (z**3).sum(), (x, z), create_graph=True)
+    second, = torch.autograd.grad(gz.sum(), z)
+    assert torch.equal(second, 6 * torch.ones(3)) and gx.shape == x.shape

@@ -31,9 +31,11 @@ class Render(torch.autograd.Function):
         rz = raster.Rasterizer(means, scales, quats, opacities, sh, 0, pair_capacity=16 * means.shape[0])
         fwd = rz.forward(cam, with_keys=False)
         ctx.rz, ctx.fwd = rz, fwd
+        ctx.save_for_backward(means, scales, quats, opacities, sh)
         return fwd["image"]
 
     @staticmethod
+    @tokens.once
     def backward(ctx, dimage):
         g = ctx.rz.backward(ctx.fwd, dimage.contiguous())
         return g["dmeans"], g["dscales"], g["dquats"], g["grad_screen"][:, 5], g["dsh"], None

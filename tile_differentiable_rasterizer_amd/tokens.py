@@ -12,11 +12,13 @@ everything else by the C calls (raster.GsError).  Work goes to the current strea
 (a workspace is given back to torch when the call returns, in stream order).
 
 ``norm_rotate``, ``cross_attention`` and ``gated8`` are the same operators as differentiable
-torch functions.
+torch functions.  Their gradients come from C calls that torch does not record: second
+derivatives through them are an error (``once``).
 """
 from __future__ import annotations
 
 import ctypes as C
+import functools
 
 import torch
 
@@ -338,6 +340,36 @@ def _on_vectors(t):
     return t if dense else t.contiguous()
 
 
+class _Linked(torch.autograd.Function):
+    """The first n tensors as they are, with every other one as a source that cannot be differentiated for."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tensors[:n]
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the gradients of the library's calls can be differentiated once only")
+
+
+def once(backward):
+    """Marks a backward pass whose gradients torch did not record.  Where they are to be differentiated again
+    (create_graph), they are linked to all that they come from (the outputs' gradients and what forward saved), so
+    that a second derivative on any such path is an error and not a sum without this part."""
+
+    @functools.wraps(backward)
+    def run(ctx, *douts):
+        if not torch.is_grad_enabled():
+            return backward(ctx, *douts)
+        with torch.no_grad():
+            grads = backward(ctx, *douts)
+        made = [g for g in grads if g is not None]
+        linked = iter(_Linked.apply(len(made), *made, *douts, *ctx.saved_tensors))
+        return tuple(None if g is None else next(linked) for g in grads)
+
+    return run
+
+
 class _NormRotate(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, wq, wk, cos, sin, pos_q, pos_k, eps, pairs):
@@ -346,6 +378,7 @@ class _NormRotate(torch.autograd.Function):
         return norm_rotate_fwd(q, k, wq, wk, cos, sin, pos_q, pos_k, eps, pairs)
 
     @staticmethod
+    @once
     def backward(ctx, dq, dk):
         return (*norm_rotate_bwd(_on_vectors(dq), _on_vectors(dk), *ctx.saved_tensors, *ctx.more), *([None] * 6))
 
@@ -364,6 +397,7 @@ class _CrossAttention(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once
     def backward(ctx, dout):
         q, k, v, out, lse, ranges, key_mask = ctx.saved_tensors
         return (*cross_attn_bwd(_on_vectors(dout), q, k, v, out, lse, ctx.scale, ranges, key_mask), None, None, None)
@@ -380,13 +414,15 @@ class _Gated8(torch.autograd.Function):
         width = h.shape[-1] // 2
         flat = h.reshape(-1, 2 * width)
         y, codes, bounds = gate8_fwd(flat[:, :width], flat[:, width:], act)
-        ctx.save_for_backward(codes, bounds)
+        link = h.new_empty(0)  # h's place in the graph, without h
+        ctx.save_for_backward(codes, bounds, link)
         ctx.act, ctx.shape = act, h.shape
-        return y.view(*h.shape[:-1], width)
+        return y.view(*h.shape[:-1], width), link
 
     @staticmethod
-    def backward(ctx, dy):
-        codes, bounds = ctx.saved_tensors
+    @once
+    def backward(ctx, dy, _):
+        codes, bounds, _ = ctx.saved_tensors
         width = codes.shape[2]
         dh = torch.empty((codes.shape[1], 2 * width), dtype=dy.dtype, device=dy.device)
         dy = dy.reshape(-1, width)
@@ -398,4 +434,4 @@ class _Gated8(torch.autograd.Function):
 def gated8(h, act: str = "silu"):
     """act(gate) * up of a projection's output h [..., 2 * width] = (gate | up), with the gradient for h from 8-bit
     codes: between the passes only the codes and their bounds are kept, a quarter (float32) or half (bfloat16) of h."""
-    return _Gated8.apply(h, act)
+    return _Gated8.apply(h, act)[0]
