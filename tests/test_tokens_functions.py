@@ -104,3 +104,32 @@ def test_second_derivatives_of_the_rest_are_not_refused(t, monkeypatch, which):
     gx, gz = torch.autograd.grad(f(x).sum() + (z**3).sum(), (x, z), create_graph=True)
     second, = torch.autograd.grad(gz.sum(), z)
     assert torch.equal(second, 6 * torch.ones(3)) and gx.shape == x.shape
+
+
+def test_a_frame_is_let_go_with_its_graph(t, monkeypatch):
+    """Render keeps its rasteriser and what the frame made until the graph goes, with no cycle for the collector to find."""
+    import gc
+    import weakref
+
+    f, x = function(t, monkeypatch, "render")
+    made = []
+
+    class Kept(Frames):
+        def __init__(self, *a, **k):
+            super().__init__(*a, **k)
+            made.append(weakref.ref(self))
+
+    from tile_differentiable_rasterizer_amd import token_decoder
+
+    monkeypatch.setattr(token_decoder.raster, "Rasterizer", Kept)
+    gc.disable()
+    try:
+        y = f(x)
+        (y * y).sum().backward()
+        del y
+        assert made[0]() is None
+        y = f(x)  # and where no backward pass comes
+        del y
+        assert made[1]() is None
+    finally:
+        gc.enable()

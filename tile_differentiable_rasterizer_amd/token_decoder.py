@@ -30,9 +30,10 @@ class Render(torch.autograd.Function):
     def forward(ctx, means, scales, quats, opacities, sh, cam):
         rz = raster.Rasterizer(means, scales, quats, opacities, sh, 0, pair_capacity=16 * means.shape[0])
         fwd = rz.forward(cam, with_keys=False)
+        image = fwd.pop("image")  # an output kept here would keep this frame's buffers from being let go
         ctx.rz, ctx.fwd = rz, fwd
         ctx.save_for_backward(means, scales, quats, opacities, sh)
-        return fwd["image"]
+        return image
 
     @staticmethod
     @tokens.once
