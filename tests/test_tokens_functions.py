@@ -133,3 +133,14 @@ def test_a_frame_is_let_go_with_its_graph(t, monkeypatch):
         assert made[1]() is None
     finally:
         gc.enable()
+
+
+def test_a_frame_whose_inputs_change_is_refused(t, monkeypatch):
+    """The backward pass reads the inputs again: changed in place between the passes they would give another frame's gradients."""
+    f, x = function(t, monkeypatch, "render")
+    z = x * 1.0
+    y = f(z)
+    with torch.no_grad():
+        z.add_(1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()

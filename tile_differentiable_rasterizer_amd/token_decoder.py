@@ -38,6 +38,7 @@ class Render(torch.autograd.Function):
     @staticmethod
     @tokens.once
     def backward(ctx, dimage):
+        ctx.saved_tensors  # read by the rasteriser again: an error if they were changed since
         g = ctx.rz.backward(ctx.fwd, dimage.contiguous())
         return g["dmeans"], g["dscales"], g["dquats"], g["grad_screen"][:, 5], g["dsh"], None
 
