@@ -723,3 +723,27 @@ def test_gate8_more_blocks_than_a_grid_axis_takes():
         d, u, e = dy[part].double(), up[part].double(), act_tol(gate[part], "silu")
         for got, want, tol, what in ((dg, d * u * da, e * (d * u).abs(), "dgate"), (du, d * a, e * d.abs(), "dup"), (y, a * u, e * u.abs(), "y")):
             close(got[part], want, tol + V * want.abs(), what)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_functions_take_gradients_off_their_boundaries(t):
+    """The gradient of a part of a cat starts at an odd element: the same results as from an aligned one."""
+    q, k, v = (x.requires_grad_() for x in qkv(t, 2, 20, 50, 4, 2, 64))
+    w, cs = torch.ones(64, device="cuda").requires_grad_(), torch.ones(50, 32, device="cuda")
+    first = torch.zeros(1, device="cuda", dtype=q.dtype)
+
+    def parts(*xs):
+        """Each tensor's gradient is a part of a larger one, from its second element on where `first` comes before it."""
+        return sum((torch.cat([first, x.flatten()])[1:] * x.detach().flatten().flip(0)).sum() for x in xs)
+
+    def grads(loss):
+        return torch.autograd.grad(loss, (q, k, v, w), allow_unused=True)
+
+    a, b = tokens.norm_rotate(q, k, w, w, cs, cs)
+    out = tokens.cross_attention(q, k, v)
+    got, want = grads(parts(a, b)), grads(sum((x.flatten() * x.detach().flatten().flip(0)).sum() for x in tokens.norm_rotate(q, k, w, w, cs, cs)))
+    assert all(torch.equal(x, y) for x, y in zip(got, want) if x is not None) and got[3] is not None
+    got = grads(parts(out))
+    out = tokens.cross_attention(q, k, v)
+    want = grads((out.flatten() * out.detach().flatten().flip(0)).sum())
+    assert all(torch.equal(x, y) for x, y in zip(got[:3], want[:3]))

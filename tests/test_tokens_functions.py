@@ -144,3 +144,20 @@ def test_a_frame_whose_inputs_change_is_refused(t, monkeypatch):
         z.add_(1.0)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.sum().backward()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradients_reach_the_calls_on_their_boundaries(dtype):
+    """A gradient that is dense but starts off a 16-byte boundary (one of several parts of a cat, say) is copied."""
+    from tile_differentiable_rasterizer_amd import tokens
+
+    whole = torch.arange(513.0).to(dtype)
+    off = whole[1:].view(1, 2, 4, 64)
+    assert off.is_contiguous() and off.data_ptr() % 16
+    got = tokens._on_vectors(off)
+    assert got.data_ptr() % 16 == 0 and got.is_contiguous() and torch.equal(got, off)
+    for taken in (whole[:512].view(1, 2, 4, 64), whole[:512].view(1, 4, 2, 64).transpose(1, 2), whole[:64].expand(1, 2, 4, 64)):
+        assert tokens._on_vectors(taken) is taken
+    for copied in (whole[:512].view(1, 2, 64, 4).transpose(2, 3), torch.zeros(1, 2, 4, 65, dtype=dtype)[..., 1:], torch.zeros((), dtype=dtype).expand(1, 2, 4, 64)):
+        got = tokens._on_vectors(copied)
+        assert got.is_contiguous() and got.data_ptr() % 16 == 0 and torch.equal(got, copied)

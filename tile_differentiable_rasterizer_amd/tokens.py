@@ -334,10 +334,10 @@ def gate8_bwd(dy, codes, bounds, act: str = "silu", with_y: bool = True, dgate=N
 
 
 def _on_vectors(t):
-    """t itself where the C calls take it as it is, a dense copy where they do not (an expanded gradient, say)."""
+    """t itself where the C calls take it as it is, a dense copy where they do not (an expanded gradient, or one that starts off 16 bytes)."""
     each = 16 // t.element_size()
     dense = t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and all(s % each == 0 or n == 1 for s, n in zip(t.stride()[:-1], t.shape))
-    return t if dense else t.contiguous()
+    return t if dense else t.clone(memory_format=torch.contiguous_format)  # (contiguous() keeps one that is only off its boundary)
 
 
 class _Linked(torch.autograd.Function):
