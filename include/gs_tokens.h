@@ -90,7 +90,8 @@ gs_status gs_norm_rotate_bwd(const gs_norm_rotate* shape, gs_heads dout_q, gs_he
 
 /* Shape and masks of gs_cross_attn_*: q[batch][q_len][q_heads][head_dim], k and v
  * [batch][k_len][kv_heads][head_dim]; q_heads is a multiple of kv_heads, and query head h reads
- * key head h / (q_heads / kv_heads).  head_dim is a multiple of 8 up to 128.
+ * key head h / (q_heads / kv_heads).  head_dim is a multiple of 8 up to 128.  scale is finite, and so is scale *
+ * log2(e) in float32 (it is below 2.3e38); 0 and below are scales like the rest.
  *  ranges      int32 pairs [first, last): the keys that a query row may see, cut to [0, k_len);
  *              row (b, i) has the pair at ranges_batch_stride b + ranges_row_stride i (strides
  *              in pairs, 0 = the same for all).  NULL: every key.

@@ -747,3 +747,27 @@ def test_functions_take_gradients_off_their_boundaries(t):
     out = tokens.cross_attention(q, k, v)
     want = grads((out.flatten() * out.detach().flatten().flip(0)).sum())
     assert all(torch.equal(x, y) for x, y in zip(got[:3], want[:3]))
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("scale, std", [(0.0, 1e16), (-0.0, 1e15), (1e-33, 3e16), (-1e-33, 3e16), (3e-39, 1e18), (1e35, 1e-18)])
+def test_cross_attn_scales_for_large_and_small_vectors(t, scale, std):
+    """No scale is too small for some finite scores: 0 makes them all 0 whatever the vectors' size, others their own."""
+    q, k, v = qkv(t, 2, 40, 150, 4, 2, 64)
+    q, k = q * std, k * std
+    ranges = torch.tensor([[[0, 150]], [[20, 90]]], device="cuda", dtype=torch.int32)
+    mask = torch.rand(2, 150, generator=gen(4), device="cuda") < 0.7
+    attn_check(q, k, v, scale=scale, ranges=ranges, mask=mask)
+
+
+def test_cross_attn_scale_of_nothing_keeps_nan():
+    """0 times a NaN or an infinity is a NaN, in the rows that hold it or see it and in no others."""
+    for t in ("f32", "bf16"):
+        q, k, v = qkv(t, 2, 40, 100, 2, 2, 64)
+        q[0, 3, 1, 5], q[0, 7, 0, 0] = math.nan, math.inf
+        k[1, 50, 0, 9] = math.inf
+        bad = torch.zeros(2, 2, 40, dtype=torch.bool, device="cuda")
+        bad[0, 1, 3] = bad[0, 0, 7] = bad[1, 0] = True
+        out, lse = tokens.cross_attn_fwd(q, k, v, scale=0.0)
+        assert torch.equal(lse.isnan(), bad) and torch.equal(out.isnan().all(-1).transpose(1, 2), bad) and torch.equal(out.isnan().any(-1).transpose(1, 2), bad)
+        assert ((lse - math.log(100))[~bad].abs() < 1e-5).all()

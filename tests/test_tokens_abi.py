@@ -175,3 +175,12 @@ def test_binding_refuses_what_the_c_calls_cannot_see():
         t.gate8_fwd(torch.zeros(2, 8), torch.zeros(2, 8), act="relu")
     with pytest.raises(ValueError):
         t.gate8_fwd(torch.zeros(2, 8, dtype=torch.float16), torch.zeros(2, 8, dtype=torch.float16))
+
+
+@pytest.mark.parametrize("bwd", [False, True])
+def test_cross_attn_refuses_a_scale_past_its_exponent(bwd):
+    """The kernels work in base 2: scale * log2(e) has to be a float32."""
+    for scale in (3e38, -2.4e38):
+        assert attn_call(bwd=bwd, scale=scale) == BAD
+    for scale in (2.3e38, -2.3e38, 0.0, 1e-45):
+        assert attn_call(bwd=bwd, scale=scale, batch=0) == OK

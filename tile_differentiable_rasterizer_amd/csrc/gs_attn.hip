@@ -56,7 +56,7 @@ __global__ __launch_bounds__(256, (kWavesOf<T, DP>)) void k_attn_fwd(AttnArgs a)
 
   Frag<T> qf[DP / 16];
 #pragma unroll
-  for (int s = 0; s < DP / 16; ++s) qf[s] = frag_flip(frag_mem<T>(head_ptr<T>(a.q, b, i, h), a.d, s, live), a.flip);
+  for (int s = 0; s < DP / 16; ++s) qf[s] = scaled_frag(a, frag_mem<T>(head_ptr<T>(a.q, b, i, h), a.d, s, live));
   f32x16 o[DP / 32];
 #pragma unroll
   for (int t = 0; t < DP / 32; ++t) o[t] = (f32x16)0.0f;

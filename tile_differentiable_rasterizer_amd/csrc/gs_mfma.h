@@ -241,6 +241,19 @@ __device__ __forceinline__ Frag<T> frag_flip(Frag<T> f, uint32_t flip) {
   return x.f;
 }
 
+// The same with every element multiplied by 0.
+template <typename T>
+__device__ __forceinline__ Frag<T> frag_zeros(Frag<T> f) {
+  union {
+    Frag<T> f;
+    __bf16 x[sizeof(Frag<T>) / 2];
+  } x;
+  x.f = f;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(Frag<T>) / 2); ++i) x.x[i] = (__bf16)((float)x.x[i] * 0.0f);
+  return x.f;
+}
+
 // max and sum with the lane of the other half that holds the same column.
 __device__ __forceinline__ float pair_max(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);

@@ -102,7 +102,7 @@ gs_status attn_shape(const gs_cross_attn* p, bool bwd) {
     return GS_ERR_INVALID_ARG;
   if (p->head_dim < 8 || p->head_dim > 128 || p->head_dim % 8) return GS_ERR_INVALID_ARG;
   if (p->type != GS_BF16 && p->type != GS_F32) return GS_ERR_INVALID_ARG;
-  if (!isfinite(p->scale)) return GS_ERR_INVALID_ARG;
+  if (!isfinite(p->scale * kLog2e)) return GS_ERR_INVALID_ARG;
   if (p->ranges && (!on(p->ranges, 4) || p->ranges_batch_stride < 0 || p->ranges_row_stride < 0)) return GS_ERR_INVALID_ARG;
   if (p->key_mask && p->key_mask_batch_stride < 0) return GS_ERR_INVALID_ARG;
   const int64_t rows = times(p->q_len, p->q_heads / p->kv_heads);
@@ -125,9 +125,8 @@ AttnArgs attn_args(const gs_cross_attn& p) {
   a.d = p.head_dim;
   a.rows = (int32_t)(p.q_len * a.group);
   a.scale = p.scale;
-  // the kernels take the maximum before they scale, so the slope is positive; a scale of 0 becomes
-  // one that no float32 score can tell from it, and keeps -inf where a key is not seen
-  a.slope = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);
+  // the kernels take the maximum before they scale, so the slope is positive
+  a.slope = p.scale == 0.0f ? 1.0f : fabsf(p.scale) * kLog2e;
   a.flip = p.scale < 0.0f ? 0x80008000u : 0u;
   a.ranges = p.ranges;
   a.ranges_b = p.ranges_batch_stride;
