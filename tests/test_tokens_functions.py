@@ -161,3 +161,59 @@ def test_gradients_reach_the_calls_on_their_boundaries(dtype):
     for copied in (whole[:512].view(1, 2, 64, 4).transpose(2, 3), torch.zeros(1, 2, 4, 65, dtype=dtype)[..., 1:], torch.zeros((), dtype=dtype).expand(1, 2, 4, 64)):
         got = tokens._on_vectors(copied)
         assert got.is_contiguous() and got.data_ptr() % 16 == 0 and torch.equal(got, copied)
+
+
+class Other:
+    """A tensor of another GPU than the current one, and a stand-in for what torch and the library do there."""
+
+    shape, dtype = (1, 2, 4, 64), torch.bfloat16
+
+    def get_device(self):
+        return 1
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_calls_run_on_their_tensors_gpu(monkeypatch, current):
+    """The tensors' GPU is the current one while a call runs (a launch on a default stream goes to whichever that is), and
+    the call gets that GPU's current stream."""
+    import contextlib
+
+    from tile_differentiable_rasterizer_amd import tokens
+
+    at = [current]
+
+    @contextlib.contextmanager
+    def device(n):
+        at.append(n)
+        yield
+        at.pop()
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: at[-1], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda n: 70 + n, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    seen = []
+    status = types.SimpleNamespace(value=0)
+
+    def call(*args):
+        seen.append((at[-1], args))
+        return status.value
+
+    monkeypatch.setattr(tokens, "lib", lambda: types.SimpleNamespace(gs_some_call=call))
+    tokens._launch("gs_some_call", Other(), 5, None)
+    assert seen == [(1, (5, None, 71))] and at == [current]
+    status.value = 1
+    with pytest.raises(tokens.raster.GsError, match="gs_some_call"):
+        tokens._launch("gs_some_call", Other(), 5, None)
+    assert at == [current]
+
+
+def test_a_stream_of_another_gpu_is_refused():
+    """Work would go to the tensors' own GPU's current stream and not to the one that was given."""
+    from tile_differentiable_rasterizer_amd import tokens
+
+    def call(*args):
+        raise AssertionError("not reached")
+
+    for n in (0, 2):
+        with pytest.raises(ValueError, match="stream"):
+            tokens._on(types.SimpleNamespace(device_index=n), call, Other())

@@ -7,8 +7,8 @@ encoder's states, and the gated activation that keeps its inputs as 8-bit codes.
 Tensors are bfloat16 or float32 on the GPU, laid out as include/gs_tokens.h says: vectors dense in
 their last axis, on 16-byte boundaries, any strides else (views of one projection's output are
 taken as they are).  Shapes and types are checked here (the C calls do not see them: ValueError),
-everything else by the C calls (raster.GsError).  Work goes to the current stream, or to
-``stream``; outputs and workspaces that are not given are torch tensors made on that same stream
+everything else by the C calls (raster.GsError).  Work goes to the current stream of the tensors' GPU, or to
+``stream``, which is one of that GPU; outputs and workspaces that are not given are torch tensors made on that same stream
 (a workspace is given back to torch when the call returns, in stream order).
 
 ``norm_rotate``, ``cross_attention`` and ``gated8`` are the same operators as differentiable
@@ -86,18 +86,28 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(t):
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
-
-
-def _on(stream, call, *args):
-    """The call with `stream` as the current one, so that what it allocates belongs to the work."""
-    with torch.cuda.stream(stream):
-        return call(*args)
-
-
 def _refuse(what):
     raise ValueError(what)
+
+
+def _launch(name, t, *args):
+    """The C call on the current stream of t's GPU, with that GPU as the current one: a default stream's work goes to
+    whichever is."""
+    call, at = getattr(lib(), name), t.get_device()
+    if at == torch._C._cuda_getDevice():
+        status = call(*args, torch._C._cuda_getCurrentRawStream(at))
+    else:
+        with torch.cuda.device(at):
+            status = call(*args, torch._C._cuda_getCurrentRawStream(at))
+    _check(status, name)
+
+
+def _on(stream, call, first, *args):
+    """The call with `stream` as the current one, so that what it allocates belongs to the work."""
+    if stream.device_index != first.get_device():
+        _refuse("a stream of the vectors' GPU")
+    with torch.cuda.stream(stream):
+        return call(first, *args)
 
 
 def _heads(t) -> GsHeads:
@@ -178,9 +188,8 @@ def norm_rotate_fwd(q, k, wq, wk, cos, sin, pos_q=None, pos_k=None, eps: float =
         oq, ok = out
         _same(q, oq, q.shape)
         _same(q, ok, k.shape)
-    _check(lib().gs_norm_rotate_fwd(p, _heads(q), _heads(k), wq.data_ptr(), wk.data_ptr(), cos.data_ptr(), sin.data_ptr(),
-                                    _ptr(pos_q), _ptr(pos_k), _heads(oq), _heads(ok), _stream(q)),
-           "gs_norm_rotate_fwd")
+    _launch("gs_norm_rotate_fwd", q, p, _heads(q), _heads(k), wq.data_ptr(), wk.data_ptr(), cos.data_ptr(), sin.data_ptr(),
+            _ptr(pos_q), _ptr(pos_k), _heads(oq), _heads(ok))
     return oq, ok
 
 
@@ -196,9 +205,9 @@ def norm_rotate_bwd(dout_q, dout_k, q, k, wq, wk, cos, sin, pos_q=None, pos_k=No
     dq, dk = torch.empty_like(q), torch.empty_like(k)
     dwq, dwk = torch.empty_like(wq), torch.empty_like(wk)
     ws, n = _workspace(workspace, L.gs_norm_rotate_workspace_bytes(p), q)
-    _check(L.gs_norm_rotate_bwd(p, _heads(dout_q), _heads(dout_k), _heads(q), _heads(k), wq.data_ptr(), wk.data_ptr(),
-                                cos.data_ptr(), sin.data_ptr(), _ptr(pos_q), _ptr(pos_k), _heads(dq), _heads(dk),
-                                dwq.data_ptr(), dwk.data_ptr(), _ptr(ws), n, _stream(q)), "gs_norm_rotate_bwd")
+    _launch("gs_norm_rotate_bwd", q, p, _heads(dout_q), _heads(dout_k), _heads(q), _heads(k), wq.data_ptr(), wk.data_ptr(),
+            cos.data_ptr(), sin.data_ptr(), _ptr(pos_q), _ptr(pos_k), _heads(dq), _heads(dk),
+            dwq.data_ptr(), dwk.data_ptr(), _ptr(ws), n)
     return dq, dk, dwq, dwk
 
 
@@ -251,8 +260,7 @@ def cross_attn_fwd(q, k, v, scale: float | None = None, ranges=None, key_mask=No
         _floats(lse, shape, q, "lse")
     L = lib()
     ws, n = _workspace(workspace, L.gs_cross_attn_fwd_workspace_bytes(p), q)
-    _check(L.gs_cross_attn_fwd(p, _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(), _ptr(ws), n,
-                               _stream(q)), "gs_cross_attn_fwd")
+    _launch("gs_cross_attn_fwd", q, p, _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(), _ptr(ws), n)
     return out, lse
 
 
@@ -268,8 +276,8 @@ def cross_attn_bwd(dout, q, k, v, out, lse, scale: float | None = None, ranges=N
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     L = lib()
     ws, n = _workspace(workspace, L.gs_cross_attn_bwd_workspace_bytes(p), q)
-    _check(L.gs_cross_attn_bwd(p, _heads(dout), _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(), _heads(dq),
-                               _heads(dk), _heads(dv), _ptr(ws), n, _stream(q)), "gs_cross_attn_bwd")
+    _launch("gs_cross_attn_bwd", q, p, _heads(dout), _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(), _heads(dq),
+            _heads(dk), _heads(dv), _ptr(ws), n)
     return dq, dk, dv
 
 
@@ -301,8 +309,8 @@ def gate8_fwd(gate, up, act: str = "silu", stream=None) -> tuple:
     y = torch.empty_like(gate)
     codes = torch.empty((2, rows, width), dtype=torch.uint8, device=dev)
     bounds = torch.empty((2, rows, (width + CODE_BLOCK - 1) // CODE_BLOCK, 2), dtype=torch.float32, device=dev)
-    _check(lib().gs_gate8_fwd(rows, width, ACTS[act], ty, gate.data_ptr(), gs, up.data_ptr(), us, y.data_ptr(), y.stride(0),
-                              codes.data_ptr(), bounds.data_ptr(), _stream(gate)), "gs_gate8_fwd")
+    _launch("gs_gate8_fwd", gate, rows, width, ACTS[act], ty, gate.data_ptr(), gs, up.data_ptr(), us, y.data_ptr(), y.stride(0),
+            codes.data_ptr(), bounds.data_ptr())
     return y, codes, bounds
 
 
@@ -324,9 +332,9 @@ def gate8_bwd(dy, codes, bounds, act: str = "silu", with_y: bool = True, dgate=N
     dgate = torch.empty_like(dy) if dgate is None else dgate
     dup = torch.empty_like(dy) if dup is None else dup
     y = torch.empty_like(dy) if with_y else None
-    _check(lib().gs_gate8_bwd(rows, width, ACTS[act], ty, dy.data_ptr(), ds, codes.data_ptr(), bounds.data_ptr(),
-                              dgate.data_ptr(), _stride(dgate, dy, rows, width), dup.data_ptr(), _stride(dup, dy, rows, width),
-                              _ptr(y), y.stride(0) if with_y else 0, _stream(dy)), "gs_gate8_bwd")
+    _launch("gs_gate8_bwd", dy, rows, width, ACTS[act], ty, dy.data_ptr(), ds, codes.data_ptr(), bounds.data_ptr(),
+            dgate.data_ptr(), _stride(dgate, dy, rows, width), dup.data_ptr(), _stride(dup, dy, rows, width),
+            _ptr(y), y.stride(0) if with_y else 0)
     return dgate, dup, y
 
 
