@@ -37,7 +37,8 @@ enum { GS_ACT_SILU = 0, GS_ACT_GELU = 1 }; /* x / (1 + e^-x); gelu in its tanh f
 
 /* Vectors of head_dim elements (dense), one for each (sequence, token, head).  data is 16-byte
  * aligned and the strides, in elements, are multiples of 16 bytes and not negative.  A stride
- * of an axis of length 1 is not used. */
+ * of an axis of length 1 is not used.  Inputs may repeat vectors (a stride of 0); the strides of an
+ * output are at least head_dim. */
 typedef struct gs_heads {
   void* data;
   int64_t batch_stride, token_stride, head_stride;

@@ -184,3 +184,31 @@ def test_cross_attn_refuses_a_scale_past_its_exponent(bwd):
         assert attn_call(bwd=bwd, scale=scale) == BAD
     for scale in (2.3e38, -2.3e38, 0.0, 1e-45):
         assert attn_call(bwd=bwd, scale=scale, batch=0) == OK
+
+
+OVERLAPS = [dict(b=0), dict(tok=0), dict(h=0), dict(b=32), dict(tok=56), dict(h=8)]
+
+
+@pytest.mark.parametrize("over", OVERLAPS, ids=str)
+def test_outputs_whose_vectors_overlap_are_refused(over):
+    """An input may repeat its vectors (a stride of 0); an output that did would hold whichever came last.  Nothing is
+    launched: the calls that are not refused have a workspace that is too small, or nothing to do."""
+    t = tokens()
+    L, x, bad = t.lib(), heads(), heads(**over)
+    n = t.GsNormRotate(batch=2, q_len=3, k_len=5, q_heads=4, k_heads=2, head_dim=64, rot_dim=32, pairs=0, type=0, eps=1e-6, n_pos=9)
+    a = t.GsCrossAttn(batch=2, q_len=7, k_len=9, q_heads=4, kv_heads=2, head_dim=64, type=0, scale=0.125)
+    for i in range(2):
+        o = [bad if j == i else x for j in range(2)]
+        assert L.gs_norm_rotate_fwd(n, x, x, A, A, A, A, None, None, *o, None) == BAD
+        assert L.gs_norm_rotate_bwd(n, x, x, x, x, A, A, A, A, None, None, *o, A, A, A, 1 << 30, None) == BAD
+    assert L.gs_cross_attn_fwd(a, x, x, x, bad, A, A, 1 << 40, None) == BAD
+    for i in range(3):
+        o = [bad if j == i else x for j in range(3)]
+        assert L.gs_cross_attn_bwd(a, x, x, x, x, x, A, *o, A, 1 << 40, None) == BAD
+    assert L.gs_cross_attn_bwd(a, bad, bad, bad, bad, bad, A, x, x, x, A, 16, None) == WORKSPACE  # as inputs
+    assert L.gs_norm_rotate_bwd(n, bad, bad, bad, bad, A, A, A, A, None, None, x, x, A, A, A, 16, None) == WORKSPACE
+    # axes of length 1 have no stride
+    n.batch = n.q_len = n.k_len = n.q_heads = n.k_heads = 1
+    assert L.gs_norm_rotate_bwd(n, x, x, x, x, A, A, A, A, None, None, bad, bad, A, A, A, 16, None) == WORKSPACE
+    a.batch = a.q_len = a.k_len = a.q_heads = a.kv_heads = 1
+    assert L.gs_cross_attn_bwd(a, x, x, x, x, x, A, bad, bad, bad, A, 16, None) == WORKSPACE

@@ -56,6 +56,13 @@ bool heads_ok(gs_heads* x, int64_t batch, int64_t len, int64_t heads, int type) 
          x->batch_stride % each == 0 && x->token_stride % each == 0 && x->head_stride % each == 0;
 }
 
+// The same for an output, whose vectors lie apart.
+bool heads_out_ok(gs_heads* x, int64_t batch, int64_t len, int64_t heads, int64_t d, int type) {
+  if (!heads_ok(x, batch, len, heads, type)) return false;
+  if (!batch || !len || !heads) return true;
+  return (batch == 1 || x->batch_stride >= d) && (len == 1 || x->token_stride >= d) && (heads == 1 || x->head_stride >= d);
+}
+
 gs_status norm_shape(const gs_norm_rotate* p) {
   if (!p) return GS_ERR_INVALID_ARG;
   if (p->batch < 0 || p->q_len < 0 || p->k_len < 0 || p->q_heads < 0 || p->k_heads < 0 || p->n_pos < 0)
@@ -78,8 +85,10 @@ gs_status norm_call(const gs_norm_rotate* p, gs_heads dout_q, gs_heads dout_k, g
   const gs_status st = norm_shape(p);
   if (st != GS_OK) return st;
   const bool has_q = p->batch && p->q_len && p->q_heads, has_k = p->batch && p->k_len && p->k_heads;
-  if (!heads_ok(&q, p->batch, p->q_len, p->q_heads, p->type) || !heads_ok(&yq, p->batch, p->q_len, p->q_heads, p->type) ||
-      !heads_ok(&k, p->batch, p->k_len, p->k_heads, p->type) || !heads_ok(&yk, p->batch, p->k_len, p->k_heads, p->type))
+  if (!heads_ok(&q, p->batch, p->q_len, p->q_heads, p->type) ||
+      !heads_out_ok(&yq, p->batch, p->q_len, p->q_heads, p->head_dim, p->type) ||
+      !heads_ok(&k, p->batch, p->k_len, p->k_heads, p->type) ||
+      !heads_out_ok(&yk, p->batch, p->k_len, p->k_heads, p->head_dim, p->type))
     return GS_ERR_INVALID_ARG;
   if ((has_q && (!wq || !on(wq, 16))) || (has_k && (!wk || !on(wk, 16)))) return GS_ERR_INVALID_ARG;
   if ((has_q || has_k) && p->rot_dim && (!cs || !sn || !on(cs, 16) || !on(sn, 16) || p->n_pos < 1)) return GS_ERR_INVALID_ARG;
@@ -185,7 +194,8 @@ gs_status gs_cross_attn_fwd(const gs_cross_attn* p, gs_heads q, gs_heads k, gs_h
                             void* workspace, size_t workspace_bytes, void* stream) {
   const gs_status st = attn_shape(p, false);
   if (st != GS_OK) return st;
-  if (!heads_ok(&q, p->batch, p->q_len, p->q_heads, p->type) || !heads_ok(&out, p->batch, p->q_len, p->q_heads, p->type) ||
+  if (!heads_ok(&q, p->batch, p->q_len, p->q_heads, p->type) ||
+      !heads_out_ok(&out, p->batch, p->q_len, p->q_heads, p->head_dim, p->type) ||
       !heads_ok(&k, p->batch, p->k_len, p->kv_heads, p->type) || !heads_ok(&v, p->batch, p->k_len, p->kv_heads, p->type) ||
       !on(lse, 4))
     return GS_ERR_INVALID_ARG;
@@ -221,10 +231,13 @@ gs_status gs_cross_attn_bwd(const gs_cross_attn* p, gs_heads dout, gs_heads q, g
                             size_t workspace_bytes, void* stream) {
   const gs_status st = attn_shape(p, true);
   if (st != GS_OK) return st;
-  for (gs_heads* x : {&dout, &q, &out, &dq})
+  for (gs_heads* x : {&dout, &q, &out})
     if (!heads_ok(x, p->batch, p->q_len, p->q_heads, p->type)) return GS_ERR_INVALID_ARG;
-  for (gs_heads* x : {&k, &v, &dk, &dv})
+  for (gs_heads* x : {&k, &v})
     if (!heads_ok(x, p->batch, p->k_len, p->kv_heads, p->type)) return GS_ERR_INVALID_ARG;
+  if (!heads_out_ok(&dq, p->batch, p->q_len, p->q_heads, p->head_dim, p->type)) return GS_ERR_INVALID_ARG;
+  for (gs_heads* x : {&dk, &dv})
+    if (!heads_out_ok(x, p->batch, p->k_len, p->kv_heads, p->head_dim, p->type)) return GS_ERR_INVALID_ARG;
   if ((attn_rows(*p) && !lse) || !on(lse, 4)) return GS_ERR_INVALID_ARG;
   const size_t need = gs_cross_attn_bwd_workspace_bytes(p);
   if (need && (!workspace || !on(workspace, 16) || workspace_bytes < need)) return GS_ERR_WORKSPACE;
