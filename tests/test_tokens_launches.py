@@ -44,13 +44,14 @@ stand_in = ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)
 sys.path[:0] = sys.argv[2:4]
 import test_tokens_abi as abi
 var = lambda name, t=ctypes.c_int: t.in_dll(stand_in, name)
-out = []
-for call, how, fail_at in json.loads(sys.argv[4]):
-    var("fail_at").value, var("launches").value, var("last").value = fail_at, 0, 0
-    status = getattr(abi, call)(**how)
-    n = var("launches").value
-    out.append((status, list(var("workgroups", ctypes.c_double * 64)[:n])))
-print(json.dumps(out))
+for line in sys.stdin:
+    out = []
+    for call, how, fail_at in json.loads(line):
+        var("fail_at").value, var("launches").value, var("last").value = fail_at, 0, 0
+        status = getattr(abi, call)(**how)
+        n = var("launches").value
+        out.append((status, list(var("workgroups", ctypes.c_double * 64)[:n])))
+    print(json.dumps(out), flush=True)
 """
 
 
@@ -61,14 +62,20 @@ def launched(tmp_path_factory):
     (where / "hip.c").write_text(STAND_IN)
     subprocess.run(["gcc", "-O1", "-fPIC", "-shared", "-o", str(where / "hip.so"), str(where / "hip.c")], check=True)
 
-    def run(calls):
-        tests = os.path.dirname(os.path.abspath(__file__))
-        r = subprocess.run([sys.executable, "-c", CHILD, str(where / "hip.so"), tests, os.path.dirname(tests), json.dumps(calls)],
-                           capture_output=True, text=True, timeout=300)
-        assert r.returncode == 0, r.stderr
-        return json.loads(r.stdout.strip().splitlines()[-1])
+    tests = os.path.dirname(os.path.abspath(__file__))
+    child = subprocess.Popen([sys.executable, "-c", CHILD, str(where / "hip.so"), tests, os.path.dirname(tests)], stdin=subprocess.PIPE,
+                             stdout=subprocess.PIPE, text=True)
 
-    return run
+    def run(calls):
+        child.stdin.write(json.dumps(calls) + "\n")
+        child.stdin.flush()
+        line = child.stdout.readline()
+        assert line, "the process ended"
+        return json.loads(line)
+
+    yield run
+    child.stdin.close()
+    assert child.wait(60) == 0
 
 
 A = 1 << 20
