@@ -217,3 +217,16 @@ def test_a_stream_of_another_gpu_is_refused():
     for n in (0, 2):
         with pytest.raises(ValueError, match="stream"):
             tokens._on(types.SimpleNamespace(device_index=n), call, Other())
+
+
+def test_gated8_shapes(t):
+    """Any leading axes, none of them or the last empty; a last axis without two halves is refused, and so is a number."""
+    for shape in ((4, 6), (2, 3, 4), (6,), (0, 6), (2, 0, 6), (3, 0), (0, 0)):
+        x = torch.ones(shape, requires_grad=True)
+        y = t.gated8(x)
+        assert y.shape == (*shape[:-1], shape[-1] // 2)
+        y.sum().backward()
+        assert x.grad.shape == x.shape
+    for shape in ((4, 5), (3, 1), (2, 2, 7), ()):
+        with pytest.raises(ValueError, match="last axis"):
+            t.gated8(torch.ones(shape))

@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+import math
 
 import torch
 
@@ -420,7 +421,7 @@ class _Gated8(torch.autograd.Function):
     @staticmethod
     def forward(ctx, h, act):
         width = h.shape[-1] // 2
-        flat = h.reshape(-1, 2 * width)
+        flat = h.reshape(math.prod(h.shape[:-1]), 2 * width)
         y, codes, bounds = gate8_fwd(flat[:, :width], flat[:, width:], act)
         link = h.new_empty(0)  # h's place in the graph, without h
         ctx.save_for_backward(codes, bounds, link)
@@ -433,7 +434,7 @@ class _Gated8(torch.autograd.Function):
         codes, bounds, _ = ctx.saved_tensors
         width = codes.shape[2]
         dh = torch.empty((codes.shape[1], 2 * width), dtype=dy.dtype, device=dy.device)
-        dy = dy.reshape(-1, width)
+        dy = dy.reshape(codes.shape[1], width)
         dy = dy if dy.stride() == (width, 1) else dy.contiguous()
         gate8_bwd(dy, codes, bounds, ctx.act, False, dh[:, :width], dh[:, width:])
         return dh.view(ctx.shape), None
@@ -442,4 +443,6 @@ class _Gated8(torch.autograd.Function):
 def gated8(h, act: str = "silu"):
     """act(gate) * up of a projection's output h [..., 2 * width] = (gate | up), with the gradient for h from 8-bit
     codes: between the passes only the codes and their bounds are kept, a quarter (float32) or half (bfloat16) of h."""
+    if h.dim() == 0 or h.shape[-1] % 2:
+        _refuse("a last axis of two halves, gate and up")
     return _Gated8.apply(h, act)[0]
