@@ -771,3 +771,102 @@ def test_cross_attn_scale_of_nothing_keeps_nan():
         out, lse = tokens.cross_attn_fwd(q, k, v, scale=0.0)
         assert torch.equal(lse.isnan(), bad) and torch.equal(out.isnan().all(-1).transpose(1, 2), bad) and torch.equal(out.isnan().any(-1).transpose(1, 2), bad)
         assert ((lse - math.log(100))[~bad].abs() < 1e-5).all()
+
+
+# -- the torch functions' gradients are the calls' own -------------------------------------------
+
+
+def same(got, want):
+    assert len(got) == len(want)
+    for i, (a, b) in enumerate(zip(got, want)):
+        assert a.shape == b.shape and a.dtype == b.dtype and torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("pairs", ["halves", "neighbours"])
+def test_norm_rotate_function(t, pairs):
+    q, k, wq, wk, cos, sin = norm_inputs((t, 2, 20, 33, 4, 2, 64, 32, pairs), True)
+    n, g = cos.shape[0], gen(3)
+    pos_q, pos_k = (torch.randint(0, n, x.shape[:2], generator=g, device="cuda", dtype=torch.int32) for x in (q, k))
+    more = (cos, sin, pos_q, pos_k, 1e-2, pairs)
+    dq, dk = normal(g, *q.shape, t=q.dtype), normal(g, *k.shape, t=k.dtype)
+    xs = [x.detach().requires_grad_() for x in (q, k, wq, wk)]
+    out = tokens.norm_rotate(*xs, *more)
+    same(out, tokens.norm_rotate_fwd(q, k, wq, wk, *more))
+    want = tokens.norm_rotate_bwd(dq, dk, q, k, wq, wk, *more)
+    assert not torch.equal(want[2], want[3])
+    same(torch.autograd.grad(out, xs, (dq, dk)), want)
+    out = tokens.norm_rotate(*xs, *more)  # one output used alone
+    got = torch.autograd.grad(out[1], xs, dk)
+    same((got[1], got[3]), (want[1], want[3]))
+    assert not got[0].any() and not got[2].any()
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_cross_attention_function(t):
+    q, k, v = qkv(t, 2, 40, 90, 4, 2, 64)
+    g = gen(7)
+    a = torch.randint(0, 60, (2, 40), generator=g, device="cuda")
+    ranges = torch.stack([a, a + 30], -1).int()
+    mask = torch.rand(2, 90, generator=g, device="cuda") < 0.7
+    dout = normal(g, *q.shape, t=q.dtype)
+    for more in ((-0.3, ranges, mask), (0.5, None, mask), (None, ranges, None)):
+        xs = [x.detach().requires_grad_() for x in (q, k, v)]
+        out = tokens.cross_attention(*xs, *more)
+        ref, lse = tokens.cross_attn_fwd(q, k, v, *more)
+        want = tokens.cross_attn_bwd(dout, q, k, v, ref, lse, *more)
+        same([out], [ref])
+        same(torch.autograd.grad(out, xs, dout), want)
+    shared = k.detach()[:1].requires_grad_()  # one sequence's keys for the batch: their gradient is the batch's sum
+    out = tokens.cross_attention(q, shared.expand(2, -1, -1, -1), v)
+    ref, lse = tokens.cross_attn_fwd(q, shared.expand(2, -1, -1, -1), v)
+    want = tokens.cross_attn_bwd(dout, q, shared.expand(2, -1, -1, -1), v, ref, lse)[1]
+    same(torch.autograd.grad(out, [shared], dout), [want.sum(0, keepdim=True)])
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gated8_function(t, act):
+    g = gen(9)
+    h, dy = normal(g, 3, 5, 600, t=TYPES[t]).requires_grad_(), normal(g, 3, 5, 300, t=TYPES[t])
+    y = tokens.gated8(h, act)
+    flat = h.detach().view(15, 600)
+    ref, codes, bounds = tokens.gate8_fwd(flat[:, :300], flat[:, 300:], act)
+    dg, du, _ = tokens.gate8_bwd(dy.view(15, 300), codes, bounds, act)
+    assert not torch.equal(dg, du)
+    same([y], [ref.view(3, 5, 300)])
+    same(torch.autograd.grad(y, [h], dy), [torch.cat([dg, du], 1).view(3, 5, 600)])
+
+
+def test_gated8_keeps_only_its_codes():
+    """Between the passes: two bytes a unit, its bounds, and what the caller keeps itself."""
+    x = torch.zeros(1 << 10, 1 << 13, device="cuda", requires_grad=True)
+    before = torch.cuda.memory_allocated()
+    y = tokens.gated8(x * 1.0)
+    kept = torch.cuda.memory_allocated() - before
+    units = y.numel()
+    assert kept <= 4 * units + 2 * units + 16 * units // 256 + (1 << 16)  # y, codes, bounds
+    y.sum().backward()
+    assert torch.isfinite(x.grad).all()
+
+
+@pytest.mark.parametrize("case", [("f32", 2, 40, 100, 2, 2, 64), ("bf16", 2, 40, 100, 2, 2, 64), ("bf16", 2, 1, 4000, 2, 2, 64)], ids=str)
+def test_cross_attn_nan_in_a_seen_key_or_value(case):
+    """A NaN in a key reaches every row that sees it, in a value its element of theirs; nothing of another head or sequence."""
+    q, k, v = qkv(*case)
+    k[1, 60, 0, 2] = float("nan")
+    v[0, 5, 1, 3] = float("nan")
+    n = torch.tensor([[[0, 100]], [[0, 100]]], device="cuda", dtype=torch.int32)
+    for ranges in (n, n - torch.tensor([[[0, 90]], [[0, 40]]], device="cuda", dtype=torch.int32)):  # the second: the key is the first past the end
+        out, lse = tokens.cross_attn_fwd(q, k, v, ranges=ranges)
+        bad, bad_lse = torch.zeros_like(out, dtype=torch.bool), torch.zeros_like(lse, dtype=torch.bool)
+        bad[0, :, 1, 3] = True
+        if ranges is n:
+            bad[1, :, 0] = bad_lse[1, 0] = True
+        assert torch.equal(out.isnan(), bad) and torch.equal(lse.isnan(), bad_lse)
+        dout = normal(gen(2), *q.shape, t=q.dtype)
+        dq, dk, dv = tokens.cross_attn_bwd(dout, q, k, v, out, lse, ranges=ranges)
+        assert dq[0, :, 1].isnan().all() and torch.isfinite(dq[0, :, 0]).all() and torch.isfinite(dq[1, :, 1]).all()
+        assert torch.isfinite(dk[0, :, 0]).all() and torch.isfinite(dv[:, :, 1]).all() and torch.isfinite(dk[1, :, 1]).all()
+        past = torch.arange(k.shape[1], device="cuda") >= ranges[:, 0, 1:]
+        assert not dk[past].any() and not dv[past].any()
