@@ -102,7 +102,9 @@ gs_status gs_norm_rotate_bwd(const gs_norm_rotate* shape, gs_heads dout_q, gs_he
  * hold.  (A value that some row sees and another does not has to be finite for the other's
  * result to be: weights of 0 are products like the rest.  So do a row's query and output gradient
  * for the gradients of keys that it does not see and others do; those of a row that sees nothing
- * are not part of any result.) */
+ * are not part of any result.)  float32 vectors enter the products as sums of three bfloat16, whose
+ * products with an infinity are NaN: where a row sees one (or 3.39e38 and more, which rounds to it), its
+ * result may be NaN also where the formula has an infinity or, at a weight of 0, a finite number. */
 typedef struct gs_cross_attn {
   int64_t batch, q_len, k_len;
   int32_t q_heads, kv_heads, head_dim, type;

@@ -870,3 +870,31 @@ def test_cross_attn_nan_in_a_seen_key_or_value(case):
         assert torch.isfinite(dk[0, :, 0]).all() and torch.isfinite(dv[:, :, 1]).all() and torch.isfinite(dk[1, :, 1]).all()
         past = torch.arange(k.shape[1], device="cuda") >= ranges[:, 0, 1:]
         assert not dk[past].any() and not dv[past].any()
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_cross_attn_infinities_that_rows_see(t):
+    """An infinity in a seen key or value is never lost: bfloat16 has the formula's results, float32 those or NaN, and
+    what does not see it is as without it."""
+    q, k, v = qkv(t, 2, 40, 100, 2, 2, 64)
+    plain, plain_lse = tokens.cross_attn_fwd(q, k, v)
+    k2, v2 = k.clone(), v.clone()
+    k2[1, 60, 0, 2] = math.inf  # scores of q[..., 2] times infinity: weight 0, or NaN
+    v2[0, 5, 1, 3] = math.inf
+    out, lse = tokens.cross_attn_fwd(q, k2, v2)
+    others = torch.ones_like(out, dtype=torch.bool)
+    others[1, :, 0] = others[0, :, 1, 3] = False
+    assert torch.equal(out[others], plain[others])
+    below, above = q[1, :, 0, 2] < 0, q[1, :, 0, 2] > 0
+    assert out[1, above, 0].isnan().all() and lse[1, 0, above].isnan().all()
+    hidden = torch.ones(2, 100, dtype=torch.bool, device="cuda")
+    hidden[1, 60] = False  # a weight of 0 is a key that is not there
+    rest, rest_lse = tokens.cross_attn_fwd(q, k, v, key_mask=hidden)
+    gone = out[1, below, 0].isnan().all(-1)
+    assert torch.equal(gone, lse[1, 0, below].isnan())
+    assert ((out[1, below, 0] - rest[1, below, 0])[~gone].abs() <= (1e-5 if t == "f32" else 0.02)).all()
+    assert ((lse[1, 0, below] - rest_lse[1, 0, below])[~gone].abs() <= 1e-5).all()
+    if t == "bf16":
+        assert not gone.any() and (out[0, :, 1, 3] == math.inf).all()
+    else:
+        assert (out[0, :, 1, 3].isnan() | (out[0, :, 1, 3] == math.inf)).all()
