@@ -16,7 +16,7 @@ struct AttnArgs {
   int32_t rows;    // q_len * group
   int32_t splits;  // of the long axis: keys (out, dq) or rows (dk, dv)
   float scale;
-  float slope;     // |scale| log2(e), above 0; 1 where the scale is 0 and scores are made of zeros (scaled_frag)
+  float slope;     // |scale| log2(e); forward 1 for a scale of 0, whose scores are made of zeros
   uint32_t flip;   // sign of the scale, to be put on the queries: 0 or the sign bits of a register
   const int32_t* ranges;
   int64_t ranges_b, ranges_r;
@@ -40,13 +40,6 @@ struct RowTile {
 template <typename T>
 __device__ __forceinline__ T* head_ptr(const gs_heads& x, int b, int t, int h) {
   return static_cast<T*>(x.data) + b * x.batch_stride + t * x.token_stride + h * x.head_stride;
-}
-
-// An operand of the scores with the scale's sign on it.  Of a scale of 0 the slope cannot tell a score from a key
-// that is not seen (0 times -inf), so the operand is multiplied by it instead: finite elements become 0, others NaN.
-template <typename T>
-__device__ __forceinline__ Frag<T> scaled_frag(const AttnArgs& a, Frag<T> f) {
-  return a.scale == 0.0f ? frag_zeros(f) : frag_flip(f, a.flip);
 }
 
 // The keys that query row i of sequence b may see, [first, last) inside [0, k_len).

@@ -56,7 +56,12 @@ __global__ __launch_bounds__(256, (kWavesOf<T, DP>)) void k_attn_fwd(AttnArgs a)
 
   Frag<T> qf[DP / 16];
 #pragma unroll
-  for (int s = 0; s < DP / 16; ++s) qf[s] = scaled_frag(a, frag_mem<T>(head_ptr<T>(a.q, b, i, h), a.d, s, live));
+  for (int s = 0; s < DP / 16; ++s) qf[s] = frag_flip(frag_mem<T>(head_ptr<T>(a.q, b, i, h), a.d, s, live), a.flip);
+  if (a.scale == 0.0f) {
+    // a slope of 0 could not tell scores from keys that are not seen (0 times -inf): the queries take it
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s) qf[s] = frag_zeros(qf[s]);
+  }
   f32x16 o[DP / 32];
 #pragma unroll
   for (int t = 0; t < DP / 32; ++t) o[t] = (f32x16)0.0f;

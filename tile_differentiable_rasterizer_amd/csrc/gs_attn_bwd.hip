@@ -67,7 +67,7 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::kWaves)) void k_attn_bwd_kv(A
   Frag<T> kf[kS], vf[kS];
 #pragma unroll
   for (int s = 0; s < kS; ++s) {
-    kf[s] = scaled_frag(a, frag_mem<T>(head_ptr<T>(a.k, b, key, hk), a.d, s, open));
+    kf[s] = frag_flip(frag_mem<T>(head_ptr<T>(a.k, b, key, hk), a.d, s, open), a.flip);
     vf[s] = frag_mem<T>(head_ptr<T>(a.v, b, key, hk), a.d, s, open);
   }
   if constexpr (Sh::kValuesInLds) {  // each wavefront's own 32 rows
@@ -248,7 +248,7 @@ __global__ __launch_bounds__(256, (kWavesOf<T, DP>)) void k_attn_bwd_q(AttnArgs 
   Frag<T> qf[kS], gf[kS];
 #pragma unroll
   for (int s = 0; s < kS; ++s) {
-    qf[s] = scaled_frag(a, frag_mem<T>(head_ptr<T>(a.q, b, i, h), a.d, s, live));
+    qf[s] = frag_flip(frag_mem<T>(head_ptr<T>(a.q, b, i, h), a.d, s, live), a.flip);
     gf[s] = frag_mem<T>(head_ptr<T>(a.dout, b, i, h), a.d, s, live);
   }
   if (t_n > kShortTiles) {

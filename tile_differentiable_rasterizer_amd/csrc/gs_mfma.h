@@ -241,7 +241,7 @@ __device__ __forceinline__ Frag<T> frag_flip(Frag<T> f, uint32_t flip) {
   return x.f;
 }
 
-// The same with every element multiplied by 0.
+// The same with every element multiplied by 0: finite ones become 0, others NaN.
 template <typename T>
 __device__ __forceinline__ Frag<T> frag_zeros(Frag<T> f) {
   union {

@@ -134,8 +134,7 @@ AttnArgs attn_args(const gs_cross_attn& p) {
   a.d = p.head_dim;
   a.rows = (int32_t)(p.q_len * a.group);
   a.scale = p.scale;
-  // the kernels take the maximum before they scale, so the slope is positive
-  a.slope = p.scale == 0.0f ? 1.0f : fabsf(p.scale) * kLog2e;
+  a.slope = fabsf(p.scale) * kLog2e;  // the kernels take the maximum before they scale: not negative
   a.flip = p.scale < 0.0f ? 0x80008000u : 0u;
   a.ranges = p.ranges;
   a.ranges_b = p.ranges_batch_stride;
@@ -208,6 +207,7 @@ gs_status gs_cross_attn_fwd(const gs_cross_attn* p, gs_heads q, gs_heads k, gs_h
   a.v = v;
   a.out = out;
   a.lse = lse;
+  if (a.slope == 0.0f) a.slope = 1.0f;
   a.splits = attn_fwd_splits(*p);
   char* at = static_cast<char*>(workspace) + order_bytes(*p);
   a.part = reinterpret_cast<float*>(at);
