@@ -168,7 +168,7 @@ gs_status gs_gate8_fwd(int64_t rows, int64_t width, int32_t act, int32_t type, c
  * lo + code * ((hi - lo) * (1 / 255)), in float32 with every operation rounded, and for NaN where
  * hi - lo is no finite float32.  With g and u these values: dgate = dy * u * act'(g), dup = dy *
  * act(g) and, where y is not NULL, y = act(g) * u again (for the weight gradient of the product
- * that follows, which then need not keep it).
+ * that follows: a backward pass that makes that gradient itself need not keep y).
  * Errors: as gs_gate8_fwd.
  */
 gs_status gs_gate8_bwd(int64_t rows, int64_t width, int32_t act, int32_t type, const void* dy, int64_t dy_stride,

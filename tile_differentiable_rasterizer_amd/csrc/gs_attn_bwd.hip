@@ -17,9 +17,9 @@
 //
 // Products and vector arithmetic take turns on the SIMDs, as in the forward kernel: busy 62% + 38% (rows) and 56% + 31%
 // (keys) of the time at D 128, 49% + 59% and 44% + 41% at 64; the keys' kernel also waits, for LDS, which it reads 2.0
-// times a product (the rows' kernel 1.3).  2 x 3907 x 8160, 32 heads of 128: rows 1.38 ms, keys 1.88 ms (1.13 and 1.11 PFLOP/s);
-// 3 x 3907 x 3600, 16 of 64, lengths 3600, 2250 and 0: 175 and 308 us; float32, 2 x 391 x 2500, 8 of 64, a quarter of
-// the keys masked: 56 and 91 us.
+// times a product (the rows' kernel 1.3).  2 x 3907 x 8160, 32 heads of 128: rows 1.40 ms, keys 1.94 ms (1.12 and 1.08 PFLOP/s);
+// 3 x 3907 x 3600, 16 of 64, lengths 3600, 2250 and 0: 165 to 170 and 291 to 308 us; float32, 2 x 391 x 2500, 8 of 64, a
+// quarter of the keys masked: 55 to 57 and 89 to 92 us.
 #include "gs_attn.h"
 
 namespace gs {

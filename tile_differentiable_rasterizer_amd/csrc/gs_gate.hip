@@ -4,7 +4,8 @@
 // "Training 10M Gaussians in 8 GB: Spirula Studio's VRAM efficiency" (mhpq.cn), quantised training
 // section: fixed-point codes with a (min, max) pair per 256 units, here over the two inputs of
 // y = act(gate) * up, which a feed-forward layer would otherwise hold until its backward pass
-// (bfloat16: 2 + 2 bytes a unit pair, and y's 2; as codes 1 + 1, with y made again).
+// (bfloat16: 2 + 2 bytes a unit pair, and y's 2; as codes 1 + 1, and y made again where the caller's backward pass
+// asks for it).
 //
 // A half wavefront takes 256 consecutive units of a row, eight a lane, of gate and of up: one read,
 // the extremes across 32 lanes, codes and y written.  The code is decided in float64, as the

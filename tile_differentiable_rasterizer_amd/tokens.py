@@ -442,7 +442,8 @@ class _Gated8(torch.autograd.Function):
 
 def gated8(h, act: str = "silu"):
     """act(gate) * up of a projection's output h [..., 2 * width] = (gate | up), with the gradient for h from 8-bit
-    codes: between the passes only the codes and their bounds are kept, a quarter (float32) or half (bfloat16) of h."""
+    codes: between the passes this keeps the codes and their bounds, a quarter (float32) or half (bfloat16) of h.  (A
+    product that follows keeps its own input; gate8_bwd makes it again where a backward pass is written by hand.)"""
     if h.dim() == 0 or h.shape[-1] % 2:
         _refuse("a last axis of two halves, gate and up")
     return _Gated8.apply(h, act)[0]
