@@ -898,3 +898,16 @@ def test_cross_attn_infinities_that_rows_see(t):
         assert not gone.any() and (out[0, :, 1, 3] == math.inf).all()
     else:
         assert (out[0, :, 1, 3].isnan() | (out[0, :, 1, 3] == math.inf)).all()
+
+
+@pytest.mark.parametrize("way", ["grad", "backward"])
+def test_functions_refuse_second_derivatives(way):
+    """A gradient's gradient is an error from the GPU's backward threads too; the first comes as without create_graph."""
+    q, k, v = (x.requires_grad_() for x in qkv("f32", 1, 6, 20, 2, 2, 32))
+    w, cs = torch.ones(32, device="cuda"), torch.ones(20, 16, device="cuda")
+    for f in (lambda: tokens.norm_rotate(q, k, w, w, cs, cs)[0], lambda: tokens.cross_attention(q, k, v), lambda: tokens.gated8(q, "gelu")):
+        plain, = torch.autograd.grad(f().square().sum() + q.square().sum(), q)
+        first, = torch.autograd.grad(f().square().sum() + q.square().sum(), q, create_graph=True)
+        assert torch.equal(first.detach(), plain)
+        with pytest.raises(RuntimeError, match="differentiated once"):
+            torch.autograd.grad(first.square().sum(), q) if way == "grad" else first.square().sum().backward()
