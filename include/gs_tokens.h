@@ -7,7 +7,9 @@
  * the norms of queries and keys with the position rotation, the attention of the tokens to the
  * states, and the gated activation of the feed-forward part, which keeps its inputs for the
  * backward pass as 8-bit codes (the fixed-point codes with a (min, max) pair per 256 units of
- * "Training 10M Gaussians in 8 GB: Spirula Studio's VRAM efficiency", here over activations).
+ * "Training 10M Gaussians in 8 GB: Spirula Studio's VRAM efficiency", here over activations).  What
+ * trains such a layer beside them: layer norm, the products of rows with their group's weights
+ * (experts), and the optimizer's step over all tensors.
  *
  * The conventions are gs_raster.h's: device pointers owned by the caller unless marked [host],
  * no allocation, scratch from a caller workspace, arguments checked before any HIP call, work
@@ -16,7 +18,7 @@
  * inputs gives the same bits.
  *
  * Element types: GS_BF16 or GS_F32, one for all gs_heads / matrix arguments of a call; norm
- * weights, their gradients, rotation tables, lse and bounds are float32 always.  Sums, norms,
+ * weights and biases, their gradients, rotation tables, lse and bounds are float32 always.  Sums, norms,
  * softmax statistics and gradients accumulate in float32.
  */
 #ifndef GS_TOKENS_H
@@ -174,6 +176,126 @@ gs_status gs_gate8_fwd(int64_t rows, int64_t width, int32_t act, int32_t type, c
 gs_status gs_gate8_bwd(int64_t rows, int64_t width, int32_t act, int32_t type, const void* dy, int64_t dy_stride,
                        const uint8_t* codes, const float* bounds, void* dgate, int64_t dgate_stride, void* dup,
                        int64_t dup_stride, void* y, int64_t y_stride, void* stream);
+
+/*
+ * gs_layer_norm_fwd -- layer norm over rows of `width` units:
+ *   xh = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps),  y = w * xh + b.
+ *  x, y    [rows][width], row strides in elements (y's at least width; inputs may repeat rows, with a stride of 0);
+ *          y may be x's own buffer with the same stride, and otherwise does not overlap x
+ *  w, b    float32 [width]; NULL: 1 and 0
+ * Any stride and alignment (of whole elements) is taken; width is at most 16384.  The variance is a float32: units up to
+ * 1e19 from their row's mean.  rows or width of 0: nothing is done.
+ * Errors: INVALID_ARG, OVERFLOW (a width past 16384, 2^31 rows or more), HIP.
+ */
+gs_status gs_layer_norm_fwd(int64_t rows, int64_t width, int32_t type, float eps, const void* x, int64_t x_stride,
+                            const float* w, const float* b, void* y, int64_t y_stride, void* stream);
+
+/*
+ * gs_layer_norm_bwd -- gradients of gs_layer_norm_fwd from its inputs (nothing is kept from the
+ * forward call) and the gradient of y.  With g = w * dy and rstd = 1 / sqrt(variance + eps):
+ *   dx = rstd (g - mean(g) - xh mean(g xh)),  dw = sum over rows of dy * xh,  db = sum over rows of dy.
+ *  dx        may be dy's or x's own buffer with the same stride, and otherwise overlaps neither
+ *  dw, db    float32 [width], overwritten (0 where there are no rows); NULL: not wanted
+ *  workspace gs_layer_norm_workspace_bytes(rows, width) bytes, 16-byte aligned (not looked at where neither dw
+ *            nor db is wanted)
+ * Errors: as the forward call, and WORKSPACE.
+ */
+size_t gs_layer_norm_workspace_bytes(int64_t rows, int64_t width);
+gs_status gs_layer_norm_bwd(int64_t rows, int64_t width, int32_t type, float eps, const void* dy, int64_t dy_stride,
+                            const void* x, int64_t x_stride, const float* w, void* dx, int64_t dx_stride, float* dw,
+                            float* db, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Weights of gs_group_mm_*, or their gradients: element (g, i, j) of [groups][k][n] is at
+ * g * group_stride + i * k_stride + j * n_stride, in elements; k_stride or n_stride is 1 (an axis of
+ * length 1 is not looked at). */
+typedef struct gs_weights {
+  void* data;
+  int64_t group_stride, k_stride, n_stride;
+} gs_weights;
+
+/* Shape of gs_group_mm_*: x[rows][k], weights[groups][k][n], y[rows][n], all of one type.  Rows are sorted by
+ * group: group g has the rows [offsets[g], offsets[g + 1]).  offsets (device, int32 [groups + 1]) do not
+ * decrease; they are cut to [0, rows], and nothing outside of the matrices is read or written whatever they
+ * hold.  Rows before the first group's and behind the last one's belong to none. */
+typedef struct gs_group_mm {
+  int64_t rows, k, n;
+  int32_t groups, type;
+  const int32_t* offsets;
+} gs_group_mm;
+
+/*
+ * gs_group_mm_fwd -- the product of every row with its group's weights: y[r] = x[r] W[g(r)].  Rows that
+ * belong to no group get 0, whatever x holds there.
+ *  x, y        row strides in elements (y's at least n; inputs may repeat rows, and weights, with a stride of 0); y overlaps
+ *              no input
+ *  workspace   gs_group_mm_fwd_workspace_bytes(p) bytes, 16-byte aligned (0 for many shapes: it holds the
+ *              parts of a long sum that is split over workgroups)
+ * Any sizes, strides and alignment (of whole elements) are taken; matrices that all start rows at 16-byte boundaries
+ * go faster.  k of 0: y is 0.
+ * Errors: INVALID_ARG, OVERFLOW (2^31 rows or more, k or n past 2^24, more than 65536 groups, or 2^24 tiles of results or
+ * more), WORKSPACE, HIP.
+ */
+size_t gs_group_mm_fwd_workspace_bytes(const gs_group_mm* p);
+gs_status gs_group_mm_fwd(const gs_group_mm* p, const void* x, int64_t x_stride, gs_weights w, void* y,
+                          int64_t y_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gs_group_mm_bwd -- gradients of gs_group_mm_fwd from its inputs and the gradient of y:
+ *   dx[r] = dy[r] W[g(r)]^T,  dW[g] = sum over the group's rows of x[r]^T dy[r].
+ * Everything is overwritten; rows of no group and weights of a group without rows get 0.  dx (then w is
+ * not looked at) or dw.data may be NULL: not wanted.  Outputs overlap nothing else.
+ *  workspace   gs_group_mm_bwd_workspace_bytes(p) bytes, 16-byte aligned
+ * Errors: as the forward call.
+ */
+size_t gs_group_mm_bwd_workspace_bytes(const gs_group_mm* p);
+gs_status gs_group_mm_bwd(const gs_group_mm* p, const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                          gs_weights w, void* dx, int64_t dx_stride, gs_weights dw, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* A tensor of gs_adamw: n units, dense, aligned to whole elements. */
+typedef struct gs_adamw_tensor {
+  float* param;       /* updated in place */
+  const void* grad;   /* float32 or bfloat16 */
+  void* copy;         /* bfloat16: receives the new parameters, rounded; NULL: none */
+  int64_t n;
+  double decay;       /* its weight decay */
+} gs_adamw_tensor;
+
+/* Hyper-parameters of gs_adamw (values, host). */
+typedef struct gs_adamw_params {
+  double lr, beta1, beta2, eps; /* learning rate, moment decays in [0, 1), epsilon (at least 0) */
+  int64_t step;                 /* 1-based step number (bias correction 1 - beta^step) */
+} gs_adamw_params;
+
+/*
+ * gs_adamw -- one step of AdamW (Loshchilov and Hutter) over `count` tensors at once:
+ *   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2,
+ *   p = p (1 - lr decay) - lr (m / (1 - b1^step)) / (sqrt(v / (1 - b2^step)) + eps),
+ * computed in float64 (the quotient to float32's accuracy), p rounded once.
+ *  tensors     [host] read before the call returns; no two of them overlap
+ *  grad_type   GS_F32 or GS_BF16, of all gradients; grad_scale (device, one float32; NULL: 1) multiplies
+ *              them: a loss scale's reciprocal, or the factor that clips their norm
+ *  bits        32: moments m, v are float32.  8: int8 and uint8 codes with bounds float32 (M, V) for each 256
+ *              units of a tensor, the largest |m| and v: m = M (c / 127)^2 with c's sign, c = rint(127 sqrt(|m| / M));
+ *              v = V (c / 255)^4, c = rint(255 (v / V)^(1/4)), at least 1 where v > 0.  Codes are decided in float64.
+ *              A block with a moment that is no finite float32 has NaN for its bound and codes 0.
+ *  m, v, bounds   the moments of all tensors one after another, each starting at a multiple of 256 units: tensor
+ *              i's at 256 * sum over j < i of ceil(n_j / 256); bounds [blocks][2] (8 bits; else not looked at), m and v 16-byte,
+ *              bounds 8-byte aligned.  All zeros is the start, and what stands behind a tensor's last unit stays 0.
+ * lr and step are values of the call: a captured graph repeats them.
+ * Errors: INVALID_ARG (also count < 0, n < 0, hyper-parameters that are not finite or out of range), OVERFLOW (2^35 units or
+ * more with every tensor's rounded up to 256), HIP.
+ */
+gs_status gs_adamw(int32_t count, const gs_adamw_tensor* tensors, int32_t grad_type, int32_t bits, void* m, void* v,
+                   float* bounds, const gs_adamw_params* hyper, const float* grad_scale, void* stream);
+
+/*
+ * gs_adamw_moments -- what the codes of `blocks` blocks of 256 units stand for: out_m and out_v float32
+ * [256 * blocks], 16-byte aligned.
+ * Errors: INVALID_ARG, OVERFLOW (2^27 blocks or more), HIP.
+ */
+gs_status gs_adamw_moments(int64_t blocks, const int8_t* m, const uint8_t* v, const float* bounds, float* out_m,
+                           float* out_v, void* stream);
 
 #ifdef __cplusplus
 }

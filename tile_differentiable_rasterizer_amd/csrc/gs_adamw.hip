@@ -1,0 +1,272 @@
+// gs_adamw.hip -- one step of AdamW over many tensors at once, moments in float32 or as 8-bit codes
+// with bounds for each 256 units, for gfx950.
+//
+//   m = b1 m + (1 - b1) g, v = b2 v + (1 - b2) g^2,
+//   p = p (1 - lr decay) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps).
+//
+// Codes are spaced for what they feed: sqrt(v) divides the step, and moments of one block lie orders of
+// magnitude apart, so m goes by the square of its code and v by the fourth power (sqrt(v) by the square), down
+// to 1/16129 and 1/65025 of the block's largest.  v > 0 keeps a code of 1 at least: a second moment
+// of 0 beside a first moment would make a step of m / eps.
+//
+// A half wavefront takes a block of 256 units, eight a lane.  Moments are updated, and codes decided, in
+// float64 (the device's float64 rate is its float32 rate): a code is found with float32 roots and set right
+// against its two borders, which are exact.  The tensors' table travels in the kernel's arguments, 64
+// tensors a launch, so that nothing is copied to the device and a captured graph holds its own.
+#include <algorithm>
+
+#include "gs_device.h"
+#include "gs_elem.h"
+
+namespace gs {
+
+constexpr int kAdamwBlock = 256, kAdamwTensors = 64;
+
+struct AdamwTable {
+  float* param[kAdamwTensors];
+  const void* grad[kAdamwTensors];
+  __bf16* copy[kAdamwTensors];
+  int64_t n[kAdamwTensors];
+  double keep[kAdamwTensors];      // 1 - lr decay
+  uint32_t first[kAdamwTensors];   // the tensor's first block in this launch (past the last tensor: all ones)
+  void *m, *v;                     // of the launch's first block
+  float2* bounds;
+  const float* grad_scale;
+  double b1, b2, c1, c2, ib1, ib2, lr, eps;
+  uint32_t blocks;
+};
+
+template <typename T>
+__device__ __forceinline__ void adamw_load(const T* p, int n, float (&x)[8]) {
+  if (n >= 8) {
+    typedef T V __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
+    constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < 8; i += kPer) {
+      const V v = *reinterpret_cast<const V*>(p + i);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) x[i + j] = (float)v[j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = i < n ? (float)p[i] : 0.0f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void adamw_store(T* p, int n, const float (&x)[8]) {
+  if (n >= 8) {
+    typedef T V __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
+    constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < 8; i += kPer) {
+      V v;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) v[j] = (T)x[i + j];
+      *reinterpret_cast<V*>(p + i) = v;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = (T)x[i];
+  }
+}
+
+__device__ __forceinline__ float half_top(float v) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+  return v;
+}
+
+// What codes stand for, before the block's bound / 127^2 or / 255^4.
+__device__ __forceinline__ double adamw_m_of(int c) { return (double)(c * abs(c)); }
+__device__ __forceinline__ double adamw_v_of(uint32_t c) { return (double)(c * c * (c * c)); }
+constexpr double kAdamwM = 127.0 * 127.0, kAdamwV = 255.0 * 255.0 * 255.0 * 255.0;
+
+// rint(sqrt(t)) for t in [0, 127^2]: float32's, and a step where t lies past a border.
+__device__ __forceinline__ int adamw_code_m(double t) {
+  float r = rintf(__builtin_amdgcn_sqrtf((float)t));
+  const float s = fmaf(r, r, 0.25f);  // exact
+  if (t > (double)(s + r)) r += 1.0f;
+  if (r > 0.0f && t < (double)(s - r)) r -= 1.0f;
+  return min((int)r, 127);
+}
+// rint(sqrt(sqrt(t))) for t in [0, 255^4].
+__device__ __forceinline__ int adamw_code_v(double t) {
+  float r = rintf(__builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf((float)t)));
+  const double hi = (double)(r + 0.5f), lo = (double)(r - 0.5f);
+  const double hi2 = hi * hi, lo2 = lo * lo;
+  if (t > hi2 * hi2) r += 1.0f;
+  if (r > 0.0f && t < lo2 * lo2) r -= 1.0f;
+  return min((int)r, 255);
+}
+
+template <typename TG, int BITS>
+__global__ __launch_bounds__(256) void k_adamw(AdamwTable a) {
+#pragma clang fp contract(off)
+  const uint32_t blk = blockIdx.x * 8 + threadIdx.x / 32;
+  // the tensor: a lane looks at each one's first block
+  const uint32_t first = a.first[__lane_id()];
+  const uint32_t lead = blockIdx.x * 8 + (threadIdx.x / 64) * 2;  // the wavefront's two blocks
+  const int t0 = __popcll(__ballot(first <= lead)) - 1, t1 = __popcll(__ballot(first <= lead + 1)) - 1;
+  if (blk >= a.blocks) return;  // whole half wavefronts, which do not exchange with each other
+  const int t = (threadIdx.x & 32) ? t1 : t0;
+  const int64_t u0 = (int64_t)(blk - a.first[t]) * kAdamwBlock + (threadIdx.x & 31) * 8;
+  const int64_t left = a.n[t] - u0;
+  const int n = left >= 8 ? 8 : left > 0 ? (int)left : 0;
+  const double keep = a.keep[t], scale = a.grad_scale ? (double)*a.grad_scale : 1.0;
+  float p[8], gf[8];
+  adamw_load(a.param[t] + u0, n, p);
+  adamw_load(static_cast<const TG*>(a.grad[t]) + u0, n, gf);
+  const int64_t at = (int64_t)blk * kAdamwBlock + (threadIdx.x & 31) * 8;
+  double m[8], v[8];
+  if constexpr (BITS == 32) {
+    float mf[8], vf[8];
+    load_elems<8>(static_cast<const float*>(a.m) + at, mf);
+    load_elems<8>(static_cast<const float*>(a.v) + at, vf);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      m[i] = mf[i];
+      v[i] = vf[i];
+    }
+  } else {
+    const uint2 cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.m) + at);
+    const uint2 cv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.v) + at);
+    const float2 top = a.bounds[blk];
+    const double sm = (double)top.x * (1.0 / kAdamwM), sv = (double)top.y * (1.0 / kAdamwV);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t wm = i < 4 ? cm.x : cm.y, wv = i < 4 ? cv.x : cv.y;
+      m[i] = sm * adamw_m_of((int)(int8_t)(wm >> (8 * (i & 3))));
+      v[i] = sv * adamw_v_of((wv >> (8 * (i & 3))) & 255u);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const double g = (double)gf[i] * scale;
+    m[i] = a.b1 * m[i] + a.c1 * g;
+    v[i] = a.b2 * v[i] + a.c2 * (g * g);
+    const double den = sqrt(v[i] * a.ib2) + a.eps;
+    p[i] = (float)((double)p[i] * keep - a.lr * (m[i] * a.ib1 / den));
+  }
+  adamw_store(a.param[t] + u0, n, p);
+  if (a.copy[t]) adamw_store(a.copy[t] + u0, n, p);
+  if constexpr (BITS == 32) {
+    float mf[8], vf[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      mf[i] = i < n ? (float)m[i] : 0.0f;
+      vf[i] = i < n ? (float)v[i] : 0.0f;
+    }
+    store_elems<8>(static_cast<float*>(a.m) + at, mf);
+    store_elems<8>(static_cast<float*>(a.v) + at, vf);
+  } else {
+    float mt = 0.0f, vt = 0.0f;
+    bool bm = false, bv = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= n) m[i] = v[i] = 0.0;
+      const float x = fabsf((float)m[i]), y = (float)v[i];
+      bm |= !(x < INFINITY);
+      bv |= !(y < INFINITY);
+      mt = fmaxf(mt, x);
+      vt = fmaxf(vt, y);
+    }
+    const uint64_t half = (threadIdx.x & 32) ? 0xFFFFFFFF00000000ull : 0xFFFFFFFFull;
+    mt = (__ballot(bm) & half) ? __int_as_float(0x7fc00000) : half_top(mt);
+    vt = (__ballot(bv) & half) ? __int_as_float(0x7fc00000) : half_top(vt);
+    const double im = mt > 0.0f ? kAdamwM / (double)mt : 0.0, iv = vt > 0.0f ? kAdamwV / (double)vt : 0.0;
+    uint32_t cm[2] = {0, 0}, cv[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // a bound of NaN or 0 makes codes of 0
+      int c = im > 0.0 ? adamw_code_m(fabs(m[i]) * im) : 0;
+      c = m[i] < 0.0 ? -c : c;
+      int e = iv > 0.0 ? adamw_code_v(v[i] * iv) : 0;
+      if (iv > 0.0 && v[i] > 0.0) e = max(e, 1);
+      cm[i >> 2] |= ((uint32_t)c & 255u) << (8 * (i & 3));
+      cv[i >> 2] |= (uint32_t)e << (8 * (i & 3));
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + at) = make_uint2(cm[0], cm[1]);
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + at) = make_uint2(cv[0], cv[1]);
+    if ((threadIdx.x & 31) == 0) a.bounds[blk] = make_float2(mt, vt);
+  }
+}
+
+// What the codes stand for, rounded once.
+__global__ __launch_bounds__(256) void k_adamw_moments(uint32_t blocks, const uint8_t* __restrict__ m,
+                                                       const uint8_t* __restrict__ v,
+                                                       const float2* __restrict__ bounds, float* __restrict__ out_m,
+                                                       float* __restrict__ out_v) {
+#pragma clang fp contract(off)
+  const uint32_t blk = blockIdx.x * 8 + threadIdx.x / 32;
+  if (blk >= blocks) return;
+  const int64_t at = (int64_t)blk * kAdamwBlock + (threadIdx.x & 31) * 8;
+  const uint2 cm = *reinterpret_cast<const uint2*>(m + at), cv = *reinterpret_cast<const uint2*>(v + at);
+  const float2 top = bounds[blk];
+  const double sm = (double)top.x * (1.0 / kAdamwM), sv = (double)top.y * (1.0 / kAdamwV);
+  float mf[8], vf[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t wm = i < 4 ? cm.x : cm.y, wv = i < 4 ? cv.x : cv.y;
+    mf[i] = (float)(sm * adamw_m_of((int)(int8_t)(wm >> (8 * (i & 3)))));
+    vf[i] = (float)(sv * adamw_v_of((wv >> (8 * (i & 3))) & 255u));
+  }
+  store_elems<8>(out_m + at, mf);
+  store_elems<8>(out_v + at, vf);
+}
+
+hipError_t launch_adamw(int count, const gs_adamw_tensor* tensors, int grad_type, int bits, void* m, void* v,
+                        float* bounds, const gs_adamw_params& h, const float* grad_scale, hipStream_t s) {
+  AdamwTable a{};
+  a.grad_scale = grad_scale;
+  a.b1 = h.beta1;
+  a.b2 = h.beta2;
+  a.c1 = 1.0 - h.beta1;
+  a.c2 = 1.0 - h.beta2;
+  a.ib1 = 1.0 / (1.0 - pow(h.beta1, (double)h.step));
+  a.ib2 = 1.0 / (1.0 - pow(h.beta2, (double)h.step));
+  a.lr = h.lr;
+  a.eps = h.eps;
+  char *mp = static_cast<char*>(m), *vp = static_cast<char*>(v);
+  const int64_t each = (int64_t)kAdamwBlock * (bits / 8);
+  int64_t done = 0;  // blocks of the launches before
+  for (int i = 0; i < count;) {
+    int k = 0;
+    uint32_t blocks = 0;
+    for (; i < count && k < kAdamwTensors; ++i) {
+      const gs_adamw_tensor& x = tensors[i];
+      if (x.n == 0) continue;
+      a.param[k] = x.param;
+      a.grad[k] = x.grad;
+      a.copy[k] = static_cast<__bf16*>(x.copy);
+      a.n[k] = x.n;
+      a.keep[k] = 1.0 - h.lr * x.decay;
+      a.first[k++] = blocks;
+      blocks += (uint32_t)((x.n + kAdamwBlock - 1) / kAdamwBlock);
+    }
+    if (!blocks) break;
+    for (; k < kAdamwTensors; ++k) a.first[k] = ~0u;
+    a.blocks = blocks;
+    a.m = mp + done * each;
+    a.v = vp + done * each;
+    a.bounds = reinterpret_cast<float2*>(bounds) + (bits == 8 ? done : 0);
+    const unsigned groups = (blocks + 7) / 8;
+    if (bits == 8)
+      grad_type == GS_BF16 ? k_adamw<__bf16, 8><<<groups, 256, 0, s>>>(a) : k_adamw<float, 8><<<groups, 256, 0, s>>>(a);
+    else
+      grad_type == GS_BF16 ? k_adamw<__bf16, 32><<<groups, 256, 0, s>>>(a) : k_adamw<float, 32><<<groups, 256, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    done += blocks;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_adamw_moments(int64_t blocks, const int8_t* m, const uint8_t* v, const float* bounds, float* out_m,
+                                float* out_v, hipStream_t s) {
+  k_adamw_moments<<<(unsigned)((blocks + 7) / 8), 256, 0, s>>>((uint32_t)blocks, reinterpret_cast<const uint8_t*>(m), v,
+                                                               reinterpret_cast<const float2*>(bounds), out_m, out_v);
+  return hipGetLastError();
+}
+
+}  // namespace gs

@@ -1,0 +1,361 @@
+// gs_layer_norm.hip -- layer norm of rows and its gradient, with the sums of the weight's and the
+// bias's gradient over all rows, for gfx950.
+//
+//   xh = (x - mean) rstd, y = w xh + b;
+//   back: g = w dy, dx = rstd (g - mean(g) - xh mean(g xh)), dw = sum dy xh, db = sum dy.
+//
+// A row belongs to G lanes, J chunks of eight units each, and stays in their registers: one read of
+// memory, then the mean, then the sums over d = x - mean (its squares, and back also g and g d, all
+// in one exchange: g xh is g d rstd).  The variance is taken about the mean, not as a difference of
+// sums, so that rows far from 0 lose nothing.
+//
+// Chunks are loaded as vectors at any alignment (the memory takes them; a row of odd length starts
+// anywhere); the row's last chunk, where it is short, goes unit by unit.
+#include <algorithm>
+
+#include "gs_device.h"
+#include "gs_elem.h"
+#include "gs_wave.h"
+
+namespace gs {
+
+struct LayerNormArgs {
+  int64_t rows;
+  const void *x, *dy;
+  void* y;  // back: dx
+  int64_t xs, ds, ys;
+  const float *w, *b;
+  float* part;  // [workgroups][2][padded width]
+  float *dw, *db;
+  int32_t width;
+  float eps, inv_width;
+};
+
+constexpr int layer_norm_threads(int g) { return g > 256 ? g : 256; }
+
+// Sums over the G lanes of a row, in each of them.
+template <int G, int N>
+struct RowSum {
+  static constexpr int kWaves = G / kWave;
+  float (*space)[kWaves > 0 ? kWaves : 1][N];  // two of them, taken in turn: one barrier an exchange
+  int turn = 0;
+
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] += dpp_get<0xB1, 0xF>(v[i]);
+      v[i] += dpp_get<0x4E, 0xF>(v[i]);
+      v[i] += dpp_get<0x141, 0xF>(v[i]);
+      v[i] += dpp_get<0x140, 0xF>(v[i]);  // every lane of a row of 16 has its sum
+    }
+    if constexpr (G >= kWave) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        v[i] += __shfl_xor(v[i], 16, 64);
+        v[i] += __shfl_xor(v[i], 32, 64);
+      }
+    }
+    if constexpr (G > kWave) {
+      if (__lane_id() == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) space[turn][threadIdx.x / kWave][i] = v[i];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += space[turn][w][i];
+      turn ^= 1;
+    }
+  }
+};
+
+// The eight units at p, of which n exist (0: none); a vector load at any alignment.
+template <typename T>
+__device__ __forceinline__ void load_units(const T* p, int n, float (&x)[8]) {
+  if (n >= 8) {
+    typedef T V __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
+    constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < 8; i += kPer) {
+      const V v = *reinterpret_cast<const V*>(p + i);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) x[i + j] = (float)v[j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = i < n ? (float)p[i] : 0.0f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_units(T* p, int n, const float (&x)[8]) {
+  if (n >= 8) {
+    typedef T V __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
+    constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < 8; i += kPer) {
+      V v;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) v[j] = (T)x[i + j];
+      *reinterpret_cast<V*>(p + i) = v;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = (T)x[i];
+  }
+}
+
+template <typename T, int G, int J, bool BWD>
+__global__ __launch_bounds__(layer_norm_threads(G)) void k_layer_norm(LayerNormArgs a) {
+  constexpr int kThreads = layer_norm_threads(G), kRows = kThreads / G;  // rows of a workgroup at once
+  constexpr int kWaves = G / kWave > 0 ? G / kWave : 1;
+  __shared__ float space1[2][kWaves][1], space3[2][kWaves][BWD ? 3 : 1];
+  RowSum<G, 1> sum_x{space1};
+  RowSum<G, BWD ? 3 : 1> sum_d{space3};
+  const int lane = threadIdx.x % G, sub = threadIdx.x / G;
+  int n[J];  // units of each chunk
+#pragma unroll
+  for (int j = 0; j < J; ++j) n[j] = min(max(a.width - (lane + G * j) * 8, 0), 8);
+  float w[J][8], b[J][8], dw[J][8] = {}, db[J][8] = {};
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[j][i] = 1.0f;
+      b[j][i] = 0.0f;
+    }
+    if (a.w) load_units(a.w + (lane + G * j) * 8, n[j], w[j]);
+    if (!BWD && a.b) load_units(a.b + (lane + G * j) * 8, n[j], b[j]);
+  }
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  for (int64_t row = (int64_t)blockIdx.x * kRows + sub; row < a.rows; row += step) {  // uniform over the row's lanes
+    float x[J][8], g[J][8], s[1] = {0.0f};
+    const T* xp = static_cast<const T*>(a.x) + row * a.xs + lane * 8;
+#pragma unroll
+    for (int j = 0; j < J; ++j) load_units(xp + G * j * 8, n[j], x[j]);
+    if constexpr (BWD) {
+      const T* gp = static_cast<const T*>(a.dy) + row * a.ds + lane * 8;
+#pragma unroll
+      for (int j = 0; j < J; ++j) load_units(gp + G * j * 8, n[j], g[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[0] += x[j][i];
+    sum_x(s);
+    const float mean = s[0] * a.inv_width;
+    float t[BWD ? 3 : 1] = {};
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = i < n[j] ? x[j][i] - mean : 0.0f;
+        x[j][i] = d;
+        t[0] = fmaf(d * a.inv_width, d, t[0]);  // the mean of squares: their sum overflows before it
+        if constexpr (BWD) {
+          const float gw = g[j][i] * w[j][i];
+          t[1] += gw;
+          t[2] = fmaf(gw, d, t[2]);
+        }
+      }
+    sum_d(t);
+    const float rstd = 1.0f / sqrtf(t[0] + a.eps);
+    T* yp = static_cast<T*>(a.y) + row * a.ys + lane * 8;
+    if constexpr (!BWD) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[j][i] = fmaf(x[j][i] * rstd, w[j][i], b[j][i]);
+        store_units(yp + G * j * 8, n[j], x[j]);
+      }
+    } else {
+      const float mg = t[1] * a.inv_width, mgx = t[2] * rstd * a.inv_width;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        float r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float xh = x[j][i] * rstd;
+          dw[j][i] = fmaf(g[j][i], xh, dw[j][i]);
+          db[j][i] += g[j][i];
+          r[i] = rstd * (fmaf(g[j][i], w[j][i], -mg) - xh * mgx);
+        }
+        store_units(yp + G * j * 8, n[j], r);
+      }
+    }
+  }
+  if constexpr (BWD) {
+    if (!a.dw && !a.db) return;
+    // the workgroup's sum for each unit, over its rows at once in a fixed order
+    constexpr int kUnits = 8 * G * J;
+    const int padded = (a.width + 7) & ~7;
+    float* part = a.part + (int64_t)blockIdx.x * 2 * padded;
+    if constexpr (kRows > 1) {
+      __shared__ float both[2][kUnits];
+#pragma unroll
+      for (int d = G; d < kWave; d <<= 1)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            dw[j][i] += __shfl_xor(dw[j][i], d, 64);
+            db[j][i] += __shfl_xor(db[j][i], d, 64);
+          }
+      for (int v = 0; v < kThreads / kWave; ++v) {
+        if ((int)threadIdx.x / kWave == v && (int)__lane_id() < G) {
+#pragma unroll
+          for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int u = (lane + G * j) * 8 + i;
+              both[0][u] = v ? both[0][u] + dw[j][i] : dw[j][i];
+              both[1][u] = v ? both[1][u] + db[j][i] : db[j][i];
+            }
+        }
+        __syncthreads();
+      }
+      for (int u = threadIdx.x; u < a.width; u += kThreads) {
+        if (gridDim.x > 1) {
+          part[u] = both[0][u];
+          part[padded + u] = both[1][u];
+        } else {
+          if (a.dw) a.dw[u] = both[0][u];
+          if (a.db) a.db[u] = both[1][u];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int u = (lane + G * j) * 8;
+        if (gridDim.x > 1) {
+          if (n[j] > 0) {
+            store_elems<8>(part + u, dw[j]);
+            store_elems<8>(part + padded + u, db[j]);
+          }
+        } else {
+          if (a.dw) store_units(a.dw + u, n[j], dw[j]);
+          if (a.db) store_units(a.db + u, n[j], db[j]);
+        }
+      }
+    }
+  }
+}
+
+// dw and db from the workgroups' parts, in a fixed order: 32 units a workgroup, 32 threads a unit, then
+// a tree.
+__global__ __launch_bounds__(1024) void k_layer_norm_join(const float* __restrict__ part, int width, int padded,
+                                                          int parts, float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ float sum[16][32];
+  float* const to = blockIdx.y ? db : dw;
+  if (!to) return;
+  const int u = blockIdx.x * 32 + (threadIdx.x & 31), row = threadIdx.x >> 5;
+  float t = 0.0f;
+  if (u < width) {
+    const float* p = part + (int64_t)blockIdx.y * padded + u;
+    int k = row;
+    for (; k + 32 * 7 < parts; k += 32 * 8) {  // eight loads in flight
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = p[(int64_t)(k + 32 * i) * 2 * padded];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t += x[i];
+    }
+    for (; k < parts; k += 32) t += p[(int64_t)k * 2 * padded];
+  }
+  t += __shfl_xor(t, 32, 64);
+  if (__lane_id() < 32) sum[threadIdx.x >> 6][threadIdx.x & 31] = t;
+  __syncthreads();
+  if (threadIdx.x < 32 && u < width) {
+    t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += sum[i][threadIdx.x];
+    to[u] = t;
+  }
+}
+
+__global__ void k_layer_norm_none(int width, float* __restrict__ dw, float* __restrict__ db) {
+  const int u = blockIdx.x * 256 + threadIdx.x;
+  if (u >= width) return;
+  if (dw) dw[u] = 0.0f;
+  if (db) db[u] = 0.0f;
+}
+
+namespace {
+
+struct LayerNormPlan {
+  int g, j;
+};
+
+// Lanes of a row and their chunks.
+LayerNormPlan layer_norm_plan(int64_t, int width) {
+  const int chunks = (width + 7) / 8;
+  if (chunks <= 16) return {16, 1};
+  if (chunks <= 64) return {64, 1};
+  if (chunks <= 128) return {64, 2};
+  if (chunks <= 256) return {256, 1};
+  if (chunks <= 512) return {256, 2};
+  if (chunks <= 1024) return {1024, 1};
+  return {1024, 2};
+}
+
+int layer_norm_blocks(int64_t rows, int width, bool bwd) {
+  const LayerNormPlan p = layer_norm_plan(rows, width);
+  const int64_t each = layer_norm_threads(p.g) / p.g, need = (rows + each - 1) / each;
+  return (int)std::min<int64_t>(need, bwd ? 512 : 65536);
+}
+
+template <typename T, bool BWD>
+void layer_norm_pick(LayerNormPlan p, const LayerNormArgs& a, int blocks, hipStream_t s) {
+  const dim3 grid(blocks);
+  if (p.g == 16) k_layer_norm<T, 16, 1, BWD><<<grid, 256, 0, s>>>(a);
+  else if (p.g == 64 && p.j == 1) k_layer_norm<T, 64, 1, BWD><<<grid, 256, 0, s>>>(a);
+  else if (p.g == 64) k_layer_norm<T, 64, 2, BWD><<<grid, 256, 0, s>>>(a);
+  else if (p.g == 256 && p.j == 1) k_layer_norm<T, 256, 1, BWD><<<grid, 256, 0, s>>>(a);
+  else if (p.g == 256) k_layer_norm<T, 256, 2, BWD><<<grid, 256, 0, s>>>(a);
+  else if (p.j == 1) k_layer_norm<T, 1024, 1, BWD><<<grid, 1024, 0, s>>>(a);
+  else k_layer_norm<T, 1024, 2, BWD><<<grid, 1024, 0, s>>>(a);
+}
+
+}  // namespace
+
+size_t layer_norm_workspace_bytes(int64_t rows, int width) {
+  if (rows == 0 || width == 0) return 0;
+  const int blocks = layer_norm_blocks(rows, width, true);
+  return blocks > 1 ? (size_t)blocks * 2 * ((width + 7) & ~7) * sizeof(float) : 0;
+}
+
+// dy NULL: forward.
+hipError_t launch_layer_norm(int64_t rows, int width, int type, float eps, const void* dy, int64_t ds, const void* x,
+                             int64_t xs, const float* w, const float* b, void* y, int64_t ys, float* dw, float* db,
+                             void* ws, hipStream_t s) {
+  if (rows == 0) {
+    k_layer_norm_none<<<(width + 255) / 256, 256, 0, s>>>(width, dw, db);
+    return hipGetLastError();
+  }
+  LayerNormArgs a{};
+  a.rows = rows;
+  a.x = x; a.xs = xs;
+  a.dy = dy; a.ds = ds;
+  a.y = y; a.ys = ys;
+  a.w = w; a.b = b;
+  a.part = static_cast<float*>(ws);
+  a.dw = dw; a.db = db;
+  a.width = width;
+  a.eps = eps;
+  a.inv_width = 1.0f / (float)width;
+  const LayerNormPlan p = layer_norm_plan(rows, width);
+  const int blocks = layer_norm_blocks(rows, width, dy != nullptr);
+  if (type == GS_BF16)
+    dy ? layer_norm_pick<__bf16, true>(p, a, blocks, s) : layer_norm_pick<__bf16, false>(p, a, blocks, s);
+  else
+    dy ? layer_norm_pick<float, true>(p, a, blocks, s) : layer_norm_pick<float, false>(p, a, blocks, s);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || blocks == 1 || (!dw && !db)) return e;
+  k_layer_norm_join<<<dim3((width + 31) / 32, 2), 1024, 0, s>>>(a.part, width, (width + 7) & ~7, blocks, dw, db);
+  return hipGetLastError();
+}
+
+}  // namespace gs

@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include "gs_attn.h"
+#include "gs_group.h"
 
 namespace gs {
 size_t norm_workspace_bytes(const gs_norm_rotate& p);
@@ -24,6 +25,16 @@ hipError_t launch_gate8_fwd(bool vec, int64_t rows, int64_t width, int act, int 
 hipError_t launch_gate8_bwd(bool vec, int64_t rows, int64_t width, int act, int type, const void* dy, int64_t dys,
                             const uint8_t* codes, const float* bounds, void* dgate, int64_t gs, void* dup, int64_t us,
                             void* y, int64_t ys, hipStream_t s);
+size_t layer_norm_workspace_bytes(int64_t rows, int width);
+hipError_t launch_layer_norm(int64_t rows, int width, int type, float eps, const void* dy, int64_t ds, const void* x,
+                             int64_t xs, const float* w, const float* b, void* y, int64_t ys, float* dw, float* db,
+                             void* ws, hipStream_t s);
+int64_t group_tiles(bool over_rows, int64_t rows, int64_t m, int64_t n, int64_t groups);
+hipError_t launch_group(bool over_rows, const GroupArgs& a, int type, hipStream_t s);
+hipError_t launch_adamw(int count, const gs_adamw_tensor* tensors, int grad_type, int bits, void* m, void* v,
+                        float* bounds, const gs_adamw_params& h, const float* grad_scale, hipStream_t s);
+hipError_t launch_adamw_moments(int64_t blocks, const int8_t* m, const uint8_t* v, const float* bounds, float* out_m,
+                                float* out_v, hipStream_t s);
 }  // namespace gs
 
 using namespace gs;
@@ -306,6 +317,183 @@ gs_status gs_gate8_bwd(int64_t rows, int64_t width, int32_t act, int32_t type, c
     return GS_ERR_INVALID_ARG;
   return status_of(launch_gate8_bwd(vec, rows, width, act, type, dy, dy_stride, codes, bounds, dgate, dgate_stride, dup,
                                     dup_stride, y, y_stride, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
+constexpr int64_t kMostWidth = 16384;  // units of a row that its lanes' registers hold
+
+gs_status layer_norm_shape(int64_t rows, int64_t width, int32_t type, float eps) {
+  if (rows < 0 || width < 0 || (type != GS_BF16 && type != GS_F32) || !(eps >= 0.0f) || !(eps < INFINITY)) return GS_ERR_INVALID_ARG;
+  return rows >= kMost || width > kMostWidth ? GS_ERR_OVERFLOW : GS_OK;
+}
+
+// An input's rows: whole elements, and any stride that is not negative.
+bool rows_in_ok(const void* p, int64_t stride, int64_t rows, int type) {
+  return p && on(p, size_of(type)) && (rows <= 1 || stride >= 0);
+}
+// An output's: they do not overlap.
+bool rows_ok(const void* p, int64_t stride, int64_t rows, int64_t width, int type) {
+  bool vec = true;
+  return matrix_ok(p, stride, rows, width, type, &vec);
+}
+
+}  // namespace
+
+gs_status gs_layer_norm_fwd(int64_t rows, int64_t width, int32_t type, float eps, const void* x, int64_t x_stride,
+                            const float* w, const float* b, void* y, int64_t y_stride, void* stream) {
+  const gs_status st = layer_norm_shape(rows, width, type, eps);
+  if (st != GS_OK) return st;
+  if (!rows || !width) return GS_OK;
+  if (!rows_in_ok(x, x_stride, rows, type) || !rows_ok(y, y_stride, rows, width, type) || !on(w, 4) || !on(b, 4))
+    return GS_ERR_INVALID_ARG;
+  return status_of(launch_layer_norm(rows, (int)width, type, eps, nullptr, 0, x, x_stride, w, b, y, y_stride, nullptr, nullptr,
+                                     nullptr, static_cast<hipStream_t>(stream)));
+}
+
+size_t gs_layer_norm_workspace_bytes(int64_t rows, int64_t width) {
+  return layer_norm_shape(rows, width, GS_F32, 0.0f) == GS_OK ? layer_norm_workspace_bytes(rows, (int)width) : 0;
+}
+
+gs_status gs_layer_norm_bwd(int64_t rows, int64_t width, int32_t type, float eps, const void* dy, int64_t dy_stride,
+                            const void* x, int64_t x_stride, const float* w, void* dx, int64_t dx_stride, float* dw,
+                            float* db, void* workspace, size_t workspace_bytes, void* stream) {
+  const gs_status st = layer_norm_shape(rows, width, type, eps);
+  if (st != GS_OK) return st;
+  if (!width || (!rows && !dw && !db)) return GS_OK;
+  if (!on(w, 4) || !on(dw, 4) || !on(db, 4)) return GS_ERR_INVALID_ARG;
+  if (rows) {
+    if (!rows_in_ok(dy, dy_stride, rows, type) || !rows_in_ok(x, x_stride, rows, type) ||
+        !rows_ok(dx, dx_stride, rows, width, type))
+      return GS_ERR_INVALID_ARG;
+    const size_t need = dw || db ? layer_norm_workspace_bytes(rows, (int)width) : 0;
+    if (need && (!workspace || !on(workspace, 16) || workspace_bytes < need)) return GS_ERR_WORKSPACE;
+  }
+  return status_of(launch_layer_norm(rows, (int)width, type, eps, dy, dy_stride, x, x_stride, w, nullptr, dx, dx_stride, dw, db,
+                                     workspace, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
+gs_status group_shape(const gs_group_mm* p, bool bwd) {
+  if (!p || p->rows < 0 || p->k < 0 || p->n < 0 || p->groups < 0 || (p->type != GS_BF16 && p->type != GS_F32)) return GS_ERR_INVALID_ARG;
+  if (!p->offsets || !on(p->offsets, 4)) return GS_ERR_INVALID_ARG;
+  if (p->rows >= kMost - 256 || p->k > kGroups || p->n > kGroups || p->groups > 65536) return GS_ERR_OVERFLOW;
+  // each factor is below 2^31, the counts below 2^62
+  if (!bwd && group_tiles(false, p->rows, p->rows, p->n, p->groups) >= kGroups) return GS_ERR_OVERFLOW;
+  if (bwd && (group_tiles(false, p->rows, p->rows, p->k, p->groups) >= kGroups ||
+              group_tiles(true, p->rows, p->k, p->n, p->groups) >= kGroups))
+    return GS_ERR_OVERFLOW;
+  return GS_OK;
+}
+
+// Weights [groups][k][n], one of their axes dense; as an output the elements lie apart.
+bool weights_ok(gs_weights* w, int64_t groups, int64_t k, int64_t n, int type, bool out) {
+  if (!groups || !k || !n) return true;
+  if (groups == 1) w->group_stride = 0;
+  if (k == 1 && n == 1) w->k_stride = w->n_stride = 1;
+  else if (k == 1) w->k_stride = w->n_stride == 1 ? n : 1;
+  else if (n == 1) w->n_stride = w->k_stride == 1 ? k : 1;
+  if (!w->data || !on(w->data, size_of(type)) || w->group_stride < 0 || w->k_stride < 0 || w->n_stride < 0) return false;
+  if (w->n_stride == 1 ? w->k_stride < n && k > 1 : w->k_stride != 1 || (w->n_stride < k && n > 1)) return false;
+  const int64_t most = w->n_stride == 1 ? times(k - 1, w->k_stride) : times(n - 1, w->n_stride);  // of the last row (or column)
+  return most >= 0 && (!out || groups == 1 || w->group_stride >= most + (w->n_stride == 1 ? n : k));
+}
+
+GroupArgs group_args(const gs_group_mm& p) {
+  GroupArgs a{};
+  a.rows = (int32_t)p.rows;
+  a.groups = p.groups;
+  a.offsets = p.offsets;
+  return a;
+}
+
+}  // namespace
+
+size_t gs_group_mm_fwd_workspace_bytes(const gs_group_mm* p) {
+  return 0;
+}
+
+gs_status gs_group_mm_fwd(const gs_group_mm* p, const void* x, int64_t x_stride, gs_weights w, void* y,
+                          int64_t y_stride, void* workspace, size_t workspace_bytes, void* stream) {
+  const gs_status st = group_shape(p, false);
+  if (st != GS_OK) return st;
+  if (!p->rows || !p->n) return GS_OK;
+  if (!rows_ok(y, y_stride, p->rows, p->n, p->type) || (p->k && !rows_in_ok(x, x_stride, p->rows, p->type)) ||
+      !weights_ok(&w, p->groups, p->k, p->n, p->type, false))
+    return GS_ERR_INVALID_ARG;
+  GroupArgs a = group_args(*p);
+  a.a = x; a.a_m = x_stride; a.a_k = 1;
+  a.b = w.data; a.b_g = w.group_stride; a.b_k = w.k_stride; a.b_n = w.n_stride;
+  a.c = y; a.c_m = y_stride; a.c_n = 1;
+  a.m = a.rows; a.n = (int32_t)p->n; a.k = (int32_t)p->k;
+  return status_of(launch_group(false, a, p->type, static_cast<hipStream_t>(stream)));
+}
+
+size_t gs_group_mm_bwd_workspace_bytes(const gs_group_mm* p) {
+  return 0;
+}
+
+gs_status gs_group_mm_bwd(const gs_group_mm* p, const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                          gs_weights w, void* dx, int64_t dx_stride, gs_weights dw, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  const gs_status st = group_shape(p, true);
+  if (st != GS_OK) return st;
+  const bool has_dx = dx && p->rows && p->k, has_dw = dw.data && p->groups && p->k && p->n;
+  if (p->rows && p->n && (has_dx || has_dw) && !rows_in_ok(dy, dy_stride, p->rows, p->type)) return GS_ERR_INVALID_ARG;
+  if (has_dx && (!rows_ok(dx, dx_stride, p->rows, p->k, p->type) || !weights_ok(&w, p->groups, p->k, p->n, p->type, false)))
+    return GS_ERR_INVALID_ARG;
+  if (has_dw && ((p->rows && !rows_in_ok(x, x_stride, p->rows, p->type)) || !weights_ok(&dw, p->groups, p->k, p->n, p->type, true)))
+    return GS_ERR_INVALID_ARG;
+  if (has_dx) {
+    GroupArgs a = group_args(*p);
+    a.a = dy; a.a_m = dy_stride; a.a_k = 1;
+    a.b = w.data; a.b_g = w.group_stride; a.b_k = w.n_stride; a.b_n = w.k_stride;
+    a.c = dx; a.c_m = dx_stride; a.c_n = 1;
+    a.m = a.rows; a.n = (int32_t)p->k; a.k = (int32_t)p->n;
+    const gs_status e = status_of(launch_group(false, a, p->type, static_cast<hipStream_t>(stream)));
+    if (e != GS_OK) return e;
+  }
+  if (!has_dw) return GS_OK;
+  GroupArgs a = group_args(*p);
+  a.a = x; a.a_m = 1; a.a_k = x_stride;
+  a.b = dy; a.b_k = dy_stride; a.b_n = 1;
+  a.c = dw.data; a.c_g = dw.group_stride; a.c_m = dw.k_stride; a.c_n = dw.n_stride;
+  a.m = (int32_t)p->k; a.n = (int32_t)p->n; a.k = a.rows;
+  return status_of(launch_group(true, a, p->type, static_cast<hipStream_t>(stream)));
+}
+
+gs_status gs_adamw(int32_t count, const gs_adamw_tensor* tensors, int32_t grad_type, int32_t bits, void* m, void* v,
+                   float* bounds, const gs_adamw_params* hyper, const float* grad_scale, void* stream) {
+  if (count < 0 || (count && !tensors) || !hyper || (grad_type != GS_BF16 && grad_type != GS_F32) || (bits != 8 && bits != 32))
+    return GS_ERR_INVALID_ARG;
+  const gs_adamw_params h = *hyper;
+  if (h.step < 1 || !(h.beta1 >= 0.0 && h.beta1 < 1.0) || !(h.beta2 >= 0.0 && h.beta2 < 1.0) || !(h.eps >= 0.0 && h.eps < INFINITY) ||
+      !isfinite(h.lr) || !on(grad_scale, 4))
+    return GS_ERR_INVALID_ARG;
+  int64_t blocks = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    const gs_adamw_tensor& x = tensors[i];
+    if (x.n < 0 || !isfinite(x.decay)) return GS_ERR_INVALID_ARG;
+    if (!x.n) continue;
+    if (!x.param || !x.grad || !on(x.param, 4) || !on(x.grad, size_of(grad_type)) || !on(x.copy, 2)) return GS_ERR_INVALID_ARG;
+    if (x.n >= (int64_t)1 << 35) return GS_ERR_OVERFLOW;
+    blocks += (x.n + 255) / 256;
+    if (blocks >= (int64_t)1 << 27) return GS_ERR_OVERFLOW;
+  }
+  if (!blocks) return GS_OK;
+  if (!m || !v || !on(m, 16) || !on(v, 16) || (bits == 8 && (!bounds || !on(bounds, 8)))) return GS_ERR_INVALID_ARG;
+  return status_of(launch_adamw(count, tensors, grad_type, bits, m, v, bounds, h, grad_scale, static_cast<hipStream_t>(stream)));
+}
+
+gs_status gs_adamw_moments(int64_t blocks, const int8_t* m, const uint8_t* v, const float* bounds, float* out_m,
+                           float* out_v, void* stream) {
+  if (blocks < 0) return GS_ERR_INVALID_ARG;
+  if (blocks >= (int64_t)1 << 27) return GS_ERR_OVERFLOW;
+  if (!blocks) return GS_OK;
+  if (!m || !v || !bounds || !out_m || !out_v || !on(m, 8) || !on(v, 8) || !on(bounds, 8) || !on(out_m, 16) || !on(out_v, 16))
+    return GS_ERR_INVALID_ARG;
+  return status_of(launch_adamw_moments(blocks, m, v, bounds, out_m, out_v, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -2,17 +2,19 @@
 
 The parts of a decoder layer that predicts Gaussians from images which are not plain matrix
 products: norms of queries and keys with the position rotation, attention of the tokens to the
-encoder's states, and the gated activation that keeps its inputs as 8-bit codes.
+encoder's states, and the gated activation that keeps its inputs as 8-bit codes.  And what trains
+such layers beside them: layer norm, the products of rows with their group's weights (experts), and
+AdamW over all tensors at once.
 
 Tensors are bfloat16 or float32 on the GPU, laid out as include/gs_tokens.h says: vectors dense in
 their last axis, on 16-byte boundaries, any strides else (views of one projection's output are
-taken as they are).  Shapes and types are checked here (the C calls do not see them: ValueError),
+taken as they are; layer_norm and group_mm take any alignment).  Shapes and types are checked here (the C calls do not see them: ValueError),
 everything else by the C calls (raster.GsError).  Work goes to the current stream of the tensors' GPU, or to
 ``stream``, which is one of that GPU; outputs and workspaces that are not given are torch tensors made on that same stream
 (a workspace is given back to torch when the call returns, in stream order).
 
-``norm_rotate``, ``cross_attention`` and ``gated8`` are the same operators as differentiable
-torch functions.  Their gradients come from C calls that torch does not record: second
+``norm_rotate``, ``cross_attention``, ``gated8``, ``layer_norm`` and ``group_mm`` are the same operators as
+differentiable torch functions.  Their gradients come from C calls that torch does not record: second
 derivatives through them are an error (``once``).
 """
 from __future__ import annotations
@@ -20,6 +22,8 @@ from __future__ import annotations
 import ctypes as C
 import functools
 import math
+import struct
+from array import array
 
 import torch
 
@@ -33,7 +37,9 @@ ACTS = {"silu": 0, "gelu": 1}
 CODE_BLOCK = 256  # units of one (lo, hi) pair
 
 EXPORTS = ("gs_norm_rotate_fwd", "gs_norm_rotate_workspace_bytes", "gs_norm_rotate_bwd", "gs_cross_attn_fwd_workspace_bytes",
-           "gs_cross_attn_fwd", "gs_cross_attn_bwd_workspace_bytes", "gs_cross_attn_bwd", "gs_gate8_fwd", "gs_gate8_bwd")
+           "gs_cross_attn_fwd", "gs_cross_attn_bwd_workspace_bytes", "gs_cross_attn_bwd", "gs_gate8_fwd", "gs_gate8_bwd",
+           "gs_layer_norm_fwd", "gs_layer_norm_workspace_bytes", "gs_layer_norm_bwd", "gs_group_mm_fwd_workspace_bytes",
+           "gs_group_mm_fwd", "gs_group_mm_bwd_workspace_bytes", "gs_group_mm_bwd", "gs_adamw", "gs_adamw_moments")
 
 
 class GsHeads(C.Structure):
@@ -52,6 +58,23 @@ class GsCrossAttn(C.Structure):
                 ("kv_heads", C.c_int32), ("head_dim", C.c_int32), ("type", C.c_int32), ("scale", C.c_float),
                 ("ranges", C.c_void_p), ("ranges_batch_stride", C.c_int64), ("ranges_row_stride", C.c_int64),
                 ("key_mask", C.c_void_p), ("key_mask_batch_stride", C.c_int64)]
+
+
+class GsWeights(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("group_stride", C.c_int64), ("k_stride", C.c_int64), ("n_stride", C.c_int64)]
+
+
+class GsGroupMM(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("k", C.c_int64), ("n", C.c_int64), ("groups", C.c_int32), ("type", C.c_int32),
+                ("offsets", C.c_void_p)]
+
+
+class GsAdamWTensor(C.Structure):
+    _fields_ = [("param", C.c_void_p), ("grad", C.c_void_p), ("copy", C.c_void_p), ("n", C.c_int64), ("decay", C.c_double)]
+
+
+class GsAdamWParams(C.Structure):
+    _fields_ = [("lr", C.c_double), ("beta1", C.c_double), ("beta2", C.c_double), ("eps", C.c_double), ("step", C.c_int64)]
 
 
 _lib = None
@@ -73,6 +96,16 @@ def lib():
         L.gs_cross_attn_bwd.argtypes = [A, H, H, H, H, H, vp, H, H, H, vp, sz, vp]
         L.gs_gate8_fwd.argtypes = [i64, i64, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp]
         L.gs_gate8_bwd.argtypes = [i64, i64, i32, i32, vp, i64, vp, vp, vp, i64, vp, i64, vp, i64, vp]
+        f32, W, G = C.c_float, GsWeights, C.POINTER(GsGroupMM)
+        L.gs_layer_norm_fwd.argtypes = [i64, i64, i32, f32, vp, i64, vp, vp, vp, i64, vp]
+        L.gs_layer_norm_workspace_bytes.argtypes = [i64, i64]
+        L.gs_layer_norm_bwd.argtypes = [i64, i64, i32, f32, vp, i64, vp, i64, vp, vp, i64, vp, vp, vp, sz, vp]
+        L.gs_group_mm_fwd_workspace_bytes.argtypes = [G]
+        L.gs_group_mm_fwd.argtypes = [G, vp, i64, W, vp, i64, vp, sz, vp]
+        L.gs_group_mm_bwd_workspace_bytes.argtypes = [G]
+        L.gs_group_mm_bwd.argtypes = [G, vp, i64, vp, i64, W, vp, i64, W, vp, sz, vp]
+        L.gs_adamw.argtypes = [i32, vp, i32, i32, vp, vp, vp, C.POINTER(GsAdamWParams), vp, vp]
+        L.gs_adamw_moments.argtypes = [i64, vp, vp, vp, vp, vp, vp]
         for name in EXPORTS:
             getattr(L, name).restype = sz if name.endswith("_bytes") else i32
         _lib = L
@@ -339,6 +372,231 @@ def gate8_bwd(dy, codes, bounds, act: str = "silu", with_y: bool = True, dgate=N
     return dgate, dup, y
 
 
+# -- layer norm ------------------------------------------------------------------------------
+
+
+def _matrix(x):
+    if x.dim() != 2:
+        _refuse("matrices [rows][width]")
+    return x.shape
+
+
+def layer_norm_fwd(x, w=None, b=None, eps: float = 1e-5, out=None, stream=None):
+    """gs_layer_norm_fwd: rows of x [rows, width] with mean 0 and variance 1, times w, plus b (float32 [width]; None: 1
+    and 0).  ``out``: a tensor to write to (may be x)."""
+    if stream is not None:
+        return _on(stream, layer_norm_fwd, x, w, b, eps, out)
+    rows, width = _matrix(x)
+    ty = _type(x)
+    xs = _stride(x, x, rows, width)
+    if w is not None:
+        _floats(w, (width,), x, "w")
+    if b is not None:
+        _floats(b, (width,), x, "b")
+    if out is None:
+        out = torch.empty((rows, width), dtype=x.dtype, device=x.device)
+    _launch("gs_layer_norm_fwd", x, rows, width, ty, eps, x.data_ptr(), xs, _ptr(w), _ptr(b), out.data_ptr(), _stride(out, x, rows, width))
+    return out
+
+
+def layer_norm_bwd(dy, x, w=None, eps: float = 1e-5, with_dw: bool = True, with_db: bool = True, dx=None, workspace=None,
+                   stream=None) -> tuple:
+    """gs_layer_norm_bwd: (dx, dw or None, db or None) from the forward call's inputs and the gradient of its result;
+    ``dx``: a tensor to write to (may be dy or x)."""
+    if stream is not None:
+        return _on(stream, layer_norm_bwd, dy, x, w, eps, with_dw, with_db, dx, workspace)
+    rows, width = _matrix(x)
+    ty = _type(x)
+    xs, ds = _stride(x, x, rows, width), _stride(dy, x, rows, width)
+    if w is not None:
+        _floats(w, (width,), x, "w")
+    if dx is None:
+        dx = torch.empty((rows, width), dtype=x.dtype, device=x.device)
+    dw = torch.empty(width, dtype=torch.float32, device=x.device) if with_dw else None
+    db = torch.empty(width, dtype=torch.float32, device=x.device) if with_db else None
+    ws, n = _workspace(workspace, lib().gs_layer_norm_workspace_bytes(rows, width) if with_dw or with_db else 0, x)
+    _launch("gs_layer_norm_bwd", x, rows, width, ty, eps, dy.data_ptr(), ds, x.data_ptr(), xs, _ptr(w), dx.data_ptr(),
+            _stride(dx, x, rows, width), _ptr(dw), _ptr(db), _ptr(ws), n)
+    return dx, dw, db
+
+
+# -- products grouped by rows ----------------------------------------------------------------
+
+
+def _weights(w, x, k, n=None) -> GsWeights:
+    if w.dim() != 3:
+        _refuse("weights [groups][k][n]")
+    _same(x, w, (w.shape[0], k, w.shape[2] if n is None else n))
+    g, i, j = w.stride()
+    if j != 1 and i != 1 and w.shape[1] > 1 and w.shape[2] > 1:
+        _refuse("weights with one of their last two axes dense")
+    return GsWeights(w.data_ptr(), g, i, j)
+
+
+def _group_shape(x, w, offsets) -> tuple:
+    rows, k = _matrix(x)
+    ty = _type(x)
+    ww = _weights(w, x, k)
+    groups, _, n = w.shape
+    if (offsets.dtype != torch.int32 or offsets.shape != (groups + 1,) or not offsets.is_contiguous()
+            or offsets.get_device() != x.get_device()):
+        _refuse("offsets: int32 [groups + 1], contiguous, on the vectors' GPU")
+    return GsGroupMM(rows, k, n, groups, ty, offsets.data_ptr()), ww
+
+
+def group_mm_fwd(x, w, offsets, out=None, workspace=None, stream=None):
+    """gs_group_mm_fwd: every row of x [rows, k] times its group's weights, y [rows, n].  w [groups, k, n], either of its
+    last two axes dense (a linear layer's weights [groups, n, k] transposed); offsets int32 [groups + 1] on the GPU: group
+    g has the rows from offsets[g] to offsets[g + 1].  Rows of no group get 0."""
+    if stream is not None:
+        return _on(stream, group_mm_fwd, x, w, offsets, out, workspace)
+    p, ww = _group_shape(x, w, offsets)
+    if out is None:
+        out = torch.empty((p.rows, p.n), dtype=x.dtype, device=x.device)
+    ws, n = _workspace(workspace, lib().gs_group_mm_fwd_workspace_bytes(p), x)
+    _launch("gs_group_mm_fwd", x, p, x.data_ptr(), _stride(x, x, p.rows, p.k), ww, out.data_ptr(), _stride(out, x, p.rows, p.n),
+            _ptr(ws), n)
+    return out
+
+
+def group_mm_bwd(dy, x, w, offsets, with_dx: bool = True, with_dw: bool = True, dx=None, dw=None, workspace=None,
+                 stream=None) -> tuple:
+    """gs_group_mm_bwd: (dx or None, dw or None) from the forward call's inputs and the gradient of its result; ``dx``,
+    ``dw``: tensors to write to (dw lies as w does where it is not given)."""
+    if stream is not None:
+        return _on(stream, group_mm_bwd, dy, x, w, offsets, with_dx, with_dw, dx, dw, workspace)
+    p, ww = _group_shape(x, w, offsets)
+    ds = _stride(dy, x, p.rows, p.n)
+    if not with_dx:
+        dx = None
+    elif dx is None:
+        dx = torch.empty((p.rows, p.k), dtype=x.dtype, device=x.device)
+    if not with_dw:
+        dw = None
+    elif dw is None:
+        dw = torch.empty_like(w)
+    ws, n = _workspace(workspace, lib().gs_group_mm_bwd_workspace_bytes(p), x)
+    _launch("gs_group_mm_bwd", x, p, dy.data_ptr(), ds, x.data_ptr(), _stride(x, x, p.rows, p.k), ww, _ptr(dx),
+            0 if dx is None else _stride(dx, x, p.rows, p.k), GsWeights() if dw is None else _weights(dw, x, p.k, p.n),
+            _ptr(ws), n)
+    return dx, dw
+
+
+# -- AdamW over many tensors -----------------------------------------------------------------
+
+
+class AdamWState:
+    """Moments of a list of tensors, one after another, each from a multiple of 256 units on: float32 (bounds None), or
+    int8 and uint8 codes with bounds float32 [blocks, 2]."""
+
+    __slots__ = ("m", "v", "bounds")
+
+    def __init__(self, m, v, bounds=None):
+        self.m, self.v, self.bounds = m, v, bounds
+
+
+def _blocks(tensors) -> int:
+    return sum([(t.numel() + CODE_BLOCK - 1) // CODE_BLOCK for t in tensors])
+
+
+def adamw_state(params, bits: int = 8) -> AdamWState:
+    """Zero moments for ``params``, in 8 bits or in 32."""
+    if bits not in (8, 32):
+        _refuse("bits: 8 or 32")
+    if not params:
+        _refuse("a list of tensors")
+    blocks, dev = _blocks(params), params[0].device
+    if bits == 32:
+        return AdamWState(torch.zeros(blocks * CODE_BLOCK, device=dev), torch.zeros(blocks * CODE_BLOCK, device=dev))
+    return AdamWState(torch.zeros(blocks * CODE_BLOCK, dtype=torch.int8, device=dev), torch.zeros(blocks * CODE_BLOCK, dtype=torch.uint8, device=dev),
+                      torch.zeros((blocks, 2), device=dev))
+
+
+def _state_bits(state, blocks: int, dev: int) -> int:
+    m, v, bounds = state.m, state.v, state.bounds
+    bits = 32 if bounds is None else 8
+    for x, types in ((m, (torch.float32, torch.int8)), (v, (torch.float32, torch.uint8))):
+        if x.dtype != types[bits == 8] or x.shape != (blocks * CODE_BLOCK,) or not x.is_contiguous() or x.get_device() != dev:
+            _refuse("state: adamw_state's of these tensors")
+    if bits == 8 and (bounds.dtype != torch.float32 or bounds.shape != (blocks, 2) or not bounds.is_contiguous() or bounds.get_device() != dev):
+        _refuse("state: adamw_state's of these tensors")
+    return bits
+
+
+def adamw(params, grads, state: AdamWState, lr: float, step: int, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+          weight_decay=0.0, copies=None, grad_scale=None, stream=None) -> None:
+    """gs_adamw: one step over lists of tensors, params (float32) and state in place.  grads: all float32 or all bfloat16, of the
+    params' sizes; ``weight_decay``: a number, or one for each tensor; ``copies``: bfloat16 tensors (or None) that receive
+    the new parameters; ``grad_scale``: a float32 tensor of one element that multiplies the gradients.  Every tensor is
+    contiguous and no two of params and copies overlap."""
+    if stream is not None:
+        return _on(stream, lambda first: adamw(params, grads, state, lr, step, beta1, beta2, eps, weight_decay, copies, grad_scale), state.m)
+    count, dev = len(params), state.m.get_device()
+    if len(grads) != count or (copies is not None and len(copies) != count):
+        _refuse("a gradient (and a copy) for each tensor")
+    if not state.m.is_cuda:
+        _refuse("tensors on the GPU")
+    kind = grads[0].dtype if count else torch.float32
+    ty = TYPES.get(kind)
+    if ty is None:
+        _refuse(f"gradients: bfloat16 or float32, not {kind}")
+    sizes, at, pointers = [], [], []
+    for p, g in zip(params, grads):
+        n = p.numel()
+        if p.dtype != torch.float32 or g.dtype != kind or g.numel() != n or not p.is_contiguous() or not g.is_contiguous():
+            _refuse("params float32, gradients of one type and of the params' sizes, all contiguous")
+        if p.get_device() != dev or g.get_device() != dev:
+            _refuse("one GPU for all of a call's tensors")
+        sizes.append(n)
+        at.append(p.data_ptr())
+        pointers.append(g.data_ptr())
+    to = [0] * count
+    if copies is not None:
+        for i, c in enumerate(copies):
+            if c is not None:
+                if c.dtype != torch.bfloat16 or c.numel() != sizes[i] or not c.is_contiguous() or c.get_device() != dev:
+                    _refuse("copies: bfloat16, of the params' sizes, contiguous, on the params' GPU")
+                to[i] = c.data_ptr()
+    written = [a for a, n in zip(at + to, sizes + sizes) if a and n]
+    if len(set(written)) != len(written):
+        _refuse("a tensor is given twice")
+    bits = _state_bits(state, sum([(n + CODE_BLOCK - 1) // CODE_BLOCK for n in sizes]), dev)
+    if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1 or grad_scale.get_device() != dev):
+        _refuse("grad_scale: one float32 on the params' GPU")
+    if isinstance(weight_decay, (int, float)):
+        decay = [struct.unpack("=q", struct.pack("=d", weight_decay))[0]] * count
+    elif len(weight_decay) != count:
+        _refuse("weight_decay: a number, or one for each tensor")
+    else:
+        decay = struct.unpack(f"={count}q", struct.pack(f"={count}d", *weight_decay))
+    # GsAdamWTensor[count], a column at a time
+    table = array("q", bytes(C.sizeof(GsAdamWTensor) * count))
+    for i, column in enumerate((at, pointers, to, sizes, decay)):
+        table[i::5] = array("q", column)
+    _launch("gs_adamw", state.m, count, table.buffer_info()[0], ty, bits, state.m.data_ptr(), state.v.data_ptr(), _ptr(state.bounds),
+            GsAdamWParams(lr, beta1, beta2, eps, int(step)), _ptr(grad_scale))
+    # what torch saved of these tensors for a backward pass is no longer what it saved
+    torch.autograd.graph.increment_version(params)
+    if copies is not None:
+        torch.autograd.graph.increment_version([c for c in copies if c is not None])
+
+
+def adamw_moments(state: AdamWState, stream=None) -> tuple:
+    """(m, v) float32 as the state holds them: what its codes stand for, or its own tensors."""
+    if stream is not None:
+        return _on(stream, lambda first: adamw_moments(state), state.m)
+    if state.bounds is None:
+        return state.m, state.v
+    blocks = state.bounds.shape[0]
+    if not state.m.is_cuda:
+        _refuse("tensors on the GPU")
+    _state_bits(state, blocks, state.m.get_device())
+    m = torch.empty(blocks * CODE_BLOCK, dtype=torch.float32, device=state.m.device)
+    v = torch.empty_like(m)
+    _launch("gs_adamw_moments", state.m, blocks, state.m.data_ptr(), state.v.data_ptr(), state.bounds.data_ptr(), m.data_ptr(), v.data_ptr())
+    return m, v
+
+
 # -- as differentiable torch functions -------------------------------------------------------
 
 
@@ -447,3 +705,52 @@ def gated8(h, act: str = "silu"):
     if h.dim() == 0 or h.shape[-1] % 2:
         _refuse("a last axis of two halves, gate and up")
     return _Gated8.apply(h, act)[0]
+
+
+def _rows(t, width):
+    """t as a matrix [rows][width] with dense rows that do not overlap, as it is where it can be."""
+    t = t.reshape(math.prod(t.shape[:-1]), width)
+    dense = (t.shape[1] <= 1 or t.stride(1) == 1) and (t.shape[0] <= 1 or t.stride(0) >= t.shape[1])
+    return t if dense else t.contiguous()
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, b, eps):
+        width = x.shape[-1]
+        flat = _rows(x, width)
+        ctx.save_for_backward(flat, w)
+        ctx.eps, ctx.shape = eps, x.shape
+        return layer_norm_fwd(flat, w, b, eps).view(x.shape)
+
+    @staticmethod
+    @once
+    def backward(ctx, dy):
+        x, w = ctx.saved_tensors
+        dx, dw, db = layer_norm_bwd(_rows(dy, x.shape[1]), x, w, ctx.eps, ctx.needs_input_grad[1], ctx.needs_input_grad[2])
+        return dx.view(ctx.shape), dw, db, None
+
+
+def layer_norm(x, w=None, b=None, eps: float = 1e-5):
+    """layer_norm_fwd over the last axis of x [..., width], with gradients for x, w and b."""
+    if x.dim() == 0:
+        _refuse("a last axis to norm over")
+    return _LayerNorm.apply(x, w, b, eps)
+
+
+class _GroupMM(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, offsets):
+        ctx.save_for_backward(x, w, offsets)
+        return group_mm_fwd(x, w, offsets)
+
+    @staticmethod
+    @once
+    def backward(ctx, dy):
+        x, w, offsets = ctx.saved_tensors
+        return (*group_mm_bwd(_rows(dy, w.shape[2]), x, w, offsets, ctx.needs_input_grad[0], ctx.needs_input_grad[1]), None)
+
+
+def group_mm(x, w, offsets):
+    """group_mm_fwd with gradients for x and w."""
+    return _GroupMM.apply(x, w, offsets)
