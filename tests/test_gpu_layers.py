@@ -288,9 +288,13 @@ def test_group_mm_strides(t):
     tokens.group_mm_fwd(x, w, offs, out=y)
     tokens.group_mm_bwd(dy, x, w, offs, dx=dx, dw=dw)
     tokens.group_mm_bwd(dy, x, w, offs, with_dx=False, dw=dwt)
-    assert torch.equal(y, want[0]) and torch.equal(dx, want[1])
-    for d in (dw, dwt):
-        close(d, want[2].double(), 2 * half_step(T) * want[2].double().abs() + 2 * (rows + 16) * U * (x.double().abs().t() @ dy.double().abs()), "dw elsewhere")
+    # each is within its own tolerance of the product (alignment chooses the order of a sum), so twice that of the other
+    each = torch.repeat_interleave(torch.tensor(sizes, device="cuda"))
+    ax, ad, aw = x.double().abs(), dy.double().abs(), w.double().abs()
+    for got, ref, terms, mag in ((y, want[0], k, torch.cat([ax[each == i] @ aw[i] for i in range(4)])),
+                                 (dx, want[1], n, torch.cat([ad[each == i] @ aw[i].t() for i in range(4)])),
+                                 (dw, want[2], rows, ax.t() @ ad), (dwt, want[2], rows, ax.t() @ ad)):
+        close(got, ref.double(), 2 * (terms + 16) * U * mag + 3 * half_step(T) * ref.double().abs(), "elsewhere")
     for r, part in zip(room, (y, dx, dw, dwt)):
         part.fill_(5.0)
         assert (r == 5).all()

@@ -11,7 +11,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libgsraster.so")
 SOURCES = ["gs_project.hip", "gs_bin.hip", "gs_sort.hip", "gs_render.hip", "gs_densify.hip", "gs_adam.hip", "gs_qsh.hip",
            "gs_api.hip", "gs_norm.hip", "gs_attn.hip", "gs_attn_bwd.hip", "gs_gate.hip",
-           "gs_layer_norm.hip", "gs_group.hip", "gs_adamw.hip", "gs_tokens_api.hip"]
+           "gs_layer_norm.hip", "gs_group.hip", "gs_group_mfma.hip", "gs_adamw.hip", "gs_tokens_api.hip"]
 
 HIPCC_FLAGS = [
     "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC", "-munsafe-fp-atomics",

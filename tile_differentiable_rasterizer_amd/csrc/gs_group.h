@@ -32,39 +32,56 @@ struct GroupSpan {
   int first, last;  // rows; empty: no such tile
 };
 
-// The `tile`-th block of BM rows, spans counted one after another.  Every lane of the wavefront calls it.  Offsets that decrease
-// make other blocks than there are, never one outside of its span.
+// Blocks of BM rows, spans counted one after another.  Every lane of the wavefront calls these.  Offsets
+// that decrease make other blocks than there are, never one outside of its span.
 template <int BM>
-__device__ __forceinline__ GroupSpan group_tile(const GroupArgs& a, uint32_t tile) {
-  uint32_t run = 0;
-  const int spans = a.groups + 2;
-  for (int c = 0; c < spans; c += kWave) {
+struct GroupTiles {
+  int lo, hi;           // the lane's span of the 64 looked at
+  uint32_t mine, upto;  // its blocks, and all up to it
+
+  __device__ __forceinline__ void look(const GroupArgs& a, int c) {
     const int e = c + (int)__lane_id();
-    int lo = 0, hi = 0;
-    if (e < spans) {
+    lo = hi = 0;
+    if (e < a.groups + 2) {
       lo = group_bound(a, e);
       hi = group_bound(a, e + 1);
     }
-    const uint32_t mine = hi > lo ? (uint32_t)(hi - lo + BM - 1) / BM : 0;
-    uint32_t upto = mine;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-      const uint32_t t = __shfl_up(upto, d, 64);
-      if ((int)__lane_id() >= d) upto += t;
-    }
-    const uint64_t hit = __ballot(mine > 0 && tile - (run + upto - mine) < mine);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
-      const uint32_t before = run + __builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(mine, l);
-      GroupSpan s;
-      s.last = __builtin_amdgcn_readlane(hi, l);
-      s.first = __builtin_amdgcn_readlane(lo, l) + (int)(tile - before) * BM;
-      s.group = c + l == 0 || c + l == spans - 1 ? -1 : c + l - 1;
-      return s;
-    }
-    run += __builtin_amdgcn_readlane(upto, kWave - 1);
+    mine = hi > lo ? (uint32_t)(hi - lo + BM - 1) / BM : 0;
+    upto = wave_inclusive_scan(mine);
   }
-  return {-1, 0, 0};
-}
+  __device__ __forceinline__ uint32_t last() const { return __builtin_amdgcn_readlane(upto, kWave - 1); }
+
+  // Blocks of all spans; what look(a, 0) found stays where there are no more than 64.
+  __device__ __forceinline__ uint32_t count(const GroupArgs& a) {
+    look(a, 0);
+    uint32_t all = last();
+    for (int c = kWave; c < a.groups + 2; c += kWave) {
+      look(a, c);
+      all += last();
+    }
+    return all;
+  }
+
+  // The `tile`-th block, after count().
+  __device__ __forceinline__ GroupSpan find(const GroupArgs& a, uint32_t tile) {
+    uint32_t run = 0;
+    const int spans = a.groups + 2;
+    for (int c = 0; c < spans; c += kWave) {
+      if (spans > kWave) look(a, c);
+      const uint64_t hit = __ballot(mine > 0 && tile - (run + upto - mine) < mine);
+      if (hit) {
+        const int l = __builtin_ctzll(hit);
+        const uint32_t before = run + __builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(mine, l);
+        GroupSpan s;
+        s.last = __builtin_amdgcn_readlane(hi, l);
+        s.first = __builtin_amdgcn_readlane(lo, l) + (int)(tile - before) * BM;
+        s.group = c + l == 0 || c + l == spans - 1 ? -1 : c + l - 1;
+        return s;
+      }
+      run += last();
+    }
+    return {-1, 0, 0};
+  }
+};
 
 }  // namespace gs

@@ -8,6 +8,8 @@
 
 namespace gs {
 
+hipError_t launch_group_mfma(bool over_rows, const GroupArgs& a, hipStream_t s);
+
 constexpr int kPlainTile = 64, kPlainStep = 16;
 
 // Any strides and sizes: 64 x 64 results a workgroup, 4 x 4 a thread.
@@ -26,7 +28,9 @@ __global__ __launch_bounds__(256) void k_group_plain(GroupArgs a) {
     k0 = group_bound(a, g + 1);
     k_end = group_bound(a, g + 2);
   } else {
-    const GroupSpan s = group_tile<kPlainTile>(a, blockIdx.x / n_tiles);
+    GroupTiles<kPlainTile> tiles;
+    tiles.look(a, 0);
+    const GroupSpan s = tiles.find(a, blockIdx.x / n_tiles);
     if (s.first >= s.last) return;
     g = s.group;
     m0 = s.first;
@@ -76,6 +80,17 @@ namespace {
 
 int64_t tiles(int64_t n, int64_t each) { return (n + each - 1) / each; }
 
+// Whether every row of the three matrices starts on 16 bytes and holds whole chunks of 16, at distances that
+// a thread's 32-bit offsets reach.
+bool group_aligned(bool over_rows, const GroupArgs& a) {
+  constexpr int64_t kFar = 1 << 22;
+  const int64_t as = over_rows || a.a_k != 1 ? a.a_k : a.a_m, bs = a.b_n == 1 ? a.b_k : a.b_n;
+  for (const void* p : {a.a, a.b, static_cast<const void*>(a.c)})
+    if ((uintptr_t)p % 16) return false;
+  return as % 8 == 0 && bs % 8 == 0 && a.b_g % 8 == 0 && a.c_g % 8 == 0 && a.c_m % 8 == 0 && a.c_n == 1 && as <= kFar && bs <= kFar &&
+         a.n % 8 == 0 && (over_rows ? a.m : a.k) % 8 == 0;
+}
+
 }  // namespace
 
 // Workgroups of a launch (the caller checks that a grid takes them).
@@ -87,6 +102,7 @@ int64_t group_tiles(bool over_rows, int64_t rows, int64_t m, int64_t n, int64_t 
 hipError_t launch_group(bool over_rows, const GroupArgs& a, int type, hipStream_t s) {
   const int64_t blocks = group_tiles(over_rows, a.rows, a.m, a.n, a.groups);
   if (blocks == 0) return hipSuccess;
+  if (type == GS_BF16 && group_aligned(over_rows, a)) return launch_group_mfma(over_rows, a, s);
   if (type == GS_BF16)
     over_rows ? k_group_plain<__bf16, true><<<(unsigned)blocks, 256, 0, s>>>(a) : k_group_plain<__bf16, false><<<(unsigned)blocks, 256, 0, s>>>(a);
   else

@@ -400,6 +400,9 @@ bool weights_ok(gs_weights* w, int64_t groups, int64_t k, int64_t n, int type, b
   return most >= 0 && (!out || groups == 1 || w->group_stride >= most + (w->n_stride == 1 ? n : k));
 }
 
+// A stride of a single row is not used.
+int64_t of_rows(int64_t stride, int64_t rows) { return rows > 1 ? stride : 0; }
+
 GroupArgs group_args(const gs_group_mm& p) {
   GroupArgs a{};
   a.rows = (int32_t)p.rows;
@@ -422,6 +425,8 @@ gs_status gs_group_mm_fwd(const gs_group_mm* p, const void* x, int64_t x_stride,
   if (!rows_ok(y, y_stride, p->rows, p->n, p->type) || (p->k && !rows_in_ok(x, x_stride, p->rows, p->type)) ||
       !weights_ok(&w, p->groups, p->k, p->n, p->type, false))
     return GS_ERR_INVALID_ARG;
+  x_stride = of_rows(x_stride, p->rows);
+  y_stride = of_rows(y_stride, p->rows);
   GroupArgs a = group_args(*p);
   a.a = x; a.a_m = x_stride; a.a_k = 1;
   a.b = w.data; a.b_g = w.group_stride; a.b_k = w.k_stride; a.b_n = w.n_stride;
@@ -445,6 +450,9 @@ gs_status gs_group_mm_bwd(const gs_group_mm* p, const void* dy, int64_t dy_strid
     return GS_ERR_INVALID_ARG;
   if (has_dw && ((p->rows && !rows_in_ok(x, x_stride, p->rows, p->type)) || !weights_ok(&dw, p->groups, p->k, p->n, p->type, true)))
     return GS_ERR_INVALID_ARG;
+  dy_stride = of_rows(dy_stride, p->rows);
+  x_stride = of_rows(x_stride, p->rows);
+  dx_stride = of_rows(dx_stride, p->rows);
   if (has_dx) {
     GroupArgs a = group_args(*p);
     a.a = dy; a.a_m = dy_stride; a.a_k = 1;
@@ -455,11 +463,13 @@ gs_status gs_group_mm_bwd(const gs_group_mm* p, const void* dy, int64_t dy_strid
     if (e != GS_OK) return e;
   }
   if (!has_dw) return GS_OK;
+  // the dense axis of dw is the product's second: dW = x^T dy, or its transpose dy^T x
   GroupArgs a = group_args(*p);
-  a.a = x; a.a_m = 1; a.a_k = x_stride;
-  a.b = dy; a.b_k = dy_stride; a.b_n = 1;
-  a.c = dw.data; a.c_g = dw.group_stride; a.c_m = dw.k_stride; a.c_n = dw.n_stride;
-  a.m = (int32_t)p->k; a.n = (int32_t)p->n; a.k = a.rows;
+  const bool turned = dw.n_stride != 1;
+  a.a = turned ? dy : x; a.a_m = 1; a.a_k = turned ? dy_stride : x_stride;
+  a.b = turned ? x : dy; a.b_k = turned ? x_stride : dy_stride; a.b_n = 1;
+  a.c = dw.data; a.c_g = dw.group_stride; a.c_m = turned ? dw.n_stride : dw.k_stride; a.c_n = 1;
+  a.m = (int32_t)(turned ? p->n : p->k); a.n = (int32_t)(turned ? p->k : p->n); a.k = a.rows;
   return status_of(launch_group(true, a, p->type, static_cast<hipStream_t>(stream)));
 }
 
