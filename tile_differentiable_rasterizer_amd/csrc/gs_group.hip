@@ -87,7 +87,7 @@ bool group_aligned(bool over_rows, const GroupArgs& a) {
   const int64_t as = over_rows || a.a_k != 1 ? a.a_k : a.a_m, bs = a.b_n == 1 ? a.b_k : a.b_n;
   for (const void* p : {a.a, a.b, static_cast<const void*>(a.c)})
     if ((uintptr_t)p % 16) return false;
-  return as % 8 == 0 && bs % 8 == 0 && a.b_g % 8 == 0 && a.c_g % 8 == 0 && a.c_m % 8 == 0 && a.c_n == 1 && as <= kFar && bs <= kFar &&
+  return as % 8 == 0 && bs % 8 == 0 && a.b_g % 8 == 0 && a.c_g % 8 == 0 && a.c_m % 8 == 0 && a.c_n == 1 && as <= kFar && bs <= kFar && a.c_m <= kFar &&
          a.n % 8 == 0 && (over_rows ? a.m : a.k) % 8 == 0;
 }
 

@@ -1,6 +1,16 @@
 // gs_group_mfma.hip -- the products of rows with their group's weights on the matrix units, bfloat16, for
 // gfx950.
+//
+// A workgroup of four wavefronts makes BM x BN results, a quarter each, over tiles of 64 k that come from
+// memory straight to LDS: two of A, three of B, so that every tile has three quarters of a tile's time or more to
+// arrive.  Between two matrix instructions there is at most one read of LDS or one load, so that neither
+// queues up before the matrix unit's next work: reads are of the operands of the next 16 k, loads of the tile after the
+// next.  One barrier a tile, placed before the tile's last 16 k: by then all of it is in registers, and
+// behind it the next tile's first operands are read under its last products.
+//
+// The results are computed transposed (a lane holds one row's), so that they leave as 16 bytes a lane.
 #include <algorithm>
+#include <type_traits>
 
 #include "gs_group.h"
 #include "gs_lds.h"
@@ -8,38 +18,33 @@
 
 namespace gs {
 
-constexpr int kGroupStep = 32;   // k of a tile in LDS
-constexpr int kGroupStages = 3;  // tiles in LDS: one worked on, two on their way
+constexpr int kGroupK = 64;  // k of a tile in LDS
+constexpr int kGroupSteps = kGroupK / 16;
 
 __device__ __forceinline__ void group_barrier() { asm volatile("s_barrier" ::: "memory"); }
 
-// One operand's tile of R rows (or columns) by 32 k in LDS, and the loads of its next one.
-//   K dense in memory: 64 bytes of k for each row; 16-byte chunk c of row r lies at c ^ (r / 4 % 4).
+// One operand's tile of R rows (or columns) by 64 k in LDS, and the loads of its next one.
+//   K dense in memory: rows of 64 k; 16-byte chunk c of row r lies at c ^ (2 (r & 2) + r / 4 % 4).
 //   K not dense: R elements for each k; chunk c of k-row r lies at c ^ (4 (r % 4) + r / 4 % 4).
 // Either way what a wavefront reads at once lies in different banks (gs_mfma.h).
 template <bool K_DENSE, int R>
 struct GroupSide {
-  static constexpr int kBytes = R * kGroupStep * 2, kLoads = kBytes / 4096, kChunks = (K_DENSE ? kGroupStep : R) / 8;
+  static constexpr int kBytes = R * kGroupK * 2, kLoads = kBytes / 4096, kChunks = (K_DENSE ? kGroupK : R) / 8;
+  static_assert(kLoads * 4096 == kBytes && (K_DENSE || R >= 128), "whole chunks a thread; sixteen of them a row");
 
   const char* base;     // of the tile at k0
-  int64_t step;         // bytes of 32 k
+  int64_t step;         // bytes of 64 k
   uint32_t off[kLoads];
   int at;               // where the lane reads, from the start of a tile
 
-  static __device__ __forceinline__ int mix(int r) { return K_DENSE ? (r >> 2) & 3 : ((r & 3) << 2) | ((r >> 2) & 3); }
+  static __device__ __forceinline__ int mix(int r) {
+    return K_DENSE ? ((r & 2) << 1) | ((r >> 2) & 3) : ((r & 3) << 2) | ((r >> 2) & 3);
+  }
   static __device__ __forceinline__ int row_of(int i) { return (i * 256 + (int)threadIdx.x) / kChunks; }
   static __device__ __forceinline__ int chunk_of(int i) { return (i * 256 + (int)threadIdx.x) % kChunks ^ mix(row_of(i)); }
 
-  // p: element (row 0, k0); stride: of the axis that is not dense; rows (at least 1) exist.  Those past them are read as the last: what comes
-  // of them is not stored.  first: the wavefront's first row.
-  __device__ __forceinline__ void plan(const __bf16* p, int64_t stride, int rows, int first) {
-    base = reinterpret_cast<const char*>(p);
-    step = K_DENSE ? kGroupStep * 2 : kGroupStep * 2 * stride;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int r = row_of(i), c = chunk_of(i) * 8;
-      off[i] = K_DENSE ? (uint32_t)(min(r, rows - 1) * stride + c) * 2u : (uint32_t)(r * stride + min(c, rows - 8)) * 2u;
-    }
+  // Where the wavefront reads: its rows from `first` on.
+  __device__ __forceinline__ void place(int first) {
     const int l = __lane_id(), h = l >> 5, i = l & 15;
     if constexpr (K_DENSE) {
       const int r = l & 31;
@@ -49,18 +54,35 @@ struct GroupSide {
       at = r * (kChunks * 16) + ((c ^ mix(r)) << 4) + 8 * (i & 1);
     }
   }
-  __device__ __forceinline__ void load(uint32_t to, int tile) const {
-    const char* p = base + tile * step;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) load_to_lds16(p, off[i], to + i * 4096);
-  }
-  // The last tile, of which k < left exist: the others are 0.
-  __device__ __forceinline__ void load_part(uint32_t to, int tile, int left) const {
-    const char* p = base + tile * step;
+  // p: element (row 0, k0); stride: of the axis that is not dense; rows (at least 1) exist.  Those past them are read as
+  // the last: what comes of them is not stored.
+  __device__ __forceinline__ void plan(const __bf16* p, int64_t stride, int rows) {
+    base = reinterpret_cast<const char*>(p);
+    step = K_DENSE ? kGroupK * 2 : kGroupK * 2 * stride;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
+      const int r = row_of(i), c = chunk_of(i) * 8;
+      off[i] = K_DENSE ? (uint32_t)(min(r, rows - 1) * stride + c) * 2u : (uint32_t)(r * stride + min(c, rows - 8)) * 2u;
+    }
+  }
+  // The thread's i-th 16 bytes of the tile at p.  Where it is not whole, k < left exist and the others are 0.
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(const char* p, uint32_t to, int left, int i) const {
+    if constexpr (WHOLE) {
+      load_to_lds16(p, off[i], to + i * 4096);
+    } else {
       const bool there = (K_DENSE ? chunk_of(i) * 8 : row_of(i)) < left;
       load_to_lds16(there ? static_cast<const void*>(p + off[i]) : kZeros, to + i * 4096);
+    }
+  }
+  __device__ __forceinline__ void load_all(int tile, uint32_t to, int left) const {
+    const char* p = base + tile * step;
+    if (left >= kGroupK) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) load<true>(p, to, left, i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) load<false>(p, to, left, i);
     }
   }
   // The lane's eight k of row `first` + 32 m + l % 32, k = 16 s + 8 (l / 32) + 0..7.
@@ -83,152 +105,244 @@ struct GroupSide {
   }
 };
 
+// A block of results: rows m0 .. m_end, columns from n0 on, summed over k0 .. k_end.
+struct GroupPlace {
+  int g, m0, m_end, n0, k0, k_end;
+};
+
 template <bool A_DENSE, bool B_DENSE, bool OVER_ROWS, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(256, 2) void k_group_mfma(GroupArgs a) {
+__global__ __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) void k_group_mfma(GroupArgs a) {
   using SideA = GroupSide<A_DENSE, BM>;
   using SideB = GroupSide<B_DENSE, BN>;
-  constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
-  constexpr int kStage = SideA::kBytes + SideB::kBytes;
+  constexpr int TM = BM / WM / 32, TN = BN / WN / 32, kMma = TM * TN, kReads = TM + TN;
+  constexpr int kStores = TM * TN * 2;
   static_assert(WM * WN == 4, "four wavefronts");
-  __shared__ __align__(1024) char lds[kGroupStages * kStage];
+  __shared__ __align__(1024) char lds[2 * SideA::kBytes + 3 * SideB::kBytes];
   const int n_tiles = (a.n + BN - 1) / BN;
-  int m0, m_end, n0, k0, k_end, g;
-  const uint32_t pid = blockIdx.x;
+
+  // the blocks, an eighth to each XCD (whose workgroups are every eighth), there in patches of a few tiles of rows
+  GroupTiles<BM> spans;
+  uint32_t m_tiles, id, end;
+  int g_over = 0;
   if constexpr (OVER_ROWS) {
-    const int m_tiles = (a.m + BM - 1) / BM, each = m_tiles * n_tiles;
-    g = pid / each;
-    const int rest = pid - g * each;
-    m0 = rest % m_tiles * BM;
-    n0 = rest / m_tiles * BN;
-    m_end = a.m;
-    k0 = group_bound(a, g + 1);
-    k_end = group_bound(a, g + 2);
+    m_tiles = (a.m + BM - 1) / BM;
+    const uint32_t each = m_tiles * n_tiles;
+    g_over = blockIdx.x / each;
+    const uint32_t in = blockIdx.x - g_over * each, q = each / 8, more = each % 8;
+    const uint32_t slot = (blockIdx.x - g_over * each) % 8;
+    id = slot * q + min(slot, more) + in / 8;
+    end = id + 1;
   } else {
-    GroupTiles<BM> tiles;
-    const uint32_t m_tiles = tiles.count(a), all = m_tiles * n_tiles;
-    if (pid >= all) return;
-    // an XCD's workgroups (every eighth) side by side, in blocks of eight tiles of rows
-    const uint32_t xcd = pid % 8, each = all / 8, more = all % 8;
-    const uint32_t id = xcd * each + min(xcd, more) + pid / 8;
-    const uint32_t patch = id / (8 * n_tiles), rest = id - patch * 8 * n_tiles, high = min(8u, m_tiles - patch * 8);
-    const GroupSpan s = tiles.find(a, patch * 8 + rest % high);
-    if (s.first >= s.last) return;
-    g = s.group;
-    m0 = s.first;
-    m_end = s.last;
-    n0 = rest / high * BN;
-    k0 = 0;
-    k_end = g < 0 ? 0 : a.k;
+    m_tiles = spans.count(a);
+    const uint32_t all = m_tiles * n_tiles, q = all / 8, more = all % 8, xcd = blockIdx.x % 8;
+    id = xcd * q + min(xcd, more);
+    end = id + q + (xcd < more);
+    id += blockIdx.x / 8;
   }
-  const int wave = threadIdx.x / kWave, wm = wave % WM, wn = wave / WM;
-  const int k_tiles = k_end > k0 ? (k_end - k0 + kGroupStep - 1) / kGroupStep : 0;
-
-  f32x16 acc[TN][TM];
-#pragma unroll
-  for (int n = 0; n < TN; ++n)
-#pragma unroll
-    for (int m = 0; m < TM; ++m) acc[n][m] = (f32x16)0.0f;
-
-  if (k_tiles) {
-    SideA sa;
-    SideB sb;
-    const __bf16 *A = static_cast<const __bf16*>(a.a) + m0 * a.a_m + k0 * a.a_k;
-    const __bf16 *B = static_cast<const __bf16*>(a.b) + (OVER_ROWS ? 0 : g * a.b_g) + k0 * a.b_k + n0 * a.b_n;
-    sa.plan(A, A_DENSE ? a.a_m : a.a_k, m_end - m0, wm * TM * 32);
-    sb.plan(B, B_DENSE ? a.b_n : a.b_k, a.n - n0, wn * TN * 32);
-    const uint32_t to = lds_address(lds) + (threadIdx.x / kWave) * 1024;
-    auto load = [&](int tile, int stage) {
-      const uint32_t at = __builtin_amdgcn_readfirstlane(to + stage * kStage);
-      const int left = k_end - k0 - tile * kGroupStep;
-      if (left >= kGroupStep) {
-        sa.load(at, tile);
-        sb.load(at + SideA::kBytes, tile);
-      } else {
-        sa.load_part(at, tile, left);  // left <= 0: zeros that nothing reads, so that the loads on their way can be counted
-        sb.load_part(at + SideA::kBytes, tile, left);
-      }
-    };
-    bf16x8 fa[2][TM], fb[2][TN];
-    auto read = [&](int which, int stage, int s) {
-      const char* tile = lds + stage * kStage;
-#pragma unroll
-      for (int n = 0; n < TN; ++n) fb[which][n] = sb.read(tile + SideA::kBytes, n, s);
-#pragma unroll
-      for (int m = 0; m < TM; ++m) fa[which][m] = sa.read(tile, m, s);
-    };
-    auto multiply = [&](int which) {
-#pragma unroll
-      for (int m = 0; m < TM; ++m)
-#pragma unroll
-        for (int n = 0; n < TN; ++n) acc[n][m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[which][n], fa[which][m], acc[n][m], 0, 0, 0);
-    };
-    constexpr int kEach = SideA::kLoads + SideB::kLoads;  // loads of a tile
-    load(0, 0);
-    load(1, 1);
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kEach) : "memory");
-    group_barrier();
-    read(0, 0, 0);
-    int stage = 0;
-    for (int t = 0; t < k_tiles; ++t) {
-      const int next = stage == 2 ? 0 : stage + 1, free = stage == 0 ? 2 : stage - 1;
-      load(t + 2, free);  // the tile before was read before the last barrier
-      read(1, stage, 1);
-      multiply(0);
-      asm volatile("s_waitcnt lgkmcnt(0) vmcnt(%0)" ::"n"(kEach) : "memory");
-      group_barrier();
-      read(0, next, 0);
-      multiply(1);
-      stage = next;
+  auto find = [&](uint32_t i) {
+    constexpr uint32_t kHigh = 2048 / BM;
+    const uint32_t patch = i / (kHigh * n_tiles), rest = i - patch * kHigh * n_tiles, high = min(kHigh, m_tiles - patch * kHigh);
+    const uint32_t mt = patch * kHigh + rest % high;
+    GroupPlace p;
+    p.n0 = rest / high * BN;
+    if constexpr (OVER_ROWS) {
+      p.g = g_over;
+      p.m0 = mt * BM;
+      p.m_end = a.m;
+      p.k0 = group_bound(a, p.g + 1);
+      p.k_end = max(group_bound(a, p.g + 2), p.k0);
+    } else {
+      const GroupSpan s = spans.find(a, mt);
+      p.g = s.group;
+      p.m0 = s.first;
+      p.m_end = s.last;
+      p.k0 = 0;
+      p.k_end = s.group < 0 ? 0 : a.k;
     }
-  }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load goes to LDS that another workgroup has by then
+    return p;
+  };
+  if (id >= end) return;
+  GroupPlace p = find(id);
 
-  __bf16* C = static_cast<__bf16*>(a.c) + (OVER_ROWS ? g * a.c_g : 0);
-  const int l = __lane_id(), h = l >> 5;
-#pragma unroll
-  for (int m = 0; m < TM; ++m) {
-    const int row = m0 + (wm * TM + m) * 32 + (l & 31);
-    __bf16* to = C + row * a.c_m;
+  const int wave = threadIdx.x / kWave, wm = wave % WM, wn = wave / WM;
+  const uint32_t to = lds_address(lds) + (threadIdx.x / kWave) * 1024;
+  auto to_a = [&](int b) { return (uint32_t)__builtin_amdgcn_readfirstlane(to + b * SideA::kBytes); };
+  auto to_b = [&](int b) { return (uint32_t)__builtin_amdgcn_readfirstlane(to + 2 * SideA::kBytes + b * SideB::kBytes); };
+  SideA sa;
+  SideB sb;
+  sa.place(wm * TM * 32);
+  sb.place(wn * TN * 32);
+  // the first two tiles' loads
+  auto start = [&] {
+    const int left = p.k_end - p.k0;
+    if (left == 0) return;
+    sa.plan(static_cast<const __bf16*>(a.a) + p.m0 * a.a_m + p.k0 * a.a_k, A_DENSE ? a.a_m : a.a_k, p.m_end - p.m0);
+    sb.plan(static_cast<const __bf16*>(a.b) + (OVER_ROWS ? 0 : p.g * a.b_g) + p.k0 * a.b_k + p.n0 * a.b_n, B_DENSE ? a.b_n : a.b_k, a.n - p.n0);
+    sa.load_all(0, to_a(0), left);
+    sb.load_all(0, to_b(0), left);
+    sb.load_all(1, to_b(1), left - kGroupK);  // of k that do not exist: zeros, so that the loads can be counted
+    sa.load_all(1, to_a(1), left - kGroupK);
+  };
+
+  start();
+  bool stored = false;  // stores of the block before are on their way behind the loads
+  while (true) {
+    f32x16 acc[TN][TM];
 #pragma unroll
     for (int n = 0; n < TN; ++n)
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        union {
-          __bf16 x[8];
-          uint32_t u[4];
-          uint4 v;
-        } r;
+      for (int m = 0; m < TM; ++m) acc[n][m] = (f32x16)0.0f;
+    bf16x8 fa[2][TM], fb[2][TN];
+    auto read = [&](int which, int ba, int bb, int s, int i) {
+      if (i < TN)
+        fb[which][i] = sb.read(lds + 2 * SideA::kBytes + bb * SideB::kBytes, i, s);
+      else
+        fa[which][i - TN] = sa.read(lds + ba * SideA::kBytes, i - TN, s);
+    };
+    // 16 k, and what goes between the products: part i of kMma
+    auto multiply = [&](int which, auto&& between) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r.x[e] = (__bf16)acc[n][m][8 * q + e];
-        // a lane and the one 32 on hold fours of columns in turn: now eight in a row each
+      for (int m = 0; m < TM; ++m)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const auto w = __builtin_amdgcn_permlane32_swap(r.u[e], r.u[2 + e], false, false);
-          r.u[e] = w[0];
-          r.u[2 + e] = w[1];
+        for (int n = 0; n < TN; ++n) {
+          acc[n][m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[which][n], fa[which][m], acc[n][m], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+          between(m * TN + n);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        const int col = n0 + (wn * TN + n) * 32 + 16 * q + 8 * h;
-        if (row < m_end && col < a.n) *reinterpret_cast<uint4*>(to + col) = r.v;
+    };
+
+    // the sums stay where the matrix unit adds to them, past the branches too
+    auto keep = [&] {
+      if constexpr (kMma == 16) {
+#pragma unroll
+        for (int n = 0; n < TN; ++n)
+#pragma unroll
+          for (int m = 0; m < TM; ++m) asm volatile("" : "+a"(acc[n][m]));
       }
+    };
+    keep();
+
+    const int all = p.k_end - p.k0;
+    if (all) {
+      // loads and stores are counted together and in order
+      if (stored)
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kStores + SideA::kLoads + SideB::kLoads < 63 ? kStores + SideA::kLoads + SideB::kLoads : 63) : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(SideA::kLoads + SideB::kLoads) : "memory");
+      group_barrier();
+#pragma unroll
+      for (int i = 0; i < kReads; ++i) read(0, 0, 0, 0, i);
+      int ba = 0, bb = 0;
+      const char *pa = sa.base + 2 * sa.step, *pb = sb.base + 2 * sb.step;  // of tile t + 2
+      auto tile = [&](auto whole, int left) {  // left: k of tile t + 2 and behind
+        constexpr bool kWhole = decltype(whole)::value;
+        const int next_a = ba ^ 1, next_b = bb == 2 ? 0 : bb + 1;
+        const uint32_t ta = to_a(ba), tb = to_b(bb == 0 ? 2 : bb - 1);
+#pragma unroll
+        for (int s = 0; s + 1 < kGroupSteps; ++s)
+          multiply(s & 1, [&](int i) {
+#pragma unroll
+            for (int r = 0; r < kReads; ++r)
+              if (r * kMma / kReads == i) read((s + 1) & 1, ba, bb, s + 1, r);
+#pragma unroll
+            for (int r = 0; r < SideB::kLoads; ++r)
+              if (s == 0 && (2 * r + 1) * kMma / (2 * SideB::kLoads) == i) sb.template load<kWhole>(pb, tb, left, r);
+          });
+        asm volatile("s_waitcnt lgkmcnt(0) vmcnt(%0)" ::"n"(SideB::kLoads) : "memory");
+        group_barrier();
+        multiply((kGroupSteps - 1) & 1, [&](int i) {
+#pragma unroll
+          for (int r = 0; r < kReads; ++r)
+            if (r * kMma / kReads == i) read(0, next_a, next_b, 0, r);
+#pragma unroll
+          for (int r = 0; r < SideA::kLoads; ++r)
+            if ((2 * r + 1) * kMma / (2 * SideA::kLoads) == i) sa.template load<kWhole>(pa, ta, left, r);
+        });
+        pa += sa.step;
+        pb += sb.step;
+        ba = next_a;
+        bb = next_b;
+      };
+      int left = all - 2 * kGroupK;
+      for (; left >= kGroupK; left -= kGroupK) tile(std::true_type(), left);
+      keep();
+      for (; left > -2 * kGroupK; left -= kGroupK) tile(std::false_type(), left);
+      keep();
+      // no wavefront reads LDS any more that counts, and this one's last loads (zeros) are in
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    keep();
+    const GroupPlace done = p;
+    id += gridDim.x / 8;
+    const bool more = !OVER_ROWS && id < end;
+    if (more) {
+      p = find(id);
+      start();
+    }
+    keep();
+
+    char* C = reinterpret_cast<char*>(static_cast<__bf16*>(a.c) + (OVER_ROWS ? done.g * a.c_g : 0) + done.m0 * a.c_m + done.n0);
+    const auto out = __builtin_amdgcn_make_buffer_rsrc(C, 0, 0x7fffffff, 0x00020000);
+    const int l = __lane_id(), h = l >> 5;
+#pragma unroll
+    for (int m = 0; m < TM; ++m) {
+      const int row = (wm * TM + m) * 32 + (l & 31);
+      const uint32_t row_at = row < done.m_end - done.m0 ? (uint32_t)(row * a.c_m) * 2u : 0x80000000u;
+#pragma unroll
+      for (int n = 0; n < TN; ++n)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          union {
+            __bf16 x[8];
+            uint32_t u[4];
+            __attribute__((__vector_size__(4 * sizeof(uint32_t)))) uint32_t v;
+          } r;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) r.x[e] = (__bf16)acc[n][m][8 * q + e];
+          // a lane and the one 32 on hold fours of columns in turn: now eight in a row each
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const auto w = __builtin_amdgcn_permlane32_swap(r.u[e], r.u[2 + e], false, false);
+            r.u[e] = w[0];
+            r.u[2 + e] = w[1];
+          }
+          const int col = (wn * TN + n) * 32 + 16 * q + 8 * h;
+          // past the last row or column: past the buffer's end, where nothing is written.  So every store is made, and counted.
+          __builtin_amdgcn_raw_buffer_store_b128(r.v, out, done.n0 + col < a.n ? row_at + col * 2 : 0x80000000u, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);  // a few registers at a time
+        }
+    }
+    if (!more) return;
+    stored = true;
   }
 }
 
 namespace {
+
 int64_t tiles(int64_t n, int64_t each) { return (n + each - 1) / each; }
+
+template <int BM, int BN, int WM, int WN>
+void group_launch(bool over_rows, const GroupArgs& a, hipStream_t s) {
+  constexpr int64_t kSlots = BM * BN > 128 * 128 ? 256 : 512;  // workgroups at a time: one a CU, or two
+  if (over_rows) {
+    const int64_t blocks = a.groups * tiles(a.m, BM) * tiles(a.n, BN);
+    k_group_mfma<false, false, true, BM, BN, WM, WN><<<(unsigned)blocks, 256, 0, s>>>(a);
+    return;
+  }
+  const int64_t most = (tiles(a.rows, BM) + std::min<int64_t>(a.groups + 2, a.rows)) * tiles(a.n, BN);
+  const unsigned blocks = (unsigned)std::min(kSlots, tiles(most, 8) * 8);
+  if (a.b_k == 1)
+    k_group_mfma<true, true, false, BM, BN, WM, WN><<<blocks, 256, 0, s>>>(a);
+  else
+    k_group_mfma<true, false, false, BM, BN, WM, WN><<<blocks, 256, 0, s>>>(a);
+}
+
 }  // namespace
 
 // C's rows dense, A's and B's k dense or not.  The caller has checked alignment, sizes and the grid.
 hipError_t launch_group_mfma(bool over_rows, const GroupArgs& a, hipStream_t s) {
-  if (over_rows) {
-    const int64_t blocks = a.groups * tiles(a.m, 128) * tiles(a.n, 256);
-    k_group_mfma<false, false, true, 128, 256, 2, 2><<<(unsigned)blocks, 256, 0, s>>>(a);
-  } else {
-    const int64_t blocks = (tiles(a.rows, 128) + std::min<int64_t>(a.groups + 2, a.rows)) * tiles(a.n, 256);
-    if (a.b_k == 1)
-      k_group_mfma<true, true, false, 128, 256, 2, 2><<<(unsigned)blocks, 256, 0, s>>>(a);
-    else
-      k_group_mfma<true, false, false, 128, 256, 2, 2><<<(unsigned)blocks, 256, 0, s>>>(a);
-  }
+  group_launch<256, 256, 2, 2>(over_rows, a, s);
   return hipGetLastError();
 }
 
