@@ -36,41 +36,6 @@ struct AdamwTable {
   uint32_t blocks;
 };
 
-template <typename T>
-__device__ __forceinline__ void adamw_load(const T* p, int n, float (&x)[8]) {
-  if (n >= 8) {
-    typedef T V __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
-    constexpr int kPer = 16 / sizeof(T);
-#pragma unroll
-    for (int i = 0; i < 8; i += kPer) {
-      const V v = *reinterpret_cast<const V*>(p + i);
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) x[i + j] = (float)v[j];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = i < n ? (float)p[i] : 0.0f;
-  }
-}
-template <typename T>
-__device__ __forceinline__ void adamw_store(T* p, int n, const float (&x)[8]) {
-  if (n >= 8) {
-    typedef T V __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
-    constexpr int kPer = 16 / sizeof(T);
-#pragma unroll
-    for (int i = 0; i < 8; i += kPer) {
-      V v;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) v[j] = (T)x[i + j];
-      *reinterpret_cast<V*>(p + i) = v;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = (T)x[i];
-  }
-}
-
 __device__ __forceinline__ float half_top(float v) {
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
@@ -115,8 +80,8 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwTable a) {
   const int n = left >= 8 ? 8 : left > 0 ? (int)left : 0;
   const double keep = a.keep[t], scale = a.grad_scale ? (double)*a.grad_scale : 1.0;
   float p[8], gf[8];
-  adamw_load(a.param[t] + u0, n, p);
-  adamw_load(static_cast<const TG*>(a.grad[t]) + u0, n, gf);
+  load_units(a.param[t] + u0, n, p);
+  load_units(static_cast<const TG*>(a.grad[t]) + u0, n, gf);
   const int64_t at = (int64_t)blk * kAdamwBlock + (threadIdx.x & 31) * 8;
   double m[8], v[8];
   if constexpr (BITS == 32) {
@@ -148,8 +113,8 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwTable a) {
     const double den = sqrt(v[i] * a.ib2) + a.eps;
     p[i] = (float)((double)p[i] * keep - a.lr * (m[i] * a.ib1 / den));
   }
-  adamw_store(a.param[t] + u0, n, p);
-  if (a.copy[t]) adamw_store(a.copy[t] + u0, n, p);
+  store_units(a.param[t] + u0, n, p);
+  if (a.copy[t]) store_units(a.copy[t] + u0, n, p);
   if constexpr (BITS == 32) {
     float mf[8], vf[8];
 #pragma unroll

@@ -50,6 +50,43 @@ __device__ __forceinline__ void store_elems(float* p, const float (&x)[N]) {
   }
 }
 
+// The eight units at p, of which n exist (0: none); vector loads and stores at any alignment of whole
+// elements (the memory takes them).
+template <typename T>
+__device__ __forceinline__ void load_units(const T* p, int n, float (&x)[8]) {
+  if (n >= 8) {
+    typedef T V __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
+    constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < 8; i += kPer) {
+      const V v = *reinterpret_cast<const V*>(p + i);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) x[i + j] = (float)v[j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = i < n ? (float)p[i] : 0.0f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_units(T* p, int n, const float (&x)[8]) {
+  if (n >= 8) {
+    typedef T V __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
+    constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < 8; i += kPer) {
+      V v;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) v[j] = (T)x[i + j];
+      *reinterpret_cast<V*>(p + i) = v;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = (T)x[i];
+  }
+}
+
 // The calls' tensors with a typed base.
 template <typename T>
 struct Heads {

@@ -19,7 +19,20 @@ struct GroupArgs {
   int64_t a_m, a_k, b_g, b_k, b_n, c_g, c_m, c_n;
   int32_t rows, groups, m, n, k;  // by rows: m = rows; over rows: k = rows
   const int32_t* offsets;
+  int32_t splits;  // parts of the sum over k, each made by workgroups of its own
+  float* part;     // where there are several: [splits][rows] (over rows: [splits][groups][m]) rows of group_part_width(n)
 };
+
+__host__ __device__ constexpr int group_part_width(int n) { return (n + 7) & ~7; }
+
+// Part `split` of k0 .. k_end, in whole steps of `step`.
+__device__ __forceinline__ void group_part(const GroupArgs& a, int split, int step, int* k0, int* k_end) {
+  if (a.splits == 1) return;
+  const int steps = (*k_end - *k0 + step - 1) / step;
+  const int first = *k0 + (int)((int64_t)steps * split / a.splits) * step;
+  *k_end = min(*k_end, *k0 + (int)((int64_t)steps * (split + 1) / a.splits) * step);
+  *k0 = min(first, *k_end);
+}
 
 __device__ __forceinline__ int group_bound(const GroupArgs& a, int e) {
   if (e <= 0) return 0;

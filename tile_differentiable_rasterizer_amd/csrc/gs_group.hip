@@ -1,79 +1,256 @@
 // gs_group.hip -- products of rows with their group's weights (experts, or heads of a kind), and their
-// gradients, for gfx950.
+// gradients, for gfx950: float32, and bfloat16 matrices whose rows do not all start on 16 bytes
+// (gs_group_mfma.hip has the others).
 //
 //   y[r] = x[r] W[g(r)],  dx[r] = dy[r] W[g(r)]^T,  dW[g] = sum over the group's rows of x[r]^T dy[r].
+//
+// A workgroup of four wavefronts makes 128 x 128 results over tiles of 32 k.  Tiles pass through registers, loaded
+// a tile ahead at any alignment, and enter LDS in the matrix unit's terms: float32 as three bfloat16 that hold all of
+// its bits, split once for the workgroup (gs_mfma.h).
+//
+// Where a sum is long and the results are few, several workgroups share it: their parts go to a workspace in
+// float32, and a second kernel adds them in a fixed order.
 #include <algorithm>
 
 #include "gs_group.h"
+#include "gs_mfma.h"
 
 namespace gs {
 
-hipError_t launch_group_mfma(bool over_rows, const GroupArgs& a, hipStream_t s);
+hipError_t launch_group_mfma(bool over_rows, const GroupArgs& a, int64_t* blocks, hipStream_t s);
 
-constexpr int kPlainTile = 64, kPlainStep = 16;
+constexpr int kStagedTile = 128, kStagedK = 32;
 
-// Any strides and sizes: 64 x 64 results a workgroup, 4 x 4 a thread.
-template <typename T, bool OVER_ROWS>
-__global__ __launch_bounds__(256) void k_group_plain(GroupArgs a) {
-  __shared__ float as[kPlainStep][kPlainTile + 4], bs[kPlainStep][kPlainTile + 4];
-  const int n_tiles = (a.n + kPlainTile - 1) / kPlainTile;
-  int m0, n0, m_end, k0, k_end, g;
+// Eight elements of memory on their way to LDS.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__bf16> {
+  bf16x8 v;
+  __device__ __forceinline__ void load(const __bf16* p, int n) {
+    if (n >= 8) {
+      typedef __bf16 V __attribute__((ext_vector_type(8), aligned(2)));
+      v = *reinterpret_cast<const V*>(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : (__bf16)0.0f;
+    }
+  }
+  __device__ __forceinline__ Frag<__bf16> parts() const { return {v}; }
+};
+template <>
+struct Eight<float> {
+  f32x8 v;
+  __device__ __forceinline__ void load(const float* p, int n) {
+    float x[8];
+    load_units(p, n, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = x[i];
+  }
+  __device__ __forceinline__ Frag<float> parts() const { return frag_split(v); }
+};
+
+// One operand's tile of 128 rows (or columns) by 32 k, in LDS as gs_group_mfma.hip's but for rows of 64 bytes where k is
+// dense (chunk c of row r at c ^ (r / 4 % 4)); float32's three parts one after another.
+template <typename T, bool K_DENSE>
+struct StagedSide {
+  static constexpr int R = kStagedTile, kChunks = (K_DENSE ? kStagedK : R) / 8, kEach = 2, kPart = R * kStagedK * 2;
+  static constexpr int kParts = sizeof(Frag<T>) / sizeof(bf16x8), kBytes = kParts * kPart;
+
+  const T* base;    // of the tile at k0
+  int64_t stride;   // of the axis that is not dense
+  int rows;
+  int at;
+  Eight<T> x[kEach];
+
+  static __device__ __forceinline__ int mix(int r) { return K_DENSE ? (r >> 2) & 3 : ((r & 3) << 2) | ((r >> 2) & 3); }
+  static __device__ __forceinline__ int row_of(int i) { return (i * 256 + (int)threadIdx.x) / kChunks; }
+  static __device__ __forceinline__ int chunk_of(int i) { return (i * 256 + (int)threadIdx.x) % kChunks; }
+
+  __device__ __forceinline__ void plan(const T* p, int64_t s, int n, int first) {
+    base = p;
+    stride = s;
+    rows = n;
+    const int l = __lane_id(), h = l >> 5, i = l & 15;
+    if constexpr (K_DENSE) {
+      const int r = l & 31;
+      at = (first + r) * (kChunks * 16) + ((h ^ mix(r)) << 4);
+    } else {
+      const int r = 8 * h + (i >> 2), c = first / 8 + (2 * ((l >> 4) & 1) + ((i & 3) >> 1));
+      at = r * (kChunks * 16) + ((c ^ mix(r)) << 4) + 8 * (i & 1);
+    }
+  }
+  // Tile `tile`, of which k < left exist: the others, and rows that do not exist, are 0.
+  __device__ __forceinline__ void load(int tile, int left) {
+    const T* p = base + (K_DENSE ? (int64_t)tile * kStagedK : (int64_t)tile * kStagedK * stride);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int r = row_of(i), c = chunk_of(i) * 8;
+      const bool there = K_DENSE ? r < rows : r < left;
+      x[i].load(p + r * stride + c, there ? min(max((K_DENSE ? left : rows) - c, 0), 8) : 0);
+    }
+  }
+  __device__ __forceinline__ void store(char* tile) const {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int r = row_of(i), c = chunk_of(i);
+      union {
+        Frag<T> f;
+        bf16x8 v[kParts];
+      } u;
+      u.f = x[i].parts();
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) *reinterpret_cast<bf16x8*>(tile + k * kPart + r * (kChunks * 16) + ((c ^ mix(r)) << 4)) = u.v[k];
+    }
+  }
+  __device__ __forceinline__ Frag<T> read(const char* tile, int m, int s) const {
+    union {
+      Frag<T> f;
+      bf16x8 v[kParts];
+    } u;
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      const char* p = tile + k * kPart;
+      if constexpr (K_DENSE) {
+        u.v[k] = *reinterpret_cast<const bf16x8*>(p + (at ^ (s << 5)) + m * 32 * (kChunks * 16));
+      } else {
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+        const int o = at ^ (m << 6);
+        union {
+          s16x4 q[2];
+          bf16x8 v;
+        } w;
+        p += 16 * s * (kChunks * 16);
+        w.q[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + o));
+        w.q[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 4 * (kChunks * 16) + (o ^ 16)));
+        u.v[k] = w.v;
+      }
+    }
+    return u.f;
+  }
+};
+
+template <typename T, bool A_DENSE, bool B_DENSE, bool OVER_ROWS>
+__global__ __launch_bounds__(256, 2) void k_group_staged(GroupArgs a) {
+  using SideA = StagedSide<T, A_DENSE>;
+  using SideB = StagedSide<T, B_DENSE>;
+  __shared__ __align__(1024) char lds[SideA::kBytes + SideB::kBytes];
+  const int n_tiles = (a.n + kStagedTile - 1) / kStagedTile;
+  int m0, n0, m_end, k0, k_end, g, split;
   if constexpr (OVER_ROWS) {
-    const int m_tiles = (a.m + kPlainTile - 1) / kPlainTile, each = m_tiles * n_tiles;
+    const int m_tiles = (a.m + kStagedTile - 1) / kStagedTile, each = m_tiles * n_tiles * a.splits;
     g = blockIdx.x / each;
-    const int rest = blockIdx.x - g * each;
-    m0 = rest / n_tiles * kPlainTile;
-    n0 = rest % n_tiles * kPlainTile;
+    int rest = blockIdx.x - g * each;
+    split = rest / (m_tiles * n_tiles);
+    rest -= split * m_tiles * n_tiles;
+    m0 = rest / n_tiles * kStagedTile;
+    n0 = rest % n_tiles * kStagedTile;
     m_end = a.m;
     k0 = group_bound(a, g + 1);
-    k_end = group_bound(a, g + 2);
+    k_end = max(group_bound(a, g + 2), k0);
   } else {
-    GroupTiles<kPlainTile> tiles;
-    tiles.look(a, 0);
-    const GroupSpan s = tiles.find(a, blockIdx.x / n_tiles);
+    GroupTiles<kStagedTile> spans;
+    spans.look(a, 0);
+    const int nn = blockIdx.x % (n_tiles * a.splits);
+    const GroupSpan s = spans.find(a, blockIdx.x / (n_tiles * a.splits));
     if (s.first >= s.last) return;
     g = s.group;
     m0 = s.first;
     m_end = s.last;
-    n0 = blockIdx.x % n_tiles * kPlainTile;
+    split = nn / n_tiles;
+    n0 = (nn - split * n_tiles) * kStagedTile;
     k0 = 0;
     k_end = g < 0 ? 0 : a.k;
   }
-  const T *A = static_cast<const T*>(a.a), *B = static_cast<const T*>(a.b) + (OVER_ROWS || g < 0 ? 0 : g * a.b_g);
-  float acc[4][4] = {};
-  const int tm = (threadIdx.x >> 4) * 4, tn = (threadIdx.x & 15) * 4;
-  for (int k = k0; k < k_end; k += kPlainStep) {
+  group_part(a, split, kStagedK, &k0, &k_end);
+  const int wave = threadIdx.x / kWave, wm = wave % 2, wn = wave / 2;
+
+  f32x16 acc[2][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int at = threadIdx.x + 256 * i;
-      // consecutive threads along the axis that lies dense
-      const int am = a.a_k == 1 ? at / kPlainStep : at % kPlainTile, ak = a.a_k == 1 ? at % kPlainStep : at / kPlainTile;
-      as[ak][am] = m0 + am < m_end && k + ak < k_end ? (float)A[(int64_t)(m0 + am) * a.a_m + (int64_t)(k + ak) * a.a_k] : 0.0f;
-      const int bn = a.b_n == 1 ? at % kPlainTile : at / kPlainStep, bk = a.b_n == 1 ? at / kPlainTile : at % kPlainStep;
-      bs[bk][bn] = n0 + bn < a.n && k + bk < k_end ? (float)B[(int64_t)(k + bk) * a.b_k + (int64_t)(n0 + bn) * a.b_n] : 0.0f;
-    }
-    __syncthreads();
+  for (int n = 0; n < 2; ++n)
 #pragma unroll
-    for (int kk = 0; kk < kPlainStep; ++kk) {
-      float x[4], y[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = as[kk][tm + i];
-        y[i] = bs[kk][tn + i];
+    for (int m = 0; m < 2; ++m) acc[n][m] = (f32x16)0.0f;
+  if (k0 < k_end) {
+    SideA sa;
+    SideB sb;
+    sa.plan(static_cast<const T*>(a.a) + m0 * a.a_m + k0 * a.a_k, A_DENSE ? a.a_m : a.a_k, m_end - m0, wm * 64);
+    sb.plan(static_cast<const T*>(a.b) + (OVER_ROWS ? 0 : g * a.b_g) + k0 * a.b_k + n0 * a.b_n, B_DENSE ? a.b_n : a.b_k, a.n - n0, wn * 64);
+    int left = k_end - k0;
+    sa.load(0, left);
+    sb.load(0, left);
+    for (int t = 0; left > 0; ++t) {
+      __syncthreads();  // the tile before has been read
+      sa.store(lds);
+      sb.store(lds + SideA::kBytes);
+      __syncthreads();
+      left -= kStagedK;
+      if (left > 0) {
+        sa.load(t + 1, left);
+        sb.load(t + 1, left);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int s = 0; s < kStagedK / 16; ++s) {
+        Frag<T> fa[2], fb[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+        for (int i = 0; i < 2; ++i) {
+          fb[i] = sb.read(lds + SideA::kBytes, i, s);
+          fa[i] = sa.read(lds, i, s);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) acc[n][m] = mma(fb[n], fa[m], acc[n][m]);
+      }
     }
-    __syncthreads();
   }
+
   T* C = static_cast<T*>(a.c) + (OVER_ROWS ? g * a.c_g : 0);
+  const int width = group_part_width(a.n);
+  float* part = a.part + ((int64_t)split * (OVER_ROWS ? (int64_t)a.groups * a.m : a.rows) + (OVER_ROWS ? (int64_t)g * a.m : 0)) * width;
+  const int l = __lane_id(), h = l >> 5;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int m = 0; m < 2; ++m) {
+    const int row = m0 + (wm * 2 + m) * 32 + (l & 31);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (m0 + tm + i < m_end && n0 + tn + j < a.n) C[(int64_t)(m0 + tm + i) * a.c_m + (int64_t)(n0 + tn + j) * a.c_n] = (T)acc[i][j];
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        // a lane and the one 32 on hold fours of columns in turn: now eight in a row each
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[n][m][8 * q + e]), __float_as_uint(acc[n][m][8 * q + 4 + e]), false, false);
+          x[e] = __uint_as_float(w[0]);
+          x[4 + e] = __uint_as_float(w[1]);
+        }
+        const int col = n0 + (wn * 2 + n) * 32 + 16 * q + 8 * h;
+        if (row >= m_end || col >= a.n) continue;
+        if (a.splits > 1)
+          store_elems<8>(part + (int64_t)row * width + col, x);
+        else
+          store_units(C + row * a.c_m + col, min(a.n - col, 8), x);
+      }
+  }
+}
+
+// C from the parts: eight results a thread.
+template <typename T>
+__global__ __launch_bounds__(256) void k_group_join(GroupArgs a, int64_t rows, int outer_rows, int64_t outer_stride) {
+  const int width = group_part_width(a.n), chunks = width / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / chunks;
+  if (row >= rows) return;
+  const int col = (int)(i - row * chunks) * 8;
+  const float* p = a.part + row * width + col;
+  float x[8] = {};
+  for (int s = 0; s < a.splits; ++s) {
+    float y[8];
+    load_elems<8>(p + s * rows * width, y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] += y[e];
+  }
+  const int64_t outer = row / outer_rows, in = row - outer * outer_rows;
+  store_units(static_cast<T*>(a.c) + outer * outer_stride + in * a.c_m + col, min(a.n - col, 8), x);
 }
 
 namespace {
@@ -87,26 +264,62 @@ bool group_aligned(bool over_rows, const GroupArgs& a) {
   const int64_t as = over_rows || a.a_k != 1 ? a.a_k : a.a_m, bs = a.b_n == 1 ? a.b_k : a.b_n;
   for (const void* p : {a.a, a.b, static_cast<const void*>(a.c)})
     if ((uintptr_t)p % 16) return false;
-  return as % 8 == 0 && bs % 8 == 0 && a.b_g % 8 == 0 && a.c_g % 8 == 0 && a.c_m % 8 == 0 && a.c_n == 1 && as <= kFar && bs <= kFar && a.c_m <= kFar &&
+  return as % 8 == 0 && bs % 8 == 0 && a.b_g % 8 == 0 && a.c_g % 8 == 0 && a.c_m % 8 == 0 && as <= kFar && bs <= kFar && a.c_m <= kFar &&
          a.n % 8 == 0 && (over_rows ? a.m : a.k) % 8 == 0;
+}
+
+template <typename T>
+void staged_launch(bool over_rows, const GroupArgs& a, unsigned blocks, hipStream_t s) {
+  if (over_rows)
+    k_group_staged<T, false, false, true><<<blocks, 256, 0, s>>>(a);
+  else if (a.b_k == 1)
+    k_group_staged<T, true, true, false><<<blocks, 256, 0, s>>>(a);
+  else
+    k_group_staged<T, true, false, false><<<blocks, 256, 0, s>>>(a);
 }
 
 }  // namespace
 
-// Workgroups of a launch (the caller checks that a grid takes them).
+// Workgroups of a launch at most, before the sums are split (the caller checks that a grid takes them).
 int64_t group_tiles(bool over_rows, int64_t rows, int64_t m, int64_t n, int64_t groups) {
-  return over_rows ? groups * tiles(m, kPlainTile) * tiles(n, kPlainTile)
-                   : (tiles(rows, kPlainTile) + std::min(groups + 2, rows)) * tiles(n, kPlainTile);
+  return over_rows ? groups * tiles(m, kStagedTile) * tiles(n, kStagedTile)
+                   : (tiles(rows, kStagedTile) + std::min(groups + 2, rows)) * tiles(n, kStagedTile);
 }
 
-hipError_t launch_group(bool over_rows, const GroupArgs& a, int type, hipStream_t s) {
+// Parts of the sums: a part for each place of two workgroups a CU that would be empty, of 256 k at least.
+int group_splits(bool over_rows, int64_t rows, int64_t m, int64_t n, int64_t k, int64_t groups) {
+  const int64_t blocks = group_tiles(over_rows, rows, m, n, groups), length = over_rows ? rows / std::max<int64_t>(groups, 1) : k;
+  if (blocks == 0 || blocks > 256) return 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(512 / blocks, length / 256));
+}
+
+size_t group_part_bytes(bool over_rows, int64_t rows, int64_t m, int64_t n, int64_t k, int64_t groups) {
+  const int splits = group_splits(over_rows, rows, m, n, k, groups);
+  return splits > 1 ? (size_t)splits * (over_rows ? groups * m : rows) * group_part_width((int)n) * sizeof(float) : 0;
+}
+
+hipError_t launch_group(bool over_rows, GroupArgs a, int type, void* ws, hipStream_t s) {
   const int64_t blocks = group_tiles(over_rows, a.rows, a.m, a.n, a.groups);
   if (blocks == 0) return hipSuccess;
-  if (type == GS_BF16 && group_aligned(over_rows, a)) return launch_group_mfma(over_rows, a, s);
+  a.splits = group_splits(over_rows, a.rows, a.m, a.n, a.k, a.groups);
+  a.part = static_cast<float*>(ws);
+  if (type == GS_BF16 && group_aligned(over_rows, a)) {
+    a.splits = 1;
+    return launch_group_mfma(over_rows, a, nullptr, s);
+  }
   if (type == GS_BF16)
-    over_rows ? k_group_plain<__bf16, true><<<(unsigned)blocks, 256, 0, s>>>(a) : k_group_plain<__bf16, false><<<(unsigned)blocks, 256, 0, s>>>(a);
+    staged_launch<__bf16>(over_rows, a, (unsigned)(blocks * a.splits), s);
   else
-    over_rows ? k_group_plain<float, true><<<(unsigned)blocks, 256, 0, s>>>(a) : k_group_plain<float, false><<<(unsigned)blocks, 256, 0, s>>>(a);
+    staged_launch<float>(over_rows, a, (unsigned)(blocks * a.splits), s);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  const int64_t rows = over_rows ? (int64_t)a.groups * a.m : a.rows;
+  const int outer = over_rows ? a.m : a.rows;
+  const unsigned groups = (unsigned)tiles(rows * (group_part_width(a.n) / 8), 256);
+  if (type == GS_BF16)
+    k_group_join<__bf16><<<groups, 256, 0, s>>>(a, rows, outer, a.c_g);
+  else
+    k_group_join<float><<<groups, 256, 0, s>>>(a, rows, outer, a.c_g);
   return hipGetLastError();
 }
 

@@ -341,7 +341,7 @@ void group_launch(bool over_rows, const GroupArgs& a, hipStream_t s) {
 }  // namespace
 
 // C's rows dense, A's and B's k dense or not.  The caller has checked alignment, sizes and the grid.
-hipError_t launch_group_mfma(bool over_rows, const GroupArgs& a, hipStream_t s) {
+hipError_t launch_group_mfma(bool over_rows, const GroupArgs& a, int64_t*, hipStream_t s) {
   group_launch<256, 256, 2, 2>(over_rows, a, s);
   return hipGetLastError();
 }

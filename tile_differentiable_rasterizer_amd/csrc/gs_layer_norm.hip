@@ -72,42 +72,6 @@ struct RowSum {
   }
 };
 
-// The eight units at p, of which n exist (0: none); a vector load at any alignment.
-template <typename T>
-__device__ __forceinline__ void load_units(const T* p, int n, float (&x)[8]) {
-  if (n >= 8) {
-    typedef T V __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
-    constexpr int kPer = 16 / sizeof(T);
-#pragma unroll
-    for (int i = 0; i < 8; i += kPer) {
-      const V v = *reinterpret_cast<const V*>(p + i);
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) x[i + j] = (float)v[j];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = i < n ? (float)p[i] : 0.0f;
-  }
-}
-template <typename T>
-__device__ __forceinline__ void store_units(T* p, int n, const float (&x)[8]) {
-  if (n >= 8) {
-    typedef T V __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
-    constexpr int kPer = 16 / sizeof(T);
-#pragma unroll
-    for (int i = 0; i < 8; i += kPer) {
-      V v;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) v[j] = (T)x[i + j];
-      *reinterpret_cast<V*>(p + i) = v;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = (T)x[i];
-  }
-}
-
 template <typename T, int G, int J, bool BWD>
 __global__ __launch_bounds__(layer_norm_threads(G)) void k_layer_norm(LayerNormArgs a) {
   constexpr int kThreads = layer_norm_threads(G), kRows = kThreads / G;  // rows of a workgroup at once

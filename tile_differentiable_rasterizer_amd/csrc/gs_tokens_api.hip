@@ -30,7 +30,8 @@ hipError_t launch_layer_norm(int64_t rows, int width, int type, float eps, const
                              int64_t xs, const float* w, const float* b, void* y, int64_t ys, float* dw, float* db,
                              void* ws, hipStream_t s);
 int64_t group_tiles(bool over_rows, int64_t rows, int64_t m, int64_t n, int64_t groups);
-hipError_t launch_group(bool over_rows, const GroupArgs& a, int type, hipStream_t s);
+size_t group_part_bytes(bool over_rows, int64_t rows, int64_t m, int64_t n, int64_t k, int64_t groups);
+hipError_t launch_group(bool over_rows, GroupArgs a, int type, void* ws, hipStream_t s);
 hipError_t launch_adamw(int count, const gs_adamw_tensor* tensors, int grad_type, int bits, void* m, void* v,
                         float* bounds, const gs_adamw_params& h, const float* grad_scale, hipStream_t s);
 hipError_t launch_adamw_moments(int64_t blocks, const int8_t* m, const uint8_t* v, const float* bounds, float* out_m,
@@ -414,7 +415,7 @@ GroupArgs group_args(const gs_group_mm& p) {
 }  // namespace
 
 size_t gs_group_mm_fwd_workspace_bytes(const gs_group_mm* p) {
-  return 0;
+  return group_shape(p, false) == GS_OK ? round16(group_part_bytes(false, p->rows, p->rows, p->n, p->k, p->groups)) : 0;
 }
 
 gs_status gs_group_mm_fwd(const gs_group_mm* p, const void* x, int64_t x_stride, gs_weights w, void* y,
@@ -425,6 +426,8 @@ gs_status gs_group_mm_fwd(const gs_group_mm* p, const void* x, int64_t x_stride,
   if (!rows_ok(y, y_stride, p->rows, p->n, p->type) || (p->k && !rows_in_ok(x, x_stride, p->rows, p->type)) ||
       !weights_ok(&w, p->groups, p->k, p->n, p->type, false))
     return GS_ERR_INVALID_ARG;
+  const size_t need = gs_group_mm_fwd_workspace_bytes(p);
+  if (need && (!workspace || !on(workspace, 16) || workspace_bytes < need)) return GS_ERR_WORKSPACE;
   x_stride = of_rows(x_stride, p->rows);
   y_stride = of_rows(y_stride, p->rows);
   GroupArgs a = group_args(*p);
@@ -432,11 +435,15 @@ gs_status gs_group_mm_fwd(const gs_group_mm* p, const void* x, int64_t x_stride,
   a.b = w.data; a.b_g = w.group_stride; a.b_k = w.k_stride; a.b_n = w.n_stride;
   a.c = y; a.c_m = y_stride; a.c_n = 1;
   a.m = a.rows; a.n = (int32_t)p->n; a.k = (int32_t)p->k;
-  return status_of(launch_group(false, a, p->type, static_cast<hipStream_t>(stream)));
+  return status_of(launch_group(false, a, p->type, workspace, static_cast<hipStream_t>(stream)));
 }
 
 size_t gs_group_mm_bwd_workspace_bytes(const gs_group_mm* p) {
-  return 0;
+  if (group_shape(p, true) != GS_OK) return 0;
+  // dx's parts, then in their place dW's, whichever way it lies
+  const size_t dx = group_part_bytes(false, p->rows, p->rows, p->k, p->n, p->groups);
+  const size_t dw = group_part_bytes(true, p->rows, p->k, p->n, p->rows, p->groups), turned = group_part_bytes(true, p->rows, p->n, p->k, p->rows, p->groups);
+  return round16(dx > dw ? dx > turned ? dx : turned : dw > turned ? dw : turned);
 }
 
 gs_status gs_group_mm_bwd(const gs_group_mm* p, const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
@@ -450,6 +457,8 @@ gs_status gs_group_mm_bwd(const gs_group_mm* p, const void* dy, int64_t dy_strid
     return GS_ERR_INVALID_ARG;
   if (has_dw && ((p->rows && !rows_in_ok(x, x_stride, p->rows, p->type)) || !weights_ok(&dw, p->groups, p->k, p->n, p->type, true)))
     return GS_ERR_INVALID_ARG;
+  const size_t need = has_dx || has_dw ? gs_group_mm_bwd_workspace_bytes(p) : 0;
+  if (need && (!workspace || !on(workspace, 16) || workspace_bytes < need)) return GS_ERR_WORKSPACE;
   dy_stride = of_rows(dy_stride, p->rows);
   x_stride = of_rows(x_stride, p->rows);
   dx_stride = of_rows(dx_stride, p->rows);
@@ -459,7 +468,7 @@ gs_status gs_group_mm_bwd(const gs_group_mm* p, const void* dy, int64_t dy_strid
     a.b = w.data; a.b_g = w.group_stride; a.b_k = w.n_stride; a.b_n = w.k_stride;
     a.c = dx; a.c_m = dx_stride; a.c_n = 1;
     a.m = a.rows; a.n = (int32_t)p->k; a.k = (int32_t)p->n;
-    const gs_status e = status_of(launch_group(false, a, p->type, static_cast<hipStream_t>(stream)));
+    const gs_status e = status_of(launch_group(false, a, p->type, workspace, static_cast<hipStream_t>(stream)));
     if (e != GS_OK) return e;
   }
   if (!has_dw) return GS_OK;
@@ -470,7 +479,7 @@ gs_status gs_group_mm_bwd(const gs_group_mm* p, const void* dy, int64_t dy_strid
   a.b = turned ? x : dy; a.b_k = turned ? x_stride : dy_stride; a.b_n = 1;
   a.c = dw.data; a.c_g = dw.group_stride; a.c_m = turned ? dw.n_stride : dw.k_stride; a.c_n = 1;
   a.m = (int32_t)(turned ? p->n : p->k); a.n = (int32_t)(turned ? p->k : p->n); a.k = a.rows;
-  return status_of(launch_group(true, a, p->type, static_cast<hipStream_t>(stream)));
+  return status_of(launch_group(true, a, p->type, workspace, static_cast<hipStream_t>(stream)));
 }
 
 gs_status gs_adamw(int32_t count, const gs_adamw_tensor* tensors, int32_t grad_type, int32_t bits, void* m, void* v,
