@@ -23,6 +23,9 @@ struct GroupArgs {
   float* part;     // where there are several: [splits][rows] (over rows: [splits][groups][m]) rows of group_part_width(n)
 };
 
+// Blocks of results that a workgroup makes: on the matrix units straight from LDS, and staged through registers.
+enum { kGroup256x256, kGroup128x256, kGroup128x128, kGroup32x256, kGroup32x128, kGroupStaged, kGroupTiles };
+
 __host__ __device__ constexpr int group_part_width(int n) { return (n + 7) & ~7; }
 
 // Part `split` of k0 .. k_end, in whole steps of `step`.

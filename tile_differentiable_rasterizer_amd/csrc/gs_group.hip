@@ -11,13 +11,14 @@
 // Where a sum is long and the results are few, several workgroups share it: their parts go to a workspace in
 // float32, and a second kernel adds them in a fixed order.
 #include <algorithm>
+#include <cmath>
 
 #include "gs_group.h"
 #include "gs_mfma.h"
 
 namespace gs {
 
-hipError_t launch_group_mfma(bool over_rows, const GroupArgs& a, int64_t* blocks, hipStream_t s);
+hipError_t launch_group_mfma(bool over_rows, int tile, const GroupArgs& a, hipStream_t s);
 
 constexpr int kStagedTile = 128, kStagedK = 32;
 
@@ -286,32 +287,77 @@ int64_t group_tiles(bool over_rows, int64_t rows, int64_t m, int64_t n, int64_t 
                    : (tiles(rows, kStagedTile) + std::min(groups + 2, rows)) * tiles(n, kStagedTile);
 }
 
-// Parts of the sums: a part for each place of two workgroups a CU that would be empty, of 256 k at least.
-int group_splits(bool over_rows, int64_t rows, int64_t m, int64_t n, int64_t k, int64_t groups) {
-  const int64_t blocks = group_tiles(over_rows, rows, m, n, groups), length = over_rows ? rows / std::max<int64_t>(groups, 1) : k;
-  if (blocks == 0 || blocks > 256) return 1;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(512 / blocks, length / 256));
+namespace {
+
+struct GroupPlan {
+  int tile, splits;
+};
+
+// The block of results and the parts of the sums with the least time by a model: rounds of workgroups on the CUs' places, each a
+// start and an end and a time for 64 k, and the join of the parts.  Rows of a group are not known here: the last
+// block of rows of each is taken as half full.
+//
+// Measured, us (by rows; 256 x 256, 128 x 256, 128 x 128, 32 x 256, 32 x 128): 7814 rows of 8 groups, 2048 x 4096: 149 139 154 298
+// 295; 782 rows 46 37 40 48 50; 64 rows of 16 groups 52 49 47 43 47; 3907 rows of one, 2048 x 2048: 45 35 36 66 66; 20000 rows of 8, 512 x 256:
+// 18 13 15 19 17; 64 rows of 4, 4096 x 512, in the best number of parts: 19 17 14 14 13, in one 32 x 128: 33.  Over rows (the first
+// three): 7814 rows of 8, 2048 x 4096: 143 169 163; 20000 rows of 8, 512 x 256: 32 26 22 in 8, 8 and 4 parts, 66 in one; 40000
+// rows of one, 1024 x 512: 63 57 65 in 32, 16 and 16 parts.
+GroupPlan group_plan(bool over_rows, bool staged, bool f32, int64_t rows, int64_t m, int64_t n, int64_t k, int64_t groups) {
+  struct Shape {
+    int bm, bn, places;
+    double fix, by_rows, over;  // us
+  };
+  static const Shape kShapes[kGroupTiles] = {{256, 256, 256, 5.0, 1.5, 1.6},  {128, 256, 256, 3.0, 1.0, 1.15}, {128, 128, 512, 3.0, 1.15, 1.2},
+                                             {32, 256, 256, 2.0, 0.5, 0.0},   {32, 128, 512, 2.0, 0.5, 0.0},   {128, 128, 512, 3.0, 2.0, 2.0}};
+  const double used = (double)std::min(groups, over_rows ? groups : rows);
+  const double length = over_rows ? (double)rows / (double)std::max<int64_t>(groups, 1) : (double)k;
+  GroupPlan best{staged ? kGroupStaged : kGroup128x128, 1};
+  double least = 1e300;
+  for (int t = 0; t < kGroupTiles; ++t) {
+    const Shape& x = kShapes[t];
+    if ((t == kGroupStaged) != staged || (over_rows && x.bm < 128)) continue;
+    const double m_tiles = over_rows ? (double)(groups * tiles(m, x.bm)) : std::max(used, (double)rows / x.bm + 0.5 * used);
+    const double blocks = std::max(1.0, m_tiles * (double)tiles(n, x.bn));
+    for (int splits = 1; splits <= 32; splits *= 2) {
+      if (splits > 1 && (length < 128.0 * splits || blocks * splits > 2.0 * x.places)) break;
+      const double rounds = std::max(1.0, std::ceil(blocks * splits / x.places - 0.1));
+      const double each = (over_rows ? x.over : x.by_rows) * (staged && f32 ? 2.0 : 1.0);
+      double time = rounds * (x.fix + std::ceil(length / splits / 64.0) * each);
+      if (splits > 1) time += 5.0 + (double)splits * (double)(over_rows ? groups * m : rows) * (double)n * 8.0 / 4e6;
+      if (time < least) {
+        least = time;
+        best = {t, splits};
+      }
+    }
+  }
+  return best;
 }
 
-size_t group_part_bytes(bool over_rows, int64_t rows, int64_t m, int64_t n, int64_t k, int64_t groups) {
-  const int splits = group_splits(over_rows, rows, m, n, k, groups);
+}  // namespace
+
+// Bytes of the parts, whichever kernel makes them.
+size_t group_part_bytes(bool over_rows, int type, int64_t rows, int64_t m, int64_t n, int64_t k, int64_t groups) {
+  int splits = group_plan(over_rows, true, type == GS_F32, rows, m, n, k, groups).splits;
+  if (type == GS_BF16) splits = std::max(splits, group_plan(over_rows, false, false, rows, m, n, k, groups).splits);
   return splits > 1 ? (size_t)splits * (over_rows ? groups * m : rows) * group_part_width((int)n) * sizeof(float) : 0;
 }
 
 hipError_t launch_group(bool over_rows, GroupArgs a, int type, void* ws, hipStream_t s) {
   const int64_t blocks = group_tiles(over_rows, a.rows, a.m, a.n, a.groups);
   if (blocks == 0) return hipSuccess;
-  a.splits = group_splits(over_rows, a.rows, a.m, a.n, a.k, a.groups);
+  const GroupPlan plan = group_plan(over_rows, type == GS_F32 || !group_aligned(over_rows, a), type == GS_F32, a.rows, a.m, a.n, a.k, a.groups);
+  a.splits = plan.splits;
   a.part = static_cast<float*>(ws);
-  if (type == GS_BF16 && group_aligned(over_rows, a)) {
-    a.splits = 1;
-    return launch_group_mfma(over_rows, a, nullptr, s);
+  hipError_t e;
+  if (plan.tile != kGroupStaged) {
+    e = launch_group_mfma(over_rows, plan.tile, a, s);
+  } else {
+    if (type == GS_BF16)
+      staged_launch<__bf16>(over_rows, a, (unsigned)(blocks * a.splits), s);
+    else
+      staged_launch<float>(over_rows, a, (unsigned)(blocks * a.splits), s);
+    e = hipGetLastError();
   }
-  if (type == GS_BF16)
-    staged_launch<__bf16>(over_rows, a, (unsigned)(blocks * a.splits), s);
-  else
-    staged_launch<float>(over_rows, a, (unsigned)(blocks * a.splits), s);
-  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t rows = over_rows ? (int64_t)a.groups * a.m : a.rows;
   const int outer = over_rows ? a.m : a.rows;

@@ -105,20 +105,23 @@ struct GroupSide {
   }
 };
 
+// Workgroups that a CU's LDS (160 KB) holds at a time, two at most.
+constexpr int group_places(int bm, int bn) { return (2 * bm + 3 * bn) * kGroupK * 2 > 80 * 1024 ? 1 : 2; }
+
 // A block of results: rows m0 .. m_end, columns from n0 on, summed over k0 .. k_end.
 struct GroupPlace {
-  int g, m0, m_end, n0, k0, k_end;
+  int g, m0, m_end, n0, k0, k_end, split;
 };
 
-template <bool A_DENSE, bool B_DENSE, bool OVER_ROWS, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) void k_group_mfma(GroupArgs a) {
+template <bool A_DENSE, bool B_DENSE, bool OVER_ROWS, bool PARTS, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(256, group_places(BM, BN)) void k_group_mfma(GroupArgs a) {
   using SideA = GroupSide<A_DENSE, BM>;
   using SideB = GroupSide<B_DENSE, BN>;
   constexpr int TM = BM / WM / 32, TN = BN / WN / 32, kMma = TM * TN, kReads = TM + TN;
-  constexpr int kStores = TM * TN * 2;
+  constexpr int kStores = TM * TN * (PARTS ? 4 : 2);
   static_assert(WM * WN == 4, "four wavefronts");
   __shared__ __align__(1024) char lds[2 * SideA::kBytes + 3 * SideB::kBytes];
-  const int n_tiles = (a.n + BN - 1) / BN;
+  const int n_tiles = (a.n + BN - 1) / BN, columns = PARTS ? n_tiles * a.splits : n_tiles;  // a part's blocks beside the next one's
 
   // the blocks, an eighth to each XCD (whose workgroups are every eighth), there in patches of a few tiles of rows
   GroupTiles<BM> spans;
@@ -126,7 +129,7 @@ __global__ __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) void k_group_mfma
   int g_over = 0;
   if constexpr (OVER_ROWS) {
     m_tiles = (a.m + BM - 1) / BM;
-    const uint32_t each = m_tiles * n_tiles;
+    const uint32_t each = m_tiles * columns;
     g_over = blockIdx.x / each;
     const uint32_t in = blockIdx.x - g_over * each, q = each / 8, more = each % 8;
     const uint32_t slot = (blockIdx.x - g_over * each) % 8;
@@ -134,17 +137,19 @@ __global__ __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) void k_group_mfma
     end = id + 1;
   } else {
     m_tiles = spans.count(a);
-    const uint32_t all = m_tiles * n_tiles, q = all / 8, more = all % 8, xcd = blockIdx.x % 8;
+    const uint32_t all = m_tiles * columns, q = all / 8, more = all % 8, xcd = blockIdx.x % 8;
     id = xcd * q + min(xcd, more);
     end = id + q + (xcd < more);
     id += blockIdx.x / 8;
   }
   auto find = [&](uint32_t i) {
-    constexpr uint32_t kHigh = 2048 / BM;
-    const uint32_t patch = i / (kHigh * n_tiles), rest = i - patch * kHigh * n_tiles, high = min(kHigh, m_tiles - patch * kHigh);
+    constexpr uint32_t kHigh = BM >= 128 ? 2048 / BM : 16;
+    const uint32_t patch = i / (kHigh * columns), rest = i - patch * kHigh * columns, high = min(kHigh, m_tiles - patch * kHigh);
     const uint32_t mt = patch * kHigh + rest % high;
     GroupPlace p;
-    p.n0 = rest / high * BN;
+    const uint32_t column = rest / high;
+    p.split = PARTS ? column / n_tiles : 0;
+    p.n0 = (PARTS ? column - p.split * n_tiles : column) * BN;
     if constexpr (OVER_ROWS) {
       p.g = g_over;
       p.m0 = mt * BM;
@@ -159,6 +164,7 @@ __global__ __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) void k_group_mfma
       p.k0 = 0;
       p.k_end = s.group < 0 ? 0 : a.k;
     }
+    if constexpr (PARTS) group_part(a, p.split, kGroupK, &p.k0, &p.k_end);
     return p;
   };
   if (id >= end) return;
@@ -282,34 +288,47 @@ __global__ __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) void k_group_mfma
     }
     keep();
 
-    char* C = reinterpret_cast<char*>(static_cast<__bf16*>(a.c) + (OVER_ROWS ? done.g * a.c_g : 0) + done.m0 * a.c_m + done.n0);
+    const int width = group_part_width(a.n);
+    const int64_t c_m = PARTS ? width : a.c_m;
+    char* C = PARTS ? reinterpret_cast<char*>(a.part + ((done.split * (OVER_ROWS ? a.groups : 1) + (OVER_ROWS ? done.g : 0)) * (int64_t)a.m + done.m0) * width + done.n0)
+                    : reinterpret_cast<char*>(static_cast<__bf16*>(a.c) + (OVER_ROWS ? done.g * a.c_g : 0) + done.m0 * c_m + done.n0);
+    constexpr int kSize = PARTS ? 4 : 2;
     const auto out = __builtin_amdgcn_make_buffer_rsrc(C, 0, 0x7fffffff, 0x00020000);
     const int l = __lane_id(), h = l >> 5;
 #pragma unroll
     for (int m = 0; m < TM; ++m) {
       const int row = (wm * TM + m) * 32 + (l & 31);
-      const uint32_t row_at = row < done.m_end - done.m0 ? (uint32_t)(row * a.c_m) * 2u : 0x80000000u;
+      const uint32_t row_at = row < done.m_end - done.m0 ? (uint32_t)(row * c_m) * kSize : 0x80000000u;
 #pragma unroll
       for (int n = 0; n < TN; ++n)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
+          typedef __attribute__((__vector_size__(4 * sizeof(uint32_t)))) uint32_t u32x4;
           union {
             __bf16 x[8];
-            uint32_t u[4];
-            __attribute__((__vector_size__(4 * sizeof(uint32_t)))) uint32_t v;
+            uint32_t u[8];
+            u32x4 v[2];
           } r;
+          constexpr int kWords = PARTS ? 4 : 2;
+          if constexpr (PARTS) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) r.x[e] = (__bf16)acc[n][m][8 * q + e];
+            for (int e = 0; e < 8; ++e) r.u[e] = __float_as_uint(acc[n][m][8 * q + e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r.x[e] = (__bf16)acc[n][m][8 * q + e];
+          }
           // a lane and the one 32 on hold fours of columns in turn: now eight in a row each
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const auto w = __builtin_amdgcn_permlane32_swap(r.u[e], r.u[2 + e], false, false);
+          for (int e = 0; e < kWords; ++e) {
+            const auto w = __builtin_amdgcn_permlane32_swap(r.u[e], r.u[kWords + e], false, false);
             r.u[e] = w[0];
-            r.u[2 + e] = w[1];
+            r.u[kWords + e] = w[1];
           }
           const int col = (wn * TN + n) * 32 + 16 * q + 8 * h;
           // past the last row or column: past the buffer's end, where nothing is written.  So every store is made, and counted.
-          __builtin_amdgcn_raw_buffer_store_b128(r.v, out, done.n0 + col < a.n ? row_at + col * 2 : 0x80000000u, 0, 0);
+          const uint32_t to_at = done.n0 + col < a.n ? row_at + col * kSize : 0x80000000u;
+          __builtin_amdgcn_raw_buffer_store_b128(r.v[0], out, to_at, 0, 0);
+          if constexpr (PARTS) __builtin_amdgcn_raw_buffer_store_b128(r.v[1], out, to_at + 16, 0, 0);
           __builtin_amdgcn_sched_barrier(0);  // a few registers at a time
         }
     }
@@ -322,27 +341,40 @@ namespace {
 
 int64_t tiles(int64_t n, int64_t each) { return (n + each - 1) / each; }
 
-template <int BM, int BN, int WM, int WN>
+template <bool PARTS, int BM, int BN, int WM, int WN>
 void group_launch(bool over_rows, const GroupArgs& a, hipStream_t s) {
-  constexpr int64_t kSlots = BM * BN > 128 * 128 ? 256 : 512;  // workgroups at a time: one a CU, or two
+  constexpr int64_t kSlots = 256 * group_places(BM, BN);  // workgroups at a time
+  const int64_t columns = tiles(a.n, BN) * a.splits;
   if (over_rows) {
-    const int64_t blocks = a.groups * tiles(a.m, BM) * tiles(a.n, BN);
-    k_group_mfma<false, false, true, BM, BN, WM, WN><<<(unsigned)blocks, 256, 0, s>>>(a);
+    if constexpr (BM >= 128) k_group_mfma<false, false, true, PARTS, BM, BN, WM, WN><<<(unsigned)(a.groups * tiles(a.m, BM) * columns), 256, 0, s>>>(a);
     return;
   }
-  const int64_t most = (tiles(a.rows, BM) + std::min<int64_t>(a.groups + 2, a.rows)) * tiles(a.n, BN);
+  const int64_t most = (tiles(a.rows, BM) + std::min<int64_t>(a.groups + 2, a.rows)) * columns;
   const unsigned blocks = (unsigned)std::min(kSlots, tiles(most, 8) * 8);
   if (a.b_k == 1)
-    k_group_mfma<true, true, false, BM, BN, WM, WN><<<blocks, 256, 0, s>>>(a);
+    k_group_mfma<true, true, false, PARTS, BM, BN, WM, WN><<<blocks, 256, 0, s>>>(a);
   else
-    k_group_mfma<true, false, false, BM, BN, WM, WN><<<blocks, 256, 0, s>>>(a);
+    k_group_mfma<true, false, false, PARTS, BM, BN, WM, WN><<<blocks, 256, 0, s>>>(a);
+}
+template <int BM, int BN, int WM, int WN>
+void group_launch(bool over_rows, const GroupArgs& a, hipStream_t s) {
+  if (a.splits > 1)
+    group_launch<true, BM, BN, WM, WN>(over_rows, a, s);
+  else
+    group_launch<false, BM, BN, WM, WN>(over_rows, a, s);
 }
 
 }  // namespace
 
 // C's rows dense, A's and B's k dense or not.  The caller has checked alignment, sizes and the grid.
-hipError_t launch_group_mfma(bool over_rows, const GroupArgs& a, int64_t*, hipStream_t s) {
-  group_launch<256, 256, 2, 2>(over_rows, a, s);
+hipError_t launch_group_mfma(bool over_rows, int tile, const GroupArgs& a, hipStream_t s) {
+  switch (tile) {
+    case kGroup256x256: group_launch<256, 256, 2, 2>(over_rows, a, s); break;
+    case kGroup128x256: group_launch<128, 256, 2, 2>(over_rows, a, s); break;
+    case kGroup128x128: group_launch<128, 128, 2, 2>(over_rows, a, s); break;
+    case kGroup32x256: group_launch<32, 256, 1, 4>(over_rows, a, s); break;
+    default: group_launch<32, 128, 1, 4>(over_rows, a, s); break;
+  }
   return hipGetLastError();
 }
 

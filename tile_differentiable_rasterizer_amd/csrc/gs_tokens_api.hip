@@ -30,7 +30,7 @@ hipError_t launch_layer_norm(int64_t rows, int width, int type, float eps, const
                              int64_t xs, const float* w, const float* b, void* y, int64_t ys, float* dw, float* db,
                              void* ws, hipStream_t s);
 int64_t group_tiles(bool over_rows, int64_t rows, int64_t m, int64_t n, int64_t groups);
-size_t group_part_bytes(bool over_rows, int64_t rows, int64_t m, int64_t n, int64_t k, int64_t groups);
+size_t group_part_bytes(bool over_rows, int type, int64_t rows, int64_t m, int64_t n, int64_t k, int64_t groups);
 hipError_t launch_group(bool over_rows, GroupArgs a, int type, void* ws, hipStream_t s);
 hipError_t launch_adamw(int count, const gs_adamw_tensor* tensors, int grad_type, int bits, void* m, void* v,
                         float* bounds, const gs_adamw_params& h, const float* grad_scale, hipStream_t s);
@@ -415,7 +415,7 @@ GroupArgs group_args(const gs_group_mm& p) {
 }  // namespace
 
 size_t gs_group_mm_fwd_workspace_bytes(const gs_group_mm* p) {
-  return group_shape(p, false) == GS_OK ? round16(group_part_bytes(false, p->rows, p->rows, p->n, p->k, p->groups)) : 0;
+  return group_shape(p, false) == GS_OK ? round16(group_part_bytes(false, p->type, p->rows, p->rows, p->n, p->k, p->groups)) : 0;
 }
 
 gs_status gs_group_mm_fwd(const gs_group_mm* p, const void* x, int64_t x_stride, gs_weights w, void* y,
@@ -441,8 +441,8 @@ gs_status gs_group_mm_fwd(const gs_group_mm* p, const void* x, int64_t x_stride,
 size_t gs_group_mm_bwd_workspace_bytes(const gs_group_mm* p) {
   if (group_shape(p, true) != GS_OK) return 0;
   // dx's parts, then in their place dW's, whichever way it lies
-  const size_t dx = group_part_bytes(false, p->rows, p->rows, p->k, p->n, p->groups);
-  const size_t dw = group_part_bytes(true, p->rows, p->k, p->n, p->rows, p->groups), turned = group_part_bytes(true, p->rows, p->n, p->k, p->rows, p->groups);
+  const size_t dx = group_part_bytes(false, p->type, p->rows, p->rows, p->k, p->n, p->groups);
+  const size_t dw = group_part_bytes(true, p->type, p->rows, p->k, p->n, p->rows, p->groups), turned = group_part_bytes(true, p->type, p->rows, p->n, p->k, p->rows, p->groups);
   return round16(dx > dw ? dx > turned ? dx : turned : dw > turned ? dw : turned);
 }
 
