@@ -20,58 +20,80 @@ namespace gs {
 
 hipError_t launch_group_mfma(bool over_rows, int tile, const GroupArgs& a, hipStream_t s);
 
-constexpr int kStagedTile = 128, kStagedK = 32;
+constexpr int kStagedTile = 128, kStagedK = 32, kStagedThreads = 512;
+constexpr int kStagedAhead = 2;  // tiles on their way
 
-// Eight elements of memory on their way to LDS.
+// Eight elements of memory on their way to LDS: all of them, at any alignment, or the first n and zeros behind.
 template <typename T>
 struct Eight;
 template <>
 struct Eight<__bf16> {
   bf16x8 v;
+  __device__ __forceinline__ void load(const __bf16* p) {
+    typedef __bf16 V __attribute__((ext_vector_type(8), aligned(2)));
+    v = *reinterpret_cast<const V*>(p);
+  }
   __device__ __forceinline__ void load(const __bf16* p, int n) {
-    if (n >= 8) {
-      typedef __bf16 V __attribute__((ext_vector_type(8), aligned(2)));
-      v = *reinterpret_cast<const V*>(p);
-    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : (__bf16)0.0f;
-    }
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : (__bf16)0.0f;
   }
   __device__ __forceinline__ Frag<__bf16> parts() const { return {v}; }
 };
 template <>
 struct Eight<float> {
   f32x8 v;
-  __device__ __forceinline__ void load(const float* p, int n) {
-    float x[8];
-    load_units(p, n, x);
+  __device__ __forceinline__ void load(const float* p) {
+    typedef float V __attribute__((ext_vector_type(4), aligned(4)));
+    const V a = *reinterpret_cast<const V*>(p), b = *reinterpret_cast<const V*>(p + 4);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = x[i];
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i];
+      v[4 + i] = b[i];
+    }
+  }
+  __device__ __forceinline__ void load(const float* p, int n) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
   }
   __device__ __forceinline__ Frag<float> parts() const { return frag_split(v); }
 };
 
+// Where eight rows (or columns) are that the tile counts from `at` on (a multiple of 8), of `rows`: the last eight in the place of a few.
+template <bool NARROW>
+__device__ __forceinline__ int eight_at(int at, int rows) {
+  return NARROW ? at : min(at, rows - 8);
+}
+
 // One operand's tile of 128 rows (or columns) by 32 k, in LDS as gs_group_mfma.hip's but for rows of 64 bytes where k is
 // dense (chunk c of row r at c ^ (r / 4 % 4)); float32's three parts one after another.
-template <typename T, bool K_DENSE>
+template <typename T, bool K_DENSE, bool NARROW>
 struct StagedSide {
-  static constexpr int R = kStagedTile, kChunks = (K_DENSE ? kStagedK : R) / 8, kEach = 2, kPart = R * kStagedK * 2;
+  static constexpr int R = kStagedTile, kChunks = (K_DENSE ? kStagedK : R) / 8, kPart = R * kStagedK * 2;
+  static constexpr int kEach = R * kStagedK / 8 / kStagedThreads;
   static constexpr int kParts = sizeof(Frag<T>) / sizeof(bf16x8), kBytes = kParts * kPart;
 
   const T* base;    // of the tile at k0
+  int64_t step;     // elements of 32 k
   int64_t stride;   // of the axis that is not dense
+  int64_t off[kEach];
   int rows;
   int at;
-  Eight<T> x[kEach];
+  Eight<T> x[kStagedAhead][kEach];  // tiles on their way
 
   static __device__ __forceinline__ int mix(int r) { return K_DENSE ? (r >> 2) & 3 : ((r & 3) << 2) | ((r >> 2) & 3); }
-  static __device__ __forceinline__ int row_of(int i) { return (i * 256 + (int)threadIdx.x) / kChunks; }
-  static __device__ __forceinline__ int chunk_of(int i) { return (i * 256 + (int)threadIdx.x) % kChunks; }
+  static __device__ __forceinline__ int row_of(int i) { return (i * kStagedThreads + (int)threadIdx.x) / kChunks; }
+  static __device__ __forceinline__ int chunk_of(int i) { return (i * kStagedThreads + (int)threadIdx.x) % kChunks; }
 
   __device__ __forceinline__ void plan(const T* p, int64_t s, int n, int first) {
     base = p;
     stride = s;
     rows = n;
+    step = K_DENSE ? kStagedK : kStagedK * s;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int r = row_of(i), c = chunk_of(i) * 8;
+      off[i] = K_DENSE ? min(r, rows - 1) * stride + c : r * stride + eight_at<NARROW>(c, rows);
+    }
     const int l = __lane_id(), h = l >> 5, i = l & 15;
     if constexpr (K_DENSE) {
       const int r = l & 31;
@@ -81,17 +103,22 @@ struct StagedSide {
       at = r * (kChunks * 16) + ((c ^ mix(r)) << 4) + 8 * (i & 1);
     }
   }
-  // Tile `tile`, of which k < left exist: the others, and rows that do not exist, are 0.
-  __device__ __forceinline__ void load(int tile, int left) {
-    const T* p = base + (K_DENSE ? (int64_t)tile * kStagedK : (int64_t)tile * kStagedK * stride);
+  // Tile `tile`, all of whose k exist.  Rows (or columns) that do not are read as others: what comes of them is not stored.
+  __device__ __forceinline__ void load(int to, int tile) {
+    const T* p = base + tile * step;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) x[to][i].load(p + off[i]);
+  }
+  // Any tile, of which k < left exist: the others are 0.
+  __device__ __forceinline__ void load_part(int to, int tile, int left) {
+    const T* p = base + tile * step;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      const int r = row_of(i), c = chunk_of(i) * 8;
-      const bool there = K_DENSE ? r < rows : r < left;
-      x[i].load(p + r * stride + c, there ? min(max((K_DENSE ? left : rows) - c, 0), 8) : 0);
+      const int c = chunk_of(i) * 8;
+      x[to][i].load(p + off[i], K_DENSE ? left - c : row_of(i) >= left ? 0 : NARROW ? rows - c : 8);
     }
   }
-  __device__ __forceinline__ void store(char* tile) const {
+  __device__ __forceinline__ void store(int from, char* tile) const {
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int r = row_of(i), c = chunk_of(i);
@@ -99,7 +126,7 @@ struct StagedSide {
         Frag<T> f;
         bf16x8 v[kParts];
       } u;
-      u.f = x[i].parts();
+      u.f = x[from][i].parts();
 #pragma unroll
       for (int k = 0; k < kParts; ++k) *reinterpret_cast<bf16x8*>(tile + k * kPart + r * (kChunks * 16) + ((c ^ mix(r)) << 4)) = u.v[k];
     }
@@ -132,11 +159,39 @@ struct StagedSide {
   }
 };
 
-template <typename T, bool A_DENSE, bool B_DENSE, bool OVER_ROWS>
-__global__ __launch_bounds__(256, 2) void k_group_staged(GroupArgs a) {
-  using SideA = StagedSide<T, A_DENSE>;
-  using SideB = StagedSide<T, B_DENSE>;
-  __shared__ __align__(1024) char lds[SideA::kBytes + SideB::kBytes];
+// The running sums of a block.  float32: the products of the leading parts apart from the five smaller ones, whose sum is
+// 2^-8 of theirs, so that a sum over k is rounded once for 16 k and not six times.  (Over 6000 k, against 64 bits: 1e-6 -> 4e-7 of the
+// result's norm; a product in float32 by the library 6e-7.)
+template <typename T>
+struct Sums;
+template <>
+struct Sums<__bf16> {
+  f32x16 c = (f32x16)0.0f;
+  __device__ __forceinline__ void add(const Frag<__bf16>& a, const Frag<__bf16>& b) { c = mma(a, b, c); }
+  __device__ __forceinline__ float get(int i) const { return c[i]; }
+};
+template <>
+struct Sums<float> {
+  f32x16 c = (f32x16)0.0f, rest = (f32x16)0.0f;
+  __device__ __forceinline__ void add(const Frag<float>& a, const Frag<float>& b) {
+    rest = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[2], b.p[0], rest, 0, 0, 0);
+    rest = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[2], rest, 0, 0, 0);
+    rest = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[1], b.p[1], rest, 0, 0, 0);
+    rest = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[1], b.p[0], rest, 0, 0, 0);
+    rest = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[1], rest, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[0], c, 0, 0, 0);
+  }
+  __device__ __forceinline__ float get(int i) const { return c[i] + rest[i]; }
+};
+
+// NARROW: a matrix with rows of fewer than eight elements.
+template <typename T, bool A_DENSE, bool B_DENSE, bool OVER_ROWS, bool NARROW>
+__global__ __launch_bounds__(kStagedThreads, 2) void k_group_staged(GroupArgs a) {
+  constexpr int TM = 1, TN = 2;  // a wavefront's 32 x 64 of the block
+  using SideA = StagedSide<T, A_DENSE, NARROW>;
+  using SideB = StagedSide<T, B_DENSE, NARROW>;
+  constexpr int kTile = SideA::kBytes + SideB::kBytes;
+  __shared__ __align__(1024) char lds[2 * kTile];
   const int n_tiles = (a.n + kStagedTile - 1) / kStagedTile;
   int m0, n0, m_end, k0, k_end, g, split;
   if constexpr (OVER_ROWS) {
@@ -165,44 +220,63 @@ __global__ __launch_bounds__(256, 2) void k_group_staged(GroupArgs a) {
     k_end = g < 0 ? 0 : a.k;
   }
   group_part(a, split, kStagedK, &k0, &k_end);
-  const int wave = threadIdx.x / kWave, wm = wave % 2, wn = wave / 2;
+  const int wave = threadIdx.x / kWave, wm = wave % 4, wn = wave / 4;
 
-  f32x16 acc[2][2];
-#pragma unroll
-  for (int n = 0; n < 2; ++n)
-#pragma unroll
-    for (int m = 0; m < 2; ++m) acc[n][m] = (f32x16)0.0f;
+  Sums<T> acc[TN][TM];
   if (k0 < k_end) {
     SideA sa;
     SideB sb;
-    sa.plan(static_cast<const T*>(a.a) + m0 * a.a_m + k0 * a.a_k, A_DENSE ? a.a_m : a.a_k, m_end - m0, wm * 64);
-    sb.plan(static_cast<const T*>(a.b) + (OVER_ROWS ? 0 : g * a.b_g) + k0 * a.b_k + n0 * a.b_n, B_DENSE ? a.b_n : a.b_k, a.n - n0, wn * 64);
-    int left = k_end - k0;
-    sa.load(0, left);
-    sb.load(0, left);
-    for (int t = 0; left > 0; ++t) {
-      __syncthreads();  // the tile before has been read
-      sa.store(lds);
-      sb.store(lds + SideA::kBytes);
-      __syncthreads();
-      left -= kStagedK;
-      if (left > 0) {
-        sa.load(t + 1, left);
-        sb.load(t + 1, left);
-      }
+    sa.plan(static_cast<const T*>(a.a) + m0 * a.a_m + k0 * a.a_k, A_DENSE ? a.a_m : a.a_k, m_end - m0, wm * TM * 32);
+    sb.plan(static_cast<const T*>(a.b) + (OVER_ROWS ? 0 : g * a.b_g) + k0 * a.b_k + n0 * a.b_n, B_DENSE ? a.b_n : a.b_k, a.n - n0, wn * TN * 32);
+    auto load = [&](int to, int t) {
+      sa.load(to, t);
+      sb.load(to, t);
+    };
+    auto store = [&](int from, int buffer) {
+      sa.store(from, lds + buffer * kTile);
+      sb.store(from, lds + buffer * kTile + SideA::kBytes);
+    };
+    auto multiply = [&](int buffer) {
+      const char* tile = lds + buffer * kTile;
 #pragma unroll
       for (int s = 0; s < kStagedK / 16; ++s) {
-        Frag<T> fa[2], fb[2];
+        Frag<T> fa[TM], fb[TN];
+#pragma unroll
+        for (int n = 0; n < TN; ++n) fb[n] = sb.read(tile + SideA::kBytes, n, s);
+#pragma unroll
+        for (int m = 0; m < TM; ++m) fa[m] = sa.read(tile, m, s);
+#pragma unroll
+        for (int m = 0; m < TM; ++m)
+#pragma unroll
+          for (int n = 0; n < TN; ++n) acc[n][m].add(fb[n], fa[m]);
+      }
+    };
+    // pairs of whole tiles: while one is multiplied, the next goes to the other half of LDS and the two behind it are on
+    // their way, with no branch between a load and its use; then the rest, one by one
+    const int all = k_end - k0, whole = NARROW ? 0 : all / (2 * kStagedK) * 2;
+    if (whole) {
+      load(0, 0);
+      load(1, 1);
+      store(0, 0);
+      load(0, min(2, whole - 1));
+      __syncthreads();
+      for (int t = 0; t < whole; t += 2) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          fb[i] = sb.read(lds + SideA::kBytes, i, s);
-          fa[i] = sa.read(lds, i, s);
+          store(i ^ 1, i ^ 1);  // tile t + i + 1 (past the last: one again, for nothing)
+          load(i ^ 1, min(t + i + 3, whole - 1));
+          multiply(i);
+          __syncthreads();
         }
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int n = 0; n < 2; ++n) acc[n][m] = mma(fb[n], fa[m], acc[n][m]);
       }
+    }
+    for (int t = whole; t * kStagedK < all; ++t) {
+      sa.load_part(0, t, all - t * kStagedK);
+      sb.load_part(0, t, all - t * kStagedK);
+      store(0, 0);
+      __syncthreads();
+      multiply(0);
+      __syncthreads();
     }
   }
 
@@ -211,26 +285,30 @@ __global__ __launch_bounds__(256, 2) void k_group_staged(GroupArgs a) {
   float* part = a.part + ((int64_t)split * (OVER_ROWS ? (int64_t)a.groups * a.m : a.rows) + (OVER_ROWS ? (int64_t)g * a.m : 0)) * width;
   const int l = __lane_id(), h = l >> 5;
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const int row = m0 + (wm * 2 + m) * 32 + (l & 31);
+  for (int m = 0; m < TM; ++m) {
+    int row = m0 + (wm * TM + m) * 32 + (l & 31);
+    const bool there = A_DENSE || NARROW ? row < m_end : (row & ~7) < m_end;
+    if constexpr (!A_DENSE) row = eight_at<NARROW>(row & ~7, m_end) + (row & 7);
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < TN; ++n)
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         // a lane and the one 32 on hold fours of columns in turn: now eight in a row each
         float x[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[n][m][8 * q + e]), __float_as_uint(acc[n][m][8 * q + 4 + e]), false, false);
+          const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[n][m].get(8 * q + e)), __float_as_uint(acc[n][m].get(8 * q + 4 + e)), false, false);
           x[e] = __uint_as_float(w[0]);
           x[4 + e] = __uint_as_float(w[1]);
         }
-        const int col = n0 + (wn * 2 + n) * 32 + 16 * q + 8 * h;
-        if (row >= m_end || col >= a.n) continue;
+        int col = n0 + (wn * TN + n) * 32 + 16 * q + 8 * h;
+        if (!there || col >= a.n) continue;
+        if constexpr (!B_DENSE) col = eight_at<NARROW>(col, a.n);
+        const int some = min(a.n - col, 8);
         if (a.splits > 1)
-          store_elems<8>(part + (int64_t)row * width + col, x);
+          store_units(part + (int64_t)row * width + col, some, x);
         else
-          store_units(C + row * a.c_m + col, min(a.n - col, 8), x);
+          store_units(C + row * a.c_m + col, some, x);
       }
   }
 }
@@ -269,14 +347,21 @@ bool group_aligned(bool over_rows, const GroupArgs& a) {
          a.n % 8 == 0 && (over_rows ? a.m : a.k) % 8 == 0;
 }
 
-template <typename T>
+template <typename T, bool NARROW>
 void staged_launch(bool over_rows, const GroupArgs& a, unsigned blocks, hipStream_t s) {
   if (over_rows)
-    k_group_staged<T, false, false, true><<<blocks, 256, 0, s>>>(a);
+    k_group_staged<T, false, false, true, NARROW><<<blocks, kStagedThreads, 0, s>>>(a);
   else if (a.b_k == 1)
-    k_group_staged<T, true, true, false><<<blocks, 256, 0, s>>>(a);
+    k_group_staged<T, true, true, false, NARROW><<<blocks, kStagedThreads, 0, s>>>(a);
   else
-    k_group_staged<T, true, false, false><<<blocks, 256, 0, s>>>(a);
+    k_group_staged<T, true, false, false, NARROW><<<blocks, kStagedThreads, 0, s>>>(a);
+}
+template <typename T>
+void staged_launch(bool over_rows, const GroupArgs& a, unsigned blocks, hipStream_t s) {
+  if (a.n < 8 || (over_rows ? a.m : a.k) < 8)
+    staged_launch<T, true>(over_rows, a, blocks, s);
+  else
+    staged_launch<T, false>(over_rows, a, blocks, s);
 }
 
 }  // namespace
