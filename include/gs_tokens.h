@@ -232,8 +232,10 @@ typedef struct gs_group_mm {
  *              parts of a long sum that is split over workgroups)
  * Any sizes, strides and alignment (of whole elements) are taken; matrices that all start rows at 16-byte boundaries
  * go faster.  k of 0: y is 0.
- * Errors: INVALID_ARG, OVERFLOW (2^31 rows or more, k or n past 2^24, more than 65536 groups, or 2^24 tiles of results or
- * more), WORKSPACE, HIP.
+ * float32 enters the products as sums of three bfloat16 (see gs_cross_attn: products with an infinity, or with 3.39e38 and more,
+ * are NaN).
+ * Errors: INVALID_ARG, OVERFLOW (2^31 - 256 rows or more, k or n past 2^24, more than 65536 groups, or 2^23 blocks of 128 x 64 results
+ * or more, with one for each group), WORKSPACE, HIP.
  */
 size_t gs_group_mm_fwd_workspace_bytes(const gs_group_mm* p);
 gs_status gs_group_mm_fwd(const gs_group_mm* p, const void* x, int64_t x_stride, gs_weights w, void* y,

@@ -24,7 +24,7 @@ struct GroupArgs {
 };
 
 // Blocks of results that a workgroup makes: on the matrix units straight from LDS, and staged through registers.
-enum { kGroup256x256, kGroup128x256, kGroup128x128, kGroup32x256, kGroup32x128, kGroupStaged, kGroupTiles };
+enum { kGroup256x256, kGroup128x256, kGroup128x128, kGroup32x256, kGroup32x128, kGroupStaged128, kGroupStaged64, kGroupTiles };
 
 __host__ __device__ constexpr int group_part_width(int n) { return (n + 7) & ~7; }
 

@@ -66,10 +66,11 @@ __device__ __forceinline__ int eight_at(int at, int rows) {
 
 // One operand's tile of 128 rows (or columns) by 32 k, in LDS as gs_group_mfma.hip's but for rows of 64 bytes where k is
 // dense (chunk c of row r at c ^ (r / 4 % 4)); float32's three parts one after another.
-template <typename T, bool K_DENSE, bool NARROW>
+template <typename T, bool K_DENSE, bool NARROW, int R>
 struct StagedSide {
-  static constexpr int R = kStagedTile, kChunks = (K_DENSE ? kStagedK : R) / 8, kPart = R * kStagedK * 2;
-  static constexpr int kEach = R * kStagedK / 8 / kStagedThreads;
+  static constexpr int kChunks = (K_DENSE ? kStagedK : R) / 8, kPart = R * kStagedK * 2;
+  static constexpr int kEach = 1;  // an eight a thread, of the first threads where there are fewer
+  static_assert(R * kStagedK / 8 <= kStagedThreads && (R == 64 || R >= 128));
   static constexpr int kParts = sizeof(Frag<T>) / sizeof(bf16x8), kBytes = kParts * kPart;
 
   const T* base;    // of the tile at k0
@@ -80,9 +81,13 @@ struct StagedSide {
   int at;
   Eight<T> x[kStagedAhead][kEach];  // tiles on their way
 
-  static __device__ __forceinline__ int mix(int r) { return K_DENSE ? (r >> 2) & 3 : ((r & 3) << 2) | ((r >> 2) & 3); }
-  static __device__ __forceinline__ int row_of(int i) { return (i * kStagedThreads + (int)threadIdx.x) / kChunks; }
-  static __device__ __forceinline__ int chunk_of(int i) { return (i * kStagedThreads + (int)threadIdx.x) % kChunks; }
+  static __device__ __forceinline__ int mix(int r) {
+    if (K_DENSE) return (r >> 2) & 3;
+    return R == 64 ? ((r & 2) << 1) | ((r >> 2) & 3) : ((r & 3) << 2) | ((r >> 2) & 3);
+  }
+  static __device__ __forceinline__ int item_of(int i) { return (i * kStagedThreads + (int)threadIdx.x) % (R * kStagedK / 8); }
+  static __device__ __forceinline__ int row_of(int i) { return item_of(i) / kChunks; }
+  static __device__ __forceinline__ int chunk_of(int i) { return item_of(i) % kChunks; }
 
   __device__ __forceinline__ void plan(const T* p, int64_t s, int n, int first) {
     base = p;
@@ -119,6 +124,7 @@ struct StagedSide {
     }
   }
   __device__ __forceinline__ void store(int from, char* tile) const {
+    if (R * kStagedK / 8 < kStagedThreads && threadIdx.x >= R * kStagedK / 8) return;  // (whole wavefronts)
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int r = row_of(i), c = chunk_of(i);
@@ -185,14 +191,14 @@ struct Sums<float> {
 };
 
 // NARROW: a matrix with rows of fewer than eight elements.
-template <typename T, bool A_DENSE, bool B_DENSE, bool OVER_ROWS, bool NARROW>
-__global__ __launch_bounds__(kStagedThreads, 2) void k_group_staged(GroupArgs a) {
-  constexpr int TM = 1, TN = 2;  // a wavefront's 32 x 64 of the block
-  using SideA = StagedSide<T, A_DENSE, NARROW>;
-  using SideB = StagedSide<T, B_DENSE, NARROW>;
+template <typename T, bool A_DENSE, bool B_DENSE, bool OVER_ROWS, bool NARROW, int BN>
+__global__ __launch_bounds__(kStagedThreads, BN == 64 ? 4 : 2) void k_group_staged(GroupArgs a) {
+  constexpr int TM = 1, TN = BN / 64;  // a wavefront's 32 x 64 (or 32) of the block
+  using SideA = StagedSide<T, A_DENSE, NARROW, kStagedTile>;
+  using SideB = StagedSide<T, B_DENSE, NARROW, BN>;
   constexpr int kTile = SideA::kBytes + SideB::kBytes;
   __shared__ __align__(1024) char lds[2 * kTile];
-  const int n_tiles = (a.n + kStagedTile - 1) / kStagedTile;
+  const int n_tiles = (a.n + BN - 1) / BN;
   int m0, n0, m_end, k0, k_end, g, split;
   if constexpr (OVER_ROWS) {
     const int m_tiles = (a.m + kStagedTile - 1) / kStagedTile, each = m_tiles * n_tiles * a.splits;
@@ -201,7 +207,7 @@ __global__ __launch_bounds__(kStagedThreads, 2) void k_group_staged(GroupArgs a)
     split = rest / (m_tiles * n_tiles);
     rest -= split * m_tiles * n_tiles;
     m0 = rest / n_tiles * kStagedTile;
-    n0 = rest % n_tiles * kStagedTile;
+    n0 = rest % n_tiles * BN;
     m_end = a.m;
     k0 = group_bound(a, g + 1);
     k_end = max(group_bound(a, g + 2), k0);
@@ -215,7 +221,7 @@ __global__ __launch_bounds__(kStagedThreads, 2) void k_group_staged(GroupArgs a)
     m0 = s.first;
     m_end = s.last;
     split = nn / n_tiles;
-    n0 = (nn - split * n_tiles) * kStagedTile;
+    n0 = (nn - split * n_tiles) * BN;
     k0 = 0;
     k_end = g < 0 ? 0 : a.k;
   }
@@ -347,29 +353,33 @@ bool group_aligned(bool over_rows, const GroupArgs& a) {
          a.n % 8 == 0 && (over_rows ? a.m : a.k) % 8 == 0;
 }
 
-template <typename T, bool NARROW>
-void staged_launch(bool over_rows, const GroupArgs& a, unsigned blocks, hipStream_t s) {
+template <typename T, bool NARROW, int BN>
+void staged_launch(bool over_rows, const GroupArgs& a, hipStream_t s) {
+  const int64_t m_tiles = over_rows ? a.groups * tiles(a.m, kStagedTile) : tiles(a.rows, kStagedTile) + std::min(a.groups + 2, a.rows);
+  const unsigned blocks = (unsigned)(m_tiles * tiles(a.n, BN) * a.splits);
   if (over_rows)
-    k_group_staged<T, false, false, true, NARROW><<<blocks, kStagedThreads, 0, s>>>(a);
+    k_group_staged<T, false, false, true, NARROW, BN><<<blocks, kStagedThreads, 0, s>>>(a);
   else if (a.b_k == 1)
-    k_group_staged<T, true, true, false, NARROW><<<blocks, kStagedThreads, 0, s>>>(a);
+    k_group_staged<T, true, true, false, NARROW, BN><<<blocks, kStagedThreads, 0, s>>>(a);
   else
-    k_group_staged<T, true, false, false, NARROW><<<blocks, kStagedThreads, 0, s>>>(a);
+    k_group_staged<T, true, false, false, NARROW, BN><<<blocks, kStagedThreads, 0, s>>>(a);
 }
 template <typename T>
-void staged_launch(bool over_rows, const GroupArgs& a, unsigned blocks, hipStream_t s) {
+void staged_launch(bool over_rows, int bn, const GroupArgs& a, hipStream_t s) {
   if (a.n < 8 || (over_rows ? a.m : a.k) < 8)
-    staged_launch<T, true>(over_rows, a, blocks, s);
+    staged_launch<T, true, 128>(over_rows, a, s);
+  else if (bn == 64)
+    staged_launch<T, false, 64>(over_rows, a, s);
   else
-    staged_launch<T, false>(over_rows, a, blocks, s);
+    staged_launch<T, false, 128>(over_rows, a, s);
 }
 
 }  // namespace
 
-// Workgroups of a launch at most, before the sums are split (the caller checks that a grid takes them).
+// Workgroups of a launch at most, before the sums are split (which they are up to 2048 only), each of up to 512 threads: the
+// caller checks that a grid takes them.
 int64_t group_tiles(bool over_rows, int64_t rows, int64_t m, int64_t n, int64_t groups) {
-  return over_rows ? groups * tiles(m, kStagedTile) * tiles(n, kStagedTile)
-                   : (tiles(rows, kStagedTile) + std::min(groups + 2, rows)) * tiles(n, kStagedTile);
+  return over_rows ? groups * tiles(m, kStagedTile) * tiles(n, 64) : (tiles(rows, kStagedTile) + std::min(groups + 2, rows)) * tiles(n, 64);
 }
 
 namespace {
@@ -379,34 +389,44 @@ struct GroupPlan {
 };
 
 // The block of results and the parts of the sums with the least time by a model: rounds of workgroups on the CUs' places, each a
-// start and an end and a time for 64 k, and the join of the parts.  Rows of a group are not known here: the last
-// block of rows of each is taken as half full.
+// start and an end and a time for 64 k, and the join of the parts.  Workgroups that go from block to block end in whole rounds; the
+// staged ones fill in for each other, and have their CU to themselves where they are few.  Rows of a group are not known here: the
+// last block of rows of each is taken as half full.
 //
 // Measured, us (by rows; 256 x 256, 128 x 256, 128 x 128, 32 x 256, 32 x 128): 7814 rows of 8 groups, 2048 x 4096: 149 139 154 298
 // 295; 782 rows 46 37 40 48 50; 64 rows of 16 groups 52 49 47 43 47; 3907 rows of one, 2048 x 2048: 45 35 36 66 66; 20000 rows of 8, 512 x 256:
 // 18 13 15 19 17; 64 rows of 4, 4096 x 512, in the best number of parts: 19 17 14 14 13, in one 32 x 128: 33.  Over rows (the first
 // three): 7814 rows of 8, 2048 x 4096: 143 169 163; 20000 rows of 8, 512 x 256: 32 26 22 in 8, 8 and 4 parts, 66 in one; 40000
 // rows of one, 1024 x 512: 63 57 65 in 32, 16 and 16 parts.
+// Staged (128 x 128, 128 x 64): float32, 4000 rows of 2, 4096 x 1024: 218 248; 43816 rows of one, 40 x 528: 63 53, and back 62 36; 158 rows
+// of 37 back, 3496 x 165: 95 56; bfloat16, 1955 rows of 5, 363 x 250: 11 9.5; 20000 rows of 8, 101 x 515: 27 32.
+struct GroupShape {
+  int bm, bn, places;
+  double fix, by_rows, over;  // us: a block, and 64 k
+  int few;                    // workgroups up to which they take `alone` of that
+  double alone;
+};
+
 GroupPlan group_plan(bool over_rows, bool staged, bool f32, int64_t rows, int64_t m, int64_t n, int64_t k, int64_t groups) {
-  struct Shape {
-    int bm, bn, places;
-    double fix, by_rows, over;  // us
-  };
-  static const Shape kShapes[kGroupTiles] = {{256, 256, 256, 5.0, 1.5, 1.6},  {128, 256, 256, 3.0, 1.0, 1.15}, {128, 128, 512, 3.0, 1.15, 1.2},
-                                             {32, 256, 256, 2.0, 0.5, 0.0},   {32, 128, 512, 2.0, 0.5, 0.0},   {128, 128, 512, 3.0, 2.0, 2.0}};
+  static const GroupShape kShapes[kGroupTiles] = {
+      {256, 256, 256, 5.0, 1.5, 1.6, 0, 1.0}, {128, 256, 256, 3.0, 1.0, 1.15, 0, 1.0}, {128, 128, 512, 3.0, 1.15, 1.2, 0, 1.0},
+      {32, 256, 256, 2.0, 0.5, 0.0, 0, 1.0},  {32, 128, 512, 2.0, 0.5, 0.0, 0, 1.0},   {128, 128, 512, 4.0, 1.3, 1.3, 256, 0.7},
+      {128, 64, 1024, 4.0, 1.6, 1.6, 256, 0.45}};
+  static const GroupShape kFloat[2] = {{128, 128, 256, 6.0, 3.2, 3.2, 0, 1.0}, {128, 64, 512, 4.0, 3.8, 3.8, 256, 0.6}};
   const double used = (double)std::min(groups, over_rows ? groups : rows);
   const double length = over_rows ? (double)rows / (double)std::max<int64_t>(groups, 1) : (double)k;
-  GroupPlan best{staged ? kGroupStaged : kGroup128x128, 1};
+  GroupPlan best{staged ? kGroupStaged128 : kGroup128x128, 1};
   double least = 1e300;
   for (int t = 0; t < kGroupTiles; ++t) {
-    const Shape& x = kShapes[t];
-    if ((t == kGroupStaged) != staged || (over_rows && x.bm < 128)) continue;
+    const GroupShape& x = f32 && t >= kGroupStaged128 ? kFloat[t - kGroupStaged128] : kShapes[t];
+    if ((t >= kGroupStaged128) != staged || (over_rows && x.bm < 128)) continue;
     const double m_tiles = over_rows ? (double)(groups * tiles(m, x.bm)) : std::max(used, (double)rows / x.bm + 0.5 * used);
     const double blocks = std::max(1.0, m_tiles * (double)tiles(n, x.bn));
     for (int splits = 1; splits <= 32; splits *= 2) {
       if (splits > 1 && (length < 128.0 * splits || blocks * splits > 2.0 * x.places)) break;
-      const double rounds = std::max(1.0, std::ceil(blocks * splits / x.places - 0.1));
-      const double each = (over_rows ? x.over : x.by_rows) * (staged && f32 ? 2.0 : 1.0);
+      const double full = blocks * splits / x.places;
+      const double rounds = full <= 1.0 ? 1.0 : staged ? full + 0.3 : std::max(1.0, std::ceil(full - 0.1));
+      const double each = (over_rows ? x.over : x.by_rows) * (blocks * splits <= x.few ? x.alone : 1.0);
       double time = rounds * (x.fix + std::ceil(length / splits / 64.0) * each);
       if (splits > 1) time += 5.0 + (double)splits * (double)(over_rows ? groups * m : rows) * (double)n * 8.0 / 4e6;
       if (time < least) {
@@ -434,13 +454,13 @@ hipError_t launch_group(bool over_rows, GroupArgs a, int type, void* ws, hipStre
   a.splits = plan.splits;
   a.part = static_cast<float*>(ws);
   hipError_t e;
-  if (plan.tile != kGroupStaged) {
+  if (plan.tile < kGroupStaged128) {
     e = launch_group_mfma(over_rows, plan.tile, a, s);
   } else {
     if (type == GS_BF16)
-      staged_launch<__bf16>(over_rows, a, (unsigned)(blocks * a.splits), s);
+      staged_launch<__bf16>(over_rows, plan.tile == kGroupStaged64 ? 64 : 128, a, s);
     else
-      staged_launch<float>(over_rows, a, (unsigned)(blocks * a.splits), s);
+      staged_launch<float>(over_rows, plan.tile == kGroupStaged64 ? 64 : 128, a, s);
     e = hipGetLastError();
   }
   if (e != hipSuccess || a.splits == 1) return e;

@@ -380,10 +380,11 @@ gs_status group_shape(const gs_group_mm* p, bool bwd) {
   if (!p || p->rows < 0 || p->k < 0 || p->n < 0 || p->groups < 0 || (p->type != GS_BF16 && p->type != GS_F32)) return GS_ERR_INVALID_ARG;
   if (!p->offsets || !on(p->offsets, 4)) return GS_ERR_INVALID_ARG;
   if (p->rows >= kMost - 256 || p->k > kGroups || p->n > kGroups || p->groups > 65536) return GS_ERR_OVERFLOW;
-  // each factor is below 2^31, the counts below 2^62
-  if (!bwd && group_tiles(false, p->rows, p->rows, p->n, p->groups) >= kGroups) return GS_ERR_OVERFLOW;
-  if (bwd && (group_tiles(false, p->rows, p->rows, p->k, p->groups) >= kGroups ||
-              group_tiles(true, p->rows, p->k, p->n, p->groups) >= kGroups))
+  // each factor is below 2^31, the counts below 2^62; a workgroup has 512 threads
+  constexpr int64_t kMostTiles = kGroups / 2;
+  if (!bwd && group_tiles(false, p->rows, p->rows, p->n, p->groups) >= kMostTiles) return GS_ERR_OVERFLOW;
+  if (bwd && (group_tiles(false, p->rows, p->rows, p->k, p->groups) >= kMostTiles ||
+              group_tiles(true, p->rows, p->k, p->n, p->groups) >= kMostTiles || group_tiles(true, p->rows, p->n, p->k, p->groups) >= kMostTiles))
     return GS_ERR_OVERFLOW;
   return GS_OK;
 }
