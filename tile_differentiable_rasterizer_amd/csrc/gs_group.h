@@ -43,6 +43,20 @@ __device__ __forceinline__ int group_bound(const GroupArgs& a, int e) {
   return min(max(a.offsets[e - 1], 0), a.rows);
 }
 
+// The group with the `rank`-th most rows, so that workgroups of the longest sums start first (up to 64 groups; else by number).
+// Every lane of the wavefront calls it.
+__device__ __forceinline__ int group_by_length(const GroupArgs& a, int rank) {
+  if (a.groups > kWave) return rank;
+  const int lane = (int)__lane_id();
+  const int rows = lane < a.groups ? max(group_bound(a, lane + 2) - group_bound(a, lane + 1), 0) : -1;
+  int before = 0;  // groups that come before the lane's
+  for (int i = 0; i < a.groups; ++i) {
+    const int other = __builtin_amdgcn_readlane(rows, i);
+    before += other > rows || (other == rows && i < lane);
+  }
+  return __builtin_ctzll(__ballot(lane < a.groups && before == rank));
+}
+
 struct GroupSpan {
   int group;        // -1: none
   int first, last;  // rows; empty: no such tile

@@ -202,8 +202,9 @@ __global__ __launch_bounds__(kStagedThreads, BN == 64 ? 4 : 2) void k_group_stag
   int m0, n0, m_end, k0, k_end, g, split;
   if constexpr (OVER_ROWS) {
     const int m_tiles = (a.m + kStagedTile - 1) / kStagedTile, each = m_tiles * n_tiles * a.splits;
-    g = blockIdx.x / each;
-    int rest = blockIdx.x - g * each;
+    const int rank = blockIdx.x / each;
+    g = group_by_length(a, rank);
+    int rest = blockIdx.x - rank * each;
     split = rest / (m_tiles * n_tiles);
     rest -= split * m_tiles * n_tiles;
     m0 = rest / n_tiles * kStagedTile;
@@ -425,9 +426,10 @@ GroupPlan group_plan(bool over_rows, bool staged, bool f32, int64_t rows, int64_
     for (int splits = 1; splits <= 32; splits *= 2) {
       if (splits > 1 && (length < 128.0 * splits || blocks * splits > 2.0 * x.places)) break;
       const double full = blocks * splits / x.places;
-      const double rounds = full <= 1.0 ? 1.0 : staged ? full + 0.3 : std::max(1.0, std::ceil(full - 0.1));
+      const double rounds = full <= 1.0 ? 1.0 : staged ? full + 0.3 : 0.5 * (std::ceil(0.94 * full) + std::ceil(1.06 * full));  // (blocks are known to 6%)
       const double each = (over_rows ? x.over : x.by_rows) * (blocks * splits <= x.few ? x.alone : 1.0);
-      double time = rounds * (x.fix + std::ceil(length / splits / 64.0) * each);
+      // over rows, in one round the longest group ends last
+      double time = rounds * (x.fix + std::ceil(length * (over_rows && groups > 1 && full <= 1.0 ? 1.7 : 1.0) / splits / 64.0) * each);
       if (splits > 1) time += 5.0 + (double)splits * (double)(over_rows ? groups * m : rows) * (double)n * 8.0 / 4e6;
       if (time < least) {
         least = time;

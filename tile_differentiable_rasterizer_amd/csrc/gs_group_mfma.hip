@@ -130,9 +130,10 @@ __global__ __launch_bounds__(256, group_places(BM, BN)) void k_group_mfma(GroupA
   if constexpr (OVER_ROWS) {
     m_tiles = (a.m + BM - 1) / BM;
     const uint32_t each = m_tiles * columns;
-    g_over = blockIdx.x / each;
-    const uint32_t in = blockIdx.x - g_over * each, q = each / 8, more = each % 8;
-    const uint32_t slot = (blockIdx.x - g_over * each) % 8;
+    const uint32_t rank = blockIdx.x / each;
+    g_over = group_by_length(a, rank);
+    const uint32_t in = blockIdx.x - rank * each, q = each / 8, more = each % 8;
+    const uint32_t slot = in % 8;
     id = slot * q + min(slot, more) + in / 8;
     end = id + 1;
   } else {
