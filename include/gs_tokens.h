@@ -285,7 +285,7 @@ typedef struct gs_adamw_params {
  *              i's at 256 * sum over j < i of ceil(n_j / 256); bounds [blocks][2] (8 bits; else not looked at), m and v 16-byte,
  *              bounds 8-byte aligned.  All zeros is the start, and what stands behind a tensor's last unit stays 0.
  * lr and step are values of the call: a captured graph repeats them.
- * Errors: INVALID_ARG (also count < 0, n < 0, hyper-parameters that are not finite or out of range), OVERFLOW (2^35 units or
+ * Errors: INVALID_ARG (also count < 0, n < 0, hyper-parameters that are not finite or out of range), OVERFLOW (2^34 units or
  * more with every tensor's rounded up to 256), HIP.
  */
 gs_status gs_adamw(int32_t count, const gs_adamw_tensor* tensors, int32_t grad_type, int32_t bits, void* m, void* v,

@@ -9,7 +9,7 @@
 // to 1/16129 and 1/65025 of the block's largest.  v > 0 keeps a code of 1 at least: a second moment
 // of 0 beside a first moment would make a step of m / eps.
 //
-// A half wavefront takes a block of 256 units, eight a lane.  Moments are updated, and codes decided, in
+// A wavefront takes a block of 256 units, four a lane.  Moments are updated, and codes decided, in
 // float64 (the device's float64 rate is its float32 rate): a code is found with float32 roots and set right
 // against its two borders, which are exact.  The tensors' table travels in the kernel's arguments, 64
 // tensors a launch, so that nothing is copied to the device and a captured graph holds its own.
@@ -17,6 +17,7 @@
 
 #include "gs_device.h"
 #include "gs_elem.h"
+#include "gs_wave.h"
 
 namespace gs {
 
@@ -36,12 +37,6 @@ struct AdamwTable {
   double rate, eps;                // -lr and epsilon with the bias corrections: m / (1 - b1^t) / (sqrt(v / (1 - b2^t)) + eps)
   uint32_t blocks;
 };
-
-__device__ __forceinline__ float half_top(float v) {
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-  return v;
-}
 
 // What codes stand for, before the block's bound / 127^2 or / 255^4.
 __device__ __forceinline__ double adamw_m_of(int c) { return (double)(c * abs(c)); }
@@ -75,45 +70,42 @@ __device__ __forceinline__ double adamw_quotient(double x, double v, double eps)
 
 template <typename TG, int BITS>
 __global__ __launch_bounds__(256) void k_adamw(AdamwTable a) {
-  const uint32_t blk = blockIdx.x * 8 + threadIdx.x / 32;
+  constexpr int R = kAdamwBlock / kWave;  // units a lane
+  const uint32_t blk = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + threadIdx.x / kWave);
+  if (blk >= a.blocks) return;  // whole wavefronts, which do not exchange with each other
   // the tensor: a lane looks at each one's first block
-  const uint32_t first = a.first[__lane_id()];
-  const uint32_t lead = blockIdx.x * 8 + (threadIdx.x / 64) * 2;  // the wavefront's two blocks
-  const int t0 = __popcll(__ballot(first <= lead)) - 1, t1 = __popcll(__ballot(first <= lead + 1)) - 1;
-  if (blk >= a.blocks) return;  // whole half wavefronts, which do not exchange with each other
-  const int t = (threadIdx.x & 32) ? t1 : t0;
-  const int64_t u0 = (int64_t)(blk - a.first[t]) * kAdamwBlock + (threadIdx.x & 31) * 8;
+  const int t = __popcll(__ballot(a.first[__lane_id()] <= blk)) - 1;
+  const int64_t u0 = (int64_t)(blk - a.first[t]) * kAdamwBlock + __lane_id() * R;
   const int64_t left = a.n[t] - u0;
-  const int n = left >= 8 ? 8 : left > 0 ? (int)left : 0;
+  const int n = left >= R ? R : left > 0 ? (int)left : 0;
   const double keep = a.keep[t], scale = a.grad_scale ? (double)*a.grad_scale : 1.0;
-  float p[8], gf[8];
+  float p[R], gf[R];
   load_units(a.param[t] + u0, n, p);
   load_units(static_cast<const TG*>(a.grad[t]) + u0, n, gf);
-  const int64_t at = (int64_t)blk * kAdamwBlock + (threadIdx.x & 31) * 8;
-  double m[8], v[8];
+  const int64_t at = (int64_t)blk * kAdamwBlock + __lane_id() * R;
+  double m[R], v[R];
   if constexpr (BITS == 32) {
-    float mf[8], vf[8];
-    load_elems<8>(static_cast<const float*>(a.m) + at, mf);
-    load_elems<8>(static_cast<const float*>(a.v) + at, vf);
+    float mf[R], vf[R];
+    load_elems<R>(static_cast<const float*>(a.m) + at, mf);
+    load_elems<R>(static_cast<const float*>(a.v) + at, vf);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < R; ++i) {
       m[i] = mf[i];
       v[i] = vf[i];
     }
   } else {
-    const uint2 cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.m) + at);
-    const uint2 cv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.v) + at);
+    const uint32_t cm = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + at);
+    const uint32_t cv = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + at);
     const float2 top = a.bounds[blk];
     const double sm = (double)top.x * (1.0 / kAdamwM), sv = (double)top.y * (1.0 / kAdamwV);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t wm = i < 4 ? cm.x : cm.y, wv = i < 4 ? cv.x : cv.y;
-      m[i] = sm * adamw_m_of((int)(int8_t)(wm >> (8 * (i & 3))));
-      v[i] = sv * adamw_v_of((wv >> (8 * (i & 3))) & 255u);
+    for (int i = 0; i < R; ++i) {
+      m[i] = sm * adamw_m_of((int)(int8_t)(cm >> (8 * i)));
+      v[i] = sv * adamw_v_of((cv >> (8 * i)) & 255u);
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < R; ++i) {
     const double g = (double)gf[i] * scale;
     m[i] = fma(a.b1, m[i], a.c1 * g);
     v[i] = fma(a.b2, v[i], a.c2 * (g * g));
@@ -122,19 +114,19 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwTable a) {
   store_units(a.param[t] + u0, n, p);
   if (a.copy[t]) store_units(a.copy[t] + u0, n, p);
   if constexpr (BITS == 32) {
-    float mf[8], vf[8];
+    float mf[R], vf[R];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < R; ++i) {
       mf[i] = i < n ? (float)m[i] : 0.0f;
       vf[i] = i < n ? (float)v[i] : 0.0f;
     }
-    store_elems<8>(static_cast<float*>(a.m) + at, mf);
-    store_elems<8>(static_cast<float*>(a.v) + at, vf);
+    store_elems<R>(static_cast<float*>(a.m) + at, mf);
+    store_elems<R>(static_cast<float*>(a.v) + at, vf);
   } else {
     float mt = 0.0f, vt = 0.0f;
     bool bm = false, bv = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < R; ++i) {
       if (i >= n) m[i] = v[i] = 0.0;
       const float x = fabsf((float)m[i]), y = (float)v[i];
       bm |= !(x < INFINITY);
@@ -142,24 +134,23 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwTable a) {
       mt = fmaxf(mt, x);
       vt = fmaxf(vt, y);
     }
-    const uint64_t half = (threadIdx.x & 32) ? 0xFFFFFFFF00000000ull : 0xFFFFFFFFull;
-    mt = (__ballot(bm) & half) ? __int_as_float(0x7fc00000) : half_top(mt);
-    vt = (__ballot(bv) & half) ? __int_as_float(0x7fc00000) : half_top(vt);
+    mt = __any(bm) ? __int_as_float(0x7fc00000) : __int_as_float(wave_minmax<true>(__float_as_int(mt)));  // (not negative: ordered as integers)
+    vt = __any(bv) ? __int_as_float(0x7fc00000) : __int_as_float(wave_minmax<true>(__float_as_int(vt)));
     const double im = mt > 0.0f ? kAdamwM / (double)mt : 0.0, iv = vt > 0.0f ? kAdamwV / (double)vt : 0.0;
-    uint32_t cm[2] = {0, 0}, cv[2] = {0, 0};
+    uint32_t cm = 0, cv = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < R; ++i) {
       // a bound of NaN or 0 makes codes of 0
       int c = im > 0.0 ? adamw_code_m(fabs(m[i]) * im) : 0;
       c = m[i] < 0.0 ? -c : c;
       int e = iv > 0.0 ? adamw_code_v(v[i] * iv) : 0;
       if (iv > 0.0 && v[i] > 0.0) e = max(e, 1);
-      cm[i >> 2] |= ((uint32_t)c & 255u) << (8 * (i & 3));
-      cv[i >> 2] |= (uint32_t)e << (8 * (i & 3));
+      cm |= ((uint32_t)c & 255u) << (8 * i);
+      cv |= (uint32_t)e << (8 * i);
     }
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + at) = make_uint2(cm[0], cm[1]);
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + at) = make_uint2(cv[0], cv[1]);
-    if ((threadIdx.x & 31) == 0) a.bounds[blk] = make_float2(mt, vt);
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + at) = cm;
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + at) = cv;
+    if (__lane_id() == 0) a.bounds[blk] = make_float2(mt, vt);
   }
 }
 
@@ -219,7 +210,7 @@ hipError_t launch_adamw(int count, const gs_adamw_tensor* tensors, int grad_type
     a.m = mp + done * each;
     a.v = vp + done * each;
     a.bounds = reinterpret_cast<float2*>(bounds) + (bits == 8 ? done : 0);
-    const unsigned groups = (blocks + 7) / 8;
+    const unsigned groups = (blocks + 3) / 4;
     if (bits == 8)
       grad_type == GS_BF16 ? k_adamw<__bf16, 8><<<groups, 256, 0, s>>>(a) : k_adamw<float, 8><<<groups, 256, 0, s>>>(a);
     else

@@ -50,31 +50,31 @@ __device__ __forceinline__ void store_elems(float* p, const float (&x)[N]) {
   }
 }
 
-// The eight units at p, of which n exist (0: none); vector loads and stores at any alignment of whole
+// The N units at p, of which n exist (0: none); vector loads and stores at any alignment of whole
 // elements (the memory takes them).
-template <typename T>
-__device__ __forceinline__ void load_units(const T* p, int n, float (&x)[8]) {
-  if (n >= 8) {
-    typedef T V __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
-    constexpr int kPer = 16 / sizeof(T);
+template <int N, typename T>
+__device__ __forceinline__ void load_units(const T* p, int n, float (&x)[N]) {
+  if (n >= N) {
+    constexpr int kPer = N * sizeof(T) <= 16 ? N : 16 / sizeof(T);
+    typedef T V __attribute__((ext_vector_type(kPer), aligned(sizeof(T))));
 #pragma unroll
-    for (int i = 0; i < 8; i += kPer) {
+    for (int i = 0; i < N; i += kPer) {
       const V v = *reinterpret_cast<const V*>(p + i);
 #pragma unroll
       for (int j = 0; j < kPer; ++j) x[i + j] = (float)v[j];
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = i < n ? (float)p[i] : 0.0f;
+    for (int i = 0; i < N; ++i) x[i] = i < n ? (float)p[i] : 0.0f;
   }
 }
-template <typename T>
-__device__ __forceinline__ void store_units(T* p, int n, const float (&x)[8]) {
-  if (n >= 8) {
-    typedef T V __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
-    constexpr int kPer = 16 / sizeof(T);
+template <int N, typename T>
+__device__ __forceinline__ void store_units(T* p, int n, const float (&x)[N]) {
+  if (n >= N) {
+    constexpr int kPer = N * sizeof(T) <= 16 ? N : 16 / sizeof(T);
+    typedef T V __attribute__((ext_vector_type(kPer), aligned(sizeof(T))));
 #pragma unroll
-    for (int i = 0; i < 8; i += kPer) {
+    for (int i = 0; i < N; i += kPer) {
       V v;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) v[j] = (T)x[i + j];
@@ -82,7 +82,7 @@ __device__ __forceinline__ void store_units(T* p, int n, const float (&x)[8]) {
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < N; ++i)
       if (i < n) p[i] = (T)x[i];
   }
 }

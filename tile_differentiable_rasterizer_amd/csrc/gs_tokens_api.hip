@@ -497,9 +497,9 @@ gs_status gs_adamw(int32_t count, const gs_adamw_tensor* tensors, int32_t grad_t
     if (x.n < 0 || !isfinite(x.decay)) return GS_ERR_INVALID_ARG;
     if (!x.n) continue;
     if (!x.param || !x.grad || !on(x.param, 4) || !on(x.grad, size_of(grad_type)) || !on(x.copy, 2)) return GS_ERR_INVALID_ARG;
-    if (x.n >= (int64_t)1 << 35) return GS_ERR_OVERFLOW;
+    if (x.n >= (int64_t)1 << 34) return GS_ERR_OVERFLOW;
     blocks += (x.n + 255) / 256;
-    if (blocks >= (int64_t)1 << 27) return GS_ERR_OVERFLOW;
+    if (blocks >= (int64_t)1 << 26) return GS_ERR_OVERFLOW;
   }
   if (!blocks) return GS_OK;
   if (!m || !v || !on(m, 16) || !on(v, 16) || (bits == 8 && (!bounds || !on(bounds, 8)))) return GS_ERR_INVALID_ARG;
