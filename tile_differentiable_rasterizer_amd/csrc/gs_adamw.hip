@@ -35,7 +35,7 @@ struct AdamwTable {
   const float* grad_scale;
   double b1, b2, c1, c2;
   double rate, eps;                // -lr and epsilon with the bias corrections: m / (1 - b1^t) / (sqrt(v / (1 - b2^t)) + eps)
-  uint32_t blocks;
+  uint32_t blocks, each;  // of the launch, of a wavefront
 };
 
 // What codes stand for, before the block's bound / 127^2 or / 255^4.
@@ -68,89 +68,119 @@ __device__ __forceinline__ double adamw_quotient(double x, double v, double eps)
   return x * __builtin_amdgcn_rcp(root + eps);
 }
 
+// 1 / x to float64's accuracy, of a float32.
+__device__ __forceinline__ double adamw_inverse(float x) {
+  const double d = x;
+  double r = __builtin_amdgcn_rcp(d);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) r = fma(r, fma(-d, r, 1.0), r);
+  return r;
+}
+
+constexpr int kAdamwUnits = kAdamwBlock / kWave;  // units a lane
+
+// A block's units of a lane, as they lie in memory.
+template <int BITS>
+struct AdamwLane {
+  float p[kAdamwUnits], g[kAdamwUnits];
+  float m[BITS == 32 ? kAdamwUnits : 1], v[BITS == 32 ? kAdamwUnits : 1];
+  uint32_t cm, cv;
+  float2 top;
+};
+
 template <typename TG, int BITS>
 __global__ __launch_bounds__(256) void k_adamw(AdamwTable a) {
-  constexpr int R = kAdamwBlock / kWave;  // units a lane
-  const uint32_t blk = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + threadIdx.x / kWave);
-  if (blk >= a.blocks) return;  // whole wavefronts, which do not exchange with each other
-  // the tensor: a lane looks at each one's first block
-  const int t = __popcll(__ballot(a.first[__lane_id()] <= blk)) - 1;
-  const int64_t u0 = (int64_t)(blk - a.first[t]) * kAdamwBlock + __lane_id() * R;
-  const int64_t left = a.n[t] - u0;
-  const int n = left >= R ? R : left > 0 ? (int)left : 0;
-  const double keep = a.keep[t], scale = a.grad_scale ? (double)*a.grad_scale : 1.0;
-  float p[R], gf[R];
-  load_units(a.param[t] + u0, n, p);
-  load_units(static_cast<const TG*>(a.grad[t]) + u0, n, gf);
-  const int64_t at = (int64_t)blk * kAdamwBlock + __lane_id() * R;
-  double m[R], v[R];
-  if constexpr (BITS == 32) {
-    float mf[R], vf[R];
-    load_elems<R>(static_cast<const float*>(a.m) + at, mf);
-    load_elems<R>(static_cast<const float*>(a.v) + at, vf);
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      m[i] = mf[i];
-      v[i] = vf[i];
+  constexpr int R = kAdamwUnits;
+  const uint32_t from = __builtin_amdgcn_readfirstlane((blockIdx.x * 4 + threadIdx.x / kWave) * a.each), to = min(from + a.each, a.blocks);
+  if (from >= to) return;  // whole wavefronts, which do not exchange with each other
+  const uint32_t first = a.first[__lane_id()];
+  const double scale = a.grad_scale ? (double)*a.grad_scale : 1.0;
+  // the tensor of a block: a lane looks at each one's first
+  auto tensor = [&](uint32_t blk) { return __popcll(__ballot(first <= blk)) - 1; };
+  auto unit = [&](uint32_t blk, int t) { return (int64_t)(blk - a.first[t]) * kAdamwBlock + __lane_id() * R; };
+  auto units = [&](int64_t u0, int t) {
+    const int64_t left = a.n[t] - u0;
+    return left >= R ? R : left > 0 ? (int)left : 0;
+  };
+  auto load = [&](uint32_t blk, AdamwLane<BITS>& x) {
+    const int t = tensor(blk);
+    const int64_t u0 = unit(blk, t), at = (int64_t)blk * kAdamwBlock + __lane_id() * R;
+    const int n = units(u0, t);
+    load_units(a.param[t] + u0, n, x.p);
+    load_units(static_cast<const TG*>(a.grad[t]) + u0, n, x.g);
+    if constexpr (BITS == 32) {
+      load_elems<R>(static_cast<const float*>(a.m) + at, x.m);
+      load_elems<R>(static_cast<const float*>(a.v) + at, x.v);
+    } else {
+      x.cm = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + at);
+      x.cv = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + at);
+      x.top = a.bounds[blk];
     }
-  } else {
-    const uint32_t cm = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + at);
-    const uint32_t cv = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + at);
-    const float2 top = a.bounds[blk];
-    const double sm = (double)top.x * (1.0 / kAdamwM), sv = (double)top.y * (1.0 / kAdamwV);
+  };
+  auto step = [&](uint32_t blk, AdamwLane<BITS>& x) {
+    const int t = tensor(blk);
+    const int64_t u0 = unit(blk, t), at = (int64_t)blk * kAdamwBlock + __lane_id() * R;
+    const int n = units(u0, t);
+    const double keep = a.keep[t];
+    double m[R], v[R];
+    const double sm = BITS == 32 ? 0.0 : (double)x.top.x * (1.0 / kAdamwM), sv = BITS == 32 ? 0.0 : (double)x.top.y * (1.0 / kAdamwV);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      m[i] = sm * adamw_m_of((int)(int8_t)(cm >> (8 * i)));
-      v[i] = sv * adamw_v_of((cv >> (8 * i)) & 255u);
+      m[i] = BITS == 32 ? (double)x.m[BITS == 32 ? i : 0] : sm * adamw_m_of((int)(int8_t)(x.cm >> (8 * i)));
+      v[i] = BITS == 32 ? (double)x.v[BITS == 32 ? i : 0] : sv * adamw_v_of((x.cv >> (8 * i)) & 255u);
+      const double g = (double)x.g[i] * scale;
+      m[i] = fma(a.b1, m[i], a.c1 * g);
+      v[i] = fma(a.b2, v[i], a.c2 * (g * g));
+      x.p[i] = (float)fma((double)x.p[i], keep, adamw_quotient(a.rate * m[i], v[i], a.eps));
     }
-  }
+    store_units(a.param[t] + u0, n, x.p);
+    if (a.copy[t]) store_units(a.copy[t] + u0, n, x.p);
+    if constexpr (BITS == 32) {
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const double g = (double)gf[i] * scale;
-    m[i] = fma(a.b1, m[i], a.c1 * g);
-    v[i] = fma(a.b2, v[i], a.c2 * (g * g));
-    p[i] = (float)fma((double)p[i], keep, adamw_quotient(a.rate * m[i], v[i], a.eps));
-  }
-  store_units(a.param[t] + u0, n, p);
-  if (a.copy[t]) store_units(a.copy[t] + u0, n, p);
-  if constexpr (BITS == 32) {
-    float mf[R], vf[R];
+      for (int i = 0; i < R; ++i) {
+        x.m[i] = i < n ? (float)m[i] : 0.0f;
+        x.v[i] = i < n ? (float)v[i] : 0.0f;
+      }
+      store_elems<R>(static_cast<float*>(a.m) + at, x.m);
+      store_elems<R>(static_cast<float*>(a.v) + at, x.v);
+    } else {
+      float mt = 0.0f, vt = 0.0f;
+      bool bm = false, bv = false;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      mf[i] = i < n ? (float)m[i] : 0.0f;
-      vf[i] = i < n ? (float)v[i] : 0.0f;
-    }
-    store_elems<R>(static_cast<float*>(a.m) + at, mf);
-    store_elems<R>(static_cast<float*>(a.v) + at, vf);
-  } else {
-    float mt = 0.0f, vt = 0.0f;
-    bool bm = false, bv = false;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (i >= n) m[i] = v[i] = 0.0;
-      const float x = fabsf((float)m[i]), y = (float)v[i];
-      bm |= !(x < INFINITY);
-      bv |= !(y < INFINITY);
-      mt = fmaxf(mt, x);
-      vt = fmaxf(vt, y);
-    }
-    mt = __any(bm) ? __int_as_float(0x7fc00000) : __int_as_float(wave_minmax<true>(__float_as_int(mt)));  // (not negative: ordered as integers)
-    vt = __any(bv) ? __int_as_float(0x7fc00000) : __int_as_float(wave_minmax<true>(__float_as_int(vt)));
-    const double im = mt > 0.0f ? kAdamwM / (double)mt : 0.0, iv = vt > 0.0f ? kAdamwV / (double)vt : 0.0;
-    uint32_t cm = 0, cv = 0;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
+      for (int i = 0; i < R; ++i) {
+        if (i >= n) m[i] = v[i] = 0.0;
+        const float y = fabsf((float)m[i]), z = (float)v[i];
+        bm |= !(y < INFINITY);
+        bv |= !(z < INFINITY);
+        mt = fmaxf(mt, y);
+        vt = fmaxf(vt, z);
+      }
+      mt = __any(bm) ? __int_as_float(0x7fc00000) : __int_as_float(wave_minmax<true>(__float_as_int(mt)));  // (not negative: ordered as integers)
+      vt = __any(bv) ? __int_as_float(0x7fc00000) : __int_as_float(wave_minmax<true>(__float_as_int(vt)));
       // a bound of NaN or 0 makes codes of 0
-      int c = im > 0.0 ? adamw_code_m(fabs(m[i]) * im) : 0;
-      c = m[i] < 0.0 ? -c : c;
-      int e = iv > 0.0 ? adamw_code_v(v[i] * iv) : 0;
-      if (iv > 0.0 && v[i] > 0.0) e = max(e, 1);
-      cm |= ((uint32_t)c & 255u) << (8 * i);
-      cv |= (uint32_t)e << (8 * i);
+      const double im = mt > 0.0f ? kAdamwM * adamw_inverse(mt) : 0.0, iv = vt > 0.0f ? kAdamwV * adamw_inverse(vt) : 0.0;
+      uint32_t cm = 0, cv = 0;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        int c = im > 0.0 ? adamw_code_m(fabs(m[i]) * im) : 0;
+        c = m[i] < 0.0 ? -c : c;
+        int e = iv > 0.0 ? adamw_code_v(v[i] * iv) : 0;
+        if (iv > 0.0 && v[i] > 0.0) e = max(e, 1);
+        cm |= ((uint32_t)c & 255u) << (8 * i);
+        cv |= (uint32_t)e << (8 * i);
+      }
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + at) = cm;
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + at) = cv;
+      if (__lane_id() == 0) a.bounds[blk] = make_float2(mt, vt);
     }
-    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + at) = cm;
-    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + at) = cv;
-    if (__lane_id() == 0) a.bounds[blk] = make_float2(mt, vt);
+  };
+  // a block's loads run under the one before
+  AdamwLane<BITS> x, next;
+  load(from, x);
+  for (uint32_t blk = from; blk < to; ++blk) {
+    if (blk + 1 < to) load(blk + 1, next);
+    step(blk, x);
+    x = next;
   }
 }
 
@@ -210,7 +240,10 @@ hipError_t launch_adamw(int count, const gs_adamw_tensor* tensors, int grad_type
     a.m = mp + done * each;
     a.v = vp + done * each;
     a.bounds = reinterpret_cast<float2*>(bounds) + (bits == 8 ? done : 0);
-    const unsigned groups = (blocks + 3) / 4;
+    // two blocks a wavefront hide the second one's loads (150M units: 368 -> 347 us); few blocks are spread out (900k units: 8.1 us, two a
+    // wavefront 8.9)
+    a.each = blocks >= 65536 ? 2 : 1;
+    const unsigned groups = (blocks + 4 * a.each - 1) / (4 * a.each);
     if (bits == 8)
       grad_type == GS_BF16 ? k_adamw<__bf16, 8><<<groups, 256, 0, s>>>(a) : k_adamw<float, 8><<<groups, 256, 0, s>>>(a);
     else
