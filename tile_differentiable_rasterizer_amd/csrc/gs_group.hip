@@ -410,7 +410,7 @@ struct GroupShape {
 
 GroupPlan group_plan(bool over_rows, bool staged, bool f32, int64_t rows, int64_t m, int64_t n, int64_t k, int64_t groups) {
   static const GroupShape kShapes[kGroupTiles] = {
-      {256, 256, 256, 5.0, 1.5, 1.6, 0, 1.0}, {128, 256, 256, 3.0, 1.0, 1.15, 0, 1.0}, {128, 128, 512, 3.0, 1.15, 1.2, 0, 1.0},
+      {256, 256, 256, 6.0, 1.5, 1.6, 0, 1.0}, {128, 256, 256, 3.0, 1.0, 1.15, 0, 1.0}, {128, 128, 512, 3.0, 1.15, 1.2, 0, 1.0},
       {32, 256, 256, 2.0, 0.5, 0.0, 0, 1.0},  {32, 128, 512, 2.0, 0.5, 0.0, 0, 1.0},   {128, 128, 512, 4.0, 1.3, 1.3, 256, 0.7},
       {128, 64, 1024, 4.0, 1.6, 1.6, 256, 0.45}};
   static const GroupShape kFloat[2] = {{128, 128, 256, 6.0, 3.2, 3.2, 0, 1.0}, {128, 64, 512, 4.0, 3.8, 3.8, 256, 0.6}};

@@ -31,7 +31,7 @@ struct LayerNormArgs {
   float eps, inv_width;
 };
 
-constexpr int layer_norm_threads(int g) { return g > 256 ? g : 256; }
+constexpr int layer_norm_threads(int g) { return g > kWave ? g : 256; }  // one row of several wavefronts, or several rows
 
 // Sums over the G lanes of a row, in each of them.
 template <int G, int N>
@@ -48,12 +48,13 @@ struct RowSum {
       v[i] += dpp_get<0x141, 0xF>(v[i]);
       v[i] += dpp_get<0x140, 0xF>(v[i]);  // every lane of a row of 16 has its sum
     }
+    if constexpr (G >= 32) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], 16, 64);
+    }
     if constexpr (G >= kWave) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        v[i] += __shfl_xor(v[i], 16, 64);
-        v[i] += __shfl_xor(v[i], 32, 64);
-      }
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], 32, 64);
     }
     if constexpr (G > kWave) {
       if (__lane_id() == 0) {
@@ -287,36 +288,40 @@ struct LayerNormPlan {
   int g, j;
 };
 
-// Lanes of a row and their chunks.
-LayerNormPlan layer_norm_plan(int64_t, int width) {
+// Lanes of a row and their chunks: as few lanes as hold it with one each, so that more than half of them work; two from 8192 units on.
+LayerNormPlan layer_norm_plan(int width) {
   const int chunks = (width + 7) / 8;
-  if (chunks <= 16) return {16, 1};
-  if (chunks <= 64) return {64, 1};
-  if (chunks <= 128) return {64, 2};
-  if (chunks <= 256) return {256, 1};
-  if (chunks <= 512) return {256, 2};
-  if (chunks <= 1024) return {1024, 1};
-  return {1024, 2};
+  int g = 16;
+  while (g < chunks && g < 1024) g *= 2;
+  return {g, chunks > 1024 ? 2 : 1};
 }
 
 int layer_norm_blocks(int64_t rows, int width, bool bwd) {
-  const LayerNormPlan p = layer_norm_plan(rows, width);
+  const LayerNormPlan p = layer_norm_plan(width);
   const int64_t each = layer_norm_threads(p.g) / p.g, need = (rows + each - 1) / each;
-  // back, each leaves a part of dw and db: 3907 rows of 2048 in bfloat16 17.5 us with 512, 15.0 with 1024; 39063 of 4096 in float32, whose
-  // workgroups are twice as large, 350 and 376, and their parts' sum 5 and 9
-  return (int)std::min<int64_t>(need, bwd ? p.j == 1 && p.g < 1024 ? 1024 : 512 : 2048);
+  // Back, each leaves a part of dw and db: 3907 rows of 2048 in bfloat16 17.5 us with 512, 15.0 with 1024, 60000 of 1000 (workgroups of two
+  // wavefronts) 143 with 1024, 95 with 2048; 39063 of 4096 in float32 350 with 512, 376 with 1024, and their parts' sum 5 and 9.
+  const int most = p.g >= 512 ? 512 : p.g == 128 && rows >= 16384 ? 2048 : 1024;
+  return (int)std::min<int64_t>(need, bwd ? most : 2048);
 }
 
 template <typename T, bool BWD>
 void layer_norm_pick(LayerNormPlan p, const LayerNormArgs& a, int blocks, hipStream_t s) {
   const dim3 grid(blocks);
-  if (p.g == 16) k_layer_norm<T, 16, 1, BWD><<<grid, 256, 0, s>>>(a);
-  else if (p.g == 64 && p.j == 1) k_layer_norm<T, 64, 1, BWD><<<grid, 256, 0, s>>>(a);
-  else if (p.g == 64) k_layer_norm<T, 64, 2, BWD><<<grid, 256, 0, s>>>(a);
-  else if (p.g == 256 && p.j == 1) k_layer_norm<T, 256, 1, BWD><<<grid, 256, 0, s>>>(a);
-  else if (p.g == 256) k_layer_norm<T, 256, 2, BWD><<<grid, 256, 0, s>>>(a);
-  else if (p.j == 1) k_layer_norm<T, 1024, 1, BWD><<<grid, 1024, 0, s>>>(a);
-  else k_layer_norm<T, 1024, 2, BWD><<<grid, 1024, 0, s>>>(a);
+  const int threads = layer_norm_threads(p.g);
+  switch (p.g) {
+    case 16: k_layer_norm<T, 16, 1, BWD><<<grid, threads, 0, s>>>(a); break;
+    case 32: k_layer_norm<T, 32, 1, BWD><<<grid, threads, 0, s>>>(a); break;
+    case 64: k_layer_norm<T, 64, 1, BWD><<<grid, threads, 0, s>>>(a); break;
+    case 128: k_layer_norm<T, 128, 1, BWD><<<grid, threads, 0, s>>>(a); break;
+    case 256: k_layer_norm<T, 256, 1, BWD><<<grid, threads, 0, s>>>(a); break;
+    case 512: k_layer_norm<T, 512, 1, BWD><<<grid, threads, 0, s>>>(a); break;
+    default:
+      if (p.j == 1)
+        k_layer_norm<T, 1024, 1, BWD><<<grid, threads, 0, s>>>(a);
+      else
+        k_layer_norm<T, 1024, 2, BWD><<<grid, threads, 0, s>>>(a);
+  }
 }
 
 }  // namespace
@@ -346,7 +351,7 @@ hipError_t launch_layer_norm(int64_t rows, int width, int type, float eps, const
   a.width = width;
   a.eps = eps;
   a.inv_width = 1.0f / (float)width;
-  const LayerNormPlan p = layer_norm_plan(rows, width);
+  const LayerNormPlan p = layer_norm_plan(width);
   const int blocks = layer_norm_blocks(rows, width, dy != nullptr);
   if (type == GS_BF16)
     dy ? layer_norm_pick<__bf16, true>(p, a, blocks, s) : layer_norm_pick<__bf16, false>(p, a, blocks, s);
