@@ -294,7 +294,7 @@ gs_status gs_adamw(int32_t count, const gs_adamw_tensor* tensors, int32_t grad_t
 /*
  * gs_adamw_moments -- what the codes of `blocks` blocks of 256 units stand for: out_m and out_v float32
  * [256 * blocks], 16-byte aligned.
- * Errors: INVALID_ARG, OVERFLOW (2^27 blocks or more), HIP.
+ * Errors: INVALID_ARG, OVERFLOW (2^26 blocks or more, as gs_adamw), HIP.
  */
 gs_status gs_adamw_moments(int64_t blocks, const int8_t* m, const uint8_t* v, const float* bounds, float* out_m,
                            float* out_v, void* stream);

@@ -135,3 +135,7 @@ def test_moments_in_32_bits_are_the_states_own():
     t = tokens()
     s = t.adamw_state([torch.zeros(300), torch.zeros(0), torch.zeros(5)], bits=32)
     assert s.m.shape == (768,) and t.adamw_moments(s)[0] is s.m
+
+
+def moments_call(blocks):
+    return tokens().lib().gs_adamw_moments(blocks, A, A, A, A, A, None)

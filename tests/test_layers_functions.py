@@ -1,0 +1,90 @@
+"""CPU-side checks of layer_norm and group_mm as torch functions: the calls that need the GPU are replaced by plain
+torch, so that what is tested is the way gradients take."""
+import os
+
+import pytest
+import torch
+
+from test_tokens_abi import LIB
+
+pytestmark = pytest.mark.skipif(not os.path.exists(LIB), reason="libgsraster.so not built")
+
+
+@pytest.fixture
+def t(monkeypatch):
+    """tokens with cubes in the place of the calls."""
+    from tile_differentiable_rasterizer_amd import tokens
+
+    plain = torch.no_grad()  # the C calls are not recorded
+    asked = []
+
+    @plain
+    def norm_bwd(dy, x, w, eps, with_dw, with_db):
+        asked.append((with_dw, with_db))
+        return 3 * x * x * dy * w, (x**3 * dy).sum(0) if with_dw else None, dy.sum(0) if with_db else None
+
+    @plain
+    def mm_bwd(dy, x, w, offsets, with_dx, with_dw):
+        asked.append((with_dx, with_dw))
+        return 3 * x * x * (dy @ w[0].t()) if with_dx else None, (x**3).t()[None] @ dy if with_dw else None
+
+    monkeypatch.setattr(tokens, "layer_norm_fwd", plain(lambda x, w, b, eps: x**3 * w + b))
+    monkeypatch.setattr(tokens, "layer_norm_bwd", norm_bwd)
+    monkeypatch.setattr(tokens, "group_mm_fwd", plain(lambda x, w, offsets: x**3 @ w[0]))
+    monkeypatch.setattr(tokens, "group_mm_bwd", mm_bwd)
+    tokens_asked = asked
+    return tokens, tokens_asked
+
+
+def function(t, which):
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(6, 8, generator=g).requires_grad_()
+    w, b, m = torch.randn(8, generator=g), torch.randn(8, generator=g), torch.randn(1, 8, 4, generator=g)
+    offsets = torch.tensor([0, 6], dtype=torch.int32)
+    return ((lambda a: t.layer_norm(a, w, b)) if which == "layer_norm" else (lambda a: t.group_mm(a, m, offsets))), x
+
+
+@pytest.mark.parametrize("which", ["layer_norm", "group_mm"])
+@pytest.mark.parametrize("through", ["sum", "square"])
+def test_second_derivatives_are_refused(t, which, through):
+    """Whether the gradient that comes in depends on x as well or not."""
+    f, x = function(t[0], which)
+    y = f(x)
+    first, = torch.autograd.grad(y.sum() if through == "sum" else y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiated once"):
+        torch.autograd.grad(first.sum(), x)
+
+
+@pytest.mark.parametrize("which", ["layer_norm", "group_mm"])
+def test_a_changed_input_is_an_error(t, which):
+    f, x = function(t[0], which)
+    a = x * 1
+    y = f(a)
+    with torch.no_grad():
+        a.mul_(2)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+
+
+def test_only_what_is_wanted_is_asked_for(t):
+    tokens, asked = t
+    x, w, b = torch.ones(6, 8, requires_grad=True), torch.ones(8), torch.ones(8, requires_grad=True)
+    tokens.layer_norm(x, w, b).sum().backward()
+    tokens.group_mm(x.detach(), torch.ones(1, 8, 4, requires_grad=True), torch.tensor([0, 6], dtype=torch.int32)).sum().backward()
+    tokens.group_mm(x, torch.ones(1, 8, 4), torch.tensor([0, 6], dtype=torch.int32)).sum().backward()
+    assert asked == [(False, True), (False, True), (True, False)] and b.grad.tolist() == [6.0] * 8
+
+
+def test_leading_axes_and_gradients_that_are_not_dense(t):
+    tokens, _ = t
+    g = torch.Generator().manual_seed(6)
+    x, w, b = torch.randn(2, 3, 8, generator=g).requires_grad_(), torch.randn(8, generator=g), torch.zeros(8)
+    for view in (lambda z: z, lambda z: z.transpose(0, 1), lambda z: z[..., None].expand(2, 3, 8, 2)[..., 0]):
+        d = torch.randn(2, 3, 8, generator=g) if view(x).shape == x.shape else torch.randn(3, 2, 8, generator=g)
+        got, = torch.autograd.grad(tokens.layer_norm(view(x), w, b), x, d)
+        want, = torch.autograd.grad(view(x) ** 3 * w, x, d)
+        assert torch.allclose(got, want)
+    for shape in ((0, 8), (2, 0, 8), (8,), (3, 1, 8)):
+        z = torch.ones(shape, requires_grad=True)
+        tokens.layer_norm(z, w, b).sum().backward()
+        assert z.grad.shape == z.shape

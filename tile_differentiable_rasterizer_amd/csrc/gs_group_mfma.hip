@@ -131,7 +131,7 @@ __global__ __launch_bounds__(256, group_places(BM, BN)) void k_group_mfma(GroupA
     id = blockIdx.x;
     end = a.groups * m_tiles * columns;
   } else {
-    m_tiles = spans.count(a);
+    m_tiles = min(spans.count(a), (uint32_t)((a.rows + BM - 1) / BM + min(a.groups + 2, a.rows)));  // (less than it counts: offsets that decrease)
     const uint32_t all = m_tiles * columns, q = all / 8, more = all % 8, xcd = blockIdx.x % 8;
     id = xcd * q + min(xcd, more);
     end = id + q + (xcd < more);

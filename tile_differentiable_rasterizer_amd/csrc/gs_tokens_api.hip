@@ -509,7 +509,7 @@ gs_status gs_adamw(int32_t count, const gs_adamw_tensor* tensors, int32_t grad_t
 gs_status gs_adamw_moments(int64_t blocks, const int8_t* m, const uint8_t* v, const float* bounds, float* out_m,
                            float* out_v, void* stream) {
   if (blocks < 0) return GS_ERR_INVALID_ARG;
-  if (blocks >= (int64_t)1 << 27) return GS_ERR_OVERFLOW;
+  if (blocks >= (int64_t)1 << 26) return GS_ERR_OVERFLOW;
   if (!blocks) return GS_OK;
   if (!m || !v || !bounds || !out_m || !out_v || !on(m, 8) || !on(v, 8) || !on(bounds, 8) || !on(out_m, 16) || !on(out_v, 16))
     return GS_ERR_INVALID_ARG;

@@ -717,18 +717,17 @@ def _rows(t, width):
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, b, eps):
-        width = x.shape[-1]
-        flat = _rows(x, width)
-        ctx.save_for_backward(flat, w)
-        ctx.eps, ctx.shape = eps, x.shape
-        return layer_norm_fwd(flat, w, b, eps).view(x.shape)
+        ctx.save_for_backward(x, w)  # x itself: a view of it would hide from torch what is changed in between
+        ctx.eps = eps
+        return layer_norm_fwd(_rows(x, x.shape[-1]), w, b, eps).view(x.shape)
 
     @staticmethod
     @once
     def backward(ctx, dy):
         x, w = ctx.saved_tensors
-        dx, dw, db = layer_norm_bwd(_rows(dy, x.shape[1]), x, w, ctx.eps, ctx.needs_input_grad[1], ctx.needs_input_grad[2])
-        return dx.view(ctx.shape), dw, db, None
+        width = x.shape[-1]
+        dx, dw, db = layer_norm_bwd(_rows(dy, width), _rows(x, width), w, ctx.eps, ctx.needs_input_grad[1], ctx.needs_input_grad[2])
+        return dx.view(x.shape), dw, db, None
 
 
 def layer_norm(x, w=None, b=None, eps: float = 1e-5):
