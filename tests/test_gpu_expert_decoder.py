@@ -1,0 +1,52 @@
+"""The decoder example with layer norms, experts and AdamW over its tensors: it runs, and its gradients are those of the same
+formulas in plain torch."""
+import pytest
+import torch
+
+from tile_differentiable_rasterizer_amd import token_decoder, tokens
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("optimizer", ["adam_q16", "adamw"])
+@pytest.mark.parametrize("experts", [0, 1, 4])
+def test_decoder_runs(experts, optimizer):
+    losses = token_decoder.train(steps=4, size=64, views=2, n_tokens=27, say=None, experts=experts, optimizer=optimizer)
+    assert len(losses) == 4 and all(x == x for x in losses)
+
+
+def test_copies_are_the_parameters():
+    model = token_decoder.Decoder(27, experts=3, optimizer="adamw", seed=1)
+    before = {k: v.detach().clone() for k, v in model.p.items()}
+    sum(x.square().mean() for x in model(torch.rand(2, 3, 64, 64, device="cuda"))).backward()
+    model.step(1e-3)
+    assert (model.grad == 0).all()
+    for k, v in model.p.items():
+        assert not torch.equal(v, before[k]) or k == "router", k
+        if model.copies[k] is not None:
+            assert torch.equal(model.copies[k], v.detach().bfloat16()), k
+
+
+def test_feed_forward_against_torch():
+    """The expert part of the layer against the same formulas in 64 bits: bfloat16 between the operators and in the results
+    (2^-8 each, five on the longest way) and 8-bit codes of the activations (2^-6 of their norm each way)."""
+    model = token_decoder.Decoder(75, experts=4, seed=2)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(1, 75, 256, generator=g, device="cuda").bfloat16().requires_grad_()
+    p = {k: v.detach().bfloat16().requires_grad_() for k, v in model.p.items()}
+    d = torch.randn(1, 75, 256, generator=g, device="cuda").bfloat16()
+    y = model.feed_forward(x, p)
+    got = torch.autograd.grad(y, (x, p["up"], p["down"]), d)
+    X, up, down, router = (t.detach().double().requires_grad_() for t in (x, p["up"], p["down"], p["router"]))
+    weight, expert = torch.softmax((x[0] @ p["router"]).double(), -1).max(-1)  # the choice is the rounded router's
+    rows = []
+    soft = torch.softmax(X[0] @ router, -1)
+    for i in range(75):
+        e = int(expert[i])
+        a, b = (X[0, i] @ up[e]).chunk(2)
+        rows.append(((torch.nn.functional.silu(a) * b) @ down[e]) * soft[i, e])
+    ref = torch.stack(rows)[None]
+    want = torch.autograd.grad(ref, (X, up, down), d.double())
+    for name, a, b in zip(("y", "x", "up", "down"), (y, *got), (ref.detach(), *want)):
+        off = ((a.double() - b).norm() / b.norm()).item()
+        assert off <= 5 * 2.0**-8 + 2 * 2.0**-6, (name, off)
