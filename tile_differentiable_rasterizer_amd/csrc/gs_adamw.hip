@@ -38,10 +38,16 @@ struct AdamwTable {
   uint32_t blocks, each;  // of the launch, of a wavefront
 };
 
-// What codes stand for, before the block's bound / 127^2 or / 255^4.
-__device__ __forceinline__ double adamw_m_of(int c) { return (double)(c * abs(c)); }
-__device__ __forceinline__ double adamw_v_of(uint32_t c) { return (double)(c * c * (c * c)); }
 constexpr double kAdamwM = 127.0 * 127.0, kAdamwV = 255.0 * 255.0 * 255.0 * 255.0;
+
+// What codes stand for, with q the block's bound times 1 / 127^2 or 1 / 255^4.  With decays like 0.9 a tenth of the new bounds lies, in
+// exact arithmetic, halfway between two float32s, so that the last bit of float64 decides.  The order of the operations is therefore one
+// that float64 code comes to of itself: q c |c|, then beta times it, each rounded, and the gradient's part added in one operation.
+__device__ __forceinline__ double adamw_m_of(double q, int c) {
+  const double d = (double)c;
+  return q * d * fabs(d);
+}
+__device__ __forceinline__ double adamw_v_of(double q, uint32_t c) { return q * (double)(c * c * (c * c)); }
 
 // rint(sqrt(t)) for t in [0, 127^2]: float32's, and a step where t lies past a border.
 __device__ __forceinline__ int adamw_code_m(double t) {
@@ -126,11 +132,11 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwTable a) {
     const double sm = BITS == 32 ? 0.0 : (double)x.top.x * (1.0 / kAdamwM), sv = BITS == 32 ? 0.0 : (double)x.top.y * (1.0 / kAdamwV);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      m[i] = BITS == 32 ? (double)x.m[BITS == 32 ? i : 0] : sm * adamw_m_of((int)(int8_t)(x.cm >> (8 * i)));
-      v[i] = BITS == 32 ? (double)x.v[BITS == 32 ? i : 0] : sv * adamw_v_of((x.cv >> (8 * i)) & 255u);
+      m[i] = BITS == 32 ? (double)x.m[BITS == 32 ? i : 0] : adamw_m_of(sm, (int)(int8_t)(x.cm >> (8 * i)));
+      v[i] = BITS == 32 ? (double)x.v[BITS == 32 ? i : 0] : adamw_v_of(sv, (x.cv >> (8 * i)) & 255u);
       const double g = (double)x.g[i] * scale;
-      m[i] = fma(a.b1, m[i], a.c1 * g);
-      v[i] = fma(a.b2, v[i], a.c2 * (g * g));
+      m[i] = fma(a.c1, g, a.b1 * m[i]);
+      v[i] = fma(a.c2, g * g, a.b2 * v[i]);
       x.p[i] = (float)fma((double)x.p[i], keep, adamw_quotient(a.rate * m[i], v[i], a.eps));
     }
     store_units(a.param[t] + u0, n, x.p);
@@ -199,8 +205,8 @@ __global__ __launch_bounds__(256) void k_adamw_moments(uint32_t blocks, const ui
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t wm = i < 4 ? cm.x : cm.y, wv = i < 4 ? cv.x : cv.y;
-    mf[i] = (float)(sm * adamw_m_of((int)(int8_t)(wm >> (8 * (i & 3)))));
-    vf[i] = (float)(sv * adamw_v_of((wv >> (8 * (i & 3))) & 255u));
+    mf[i] = (float)adamw_m_of(sm, (int)(int8_t)(wm >> (8 * (i & 3))));
+    vf[i] = (float)adamw_v_of(sv, (wv >> (8 * (i & 3))) & 255u);
   }
   store_elems<8>(out_m + at, mf);
   store_elems<8>(out_v + at, vf);
