@@ -16,7 +16,7 @@ SHAPES = [
     (35343, 79, 288, 8), (20038, 44, 8, 536), (12185, 23, 8, 1432), (3664, 6, 7232, 8), (17224, 1, 8, 8), (506, 22, 8, 2624), (1770, 81, 1104, 8), (31285, 71, 8, 144),
     (6378, 14, 8, 2424), (391, 17, 5952, 72), (9452, 2, 8, 2752), (17221, 2, 80, 400), (17303, 1, 4264, 8), (8631, 5, 8, 144), (17295, 4, 96, 8), (35689, 2, 136, 144),
     (876, 16, 168, 5080), (1386, 10, 6720, 144), (1689, 28, 6424, 144), (17270, 2, 8, 2016), (11817, 22, 144, 2944), (34408, 2, 8, 2112), (28111, 89, 72, 288),
-    (10448, 1, 5448, 136), (7996, 16, 168, 4720), (9375, 35, 5568, 136), (7908, 26, 184, 5056), (5000, 70, 520, 264), (600, 66, 1032, 200),
+    (10448, 1, 5448, 136), (7996, 16, 168, 4720), (9375, 35, 5568, 136), (7908, 26, 184, 5056), (5000, 70, 520, 264), (600, 66, 1032, 200), (30039, 1, 40, 96), (70001, 1, 136, 72),
 ]
 
 
@@ -52,7 +52,8 @@ def test_aligned(rows, groups, k, n, layout):
 
 # of these every block of the kernel that stages its tiles through registers
 STAGED = [(1, 70, 8, 8), (1, 50, 664, 592), (29490, 57, 8, 8), (3, 6, 904, 1576), (26036, 18, 176, 8), (78, 87, 352, 1648), (2517, 13, 2776, 8), (1689, 28, 642, 145), (5000, 70, 7, 264),
-          (4000, 3, 515, 5), (300, 2, 4105, 263), (9001, 1, 264, 129)]
+          (4000, 3, 515, 5), (300, 2, 4105, 263), (9001, 1, 264, 129), (30039, 1, 40, 96),
+          (70001, 1, 135, 72), (13, 1, 33, 40), (65, 4, 65, 9), (40, 2, 72, 31)]
 
 
 @pytest.mark.parametrize("layout", ["kn", "nk"])

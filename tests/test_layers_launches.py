@@ -108,7 +108,7 @@ def test_products_want_their_workspace(how):
 
 
 def test_products_workspace_is_bounded():
-    """Parts are made where results are few: at most 32 of them, and of a launch's blocks."""
+    """Parts are made where results are few: at most 256 of them, and of a launch's blocks."""
     t = tokens()
     for rows in (1, 100, 5000, 1 << 20, 1 << 26):
         for k, n in ((8, 8), (512, 512), (8192, 264), (264, 8192), (1 << 20, 8)):

@@ -4,9 +4,15 @@
 //
 //   y[r] = x[r] W[g(r)],  dx[r] = dy[r] W[g(r)]^T,  dW[g] = sum over the group's rows of x[r]^T dy[r].
 //
-// A workgroup of four wavefronts makes 128 x 128 results over tiles of 32 k.  Tiles pass through registers, loaded
-// a tile ahead at any alignment, and enter LDS in the matrix unit's terms: float32 as three bfloat16 that hold all of
-// its bits, split once for the workgroup (gs_mfma.h).
+// A workgroup of eight wavefronts makes 128 x 128 results (or 128 x 64) over tiles of 32 k, in two halves of LDS.  Tiles pass through
+// registers, loaded two ahead at any alignment, and enter LDS in the matrix unit's terms: float32 as three bfloat16 that hold
+// all of its bits, split once for the workgroup while the tile before is multiplied (gs_mfma.h).  A sum's last tile ends with
+// the last k: its eights are loaded whole, and what the ones before had is cut (1955 rows of 5 groups, 363 x 250 in bfloat16, the three
+// products: 31.9 us with element loads for what 64 does not divide, 27.8 so).
+//
+// float32 is bound by the matrix units at the power they get: 7814 rows of 8, 2048 x 4096: 800 us, 164 TFLOP/s, 980 TFLOP/s of
+// bfloat16 products.  bfloat16: 18583 rows of 10, 4797 x 777, 370 to 490 TFLOP/s, by loads that start off 16 bytes (the same on 16
+// bytes: 410 to 630) and their way through registers; blocks of 256 x 128 were no faster.
 //
 // Where a sum is long and the results are few, several workgroups share it: their parts go to a workspace in
 // float32, and a second kernel adds them in a fixed order.
@@ -66,76 +72,79 @@ __device__ __forceinline__ int eight_at(int at, int rows) {
 
 // One operand's tile of 128 rows (or columns) by 32 k, in LDS as gs_group_mfma.hip's but for rows of 64 bytes where k is
 // dense (chunk c of row r at c ^ (r / 4 % 4)); float32's three parts one after another.
-template <typename T, bool K_DENSE, bool NARROW, int R>
+template <typename T, bool K_DENSE, bool OVER_ROWS, bool NARROW, int R>
 struct StagedSide {
   static constexpr int kChunks = (K_DENSE ? kStagedK : R) / 8, kPart = R * kStagedK * 2;
-  static constexpr int kEach = 1;  // an eight a thread, of the first threads where there are fewer
-  static_assert(R * kStagedK / 8 <= kStagedThreads && (R == 64 || R >= 128));
+  static_assert(R == 64 || R == 128, "an eight a thread, of the first threads where there are fewer");
   static constexpr int kParts = sizeof(Frag<T>) / sizeof(bf16x8), kBytes = kParts * kPart;
 
   const T* base;    // of the tile at k0
   int64_t step;     // elements of 32 k
   int64_t stride;   // of the axis that is not dense
-  int64_t off[kEach];
+  int64_t off, off_last;
+  int cut;          // of the last tile's eight: the first elements, which do not count
   int rows;
   int at;
-  Eight<T> x[kStagedAhead][kEach];  // tiles on their way
+  Eight<T> x[kStagedAhead];  // tiles on their way
 
   static __device__ __forceinline__ int mix(int r) {
     if (K_DENSE) return (r >> 2) & 3;
     return R == 64 ? ((r & 2) << 1) | ((r >> 2) & 3) : ((r & 3) << 2) | ((r >> 2) & 3);
   }
-  static __device__ __forceinline__ int item_of(int i) { return (i * kStagedThreads + (int)threadIdx.x) % (R * kStagedK / 8); }
-  static __device__ __forceinline__ int row_of(int i) { return item_of(i) / kChunks; }
-  static __device__ __forceinline__ int chunk_of(int i) { return item_of(i) % kChunks; }
+  static __device__ __forceinline__ int item() { return (int)threadIdx.x % (R * kStagedK / 8); }
+  static __device__ __forceinline__ int row() { return item() / kChunks; }
+  static __device__ __forceinline__ int chunk() { return item() % kChunks; }
 
-  __device__ __forceinline__ void plan(const T* p, int64_t s, int n, int first) {
+  // The last tile, of which k < left exist (of 1 to 32): its eights end with the last k, and count from where the one before ended.
+  __device__ __forceinline__ void plan(const T* p, int64_t s, int n, int left, int first) {
     base = p;
     stride = s;
     rows = n;
     step = K_DENSE ? kStagedK : kStagedK * s;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int r = row_of(i), c = chunk_of(i) * 8;
-      off[i] = K_DENSE ? min(r, rows - 1) * stride + c : r * stride + eight_at<NARROW>(c, rows);
+    const int r = row(), c = chunk() * 8;
+    if constexpr (K_DENSE) {
+      const int k = min(c, left - 8);
+      off = min(r, rows - 1) * stride;
+      off_last = off + k;
+      off += c;
+      cut = c - k;
+    } else {  // rows of k: a sum over rows may have fewer than eight
+      const int r8 = r & ~7, k = OVER_ROWS ? min(r, left - 1) : min(r8, left - 8) + r - r8, col = eight_at<NARROW>(c, rows);
+      off = r * stride + col;
+      off_last = k * stride + col;
+      cut = k < (OVER_ROWS ? r : r8) ? 8 : 0;
     }
     const int l = __lane_id(), h = l >> 5, i = l & 15;
     if constexpr (K_DENSE) {
-      const int r = l & 31;
-      at = (first + r) * (kChunks * 16) + ((h ^ mix(r)) << 4);
+      at = (first + (l & 31)) * (kChunks * 16) + ((h ^ mix(l & 31)) << 4);
     } else {
-      const int r = 8 * h + (i >> 2), c = first / 8 + (2 * ((l >> 4) & 1) + ((i & 3) >> 1));
-      at = r * (kChunks * 16) + ((c ^ mix(r)) << 4) + 8 * (i & 1);
+      const int from = 8 * h + (i >> 2), chunk_at = first / 8 + (2 * ((l >> 4) & 1) + ((i & 3) >> 1));
+      at = from * (kChunks * 16) + ((chunk_at ^ mix(from)) << 4) + 8 * (i & 1);
     }
   }
-  // Tile `tile`, all of whose k exist.  Rows (or columns) that do not are read as others: what comes of them is not stored.
-  __device__ __forceinline__ void load(int to, int tile) {
-    const T* p = base + tile * step;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) x[to][i].load(p + off[i]);
+  // A tile.  Rows (or columns) that do not exist are read as others: what comes of them is not stored.
+  __device__ __forceinline__ void load(int to, int tile, bool last) {
+    x[to].load(base + tile * step + (last ? off_last : off));
   }
-  // Any tile, of which k < left exist: the others are 0.
+  __device__ __forceinline__ void cut_last(int from) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[from].v[e] = e < cut ? (T)0.0f : x[from].v[e];
+  }
+  // NARROW: any tile, of which k < left exist; the others are 0.
   __device__ __forceinline__ void load_part(int to, int tile, int left) {
-    const T* p = base + tile * step;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int c = chunk_of(i) * 8;
-      x[to][i].load(p + off[i], K_DENSE ? left - c : row_of(i) >= left ? 0 : NARROW ? rows - c : 8);
-    }
+    const int c = chunk() * 8;
+    x[to].load(base + tile * step + off, K_DENSE ? left - c : row() >= left ? 0 : rows - c);
   }
   __device__ __forceinline__ void store(int from, char* tile) const {
     if (R * kStagedK / 8 < kStagedThreads && threadIdx.x >= R * kStagedK / 8) return;  // (whole wavefronts)
+    const int r = row(), c = chunk();
+    union {
+      Frag<T> f;
+      bf16x8 v[kParts];
+    } u;
+    u.f = x[from].parts();
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int r = row_of(i), c = chunk_of(i);
-      union {
-        Frag<T> f;
-        bf16x8 v[kParts];
-      } u;
-      u.f = x[from][i].parts();
-#pragma unroll
-      for (int k = 0; k < kParts; ++k) *reinterpret_cast<bf16x8*>(tile + k * kPart + r * (kChunks * 16) + ((c ^ mix(r)) << 4)) = u.v[k];
-    }
+    for (int k = 0; k < kParts; ++k) *reinterpret_cast<bf16x8*>(tile + k * kPart + r * (kChunks * 16) + ((c ^ mix(r)) << 4)) = u.v[k];
   }
   __device__ __forceinline__ Frag<T> read(const char* tile, int m, int s) const {
     union {
@@ -166,8 +175,8 @@ struct StagedSide {
 };
 
 // The running sums of a block.  float32: the products of the leading parts apart from the five smaller ones, whose sum is
-// 2^-8 of theirs, so that a sum over k is rounded once for 16 k and not six times.  (Over 6000 k, against 64 bits: 1e-6 -> 4e-7 of the
-// result's norm; a product in float32 by the library 6e-7.)
+// 2^-8 of theirs, so that a sum over k is rounded once for 16 k and not six times (over 3648 k, against 64 bits: 9e-7 -> 3.7e-7 of the
+// result's norm).
 template <typename T>
 struct Sums;
 template <>
@@ -194,8 +203,8 @@ struct Sums<float> {
 template <typename T, bool A_DENSE, bool B_DENSE, bool OVER_ROWS, bool NARROW, int BN>
 __global__ __launch_bounds__(kStagedThreads, BN == 64 ? 4 : 2) void k_group_staged(GroupArgs a) {
   constexpr int TM = 1, TN = BN / 64;  // a wavefront's 32 x 64 (or 32) of the block
-  using SideA = StagedSide<T, A_DENSE, NARROW, kStagedTile>;
-  using SideB = StagedSide<T, B_DENSE, NARROW, BN>;
+  using SideA = StagedSide<T, A_DENSE, OVER_ROWS, NARROW, kStagedTile>;
+  using SideB = StagedSide<T, B_DENSE, OVER_ROWS, NARROW, BN>;
   constexpr int kTile = SideA::kBytes + SideB::kBytes;
   __shared__ __align__(1024) char lds[2 * kTile];
   const int n_tiles = (a.n + BN - 1) / BN;
@@ -233,13 +242,19 @@ __global__ __launch_bounds__(kStagedThreads, BN == 64 ? 4 : 2) void k_group_stag
   if (k0 < k_end) {
     SideA sa;
     SideB sb;
-    sa.plan(static_cast<const T*>(a.a) + m0 * a.a_m + k0 * a.a_k, A_DENSE ? a.a_m : a.a_k, m_end - m0, wm * TM * 32);
-    sb.plan(static_cast<const T*>(a.b) + (OVER_ROWS ? 0 : g * a.b_g) + k0 * a.b_k + n0 * a.b_n, B_DENSE ? a.b_n : a.b_k, a.n - n0, wn * TN * 32);
-    auto load = [&](int to, int t) {
-      sa.load(to, t);
-      sb.load(to, t);
+    const int all = k_end - k0, tiles = (all + kStagedK - 1) / kStagedK, left = all - (tiles - 1) * kStagedK;
+    sa.plan(static_cast<const T*>(a.a) + m0 * a.a_m + k0 * a.a_k, A_DENSE ? a.a_m : a.a_k, m_end - m0, left, wm * TM * 32);
+    sb.plan(static_cast<const T*>(a.b) + (OVER_ROWS ? 0 : g * a.b_g) + k0 * a.b_k + n0 * a.b_n, B_DENSE ? a.b_n : a.b_k, a.n - n0, left, wn * TN * 32);
+    auto load = [&](int to, int t) {  // past the last: that one again, for nothing
+      t = min(t, tiles - 1);
+      sa.load(to, t, t == tiles - 1);
+      sb.load(to, t, t == tiles - 1);
     };
-    auto store = [&](int from, int buffer) {
+    auto store = [&](int from, int buffer, int t) {
+      if (t == tiles - 1 && left < kStagedK) {
+        sa.cut_last(from);
+        sb.cut_last(from);
+      }
       sa.store(from, lds + buffer * kTile);
       sb.store(from, lds + buffer * kTile + SideA::kBytes);
     };
@@ -258,32 +273,38 @@ __global__ __launch_bounds__(kStagedThreads, BN == 64 ? 4 : 2) void k_group_stag
           for (int n = 0; n < TN; ++n) acc[n][m].add(fb[n], fa[m]);
       }
     };
-    // pairs of whole tiles: while one is multiplied, the next goes to the other half of LDS and the two behind it are on
-    // their way, with no branch between a load and its use; then the rest, one by one
-    const int all = k_end - k0, whole = NARROW ? 0 : all / (2 * kStagedK) * 2;
-    if (whole) {
-      load(0, 0);
-      load(1, 1);
-      store(0, 0);
-      load(0, min(2, whole - 1));
-      __syncthreads();
-      for (int t = 0; t < whole; t += 2) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          store(i ^ 1, i ^ 1);  // tile t + i + 1 (past the last: one again, for nothing)
-          load(i ^ 1, min(t + i + 3, whole - 1));
-          multiply(i);
-          __syncthreads();
-        }
+    if constexpr (NARROW) {
+      for (int t = 0; t < tiles; ++t) {
+        sa.load_part(0, t, all - t * kStagedK);
+        sb.load_part(0, t, all - t * kStagedK);
+        store(0, 0, -1);
+        __syncthreads();
+        multiply(0);
+        __syncthreads();
       }
-    }
-    for (int t = whole; t * kStagedK < all; ++t) {
-      sa.load_part(0, t, all - t * kStagedK);
-      sb.load_part(0, t, all - t * kStagedK);
-      store(0, 0);
-      __syncthreads();
-      multiply(0);
-      __syncthreads();
+    } else {
+      // while a tile is multiplied, the next goes to the other half of LDS and the two behind it are on their way, with no branch
+      // between a load and its use
+      load(0, 0);
+      if (tiles > 1) {
+        load(1, 1);
+        store(0, 0, 0);
+        load(0, 2);
+        __syncthreads();
+        for (int t = 0; t + 1 < tiles; t += 2) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            store(i ^ 1, i ^ 1, t + i + 1);
+            load(i ^ 1, t + i + 3);
+            multiply(i);
+            __syncthreads();
+          }
+        }
+      } else {
+        store(0, 0, 0);
+        __syncthreads();
+      }
+      if (tiles & 1) multiply(0);
     }
   }
 
@@ -320,21 +341,37 @@ __global__ __launch_bounds__(kStagedThreads, BN == 64 ? 4 : 2) void k_group_stag
   }
 }
 
-// C from the parts: eight results a thread.
-template <typename T>
+// C from the parts, in a fixed order: eight results a thread, which adds every LANES-th part where there are many, and then the threads'
+// sums in turn.
+template <typename T, int LANES>
 __global__ __launch_bounds__(256) void k_group_join(GroupArgs a, int64_t rows, int outer_rows, int64_t outer_stride) {
+  constexpr int kResults = 256 / LANES;
   const int width = group_part_width(a.n), chunks = width / 8;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / chunks;
-  if (row >= rows) return;
+  const int at = threadIdx.x % kResults, lane = threadIdx.x / kResults;
+  const int64_t i = (int64_t)blockIdx.x * kResults + at, row = i / chunks;
   const int col = (int)(i - row * chunks) * 8;
-  const float* p = a.part + row * width + col;
   float x[8] = {};
-  for (int s = 0; s < a.splits; ++s) {
-    float y[8];
-    load_elems<8>(p + s * rows * width, y);
+  if (row < rows) {
+    const float* p = a.part + row * width + col;
+#pragma unroll 4
+    for (int s = lane; s < a.splits; s += LANES) {
+      float y[8];
+      load_elems<8>(p + s * rows * width, y);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] += y[e];
+      for (int e = 0; e < 8; ++e) x[e] += y[e];
+    }
   }
+  if constexpr (LANES > 1) {
+    __shared__ float sums[LANES][kResults][8 + 1];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[lane][at][e] = x[e];
+    __syncthreads();
+    if (lane > 0) return;
+    for (int l = 1; l < LANES; ++l)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] += sums[l][at][e];
+  }
+  if (row >= rows) return;
   const int64_t outer = row / outer_rows, in = row - outer * outer_rows;
   store_units(static_cast<T*>(a.c) + outer * outer_stride + in * a.c_m + col, min(a.n - col, 8), x);
 }
@@ -366,10 +403,10 @@ void staged_launch(bool over_rows, const GroupArgs& a, hipStream_t s) {
     k_group_staged<T, true, false, false, NARROW, BN><<<blocks, kStagedThreads, 0, s>>>(a);
 }
 template <typename T>
-void staged_launch(bool over_rows, int bn, const GroupArgs& a, hipStream_t s) {
+void staged_launch(bool over_rows, int tile, const GroupArgs& a, hipStream_t s) {
   if (a.n < 8 || (over_rows ? a.m : a.k) < 8)
     staged_launch<T, true, 128>(over_rows, a, s);
-  else if (bn == 64)
+  else if (tile == kGroupStaged64)
     staged_launch<T, false, 64>(over_rows, a, s);
   else
     staged_launch<T, false, 128>(over_rows, a, s);
@@ -398,7 +435,8 @@ struct GroupPlan {
 // 295; 782 rows 46 37 40 48 50; 64 rows of 16 groups 52 49 47 43 47; 3907 rows of one, 2048 x 2048: 45 35 36 66 66; 20000 rows of 8, 512 x 256:
 // 18 13 15 19 17; 64 rows of 4, 4096 x 512, in the best number of parts: 19 17 14 14 13, in one 32 x 128: 33.  Over rows (the first
 // three): 7814 rows of 8, 2048 x 4096: 143 169 163; 20000 rows of 8, 512 x 256: 32 26 22 in 8, 8 and 4 parts, 66 in one; 40000
-// rows of one, 1024 x 512: 63 57 65 in 32, 16 and 16 parts.
+// rows of one, 1024 x 512: 63 57 65 in 32, 16 and 16 parts.  Many parts: 200000 rows of one, 256 x 256: 74 in 32, 50 in 64, 46 in 128;
+// float32, 30039 rows of one, 40 x 96: 39 in 32, 26 in 64, 19.5 in 128.
 // Staged (128 x 128, 128 x 64): float32, 4000 rows of 2, 4096 x 1024: 218 248; 43816 rows of one, 40 x 528: 63 53, and back 62 36; 158 rows
 // of 37 back, 3496 x 165: 95 56; bfloat16, 1955 rows of 5, 363 x 250: 11 9.5; 20000 rows of 8, 101 x 515: 27 32.
 struct GroupShape {
@@ -423,7 +461,7 @@ GroupPlan group_plan(bool over_rows, bool staged, bool f32, int64_t rows, int64_
     if ((t >= kGroupStaged128) != staged || (over_rows && x.bm < 128)) continue;
     const double m_tiles = over_rows ? (double)(groups * tiles(m, x.bm)) : std::max(used, (double)rows / x.bm + 0.5 * used);
     const double blocks = std::max(1.0, m_tiles * (double)tiles(n, x.bn));
-    for (int splits = 1; splits <= 32; splits *= 2) {
+    for (int splits = 1; splits <= 256; splits *= 2) {
       if (splits > 1 && (length < 128.0 * splits || blocks * splits > 2.0 * x.places)) break;
       const double full = blocks * splits / x.places;
       const double rounds = full <= 1.0 ? 1.0 : staged ? full + 0.3 : 0.5 * (std::ceil(0.94 * full) + std::ceil(1.06 * full));  // (blocks are known to 6%)
@@ -460,19 +498,22 @@ hipError_t launch_group(bool over_rows, GroupArgs a, int type, void* ws, hipStre
     e = launch_group_mfma(over_rows, plan.tile, a, s);
   } else {
     if (type == GS_BF16)
-      staged_launch<__bf16>(over_rows, plan.tile == kGroupStaged64 ? 64 : 128, a, s);
+      staged_launch<__bf16>(over_rows, plan.tile, a, s);
     else
-      staged_launch<float>(over_rows, plan.tile == kGroupStaged64 ? 64 : 128, a, s);
+      staged_launch<float>(over_rows, plan.tile, a, s);
     e = hipGetLastError();
   }
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t rows = over_rows ? (int64_t)a.groups * a.m : a.rows;
   const int outer = over_rows ? a.m : a.rows;
-  const unsigned groups = (unsigned)tiles(rows * (group_part_width(a.n) / 8), 256);
-  if (type == GS_BF16)
-    k_group_join<__bf16><<<groups, 256, 0, s>>>(a, rows, outer, a.c_g);
-  else
-    k_group_join<float><<<groups, 256, 0, s>>>(a, rows, outer, a.c_g);
+  const int64_t results = rows * (group_part_width(a.n) / 8);
+  if (a.splits >= 16) {
+    const unsigned groups = (unsigned)tiles(results, 32);
+    type == GS_BF16 ? k_group_join<__bf16, 8><<<groups, 256, 0, s>>>(a, rows, outer, a.c_g) : k_group_join<float, 8><<<groups, 256, 0, s>>>(a, rows, outer, a.c_g);
+  } else {
+    const unsigned groups = (unsigned)tiles(results, 256);
+    type == GS_BF16 ? k_group_join<__bf16, 1><<<groups, 256, 0, s>>>(a, rows, outer, a.c_g) : k_group_join<float, 1><<<groups, 256, 0, s>>>(a, rows, outer, a.c_g);
+  }
   return hipGetLastError();
 }
 
