@@ -29,6 +29,28 @@ hipError_t launch_group_mfma(bool over_rows, int tile, const GroupArgs& a, hipSt
 constexpr int kStagedTile = 128, kStagedK = 32, kStagedThreads = 512;
 constexpr int kStagedAhead = 2;  // tiles on their way
 
+// x as a sum of three bfloat16, two elements at a time: 88 operations for a thread's sixteen where frag_split, which keeps an infinity apart
+// (here it makes NaNs), takes 156; splitting, not the products, is what a tile waits for.
+__device__ __forceinline__ Frag<float> group_split(f32x8 x) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  union {
+    Frag<float> f;
+    uint32_t u[3][4];
+  } r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f32x2 y = {x[2 * j], x[2 * j + 1]};
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      r.u[k][j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(y, bf16x2));
+      y[0] -= __uint_as_float(r.u[k][j] << 16);
+      y[1] -= __uint_as_float(r.u[k][j] & 0xffff0000u);
+    }
+  }
+  return r.f;
+}
+
 // Eight elements of memory on their way to LDS: all of them, at any alignment, or the first n and zeros behind.
 template <typename T>
 struct Eight;
@@ -61,7 +83,7 @@ struct Eight<float> {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
   }
-  __device__ __forceinline__ Frag<float> parts() const { return frag_split(v); }
+  __device__ __forceinline__ Frag<float> parts() const { return group_split(v); }
 };
 
 // Where eight rows (or columns) are that the tile counts from `at` on (a multiple of 8), of `rows`: the last eight in the place of a few.
