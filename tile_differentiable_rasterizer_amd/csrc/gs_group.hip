@@ -459,8 +459,9 @@ struct GroupPlan {
 // three): 7814 rows of 8, 2048 x 4096: 143 169 163; 20000 rows of 8, 512 x 256: 32 26 22 in 8, 8 and 4 parts, 66 in one; 40000
 // rows of one, 1024 x 512: 63 57 65 in 32, 16 and 16 parts.  Many parts: 200000 rows of one, 256 x 256: 74 in 32, 50 in 64, 46 in 128;
 // float32, 30039 rows of one, 40 x 96: 39 in 32, 26 in 64, 19.5 in 128.
-// Staged (128 x 128, 128 x 64): float32, 4000 rows of 2, 4096 x 1024: 218 248; 43816 rows of one, 40 x 528: 63 53, and back 62 36; 158 rows
-// of 37 back, 3496 x 165: 95 56; bfloat16, 1955 rows of 5, 363 x 250: 11 9.5; 20000 rows of 8, 101 x 515: 27 32.
+// Staged (128 x 128, 128 x 64): float32, 4000 rows of 2, 4096 x 1024: 221 244; 800 rows of 4, 512 x 1024: 22 17; 43816 rows of one, 40 x 528,
+// back: 50 31; 158 rows of 37, 3496 x 165: 78 49; 51701 rows of 13, 82 x 82, by rows 19 23, over rows 32 28;
+// bfloat16, 1955 rows of 5, 363 x 250: 9.5 9.0; 20000 rows of 8, 513 x 257: 25 39.
 struct GroupShape {
   int bm, bn, places;
   double fix, by_rows, over;  // us: a block, and 64 k
