@@ -375,6 +375,11 @@ def gate8_bwd(dy, codes, bounds, act: str = "silu", with_y: bool = True, dgate=N
 # -- layer norm ------------------------------------------------------------------------------
 
 
+def _new(x, rows, width):
+    """A dense matrix of x's type on its GPU (the shortest of torch's ways to make one: 1.3 us, or 1.6)."""
+    return torch.empty_like(x) if x.shape == (rows, width) and x.is_contiguous() else x.new_empty((rows, width))
+
+
 def _matrix(x):
     if x.dim() != 2:
         _refuse("matrices [rows][width]")
@@ -394,7 +399,7 @@ def layer_norm_fwd(x, w=None, b=None, eps: float = 1e-5, out=None, stream=None):
     if b is not None:
         _floats(b, (width,), x, "b")
     if out is None:
-        out = torch.empty((rows, width), dtype=x.dtype, device=x.device)
+        out = _new(x, rows, width)
     _launch("gs_layer_norm_fwd", x, rows, width, ty, eps, x.data_ptr(), xs, _ptr(w), _ptr(b), out.data_ptr(), _stride(out, x, rows, width))
     return out
 
@@ -411,7 +416,7 @@ def layer_norm_bwd(dy, x, w=None, eps: float = 1e-5, with_dw: bool = True, with_
     if w is not None:
         _floats(w, (width,), x, "w")
     if dx is None:
-        dx = torch.empty((rows, width), dtype=x.dtype, device=x.device)
+        dx = _new(x, rows, width)
     dw = torch.empty(width, dtype=torch.float32, device=x.device) if with_dw else None
     db = torch.empty(width, dtype=torch.float32, device=x.device) if with_db else None
     ws, n = _workspace(workspace, lib().gs_layer_norm_workspace_bytes(rows, width) if with_dw or with_db else 0, x)
@@ -452,7 +457,7 @@ def group_mm_fwd(x, w, offsets, out=None, workspace=None, stream=None):
         return _on(stream, group_mm_fwd, x, w, offsets, out, workspace)
     p, ww = _group_shape(x, w, offsets)
     if out is None:
-        out = torch.empty((p.rows, p.n), dtype=x.dtype, device=x.device)
+        out = _new(x, p.rows, p.n)
     ws, n = _workspace(workspace, lib().gs_group_mm_fwd_workspace_bytes(p), x)
     _launch("gs_group_mm_fwd", x, p, x.data_ptr(), _stride(x, x, p.rows, p.k), ww, out.data_ptr(), _stride(out, x, p.rows, p.n),
             _ptr(ws), n)
@@ -470,7 +475,7 @@ def group_mm_bwd(dy, x, w, offsets, with_dx: bool = True, with_dw: bool = True, 
     if not with_dx:
         dx = None
     elif dx is None:
-        dx = torch.empty((p.rows, p.k), dtype=x.dtype, device=x.device)
+        dx = _new(x, p.rows, p.k)
     if not with_dw:
         dw = None
     elif dw is None:
