@@ -150,19 +150,21 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwTable a) {
       store_elems<R>(static_cast<float*>(a.m) + at, x.m);
       store_elems<R>(static_cast<float*>(a.v) + at, x.v);
     } else {
-      float mt = 0.0f, vt = 0.0f;
-      bool bm = false, bv = false;
+      if (__any(n < R)) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (i >= n) m[i] = v[i] = 0.0;
+      }
+      // largest as integers: float32s of one sign are ordered so, infinities and NaNs above them
+      uint32_t mu = 0, vu = 0;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        if (i >= n) m[i] = v[i] = 0.0;
-        const float y = fabsf((float)m[i]), z = (float)v[i];
-        bm |= !(y < INFINITY);
-        bv |= !(z < INFINITY);
-        mt = fmaxf(mt, y);
-        vt = fmaxf(vt, z);
+        mu = max(mu, __float_as_uint((float)m[i]) & 0x7fffffffu);
+        vu = max(vu, __float_as_uint((float)v[i]) & 0x7fffffffu);
       }
-      mt = __any(bm) ? __int_as_float(0x7fc00000) : __int_as_float(wave_minmax<true>(__float_as_int(mt)));  // (not negative: ordered as integers)
-      vt = __any(bv) ? __int_as_float(0x7fc00000) : __int_as_float(wave_minmax<true>(__float_as_int(vt)));
+      mu = (uint32_t)wave_minmax<true>((int)mu);
+      vu = (uint32_t)wave_minmax<true>((int)vu);
+      const float mt = __uint_as_float(mu < 0x7f800000u ? mu : 0x7fc00000u), vt = __uint_as_float(vu < 0x7f800000u ? vu : 0x7fc00000u);
       // a bound of NaN or 0 makes codes of 0
       const double im = mt > 0.0f ? kAdamwM * adamw_inverse(mt) : 0.0, iv = vt > 0.0f ? kAdamwV * adamw_inverse(vt) : 0.0;
       // float32's roots decide all codes but those next to a border between two: they are off by 1.25 and 1.63 times 2^-23 at most (a
