@@ -27,6 +27,20 @@ def test_copies_are_the_parameters():
             assert torch.equal(model.copies[k], v.detach().bfloat16()), k
 
 
+def test_parameters_that_something_else_changes():
+    """The next pass multiplies with what a parameter holds then, whoever wrote it."""
+    model, other = (token_decoder.Decoder(27, optimizer="adamw", seed=s) for s in (1, 2))
+    images = torch.rand(2, 3, 64, 64, device="cuda")
+    for step in range(2):
+        want = other(images)
+        sum(x.square().mean() for x in model(images)).backward()
+        model.step(1e-3)
+        with torch.no_grad():
+            for k, v in model.p.items():
+                v.copy_(other.p[k])
+        assert all(torch.equal(a, b) for a, b in zip(model(images), want)), step
+
+
 def test_feed_forward_against_torch():
     """The expert part of the layer against the same formulas in 64 bits: bfloat16 between the operators and in the results
     (2^-8 each, five on the longest way) and 8-bit codes of the activations (2^-6 of their norm each way)."""

@@ -88,3 +88,20 @@ def test_leading_axes_and_gradients_that_are_not_dense(t):
         z = torch.ones(shape, requires_grad=True)
         tokens.layer_norm(z, w, b).sum().backward()
         assert z.grad.shape == z.shape
+
+
+def test_adamw_wants_every_gradient(monkeypatch):
+    """A parameter without a gradient is refused before anything is read."""
+    from tile_differentiable_rasterizer_amd import tokens
+
+    class State:
+        class m:
+            is_cuda = True
+
+            @staticmethod
+            def get_device():
+                return 0
+
+    for grads in ([None], [torch.ones(3), None]):
+        with pytest.raises(ValueError, match="gradient for each"):
+            tokens.adamw([torch.ones(3)] * len(grads), grads, State, 1e-3, 1)

@@ -103,7 +103,8 @@ class Decoder:
         if optimizer == "adamw":
             self.state = tokens.adamw_state(list(self.p.values()), bits=8)
             # what the products multiply with: kept up to date by the step; a vector has none
-            self.copies = {k: None if k in VECTORS else v.detach().to(torch.bfloat16) for k, v in self.p.items()}
+            self.copies = {k: None if k in VECTORS else torch.empty_like(v, dtype=torch.bfloat16) for k, v in self.p.items()}
+            self.copied = {}
         # each group's home, on a grid around the origin: the head moves its Gaussians from there
         side = math.ceil(n_tokens ** (1 / 3))
         i = torch.arange(n_tokens, device=device)
@@ -119,6 +120,10 @@ class Decoder:
     def __call__(self, images: torch.Tensor):
         """Gaussians (means, scales, quats, opacities, sh) from images [views, 3, H, W], H and W multiples of 16."""
         if self.optimizer == "adamw":
+            for k, v in self.p.items():
+                if k not in VECTORS and self.copied.get(k) != v._version:  # changed by something else than the step
+                    self.copies[k].copy_(v.detach())
+                    self.copied[k] = v._version
             p = {k: v if k in VECTORS else Rounded.apply(v, self.copies[k]) for k, v in self.p.items()}
         else:
             p = {k: v.to(torch.bfloat16) if k not in VECTORS else v for k, v in self.p.items()}
@@ -159,6 +164,7 @@ class Decoder:
         if self.optimizer == "adamw":
             tokens.adamw(list(self.p.values()), [v.grad for v in self.p.values()], self.state, lr, self.steps, copies=list(self.copies.values()),
                          weight_decay=[0.0 if k in VECTORS or k == "start" else 0.01 for k in self.p])
+            self.copied = {k: v._version for k, v in self.p.items()}
             self.grad.zero_()
             return
         raster.adam_q16(self.flat, self.grad, self.adam, self.bounds, lr=lr, step=self.steps)

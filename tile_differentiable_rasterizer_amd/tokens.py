@@ -541,6 +541,8 @@ def adamw(params, grads, state: AdamWState, lr: float, step: int, beta1: float =
         _refuse("a gradient (and a copy) for each tensor")
     if not state.m.is_cuda:
         _refuse("tensors on the GPU")
+    if not all(map(torch.is_tensor, grads)):
+        _refuse("a gradient for each tensor (None is none)")
     kind = grads[0].dtype if count else torch.float32
     ty = TYPES.get(kind)
     if ty is None:
