@@ -9,6 +9,9 @@
 // to 1/16129 and 1/65025 of the block's largest.  v > 0 keeps a code of 1 at least: a second moment
 // of 0 beside a first moment would make a step of m / eps.
 //
+// Memory bounds it: 48M units with moments in 32 bits take 249 us, 5.4 TB/s; 100M in 8 bits with bfloat16 gradients and copies 321 us,
+// 5.0 TB/s (there the vector units are as busy), and the moments that the codes stand for 5.5 TB/s.
+//
 // A wavefront takes a block of 256 units, four a lane.  Moments are updated, and codes decided, in
 // float64 (the device's float64 rate is its float32 rate): a code is found with float32 roots and set right
 // against its two borders, which are exact.  The tensors' table travels in the kernel's arguments, 64
@@ -266,8 +269,8 @@ hipError_t launch_adamw(int count, const gs_adamw_tensor* tensors, int grad_type
     a.m = mp + done * each;
     a.v = vp + done * each;
     a.bounds = reinterpret_cast<float2*>(bounds) + (bits == 8 ? done : 0);
-    // two blocks a wavefront hide the second one's loads (150M units: 368 -> 347 us); few blocks are spread out (900k units: 8.1 us, two a
-    // wavefront 8.9)
+    // two blocks a wavefront hide the second one's loads (100M units, of 368 us then: 347); few blocks are spread out (900k units: 8.1 us,
+    // two a wavefront 8.9)
     a.each = blocks >= 65536 ? 2 : 1;
     const unsigned groups = (blocks + 4 * a.each - 1) / (4 * a.each);
     if (bits == 8)
