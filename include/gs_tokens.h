@@ -216,7 +216,8 @@ typedef struct gs_weights {
 /* Shape of gs_group_mm_*: x[rows][k], weights[groups][k][n], y[rows][n], all of one type.  Rows are sorted by
  * group: group g has the rows [offsets[g], offsets[g + 1]).  offsets (device, int32 [groups + 1]) do not
  * decrease; they are cut to [0, rows], and nothing outside of the matrices is read or written whatever they
- * hold.  Rows before the first group's and behind the last one's belong to none. */
+ * hold.  Rows before the first group's and behind the last one's belong to none.  Groups are looked up 64 at a time: from about 1024 on
+ * the time grows with their square (16384 groups: 3 ms). */
 typedef struct gs_group_mm {
   int64_t rows, k, n;
   int32_t groups, type;
