@@ -729,3 +729,31 @@ def test_two_graphs_on_one_workspace():
         graphs[i].replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got[i], want[i]))
+
+
+def test_functions_in_a_graph():
+    """Forward and gradients of the torch functions captured together, replayed with eager work between."""
+    x, dy, w, params, copies, states, offs = layer_setup(33)
+    leaf = [t.detach().clone().requires_grad_() for t in (x, w["norm"], w["bias"], copies[0])]
+
+    def run():
+        a, n, b, up = leaf
+        y = tokens.group_mm(tokens.layer_norm(a, n, b), up, offs)
+        return [y.detach(), *torch.autograd.grad(y, leaf, dy.new_ones(y.shape))]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for i in range(3):
+        with torch.no_grad():
+            leaf[0].copy_(normal(gen(70 + i), *x.shape, t=x.dtype))
+        want = run()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), i

@@ -15,7 +15,8 @@ everything else by the C calls (raster.GsError).  Work goes to the current strea
 
 ``norm_rotate``, ``cross_attention``, ``gated8``, ``layer_norm`` and ``group_mm`` are the same operators as
 differentiable torch functions.  Their gradients come from C calls that torch does not record: second
-derivatives through them are an error (``once``).
+derivatives through them are an error (``once``).  Calls and functions may be captured into a graph (lr and step of ``adamw`` as they were then);
+torch's own rule for a captured ``backward()`` holds: no graph made before, on another stream, may still hold the same leaves.
 """
 from __future__ import annotations
 
