@@ -350,7 +350,7 @@ void group_launch(bool over_rows, const GroupArgs& a, hipStream_t s) {
   const int64_t columns = tiles(a.n, BN) * a.splits;
   if (over_rows) {
     // sums of few rows go from block to block as well (64 rows of 16 groups, 2048 x 4096: 88 -> 77 us); long ones, of different lengths, are left
-    // to whichever place is free
+    // to whichever place is free (40000 rows of 40 groups: 57 us, from block to block 67)
     const int64_t all = a.groups * tiles(a.m, BM) * columns;
     const unsigned blocks = (unsigned)(a.rows / a.groups < 512 ? std::min(kSlots, all) : all);
     if constexpr (BM >= 128) k_group_mfma<false, false, true, PARTS, BM, BN, WM, WN><<<blocks, 256, 0, s>>>(a);
