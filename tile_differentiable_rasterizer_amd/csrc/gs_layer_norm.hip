@@ -65,12 +65,15 @@ struct RowSum {
         for (int i = 0; i < N; ++i) space[turn][threadIdx.x / kWave][i] = v[i];
       }
       __syncthreads();
+      // every lane takes one wavefront's, and adds those of its neighbours
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += space[turn][w][i];
+      for (int i = 0; i < N; ++i) {
+        v[i] = space[turn][__lane_id() % kWaves][i];
+        v[i] += dpp_get<0xB1, 0xF>(v[i]);
+        if constexpr (kWaves >= 4) v[i] += dpp_get<0x4E, 0xF>(v[i]);
+        if constexpr (kWaves >= 8) v[i] += dpp_get<0x141, 0xF>(v[i]);
+        if constexpr (kWaves >= 16) v[i] += dpp_get<0x140, 0xF>(v[i]);
+      }
       turn ^= 1;
     }
   }
@@ -130,19 +133,21 @@ __global__ __launch_bounds__(layer_norm_threads(G)) void k_layer_norm(LayerNormA
       for (int j = 0; j < J; ++j) next_g[j].load(gp + G * j * 8, n[j]);
     }
   };
-  // forward, a row's loads run under the row before; back, where the sums take the registers, other workgroups' do (39063 rows of 4096 in
-  // float32: forward 245 -> 228 us, back 350 -> 382)
+  // Forward, a row's loads run under the row before (39063 rows of 4096 in float32: 245 -> 228 us).  Back, where the sums take the
+  // registers, other workgroups' do (there 350 -> 382; bfloat16, 15000 rows of 5000: 126 -> 194), but for rows of two wavefronts in
+  // bfloat16 (60000 of 1000: 95 -> 86).
+  constexpr bool kAhead = !BWD || (sizeof(T) == 2 && G == 128);
   int64_t row = (int64_t)blockIdx.x * kRows + sub;
-  if (!BWD && row < a.rows) load(row);
+  if (kAhead && row < a.rows) load(row);
   for (; row < a.rows; row += step) {  // uniform over the row's lanes
     float x[J][8], g[J][8], s[1] = {0.0f};
-    if (BWD) load(row);
+    if (!kAhead) load(row);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       next_x[j].get(x[j]);
       if constexpr (BWD) next_g[j].get(g[j]);
     }
-    if (!BWD && row + step < a.rows) load(row + step);
+    if (kAhead && row + step < a.rows) load(row + step);
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -299,13 +304,23 @@ LayerNormPlan layer_norm_plan(int width) {
   return {g, chunks > 1024 ? 2 : 1};
 }
 
-int layer_norm_blocks(int64_t rows, int width, bool bwd) {
+// Back, each workgroup leaves a part of dw and db.  Rows of one workgroup, us: float32, 39063 of 4096: 350 with 512 workgroups, 366 with 768,
+// 376 with 1024 (and their parts' sum 5 and 9); bfloat16, of which half as much is on its way, 30000 of 3907: 227 with 512, 186 with 768,
+// 250 with 1024; 10000 of 8192: 106 with 512, 120 with 1024.  Rows of four wavefronts in bfloat16, 3907 of 2048: 17.5 with 512, 15.0 with
+// 1024, 17 with 1536; 50000 of 1500, whose last lanes are idle: 149 with 1024, 117 with 1536; 50000 of 2048: 122 and 129.  Of two
+// wavefronts, 60000 of 1000: 143 with 1024, 95 with 2048.
+int layer_norm_blocks(int64_t rows, int width, bool bwd, int type) {
   const LayerNormPlan p = layer_norm_plan(width);
   const int64_t each = layer_norm_threads(p.g) / p.g, need = (rows + each - 1) / each;
-  // Back, each leaves a part of dw and db: 3907 rows of 2048 in bfloat16 17.5 us with 512, 15.0 with 1024, 60000 of 1000 (workgroups of two
-  // wavefronts) 143 with 1024, 95 with 2048; 39063 of 4096 in float32 350 with 512, 376 with 1024, and their parts' sum 5 and 9.
-  const int most = p.g >= 512 ? 512 : p.g == 128 && rows >= 16384 ? 2048 : 1024;
-  return (int)std::min<int64_t>(need, bwd ? most : 2048);
+  int most = 2048;
+  if (bwd) {
+    most = 1024;
+    if (p.g == 1024) most = 512;
+    if (p.g == 512) most = type == GS_BF16 ? 768 : 512;
+    if (p.g == 256 && type == GS_BF16 && width <= 1536 && rows >= 16384) most = 1536;
+    if (p.g == 128 && rows >= 16384) most = 2048;
+  }
+  return (int)std::min<int64_t>(need, most);
 }
 
 template <typename T, bool BWD>
@@ -331,7 +346,7 @@ void layer_norm_pick(LayerNormPlan p, const LayerNormArgs& a, int blocks, hipStr
 
 size_t layer_norm_workspace_bytes(int64_t rows, int width) {
   if (rows == 0 || width == 0) return 0;
-  const int blocks = layer_norm_blocks(rows, width, true);
+  const int blocks = std::max(layer_norm_blocks(rows, width, true, GS_BF16), layer_norm_blocks(rows, width, true, GS_F32));
   return blocks > 1 ? (size_t)blocks * 2 * ((width + 7) & ~7) * sizeof(float) : 0;
 }
 
@@ -355,7 +370,7 @@ hipError_t launch_layer_norm(int64_t rows, int width, int type, float eps, const
   a.eps = eps;
   a.inv_width = 1.0f / (float)width;
   const LayerNormPlan p = layer_norm_plan(width);
-  const int blocks = layer_norm_blocks(rows, width, dy != nullptr);
+  const int blocks = layer_norm_blocks(rows, width, dy != nullptr, type);
   if (type == GS_BF16)
     dy ? layer_norm_pick<__bf16, true>(p, a, blocks, s) : layer_norm_pick<__bf16, false>(p, a, blocks, s);
   else
