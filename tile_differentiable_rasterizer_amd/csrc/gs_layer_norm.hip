@@ -297,10 +297,16 @@ struct LayerNormPlan {
 };
 
 // Lanes of a row and their chunks: as few lanes as hold it with one each, so that more than half of them work; two from 8192 units on.
-LayerNormPlan layer_norm_plan(int width) {
+// Half as many lanes with two chunks each, where a quarter of the lanes or more would be idle, us: rows of one wavefront instead of two, 60000 of
+// 700: bfloat16 45 -> 32 and back 72 -> 52, float32 72 -> 75 and back 115 -> 105; of four instead of eight, 30000 of 2500: bfloat16 81 -> 77 (40000
+// of 3000: 99 -> 109) and back 145 -> 122, float32 120 -> 128 and back 165 -> 184; of eight instead of sixteen, 15000 of 5000: bfloat16 87 -> 69
+// and back 126 -> 149, float32 121 -> 113 and back 184 either way.  (Of two instead of four: 50000 of 1500 in bfloat16 64 -> 68, back 117 -> 107,
+// 8000 of 1536 back 23 -> 25: left.)
+LayerNormPlan layer_norm_plan(int width, int type, bool bwd) {
   const int chunks = (width + 7) / 8;
   int g = 16;
   while (g < chunks && g < 1024) g *= 2;
+  if (chunks * 4 <= 3 * g && (g == 128 ? type == GS_BF16 || bwd : g == 512 ? type == GS_BF16 && bwd : g == 1024 && !bwd)) return {g / 2, 2};
   return {g, chunks > 1024 ? 2 : 1};
 }
 
@@ -310,7 +316,7 @@ LayerNormPlan layer_norm_plan(int width) {
 // 1024, 17 with 1536; 50000 of 1500, whose last lanes are idle: 149 with 1024, 117 with 1536; 50000 of 2048: 122 and 129.  Of two
 // wavefronts, 60000 of 1000: 143 with 1024, 95 with 2048.
 int layer_norm_blocks(int64_t rows, int width, bool bwd, int type) {
-  const LayerNormPlan p = layer_norm_plan(width);
+  const LayerNormPlan p = layer_norm_plan(width, type, bwd);
   const int64_t each = layer_norm_threads(p.g) / p.g, need = (rows + each - 1) / each;
   int most = 2048;
   if (bwd) {
@@ -327,18 +333,36 @@ template <typename T, bool BWD>
 void layer_norm_pick(LayerNormPlan p, const LayerNormArgs& a, int blocks, hipStream_t s) {
   const dim3 grid(blocks);
   const int threads = layer_norm_threads(p.g);
-  switch (p.g) {
-    case 16: k_layer_norm<T, 16, 1, BWD><<<grid, threads, 0, s>>>(a); break;
-    case 32: k_layer_norm<T, 32, 1, BWD><<<grid, threads, 0, s>>>(a); break;
-    case 64: k_layer_norm<T, 64, 1, BWD><<<grid, threads, 0, s>>>(a); break;
-    case 128: k_layer_norm<T, 128, 1, BWD><<<grid, threads, 0, s>>>(a); break;
-    case 256: k_layer_norm<T, 256, 1, BWD><<<grid, threads, 0, s>>>(a); break;
-    case 512: k_layer_norm<T, 512, 1, BWD><<<grid, threads, 0, s>>>(a); break;
-    default:
-      if (p.j == 1)
-        k_layer_norm<T, 1024, 1, BWD><<<grid, threads, 0, s>>>(a);
-      else
-        k_layer_norm<T, 1024, 2, BWD><<<grid, threads, 0, s>>>(a);
+  switch (p.g * p.j) {
+    case 16: k_layer_norm<T, 16, 1, BWD><<<grid, threads, 0, s>>>(a); return;
+    case 32: k_layer_norm<T, 32, 1, BWD><<<grid, threads, 0, s>>>(a); return;
+    case 64: k_layer_norm<T, 64, 1, BWD><<<grid, threads, 0, s>>>(a); return;
+    case 128:
+      if constexpr (BWD || sizeof(T) == 2)
+        if (p.j == 2) {
+          k_layer_norm<T, 64, 2, BWD><<<grid, threads, 0, s>>>(a);
+          return;
+        }
+      k_layer_norm<T, 128, 1, BWD><<<grid, threads, 0, s>>>(a);
+      return;
+    case 256: k_layer_norm<T, 256, 1, BWD><<<grid, threads, 0, s>>>(a); return;
+    case 512:
+      if constexpr (BWD && sizeof(T) == 2)
+        if (p.j == 2) {
+          k_layer_norm<T, 256, 2, BWD><<<grid, threads, 0, s>>>(a);
+          return;
+        }
+      k_layer_norm<T, 512, 1, BWD><<<grid, threads, 0, s>>>(a);
+      return;
+    case 1024:
+      if constexpr (!BWD)
+        if (p.j == 2) {
+          k_layer_norm<T, 512, 2, BWD><<<grid, threads, 0, s>>>(a);
+          return;
+        }
+      k_layer_norm<T, 1024, 1, BWD><<<grid, threads, 0, s>>>(a);
+      return;
+    default: k_layer_norm<T, 1024, 2, BWD><<<grid, threads, 0, s>>>(a);
   }
 }
 
@@ -369,7 +393,7 @@ hipError_t launch_layer_norm(int64_t rows, int width, int type, float eps, const
   a.width = width;
   a.eps = eps;
   a.inv_width = 1.0f / (float)width;
-  const LayerNormPlan p = layer_norm_plan(width);
+  const LayerNormPlan p = layer_norm_plan(width, type, dy != nullptr);
   const int blocks = layer_norm_blocks(rows, width, dy != nullptr, type);
   if (type == GS_BF16)
     dy ? layer_norm_pick<__bf16, true>(p, a, blocks, s) : layer_norm_pick<__bf16, false>(p, a, blocks, s);
