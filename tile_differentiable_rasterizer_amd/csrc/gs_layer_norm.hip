@@ -122,6 +122,7 @@ __global__ __launch_bounds__(layer_norm_threads(G)) void k_layer_norm(LayerNormA
     if (!BWD && a.b) load_units(a.b + (lane + G * j) * 8, n[j], b[j]);
   }
   const int64_t step = (int64_t)gridDim.x * kRows;
+  const bool ragged = a.width % 8 != 0;
   RowUnits<T> next_x[J], next_g[J];
   auto load = [&](int64_t row) {
     const T* xp = static_cast<const T*>(a.x) + row * a.xs + lane * 8;
@@ -156,11 +157,23 @@ __global__ __launch_bounds__(layer_norm_threads(G)) void k_layer_norm(LayerNormA
     const float mean = s[0] * a.inv_width;
     float t[BWD ? 3 : 1] = {};
 #pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const float mu = n[j] > 0 ? mean : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[j][i] -= mu;
+    }
+    if (ragged) {  // (a row's last chunk may be short)
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i >= n[j]) x[j][i] = 0.0f;
+    }
+#pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float d = i < n[j] ? x[j][i] - mean : 0.0f;
-        x[j][i] = d;
+        const float d = x[j][i];
         t[0] = fmaf(d * a.inv_width, d, t[0]);  // the mean of squares: their sum overflows before it
         if constexpr (BWD) {
           const float gw = g[j][i] * w[j][i];
