@@ -3,8 +3,8 @@
 //
 // What bounds it: with many rows the matrix units, at the clock that their power leaves (78126 rows of 16 groups, 2048 x 8192: forward
 // 2145 us, dx 2120, dW 2090, 1220 to 1255 TFLOP/s, units busy 74 to 81% of the time); with few, the weights' way from
-// memory (64 rows of 16, 2048 x 4096: 38 us, 6.6 TB/s: a part of them stays in the last cache between calls).  In between, rounds of blocks that are not full: 7814 rows of 8,
-// 2048 x 4096: 140, 123 and 135 us, 940 to 1070 TFLOP/s; blocks of 192 x 256, which fill them better, took as long.
+// memory (64 rows of 16, 2048 x 4096: 38 us, 6.6 TB/s: a part of them stays in the last cache between calls).  In between, smaller blocks' tiles from the L2 cache, and
+// their start and end: 7814 rows of 8, 2048 x 4096: 143, 126 and 137 us, 920 to 1040 TFLOP/s (units busy 50 to 62%); blocks of 192 x 256 took as long.
 //
 // A workgroup of four wavefronts makes BM x BN results, a quarter each, over tiles of 64 k that come from
 // memory straight to LDS: two of A, three of B, so that every tile has three quarters of a tile's time or more to

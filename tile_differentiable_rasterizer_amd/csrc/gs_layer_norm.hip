@@ -9,8 +9,8 @@
 // in one exchange: g xh is g d rstd).  The variance is taken about the mean, not as a difference of
 // sums, so that rows far from 0 lose nothing.
 //
-// Memory bounds it: 39063 rows of 4096 in float32 take 226 us forward and 354 + 5 back, 5.7 and 5.4 TB/s.  Short of that, with 3907 rows of
-// 2048 in bfloat16 (8.5 us, 14.4 + 4.1 back), the arithmetic of a unit (vector units busy 85% and 68%) and the sum of the parts.
+// Memory bounds it: 39063 rows of 4096 in float32 take 227 us forward and 360 + 5 back, 5.6 and 5.3 TB/s.  Short of that, with 3907 rows of
+// 2048 in bfloat16 (8.6 us, 14.7 + 4.0 back), the arithmetic of a unit (vector units busy 85% and 68%) and the sum of the parts.
 //
 // Chunks are loaded as vectors at any alignment (the memory takes them; a row of odd length starts
 // anywhere); the row's last chunk, where it is short, goes unit by unit.
