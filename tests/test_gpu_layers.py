@@ -757,3 +757,18 @@ def test_functions_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want)), i
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("order", [(1, 0, 2), (2, 0, 1), (1, 2, 0), (0, 2, 1), (2, 1, 0)])
+def test_group_mm_weights_in_any_order(t, order):
+    """Axes of the weights in any order in memory, so long as one of the last two is dense; gradients lie as they do."""
+    x, w, offs, dy = mm_case(t, [30, 0, 50], 64, 40)
+    lies = w.permute(order).contiguous().permute([order.index(i) for i in range(3)])
+    assert torch.equal(lies, w)
+    if 1 not in lies.stride()[1:]:
+        with pytest.raises(ValueError, match="dense"):
+            tokens.group_mm_fwd(x, lies, offs)
+        return
+    mm_check(x, lies, offs, dy, str(order))
+    assert tokens.group_mm_bwd(dy, x, lies, offs)[1].stride() == lies.stride()

@@ -139,3 +139,10 @@ def test_moments_in_32_bits_are_the_states_own():
 
 def moments_call(blocks):
     return tokens().lib().gs_adamw_moments(blocks, A, A, A, A, A, None)
+
+
+def test_weights_gradients_that_lie_between_each_other():
+    """[k][groups][n] and [n][groups][k] are taken as an output; a row that starts inside of another's is not."""
+    for strides, ok in (((96, 288, 1), True), ((96, 287, 1), False), ((95, 288, 1), False), ((64, 1, 192), True), ((64, 1, 191), False), ((63, 1, 192), False), ((6144, 96, 1), True)):
+        how = dict(bwd=True, dx=None, dw_strides=strides)
+        assert (group_call(rows=0, x=None, y=None, w=None, ws=None, **how) != BAD) == ok, strides

@@ -389,7 +389,7 @@ gs_status group_shape(const gs_group_mm* p, bool bwd) {
   return GS_OK;
 }
 
-// Weights [groups][k][n], one of their axes dense; as an output the elements lie apart.
+// Weights [groups][k][n], one of their last two axes dense; as an output the elements lie apart.
 bool weights_ok(gs_weights* w, int64_t groups, int64_t k, int64_t n, int type, bool out) {
   if (!groups || !k || !n) return true;
   if (groups == 1) w->group_stride = 0;
@@ -398,8 +398,12 @@ bool weights_ok(gs_weights* w, int64_t groups, int64_t k, int64_t n, int type, b
   else if (n == 1) w->n_stride = w->k_stride == 1 ? k : 1;
   if (!w->data || !on(w->data, size_of(type)) || w->group_stride < 0 || w->k_stride < 0 || w->n_stride < 0) return false;
   if (w->n_stride == 1 ? w->k_stride < n && k > 1 : w->k_stride != 1 || (w->n_stride < k && n > 1)) return false;
-  const int64_t most = w->n_stride == 1 ? times(k - 1, w->k_stride) : times(n - 1, w->n_stride);  // of the last row (or column)
-  return most >= 0 && (!out || groups == 1 || w->group_stride >= most + (w->n_stride == 1 ? n : k));
+  const bool along_n = w->n_stride == 1;
+  const int64_t rows = along_n ? k : n, each = along_n ? n : k, stride = along_n ? w->k_stride : w->n_stride;
+  const int64_t most = times(rows - 1, stride), between = times(groups - 1, w->group_stride);  // of the last row, of the last group
+  if (most < 0 || between < 0) return false;
+  // a group's rows one after another, or all groups' first rows, then all their second ones
+  return !out || groups == 1 || w->group_stride >= most + each || (w->group_stride >= each && (rows == 1 || stride >= between + each));
 }
 
 // A stride of a single row is not used.
