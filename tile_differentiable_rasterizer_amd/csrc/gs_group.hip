@@ -11,8 +11,8 @@
 // products: 31.9 us with element loads for what 64 does not divide, 27.8 so).
 //
 // float32 is bound by the matrix units at the power they get: 7814 rows of 8, 2048 x 4096: 800 us, 164 TFLOP/s, 980 TFLOP/s of
-// bfloat16 products.  bfloat16: 18583 rows of 10, 4797 x 777, 370 to 490 TFLOP/s, by loads that start off 16 bytes (the same on 16
-// bytes: 410 to 630) and their way through registers; blocks of 256 x 128 were no faster.
+// bfloat16 products.  bfloat16: 18583 rows of 10, 4797 x 777, 390 to 570 TFLOP/s, by loads that start off 16 bytes (rows on 16 bytes
+// are 10 to 30% faster) and their way through registers; blocks of 256 x 128 were no faster.
 //
 // Where a sum is long and the results are few, several workgroups share it: their parts go to a workspace in
 // float32, and a second kernel adds them in a fixed order.
@@ -221,6 +221,13 @@ struct Sums<float> {
   __device__ __forceinline__ float get(int i) const { return c[i] + rest[i]; }
 };
 
+// The place in a row of `all` that a workgroup takes, which is the `i`-th to start: an eighth of the row to each XCD, whose workgroups are
+// every eighth.
+__device__ __forceinline__ uint32_t group_dealt(uint32_t i, uint32_t all) {
+  const uint32_t q = all / 8, more = all % 8, xcd = i % 8;
+  return xcd * q + min(xcd, more) + i / 8;
+}
+
 // NARROW: a matrix with rows of fewer than eight elements.
 template <typename T, bool A_DENSE, bool B_DENSE, bool OVER_ROWS, bool NARROW, int BN>
 __global__ __launch_bounds__(kStagedThreads, BN == 64 ? 4 : 2) void k_group_staged(GroupArgs a) {
@@ -232,12 +239,11 @@ __global__ __launch_bounds__(kStagedThreads, BN == 64 ? 4 : 2) void k_group_stag
   const int n_tiles = (a.n + BN - 1) / BN;
   int m0, n0, m_end, k0, k_end, g, split;
   if constexpr (OVER_ROWS) {
-    const int m_tiles = (a.m + kStagedTile - 1) / kStagedTile, each = m_tiles * n_tiles * a.splits;
-    const int rank = blockIdx.x / each;
+    const uint32_t m_tiles = (a.m + kStagedTile - 1) / kStagedTile, each = m_tiles * n_tiles * a.splits;
+    const uint32_t rank = blockIdx.x / each, in = blockIdx.x - rank * each;
     g = group_by_length(a, rank);
-    int rest = blockIdx.x - rank * each;
-    split = rest / (m_tiles * n_tiles);
-    rest -= split * m_tiles * n_tiles;
+    const uint32_t i = group_dealt(in, each), rest = i % (m_tiles * n_tiles);
+    split = i / (m_tiles * n_tiles);
     m0 = rest / n_tiles * kStagedTile;
     n0 = rest % n_tiles * BN;
     m_end = a.m;
@@ -245,15 +251,27 @@ __global__ __launch_bounds__(kStagedThreads, BN == 64 ? 4 : 2) void k_group_stag
     k_end = max(group_bound(a, g + 2), k0);
   } else {
     GroupTiles<kStagedTile> spans;
-    spans.look(a, 0);
-    const int nn = blockIdx.x % (n_tiles * a.splits);
-    const GroupSpan s = spans.find(a, blockIdx.x / (n_tiles * a.splits));
+    const uint32_t m_tiles = min(spans.count(a), (uint32_t)((a.rows + kStagedTile - 1) / kStagedTile + min(a.groups + 2, a.rows)));
+    const uint32_t columns = n_tiles * a.splits;
+    if (blockIdx.x >= m_tiles * columns) return;
+    // many blocks of rows: an eighth of them to each XCD, there in patches of sixteen by some columns, so that its cache holds what they share
+    // (bfloat16, 5101 rows of 18, 2625 x 513: 52 -> 39 us; 4001 rows of 2, 4097 x 1025: 130 -> 109); few (float32, 800 rows of 4, 512 x 1024,
+    // back: 20.0, so 22.6): one after another
+    uint32_t mt = blockIdx.x / columns, column = blockIdx.x - mt * columns;
+    constexpr uint32_t kHigh = 16;
+    if (m_tiles > kHigh) {
+      const uint32_t i = group_dealt(blockIdx.x, m_tiles * columns);
+      const uint32_t patch = i / (kHigh * columns), rest = i - patch * kHigh * columns, high = min(kHigh, m_tiles - patch * kHigh);
+      mt = patch * kHigh + rest % high;
+      column = rest / high;
+    }
+    const GroupSpan s = spans.find(a, mt);
     if (s.first >= s.last) return;
     g = s.group;
     m0 = s.first;
     m_end = s.last;
-    split = nn / n_tiles;
-    n0 = (nn - split * n_tiles) * BN;
+    split = column / n_tiles;
+    n0 = (column - split * n_tiles) * BN;
     k0 = 0;
     k_end = g < 0 ? 0 : a.k;
   }
