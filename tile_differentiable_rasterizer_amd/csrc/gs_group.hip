@@ -251,9 +251,13 @@ __global__ __launch_bounds__(kStagedThreads, BN == 64 ? 4 : 2) void k_group_stag
     k_end = max(group_bound(a, g + 2), k0);
   } else {
     GroupTiles<kStagedTile> spans;
-    const uint32_t m_tiles = min(spans.count(a), (uint32_t)((a.rows + kStagedTile - 1) / kStagedTile + min(a.groups + 2, a.rows)));
     const uint32_t columns = n_tiles * a.splits;
-    if (blockIdx.x >= m_tiles * columns) return;
+    uint32_t m_tiles = 0;
+    spans.look(a, 0);
+    if (a.groups + 2 <= kWave) {  // (else counting them would take as long again as finding one)
+      m_tiles = min(spans.last(), (uint32_t)((a.rows + kStagedTile - 1) / kStagedTile + min(a.groups + 2, a.rows)));
+      if (blockIdx.x >= m_tiles * columns) return;
+    }
     // many blocks of rows: an eighth of them to each XCD, there in patches of sixteen by some columns, so that its cache holds what they share
     // (bfloat16, 5101 rows of 18, 2625 x 513: 52 -> 39 us; 4001 rows of 2, 4097 x 1025: 130 -> 109); few (float32, 800 rows of 4, 512 x 1024,
     // back: 20.0, so 22.6): one after another
