@@ -279,8 +279,9 @@ typedef struct gs_adamw_params {
  *  grad_type   GS_F32 or GS_BF16, of all gradients; grad_scale (device, one float32; NULL: 1) multiplies
  *              them: a loss scale's reciprocal, or the factor that clips their norm
  *  bits        32: moments m, v are float32.  8: int8 and uint8 codes with bounds float32 (M, V) for each 256
- *              units of a tensor, the largest |m| and v: m = M (c / 127)^2 with c's sign, c = rint(127 sqrt(|m| / M));
- *              v = V (c / 255)^4, c = rint(255 (v / V)^(1/4)), at least 1 where v > 0.  Codes are decided in float64.
+ *              units of a tensor, the largest |m| and v, rounded: m = M (c / 127)^2 with c's sign, c = rint(127 sqrt(|m| / M)), at
+ *              most 127; v = V (c / 255)^4, c = rint(255 (v / V)^(1/4)), at most 255 and, where v > 0 and V > 0, at least 1.  Codes
+ *              are decided in float64.
  *              A block with a moment that is no finite float32 has NaN for its bound and codes 0.
  *  m, v, bounds   the moments of all tensors one after another, each starting at a multiple of 256 units: tensor
  *              i's at 256 * sum over j < i of ceil(n_j / 256); bounds [blocks][2] (8 bits; else not looked at), m and v 16-byte,

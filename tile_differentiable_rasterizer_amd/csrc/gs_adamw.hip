@@ -174,7 +174,8 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwTable a) {
       // conversion's 2^-24 under one root and two, and 2^-23 for each root), 1.9e-5 of 127 and 5e-5 of 255
       uint32_t cm = 0, cv = 0;
       bool near = true;
-      if (im > 0.0 && iv > 0.0) {
+      // bounds below float32's normal numbers may be a half and more below their largest moments, whose codes then need their limits
+      if (mt >= 0x1p-126f && vt >= 0x1p-126f) {
         near = false;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
