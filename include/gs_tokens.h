@@ -184,7 +184,7 @@ gs_status gs_gate8_bwd(int64_t rows, int64_t width, int32_t act, int32_t type, c
  *          y may be x's own buffer with the same stride, and otherwise does not overlap x
  *  w, b    float32 [width]; NULL: 1 and 0
  * Any stride and alignment (of whole elements) is taken; width is at most 16384.  The variance is a float32: units up to
- * 1e19 from their row's mean.  rows or width of 0: nothing is done.
+ * 1e19 from their row's mean, which is any up to 3e38.  rows or width of 0: nothing is done.
  * Errors: INVALID_ARG, OVERFLOW (a width past 16384, 2^31 rows or more), HIP.
  */
 gs_status gs_layer_norm_fwd(int64_t rows, int64_t width, int32_t type, float eps, const void* x, int64_t x_stride,
@@ -194,6 +194,7 @@ gs_status gs_layer_norm_fwd(int64_t rows, int64_t width, int32_t type, float eps
  * gs_layer_norm_bwd -- gradients of gs_layer_norm_fwd from its inputs (nothing is kept from the
  * forward call) and the gradient of y.  With g = w * dy and rstd = 1 / sqrt(variance + eps):
  *   dx = rstd (g - mean(g) - xh mean(g xh)),  dw = sum over rows of dy * xh,  db = sum over rows of dy.
+ * The sums over a row are float32s: g, and g times a unit's distance from the mean, up to 1e34.
  *  dx        may be dy's or x's own buffer with the same stride, and otherwise overlaps neither
  *  dw, db    float32 [width], overwritten (0 where there are no rows); NULL: not wanted
  *  workspace gs_layer_norm_workspace_bytes(rows, width) bytes, 16-byte aligned (not looked at where neither dw

@@ -34,6 +34,10 @@ struct LayerNormArgs {
   float eps, inv_width;
 };
 
+// A row is summed as 2^-15 of its units, 16384 at most, so that its sum is a float32 wherever its mean is one.  A power of two changes
+// no bit of the mean (but for sums below 2^-111, which no variance that float32 holds has beside it).
+constexpr float kRowScale = 0x1p-15f;
+
 constexpr int layer_norm_threads(int g) { return g > kWave ? g : 256; }  // one row of several wavefronts, or several rows
 
 // Sums over the G lanes of a row, in each of them.
@@ -152,9 +156,9 @@ __global__ __launch_bounds__(layer_norm_threads(G)) void k_layer_norm(LayerNormA
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[0] += x[j][i];
+      for (int i = 0; i < 8; ++i) s[0] = fmaf(x[j][i], kRowScale, s[0]);
     sum_x(s);
-    const float mean = s[0] * a.inv_width;
+    const float mean = s[0] * (a.inv_width / kRowScale);
     float t[BWD ? 3 : 1] = {};
 #pragma unroll
     for (int j = 0; j < J; ++j) {
