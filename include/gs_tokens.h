@@ -208,7 +208,7 @@ gs_status gs_layer_norm_bwd(int64_t rows, int64_t width, int32_t type, float eps
 
 /* Weights of gs_group_mm_*, or their gradients: element (g, i, j) of [groups][k][n] is at
  * g * group_stride + i * k_stride + j * n_stride, in elements; k_stride or n_stride is 1 (an axis of
- * length 1 is not looked at). */
+ * length 1 is not looked at).  The others of an input may be 0: groups, rows or columns that repeat. */
 typedef struct gs_weights {
   void* data;
   int64_t group_stride, k_stride, n_stride;
@@ -228,7 +228,7 @@ typedef struct gs_group_mm {
 /*
  * gs_group_mm_fwd -- the product of every row with its group's weights: y[r] = x[r] W[g(r)].  Rows that
  * belong to no group get 0, whatever x holds there.
- *  x, y        row strides in elements (y's at least n; inputs may repeat rows, and weights, with a stride of 0); y overlaps
+ *  x, y        row strides in elements (y's at least n; inputs may repeat rows with a stride of 0); y overlaps
  *              no input
  *  workspace   gs_group_mm_fwd_workspace_bytes(p) bytes, 16-byte aligned (0 for many shapes: it holds the
  *              parts of a long sum that is split over workgroups)

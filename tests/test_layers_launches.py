@@ -119,3 +119,17 @@ def test_products_workspace_is_bounded():
 
 def test_layer_norm_of_one_workgroup_wants_none():
     assert layer_norm_call(bwd=True, rows=0, ws=None) != WORKSPACE and tokens().lib().gs_layer_norm_workspace_bytes(16, 64) == 0
+
+
+@pytest.mark.parametrize("type", [0, 1])
+def test_weights_that_repeat(launched, type):
+    """Weights, as an input, may repeat along any axis but the dense one; as an output they may not."""
+    hows = [dict(w_strides=s, k=k, n=n) for s, k, n in (((0, 96, 1), 64, 96), ((6144, 0, 1), 64, 96), ((0, 0, 1), 64, 96), ((6144, 1, 0), 64, 96), ((64, 1, 0), 64, 96), ((96, 0, 1), 64, 96),
+                                                        ((64, 1, 0), 64, 1), ((1, 0, 0), 1, 96), ((1, 0, 0), 64, 1), ((0, 0, 0), 1, 1))]
+    for how, (status, launches) in zip(hows, launched([("group_call", dict(how, type=type), -1) for how in hows])):
+        assert status == OK and launches, how
+    for how, (status, launches) in zip(hows, launched([("group_call", dict(how, type=type, bwd=True, dw=None), -1) for how in hows])):
+        assert status == OK and launches, how
+    hows = [how for how in hows if (how["w_strides"], how["n"]) != ((64, 1, 0), 1)]  # (an axis of length 1)
+    for how, (status, _) in zip(hows, launched([("group_call", dict(how, type=type, bwd=True, w_strides=None, dw_strides=how["w_strides"]), -1) for how in hows])):
+        assert status == 1, how

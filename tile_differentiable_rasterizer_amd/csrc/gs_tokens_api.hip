@@ -389,7 +389,8 @@ gs_status group_shape(const gs_group_mm* p, bool bwd) {
   return GS_OK;
 }
 
-// Weights [groups][k][n], one of their last two axes dense; as an output the elements lie apart.
+// Weights [groups][k][n], one of their last two axes dense; an input may repeat along the others (a stride of 0), an output's elements lie
+// apart.
 bool weights_ok(gs_weights* w, int64_t groups, int64_t k, int64_t n, int type, bool out) {
   if (!groups || !k || !n) return true;
   if (groups == 1) w->group_stride = 0;
@@ -397,9 +398,10 @@ bool weights_ok(gs_weights* w, int64_t groups, int64_t k, int64_t n, int type, b
   else if (k == 1) w->k_stride = w->n_stride == 1 ? n : 1;
   else if (n == 1) w->n_stride = w->k_stride == 1 ? k : 1;
   if (!w->data || !on(w->data, size_of(type)) || w->group_stride < 0 || w->k_stride < 0 || w->n_stride < 0) return false;
-  if (w->n_stride == 1 ? w->k_stride < n && k > 1 : w->k_stride != 1 || (w->n_stride < k && n > 1)) return false;
+  if (w->n_stride != 1 && w->k_stride != 1) return false;
   const bool along_n = w->n_stride == 1;
   const int64_t rows = along_n ? k : n, each = along_n ? n : k, stride = along_n ? w->k_stride : w->n_stride;
+  if (rows > 1 && stride < each && (out || stride)) return false;
   const int64_t most = times(rows - 1, stride), between = times(groups - 1, w->group_stride);  // of the last row, of the last group
   if (most < 0 || between < 0) return false;
   // a group's rows one after another, or all groups' first rows, then all their second ones
