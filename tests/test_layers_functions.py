@@ -105,3 +105,31 @@ def test_adamw_wants_every_gradient(monkeypatch):
     for grads in ([None], [torch.ones(3), None]):
         with pytest.raises(ValueError, match="gradient for each"):
             tokens.adamw([torch.ones(3)] * len(grads), grads, State, 1e-3, 1)
+
+
+def test_matrices_that_are_not_dense(t):
+    """group_mm takes a matrix whose rows are not dense, as layer_norm does, and still knows when it was changed."""
+    tokens, _ = t
+    dense = []
+    fwd, bwd = tokens.group_mm_fwd, tokens.group_mm_bwd
+    tokens.group_mm_fwd = lambda x, *more: dense.append(x.stride(1) == 1) or fwd(x, *more)
+    tokens.group_mm_bwd = lambda dy, x, *more: dense.append(x.stride(1) == 1) or bwd(dy, x, *more)
+    g = torch.Generator().manual_seed(7)
+    w, offsets, d = torch.randn(1, 8, 4, generator=g).double(), torch.tensor([0, 6], dtype=torch.int32), torch.randn(6, 4, generator=g).double()
+    for shape, view in (((8, 6), lambda z: z.t()), ((6, 16), lambda z: z[:, ::2]), ((6, 1), lambda z: z.expand(6, 8))):
+        z = torch.randn(shape, generator=g).double().requires_grad_()
+        got, = torch.autograd.grad(tokens.group_mm(view(z), w, offsets), z, d)
+        want, = torch.autograd.grad(view(z) ** 3 @ w[0], z, d)
+        assert torch.allclose(got, want)
+        x = view(z).detach()
+        x = x.clone(memory_format=torch.preserve_format).requires_grad_()
+        a = x * 1
+        y = tokens.group_mm(a, w, offsets)
+        with torch.no_grad():
+            a.mul_(2)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
+    assert dense and all(dense)
+    for wrong in (torch.zeros(8), torch.zeros(2, 3, 8)):
+        with pytest.raises(ValueError, match="matrices"):
+            tokens.group_mm(wrong, w, offsets)

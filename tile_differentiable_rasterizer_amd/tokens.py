@@ -750,19 +750,24 @@ def layer_norm(x, w=None, b=None, eps: float = 1e-5):
     return _LayerNorm.apply(x, w, b, eps)
 
 
+def _dense(x):
+    """The matrix x as it is, or a copy where its rows are not dense."""
+    return x if _matrix(x)[1] <= 1 or x.stride(1) == 1 else x.contiguous()
+
+
 class _GroupMM(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, offsets):
-        ctx.save_for_backward(x, w, offsets)
-        return group_mm_fwd(x, w, offsets)
+        ctx.save_for_backward(x, w, offsets)  # x itself, as _LayerNorm has it
+        return group_mm_fwd(_dense(x), w, offsets)
 
     @staticmethod
     @once
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
-        return (*group_mm_bwd(_rows(dy, w.shape[2]), x, w, offsets, ctx.needs_input_grad[0], ctx.needs_input_grad[1]), None)
+        return (*group_mm_bwd(_rows(dy, w.shape[2]), _dense(x), w, offsets, ctx.needs_input_grad[0], ctx.needs_input_grad[1]), None)
 
 
 def group_mm(x, w, offsets):
-    """group_mm_fwd with gradients for x and w."""
+    """group_mm_fwd with gradients for x and w; an x whose rows are not dense is copied."""
     return _GroupMM.apply(x, w, offsets)
