@@ -64,3 +64,38 @@ def test_feed_forward_against_torch():
     for name, a, b in zip(("y", "x", "up", "down"), (y, *got), (ref.detach(), *want)):
         off = ((a.double() - b).norm() / b.norm()).item()
         assert off <= 5 * 2.0**-8 + 2 * 2.0**-6, (name, off)
+
+
+def test_router_gradient_against_torch():
+    """The router learns through the weight that its softmax gives the chosen expert.  Beside the part's own error (five roundings to
+    bfloat16 and the codes, as above) that gradient has the logits' (half a step of up to 4), the products' with the gradient that comes
+    in, their sum's, its own as a logit's, and the result's: eight more of 2^-8."""
+    model = token_decoder.Decoder(75, experts=4, seed=2)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(1, 75, 256, generator=g, device="cuda").bfloat16()
+    p = {k: v.detach().bfloat16().requires_grad_() for k, v in model.p.items()}
+    d = torch.randn(1, 75, 256, generator=g, device="cuda").bfloat16()
+    got, = torch.autograd.grad(model.feed_forward(x, p), p["router"], d)
+    X, up, down, router = (t.detach().double() for t in (x[0], p["up"], p["down"], p["router"]))
+    router.requires_grad_()
+    expert = torch.softmax((x[0] @ p["router"].detach()).double(), -1).argmax(-1)
+    soft = torch.softmax(X @ router, -1)
+    a, b = torch.matmul(X[:, None], up[expert])[:, 0].chunk(2, -1)
+    y = torch.matmul((torch.nn.functional.silu(a) * b)[:, None], down[expert])[:, 0]
+    want, = torch.autograd.grad(y * soft.gather(1, expert[:, None]), router, d[0].double())
+    off = ((got.double() - want).norm() / want.norm()).item()
+    assert off <= 13 * 2.0**-8 + 2 * 2.0**-6, off
+
+
+@pytest.mark.parametrize("optimizer", ["adam_q16", "adamw"])
+def test_router_moves(optimizer):
+    """A step through the whole model changes the router, and its losses are numbers."""
+    model = token_decoder.Decoder(64, experts=4, optimizer=optimizer, seed=5)
+    before = model.p["router"].detach().clone()
+    sum(x.square().mean() for x in model(torch.rand(2, 3, 64, 64, generator=torch.Generator(device="cuda").manual_seed(6), device="cuda"))).backward()
+    grad = model.p["router"].grad.clone()
+    assert torch.isfinite(grad).all() and (grad != 0).any()
+    model.step(1e-3)
+    assert torch.isfinite(model.p["router"]).all() and not torch.equal(model.p["router"], before)
+    losses = token_decoder.train(steps=8, size=64, views=2, n_tokens=64, say=None, experts=4, optimizer=optimizer)
+    assert len(losses) == 8 and all(abs(x) < float("inf") for x in losses)
