@@ -282,7 +282,12 @@ typedef struct gs_adamw_params {
  *  bits        32: moments m, v are float32.  8: int8 and uint8 codes with bounds float32 (M, V) for each 256
  *              units of a tensor, the largest |m| and v, rounded: m = M (c / 127)^2 with c's sign, c = rint(127 sqrt(|m| / M)), at
  *              most 127; v = V (c / 255)^4, c = rint(255 (v / V)^(1/4)), at most 255 and, where v > 0 and V > 0, at least 1.  Codes
- *              are decided in float64.
+ *              are decided in float64.  They are rounded to nearest after every step, so that a moment decays by whole codes only.
+ *              While another unit holds the block's bound, m's codes of up to 0.5 / (1 - sqrt(beta1)) stay as they are (9 with a beta1
+ *              of 0.9: 0.5% of M), and v's of up to 0.5 / (1 - beta2^(1/4)) (199 with a beta2 of 0.99, all with 0.999): a unit whose
+ *              gradients end or shrink beside such a one keeps that much of a first moment, and a second one that is too large for
+ *              them, for as long as the other lasts.  A block whose gradients end together decays as a whole.  Where units of a
+ *              block fare differently for long, 32 bits hold the averages that the formula means.
  *              A block with a moment that is no finite float32 has NaN for its bound and codes 0.
  *  m, v, bounds   the moments of all tensors one after another, each starting at a multiple of 256 units: tensor
  *              i's at 256 * sum over j < i of ceil(n_j / 256); bounds [blocks][2] (8 bits; else not looked at), m and v 16-byte,

@@ -89,3 +89,28 @@ def test_moments_that_die_out_keep_their_signs():
         tokens.adamw([p], [zero], state, 1e-3, step)
         if step > 700:
             assert (state.m.sign() * sign >= 0).all(), step
+
+
+@pytest.mark.parametrize("beta2, last", [(0.999, 255), (0.99, 199), (0.95, 39)])
+def test_codes_that_stay(beta2, last):
+    """What the header says of a run: beside a unit that holds the bounds, codes without gradients fall to 0.5 / (1 - beta^(1 / power)) and
+    stay there; without that unit's gradient the block decays as a whole, its codes unchanged."""
+    assert int(0.5 / (1 - 0.9**0.5)) == 9 and min(int(0.5 / (1 - beta2**0.25)), 255) == last
+    p, grad = torch.zeros(256, device="cuda"), torch.zeros(256, device="cuda")
+    state = tokens.adamw_state([p])
+    m = (torch.arange(256) % 128 * (1 - torch.arange(256) // 128 * 2)).to(torch.int8)
+    v = torch.arange(256).clamp(min=1).to(torch.uint8)
+    m[255], v[255] = 127, 255
+    state.m.copy_(m), state.v.copy_(v), state.bounds.fill_(1.0)
+    grad[255] = 1.0  # with moments of 1 already: they stay
+    for step in range(1, 2001):
+        tokens.adamw([p], [grad], state, 1e-3, step, 0.9, beta2)
+    want_m, want_v = m.int().clamp(-9, 9), v.int().clamp(max=last)
+    want_m[255], want_v[255] = 127, 255
+    assert torch.equal(state.m.cpu().int(), want_m) and torch.equal(state.v.cpu().int(), want_v)
+    grad.zero_()
+    for step in range(2001, 2101):
+        tokens.adamw([p], [grad], state, 1e-3, step, 0.9, beta2)
+    assert torch.equal(state.m.cpu().int(), want_m) and torch.equal(state.v.cpu().int(), want_v)
+    want = torch.tensor([0.9**100, beta2**100], dtype=torch.float64)
+    assert ((state.bounds[0].cpu().double() - want).abs() <= 101 * 2.0**-24 * want).all()  # a bound is rounded once a step

@@ -510,7 +510,9 @@ def _blocks(tensors) -> int:
 
 
 def adamw_state(params, bits: int = 8) -> AdamWState:
-    """Zero moments for ``params``, in 8 bits or in 32."""
+    """Zero moments for ``params``, in 8 bits or in 32.  In 8 bits a moment decays by whole codes only: beside a unit that keeps the
+    bound of its 256 up, small first moments and (with a beta2 past 0.992) all second ones stay as they are while their gradients are
+    0, so tensors whose neighbouring units fare differently for long want 32."""
     if bits not in (8, 32):
         _refuse("bits: 8 or 32")
     if not params:
