@@ -349,10 +349,13 @@ void group_launch(bool over_rows, const GroupArgs& a, hipStream_t s) {
   constexpr int64_t kSlots = 256 * group_places(BM, BN);  // workgroups at a time
   const int64_t columns = tiles(a.n, BN) * a.splits;
   if (over_rows) {
-    // sums of few rows go from block to block as well (64 rows of 16 groups, 2048 x 4096: 88 -> 77 us); long ones, of different lengths, are left
-    // to whichever place is free (40000 rows of 40 groups: 57 us, from block to block 67)
+    // Short sums go from block to block as well; long ones, of different lengths, are left to whichever place is free.  us, left and from block
+    // to block, groups of one length and of lengths between 0 and 4 times that: 16 groups, 2048 x 4096, of 4 rows: 93.5, 81.0 and 86.8, 75.4; 128:
+    // 113, 107 and 114, 104; 256: 136, 130 and 134, 132; 384: 162, 158 and 158, 157; 1024: 266, 275 and 271, 282.  40 groups, 1024 x 1024, of 64:
+    // 38.1, 36.0 and 35.8, 35.4; 128: 43.3, 41.1 and 38.4, 40.8; 256: 50.7, 49.5 and 44.7, 51.0; 1024: 101, 104 and 89, 117.  64 groups, 512 x 2048, of
+    // 128: 62.1, 61.3 and 59.1, 56.7; 256: 76.8, 69.7 and 71.0, 70.3; 512: 107, 104 and 102, 115.
     const int64_t all = a.groups * tiles(a.m, BM) * columns;
-    const unsigned blocks = (unsigned)(a.rows / a.groups < 512 ? std::min(kSlots, all) : all);
+    const unsigned blocks = (unsigned)(a.rows / a.groups < 256 ? std::min(kSlots, all) : all);
     if constexpr (BM >= 128) k_group_mfma<false, false, true, PARTS, BM, BN, WM, WN><<<blocks, 256, 0, s>>>(a);
     return;
   }
