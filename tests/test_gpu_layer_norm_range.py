@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from test_gpu_layers import ln_check
 from test_gpu_tokens import TYPES, U, close, gen, half_step, normal
 from tile_differentiable_rasterizer_amd import tokens
 
@@ -44,3 +45,11 @@ def test_mixed_with_ordinary_rows(t, width):
     far[::3] = 2e38
     keep = [i for i in range(12) if i % 3]
     assert torch.equal(tokens.layer_norm_fwd(far, w)[keep], y[keep]) and torch.equal(tokens.layer_norm_bwd(dy, far, w)[0][keep], dx[keep])
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("rows, width", [(12287, 800), (12288, 800), (12289, 1024), (12290, 1300), (12300, 2047), (12301, 2048), (12302, 600)])
+def test_many_rows_by_workgroups(rows, width, t):
+    """Each side of where the backward pass takes more workgroups."""
+    g = gen(rows)
+    ln_check(normal(g, rows, width, t=TYPES[t]), normal(g, width) + 1, None, 1e-5, normal(g, rows, width, t=TYPES[t]))

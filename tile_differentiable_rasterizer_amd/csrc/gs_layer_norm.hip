@@ -327,11 +327,17 @@ LayerNormPlan layer_norm_plan(int width, int type, bool bwd) {
   return {g, chunks > 1024 ? 2 : 1};
 }
 
-// Back, each workgroup leaves a part of dw and db.  Rows of one workgroup, us: float32, 39063 of 4096: 350 with 512 workgroups, 366 with 768,
-// 376 with 1024 (and their parts' sum 5 and 9); bfloat16, of which half as much is on its way, 30000 of 3907: 227 with 512, 186 with 768,
-// 250 with 1024; 10000 of 8192: 106 with 512, 120 with 1024.  Rows of four wavefronts in bfloat16, 3907 of 2048: 17.5 with 512, 15.0 with
-// 1024, 17 with 1536; 50000 of 1500, whose last lanes are idle: 149 with 1024, 117 with 1536; 50000 of 2048: 122 and 129.  Of two
-// wavefronts, 60000 of 1000: 143 with 1024, 95 with 2048.
+// Back, each workgroup leaves a part of dw and db, and few rows are not worth many parts.  Workgroups at most, us with the parts' sum:
+//   16 and 8 wavefronts a row.  float32: 8192 rows of 4096: 81.5 with 512, 82.3 with 768, 85.4 with 1024; 10000 of 8192: 106 with 512, 120 with
+//   1024.  bfloat16, of which half as much is on its way: 1024 of 3500: 18.7 with 512, 19.7 with 768, 24.2 with 1024; 8192: 47.4, 42.7, 50.4; 30000:
+//   193, 156, 201; of 4096: 149.6, 150.4, 178.
+//   Four, from 12288 rows on bfloat16 1536 but for rows of 2048, else 1024.  50000 rows, with 1024 and 1536: of 1100 138, 110; 1536 103, 98; 1900 160,
+//   130; 2047 183, 156; 2048 119, 125.  12288 rows: of 1100 35.2, 32.2; 1536 29.5, 29.1; 1800 36.0, 35.6.  8192: 26.7, 25.5; 23.2, 23.9; 28.0, 29.0.
+//   4096: 19.5, 20.3; 17.3, 18.5; 21.1, 22.3.  float32, 50000: of 1032 128, 136; 2048 245, 254.
+//   Two, from 12288 rows on bfloat16 2048, float32 1536 but for rows of 1024, else 1024.  60000 rows, with 1024, 1536 and 2048: bfloat16 of 800 112, 91,
+//   77; 1024 81, 81, 77; float32 of 800 129, 114, 120; 1000 144, 145, 153; 1024 135, 141, 147.  12288 rows: bfloat16 of 800 26.6, 24.1, 23.2; 1000 28.0,
+//   26.3, 26.3; float32 of 800 28.3, 26.6, 27.3; 1000 33.0, 32.5, 34.1.  8192: 20.8, 19.7, 19.5; 22.6, 22.0, 22.8; 22.2, 21.4, 22.2; 26.0, 25.8, 27.0 (of 1024
+//   in bfloat16 19.0, 20.0, 20.9).  4096: 15.4, 16.5, 17.8; 18.1, 19.7, 21.7; 15.6, 15.6, 16.7; 18.4, 19.3, 21.2.
 int layer_norm_blocks(int64_t rows, int width, bool bwd, int type) {
   const LayerNormPlan p = layer_norm_plan(width, type, bwd);
   const int64_t each = layer_norm_threads(p.g) / p.g, need = (rows + each - 1) / each;
@@ -340,8 +346,9 @@ int layer_norm_blocks(int64_t rows, int width, bool bwd, int type) {
     most = 1024;
     if (p.g == 1024) most = 512;
     if (p.g == 512) most = type == GS_BF16 ? 768 : 512;
-    if (p.g == 256 && type == GS_BF16 && width <= 1536 && rows >= 16384) most = 1536;
-    if (p.g == 128 && rows >= 16384) most = 2048;
+    if (rows >= 12288 && p.g == 256 && type == GS_BF16 && width < 2048) most = 1536;
+    if (rows >= 12288 && p.g == 128 && type == GS_BF16) most = 2048;
+    if (rows >= 12288 && p.g == 128 && type == GS_F32 && width < 1024) most = 1536;
   }
   return (int)std::min<int64_t>(need, most);
 }
