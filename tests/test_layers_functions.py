@@ -133,3 +133,44 @@ def test_matrices_that_are_not_dense(t):
     for wrong in (torch.zeros(8), torch.zeros(2, 3, 8)):
         with pytest.raises(ValueError, match="matrices"):
             tokens.group_mm(wrong, w, offsets)
+
+
+@pytest.fixture
+def reached(monkeypatch):
+    """tokens on CPU tensors, and the C calls that would be made (their arguments are checked, nothing runs)."""
+    from tile_differentiable_rasterizer_amd import tokens
+
+    calls = []
+    monkeypatch.setattr(tokens, "_type", lambda t: tokens.TYPES[t.dtype])
+    monkeypatch.setattr(tokens, "_launch", lambda name, *args: calls.append(name))
+    return tokens, calls
+
+
+def test_weights_gradients_of_another_number_of_groups_are_refused(reached):
+    """Fewer groups than the weights have would be written past their end."""
+    tokens, calls = reached
+    x, dy, w, offsets = torch.zeros(6, 8), torch.zeros(6, 4), torch.zeros(3, 8, 4), torch.zeros(4, dtype=torch.int32)
+    for shape in ((1, 8, 4), (2, 8, 4), (4, 8, 4), (0, 8, 4), (3, 4, 8), (3, 8, 5), (3, 7, 4), (8, 4)):
+        with pytest.raises(ValueError):
+            tokens.group_mm_bwd(dy, x, w, offsets, dw=torch.zeros(shape))
+    assert not calls
+    dw = torch.zeros(3, 8, 4)
+    assert tokens.group_mm_bwd(dy, x, w, offsets, dw=dw)[1] is dw and calls == ["gs_group_mm_bwd"]
+
+
+def test_outputs_and_state_of_other_sizes_are_refused(reached):
+    """What the other calls write to has the size that they write."""
+    tokens, calls = reached
+    x, w = torch.zeros(6, 8), torch.zeros(3, 8, 4)
+    offsets = torch.zeros(4, dtype=torch.int32)
+    for wrong in (torch.zeros(5, 8), torch.zeros(6, 7), torch.zeros(7, 8), torch.zeros(6, 8, dtype=torch.bfloat16), torch.zeros(8, 6).t()):
+        for call in (lambda: tokens.layer_norm_fwd(x, out=wrong), lambda: tokens.layer_norm_bwd(x, x, dx=wrong), lambda: tokens.layer_norm_bwd(wrong, x),
+                     lambda: tokens.group_mm_bwd(torch.zeros(6, 4), x, w, offsets, dx=wrong)):
+            with pytest.raises(ValueError):
+                call()
+    for call in (lambda: tokens.group_mm_fwd(x, w, offsets, out=torch.zeros(6, 5)), lambda: tokens.group_mm_fwd(x, w, offsets, out=torch.zeros(5, 4)), lambda: tokens.group_mm_fwd(x, w, offsets[:3]),
+                 lambda: tokens.group_mm_fwd(x, w[:, :7], offsets), lambda: tokens.group_mm_bwd(torch.zeros(6, 5), x, w, offsets), lambda: tokens.layer_norm_fwd(x, torch.zeros(7)),
+                 lambda: tokens.layer_norm_fwd(x, None, torch.zeros(9)), lambda: tokens.layer_norm_bwd(x, x, torch.zeros(7))):
+        with pytest.raises(ValueError):
+            call()
+    assert not calls

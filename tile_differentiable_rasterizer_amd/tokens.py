@@ -430,10 +430,11 @@ def layer_norm_bwd(dy, x, w=None, eps: float = 1e-5, with_dw: bool = True, with_
 # -- products grouped by rows ----------------------------------------------------------------
 
 
-def _weights(w, x, k, n=None) -> GsWeights:
+def _weights(w, x, k, of=None) -> GsWeights:
+    """Weights for rows of k units; ``of``: the weights that these are the gradients of."""
     if w.dim() != 3:
         _refuse("weights [groups][k][n]")
-    _same(x, w, (w.shape[0], k, w.shape[2] if n is None else n))
+    _same(x, w, (w.shape[0], k, w.shape[2]) if of is None else of.shape)
     g, i, j = w.stride()
     if j != 1 and i != 1 and w.shape[1] > 1 and w.shape[2] > 1:
         _refuse("weights with one of their last two axes dense")
@@ -484,7 +485,7 @@ def group_mm_bwd(dy, x, w, offsets, with_dx: bool = True, with_dw: bool = True, 
         dw = torch.empty_like(w)
     ws, n = _workspace(workspace, lib().gs_group_mm_bwd_workspace_bytes(p), x)
     _launch("gs_group_mm_bwd", x, p, dy.data_ptr(), ds, x.data_ptr(), _stride(x, x, p.rows, p.k), ww, _ptr(dx),
-            0 if dx is None else _stride(dx, x, p.rows, p.k), GsWeights() if dw is None else _weights(dw, x, p.k, p.n),
+            0 if dx is None else _stride(dx, x, p.rows, p.k), GsWeights() if dw is None else _weights(dw, x, p.k, w),
             _ptr(ws), n)
     return dx, dw
 
