@@ -26,6 +26,7 @@ struct GroupArgs {
 // Blocks of results that a workgroup makes: on the matrix units straight from LDS, and staged through registers.
 enum { kGroup256x256, kGroup128x256, kGroup128x128, kGroup32x256, kGroup32x128, kGroupStaged128, kGroupStaged64, kGroupTiles };
 
+inline int64_t tiles(int64_t n, int64_t each) { return (n + each - 1) / each; }
 __host__ __device__ constexpr int group_part_width(int n) { return (n + 7) & ~7; }
 
 // Part `split` of k0 .. k_end, in whole steps of `step`.

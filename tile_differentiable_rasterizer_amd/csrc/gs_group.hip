@@ -422,8 +422,6 @@ __global__ __launch_bounds__(256) void k_group_join(GroupArgs a, int64_t rows, i
 
 namespace {
 
-int64_t tiles(int64_t n, int64_t each) { return (n + each - 1) / each; }
-
 // Whether every row of the three matrices starts on 16 bytes and holds whole chunks of 16, at distances that
 // a thread's 32-bit offsets reach.
 bool group_aligned(bool over_rows, const GroupArgs& a) {

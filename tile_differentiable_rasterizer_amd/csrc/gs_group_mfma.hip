@@ -342,8 +342,6 @@ __global__ __launch_bounds__(256, group_places(BM, BN)) void k_group_mfma(GroupA
 
 namespace {
 
-int64_t tiles(int64_t n, int64_t each) { return (n + each - 1) / each; }
-
 template <bool PARTS, int BM, int BN, int WM, int WN>
 void group_launch(bool over_rows, const GroupArgs& a, hipStream_t s) {
   constexpr int64_t kSlots = 256 * group_places(BM, BN);  // workgroups at a time

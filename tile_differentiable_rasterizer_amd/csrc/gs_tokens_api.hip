@@ -43,7 +43,9 @@ using namespace gs;
 namespace {
 
 constexpr int64_t kMost = (int64_t)1 << 31;    // lengths, vectors, blocks of codes: counted in 31 bits
-constexpr int64_t kGroups = (int64_t)1 << 24;  // workgroups of 256 threads: a grid has fewer than 2^32 work items
+constexpr int64_t kGrid = (int64_t)1 << 24;    // workgroups of 256 threads: a grid has fewer than 2^32 work items
+constexpr int64_t kMostUnits = 1 << 24;        // k and n of a grouped product: with a tile more they are still counted in 31 bits
+constexpr int64_t kMostGroups = 1 << 16;
 
 bool on(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 int64_t size_of(int type) { return type == GS_BF16 ? 2 : 4; }
@@ -132,7 +134,7 @@ gs_status attn_shape(const gs_cross_attn* p, bool bwd) {
   const int64_t vq = times(all, rows), vk = times(all, p->k_len);
   // workgroups: 128 rows, and 128 keys for the gradients (in parts only where there are few)
   const int64_t wide = times(all, ((bwd && p->k_len > rows ? p->k_len : rows) + 127) / 128);
-  if (vq < 0 || vk < 0 || wide < 0 || wide >= kGroups || vq / 2 >= kMost || vk / 2 >= kMost) return GS_ERR_OVERFLOW;
+  if (vq < 0 || vk < 0 || wide < 0 || wide >= kGrid || vq / 2 >= kMost || vk / 2 >= kMost) return GS_ERR_OVERFLOW;
   return GS_OK;
 }
 
@@ -379,9 +381,9 @@ namespace {
 gs_status group_shape(const gs_group_mm* p, bool bwd) {
   if (!p || p->rows < 0 || p->k < 0 || p->n < 0 || p->groups < 0 || (p->type != GS_BF16 && p->type != GS_F32)) return GS_ERR_INVALID_ARG;
   if (!p->offsets || !on(p->offsets, 4)) return GS_ERR_INVALID_ARG;
-  if (p->rows >= kMost - 256 || p->k > kGroups || p->n > kGroups || p->groups > 65536) return GS_ERR_OVERFLOW;
+  if (p->rows >= kMost - 256 || p->k > kMostUnits || p->n > kMostUnits || p->groups > kMostGroups) return GS_ERR_OVERFLOW;
   // each factor is below 2^31, the counts below 2^62; a workgroup has 512 threads
-  constexpr int64_t kMostTiles = kGroups / 2;
+  constexpr int64_t kMostTiles = kGrid / 2;
   if (!bwd && group_tiles(false, p->rows, p->rows, p->n, p->groups) >= kMostTiles) return GS_ERR_OVERFLOW;
   if (bwd && (group_tiles(false, p->rows, p->rows, p->k, p->groups) >= kMostTiles ||
               group_tiles(true, p->rows, p->k, p->n, p->groups) >= kMostTiles || group_tiles(true, p->rows, p->n, p->k, p->groups) >= kMostTiles))
