@@ -218,7 +218,8 @@ typedef struct gs_weights {
  * group: group g has the rows [offsets[g], offsets[g + 1]).  offsets (device, int32 [groups + 1]) do not
  * decrease; they are cut to [0, rows], and nothing outside of the matrices is read or written whatever they
  * hold.  Rows before the first group's and behind the last one's belong to none.  Groups are looked up 64 at a time: from about 1024 on
- * the time grows with their square (16384 groups: 3 ms). */
+ * the time grows with their square (16384 groups: 3.4 ms in bfloat16
+ * with rows on 16 bytes, 2.0 ms otherwise). */
 typedef struct gs_group_mm {
   int64_t rows, k, n;
   int32_t groups, type;

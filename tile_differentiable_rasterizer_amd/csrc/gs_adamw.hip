@@ -9,8 +9,8 @@
 // to 1/16129 and 1/65025 of the block's largest.  v > 0 keeps a code of 1 at least: a second moment
 // of 0 beside a first moment would make a step of m / eps.
 //
-// Memory bounds it: 48M units with moments in 32 bits take 249 us, 5.4 TB/s; 100M in 8 bits with bfloat16 gradients and copies 316 us,
-// 5.1 TB/s (there the vector units are as busy), and the moments that the codes stand for 5.5 TB/s.
+// Memory bounds it: 48M units with moments in 32 bits take 249 us, 5.4 TB/s; 100M in 8 bits with bfloat16 gradients and copies 313 us,
+// 5.1 TB/s (the vector units are busy 85% of it), and the moments that the codes stand for 5.6 TB/s.
 //
 // A wavefront takes a block of 256 units, four a lane.  Moments are updated, and codes decided, in
 // float64 (the device's float64 rate is its float32 rate): a code is found with float32 roots and set right

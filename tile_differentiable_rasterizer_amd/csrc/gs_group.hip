@@ -11,8 +11,9 @@
 // products: 31.9 us with element loads for what 64 does not divide, 27.8 so).
 //
 // float32 is bound by the matrix units at the power they get: 7814 rows of 8, 2048 x 4096: 800 us, 164 TFLOP/s, 980 TFLOP/s of
-// bfloat16 products.  bfloat16: 18583 rows of 10, 4797 x 777, 390 to 570 TFLOP/s, by loads that start off 16 bytes (rows on 16 bytes
-// are 10 to 30% faster) and their way through registers; blocks of 256 x 128 were no faster.
+// bfloat16 products.  bfloat16: 18583 rows of 10, 4797 x 777, 352, 380 and 270 us, 365 to 515 TFLOP/s, by loads that start off 16 bytes
+// (this kernel is 10 to 30% faster on rows on 16 bytes, the other takes 214, 199 and 194 us for 4800 x 776) and their way through registers; blocks of 256 x 128
+// were no faster.
 //
 // Where a sum is long and the results are few, several workgroups share it: their parts go to a workspace in
 // float32, and a second kernel adds them in a fixed order.
