@@ -455,7 +455,7 @@ def _group_shape(x, w, offsets) -> tuple:
 def group_mm_fwd(x, w, offsets, out=None, workspace=None, stream=None):
     """gs_group_mm_fwd: every row of x [rows, k] times its group's weights, y [rows, n].  w [groups, k, n], either of its
     last two axes dense (a linear layer's weights [groups, n, k] transposed); offsets int32 [groups + 1] on the GPU: group
-    g has the rows from offsets[g] to offsets[g + 1].  Rows of no group get 0."""
+    g has the rows from offsets[g] to offsets[g + 1].  Rows of no group get 0.  ``out``: a tensor to write to, apart from the inputs."""
     if stream is not None:
         return _on(stream, group_mm_fwd, x, w, offsets, out, workspace)
     p, ww = _group_shape(x, w, offsets)
@@ -470,7 +470,7 @@ def group_mm_fwd(x, w, offsets, out=None, workspace=None, stream=None):
 def group_mm_bwd(dy, x, w, offsets, with_dx: bool = True, with_dw: bool = True, dx=None, dw=None, workspace=None,
                  stream=None) -> tuple:
     """gs_group_mm_bwd: (dx or None, dw or None) from the forward call's inputs and the gradient of its result; ``dx``,
-    ``dw``: tensors to write to (dw lies as w does where it is not given)."""
+    ``dw``: tensors to write to, apart from the inputs and each other (dw lies as w does where it is not given)."""
     if stream is not None:
         return _on(stream, group_mm_bwd, dy, x, w, offsets, with_dx, with_dw, dx, dw, workspace)
     p, ww = _group_shape(x, w, offsets)
